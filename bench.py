@@ -42,7 +42,7 @@ GB = 1e9
 # sources hash to the value recorded in it
 DECODE_PROFILE = os.path.join(ROOT, "profiles", "decode_split_kernel_long_context.md")
 DECODE_SOURCES = [os.path.join(ROOT, "nvfp4_paged_kv_gb300", "csrc", f)
-                  for f in ("decode.cu", "common.cuh")]
+                  for f in ("decode.cu", "decode_kernel.cuh", "common.cuh")]
 METRIC = "NVFP4 paged decode-attn KV GB/s + quant/dequant GB/s, % of GB300 HBM peak"
 WORKLOAD = ("page round-trip 4096x32x8x128 K+V (amax, encode, decode->BF16, decode->FP8) + "
             "long-context decode 8 seqs U[32K,128K] 64q/8kv d128 page64 split-KV")

@@ -91,6 +91,7 @@ typedef enum nvfp4kv_status {
 #define NVFP4KV_STATUS_PAGE_OOB 0x1      /* a page id was outside [0, pool_pages): skipped        */
 #define NVFP4KV_STATUS_BAD_SEQ_LEN 0x2   /* seq_len < 0 or > max_pages_per_seq * T: seq skipped   */
 #define NVFP4KV_STATUS_TIMEOUT 0x4       /* a bounded retry loop on a workspace word gave up       */
+#define NVFP4KV_STATUS_BAD_POSITION 0x8  /* a row's position was outside its table: row skipped    */
 
 typedef enum nvfp4kv_packing {
     NVFP4KV_PACK_DIM_PAIRS = 0,   /* a byte holds two head dims of one token (K cache)          */
@@ -331,6 +332,148 @@ nvfp4kv_status nvfp4_paged_decode_attention_noalloc(
     int32_t pool_pages, const int32_t* page_table, int32_t max_pages_per_seq,
     const int32_t* seq_lens, float sm_scale, int32_t max_num_splits, void* out, float* lse,
     int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Append of a step's rows to the cache: the K and V rows that a projection just produced (one per
+ * new token, any number of tokens of any sequences) are rotated by their positions and written as
+ * NVFP4 at their token slots, and the queries are rotated with them. The source pages write whole
+ * pages of a chunk ("Path 2: Chunked prefill / Extend") and quantize the current token on the way
+ * into the cache in "Path 3: Decode"; this call serves both, a token at a time.
+ *
+ * Row n goes to token slot slots[n] = page * T + token. With (c, s) the table row of positions[n],
+ * every rotated pair (x1, x2) of q and k becomes
+ *   x1' = fp32(fp32(x1 c) - fp32(x2 s)),  x2' = fp32(fp32(x2 c) + fp32(x1 s))
+ * and K (rotated, not rounded to 16 bits in between) and V are encoded as in
+ * nvfp4_kv_quantize_pages: K in NVFP4KV_PACK_DIM_PAIRS, V in NVFP4KV_PACK_TOKEN_PAIRS
+ * (layout.packing is not read). The cache bytes of every other token keep their values: the other
+ * nibbles of a V byte whose second token is not written by the call are left alone, also while
+ * another call writes them.
+ *   src_dtype      of q, k and v: NVFP4KV_BF16 or NVFP4KV_FP16 (else NVFP4KV_ERR_UNSUPPORTED)
+ *   num_rows       rows of q, k, v; num_q_heads = 0 appends K and V alone (q, q_out not read)
+ *   q, k, v        row n of q at q + n * q_row_stride elements, [heads][D] contiguous in a row (so
+ *                  the three may be slices of one projection); 16-byte aligned, strides multiples
+ *                  of 8 and at least heads * D
+ *   slots          int64 [num_rows]; -1 marks a padding row: nothing of it is read or written. Two
+ *                  rows of a call with the same slot race (the slot then holds bytes of either)
+ *   rotary         host pointer, NULL = no rotation (positions is not read then)
+ *   positions      int32 [num_rows], 0 <= position < rotary->max_positions
+ *   k_global_scale, v_global_scale   device scalars g (NULL = 1)
+ *   k_data, k_scales, v_data, v_scales, pool_pages   the NVFP4 pools
+ *   out_dtype      of q_out, k_out, v_out: NVFP4KV_BF16 or NVFP4KV_FP16
+ *   q_out          rotated queries, row stride q_out_row_stride (as for q); must not overlap q
+ *   k_out, v_out   optional [num_rows][H][D]: the rows as the cache now holds them (the values of
+ *                  nvfp4_kv_dequantize_pages), for attention within the chunk itself
+ * A slot outside the pool (PAGE_OOB) or a position outside the table (BAD_POSITION) skips its row:
+ * the cache and the outputs of that row keep what they held. Supported: head_dim 64, 128 or 256;
+ * an even page_size.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum nvfp4kv_rotary_style {
+    NVFP4KV_ROTARY_HALVES = 0, /* dim i pairs with dim i + dims/2 of the rotated dims */
+    NVFP4KV_ROTARY_PAIRS = 1   /* dim 2i pairs with dim 2i + 1 */
+} nvfp4kv_rotary_style;
+
+typedef struct nvfp4kv_rotary {
+    int32_t style;         /* nvfp4kv_rotary_style */
+    int32_t first_dim;     /* first rotated head dim, a multiple of 16 */
+    int32_t dims;          /* rotated dims, a multiple of 32; first_dim + dims <= head_dim */
+    int32_t max_positions; /* rows of the table */
+    const float* cos_sin;  /* device [max_positions][dims]: dims/2 cosines, then dims/2 sines;
+                              16-byte aligned */
+} nvfp4kv_rotary;
+
+nvfp4kv_status nvfp4_kv_append(
+    const nvfp4kv_layout* layout, nvfp4kv_dtype src_dtype, int32_t num_rows, int32_t num_q_heads,
+    const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+    int64_t v_row_stride, const int64_t* slots, const nvfp4kv_rotary* rotary,
+    const int32_t* positions, const float* k_global_scale, const float* v_global_scale,
+    uint8_t* k_data, uint8_t* k_scales, uint8_t* v_data, uint8_t* v_scales, int32_t pool_pages,
+    nvfp4kv_dtype out_dtype, void* q_out, int64_t q_out_row_stride, void* k_out, void* v_out,
+    int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Sparse decode over selected pages, in three calls: bounds of each page's keys (once, when the
+ * page is full), selection of the pages a step reads, and attention over them. The source pages
+ * have no counterpart; the calls cut the decode's bytes where a context is much longer than what
+ * one query attends to.
+ *
+ * Bounds of the listed pages. For every KV head and head dim, over the page's first
+ * page_tokens[i] tokens, v = e2m1(code) * e4m3(s) (without the tensor's g, which scales every
+ * page alike):
+ *   a = max_d max(|max_t v|, |min_t v|),  s = fp32(a / 127)
+ *   hi = min(127, ceil(fp32(max_t v / s))),  lo = max(-127, floor(fp32(min_t v / s)))
+ * and 0 everywhere when a is 0 or the page has no tokens.
+ *   k_data, k_scales, pool_pages   NVFP4 K pool in NVFP4KV_PACK_DIM_PAIRS
+ *   page_ids       [num_pages] pages to do (NULL = 0 .. num_pages-1); -1 = no page (padding)
+ *   page_tokens    [num_pages], 0 .. T (NULL = T for all)
+ *   bounds         int8 [pool_pages][H][2][D]: hi, then lo; only the listed pages are written
+ *   bound_scales   float [pool_pages][H]
+ * A page id outside the pool (PAGE_OOB) or a token count outside 0 .. T (BAD_SEQ_LEN) skips the
+ * page. Supported: head_dim 64, 128 or 256.
+ * ------------------------------------------------------------------------------------------ */
+nvfp4kv_status nvfp4_kv_page_bounds(
+    const nvfp4kv_layout* layout, const uint8_t* k_data, const uint8_t* k_scales,
+    int32_t pool_pages, const int32_t* page_ids, const int32_t* page_tokens, int32_t num_pages,
+    int8_t* bounds, float* bound_scales, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Selection. For sequence b and KV head h, with n = ceil(seq_lens[b] / T) pages, the first
+ * sink_pages and the last recent_pages are always taken, and the rest of `budget` goes to the
+ * pages of the highest score, ties to the lowest page. With each query head of the group brought
+ * to integers q_i = rint(fp32(q / f)), f = fp32(max|q| / 255) (all 0 when max|q| is 0 or a value
+ * is not finite), the score of a page is the largest over the group of
+ *   fp32(fp32(S f) s),  S = sum_d (q_i[d] > 0 ? q_i[d] hi[d] : q_i[d] lo[d])
+ * which bounds the product of the query with every key of the page from above (in units of g).
+ * S is exact, so the result does not depend on how the work is split. When n <= budget every page
+ * is taken.
+ *   q              BF16 [batch][num_q_heads][D]
+ *   bounds, bound_scales   as written by nvfp4_kv_page_bounds; those of the always-taken pages are
+ *                  not read, so the last, growing page needs none
+ *   page_table, seq_lens   as in nvfp4_paged_decode_attention
+ *   budget         pages to take per (sequence, KV head), >= sink_pages + recent_pages
+ *   recent_pages   >= 1: the last page, the only one that may be partial, is always taken
+ *   sel_page_table int32 [batch][H][budget]: the page ids taken, in the order of the sequence, then -1
+ *   sel_lens       int32 [batch][H]: tokens in those pages (0 for an empty or invalid sequence)
+ *   sel_index      optional int32 [batch][H][budget]: the positions of those pages in the sequence's
+ *                  page table, then -1
+ *   scores         optional float [batch][H][max_pages_per_seq]: the scores (+inf for the
+ *                  always-taken pages, -inf for a page id outside the pool); entries past n are
+ *                  left as they were
+ * sel_page_table and sel_lens are what nvfp4_paged_sparse_decode_attention takes. Supported:
+ * head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; batch * num_kv_heads <= 65535;
+ * max_pages_per_seq <= 393216.
+ * ------------------------------------------------------------------------------------------ */
+nvfp4kv_status nvfp4_kv_select_pages(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_q_heads, const void* q,
+    const int8_t* bounds, const float* bound_scales, int32_t pool_pages,
+    const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+    int32_t budget, int32_t sink_pages, int32_t recent_pages, int32_t* sel_page_table,
+    int32_t* sel_lens, int32_t* sel_index, float* scores, int32_t* status,
+    nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * nvfp4_paged_decode_attention over selected pages: the same formula, numerics and pools, with a
+ * page table and a length for each (sequence, KV head) pair, shared by the pair's query heads.
+ *   sel_page_table int32 [batch][H][max_sel_pages]
+ *   sel_lens       int32 [batch][H] tokens of the pair's pages, 0 <= len <= max_sel_pages * T; every
+ *                  page but the last is full. Table entries past ceil(len / T) are not read. A length
+ *                  of 0 gives out = 0 and lse = -inf, as does one outside the range (BAD_SEQ_LEN)
+ *   workspace      device scratch of nvfp4_paged_sparse_decode_workspace_size(...) bytes; needs no
+ *                  clearing, and calls that can overlap on the GPU must not share it
+ * The other arguments are those of nvfp4_paged_decode_attention. A page id outside the pool sets
+ * PAGE_OOB and its tokens are left out. A page listed twice counts twice. Supported: head_dim 64,
+ * 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; page_size % 16 == 0; batch * num_kv_heads <=
+ * 65535.
+ * ------------------------------------------------------------------------------------------ */
+size_t nvfp4_paged_sparse_decode_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
+                                                int32_t num_q_heads, int32_t max_sel_pages);
+
+nvfp4kv_status nvfp4_paged_sparse_decode_attention(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_q_heads, const void* q,
+    const uint8_t* k_data, const uint8_t* k_scales, const float* k_global_scale,
+    const uint8_t* v_data, const uint8_t* v_scales, const float* v_global_scale,
+    int32_t pool_pages, const int32_t* sel_page_table, int32_t max_sel_pages,
+    const int32_t* sel_lens, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, int32_t* status, nvfp4kv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Cold-page codec ("KV Cache Compression in TensorRT LLM", NVIDIA: "NVFP4 Cold-Page

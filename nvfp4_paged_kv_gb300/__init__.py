@@ -31,12 +31,16 @@ __all__ = [
     "ColdBlockLayout", "ColdRope", "ROPE_QUANTIZE", "ROPE_SKIP", "ROPE_2FP4",
     "nvfp4_kv_cold_block_layout", "nvfp4_kv_offload_pages",
     "nvfp4_kv_onboard_pages",
+    "STATUS_BAD_POSITION", "Rotary", "ROTARY_HALVES", "ROTARY_PAIRS", "nvfp4_kv_append",
+    "nvfp4_kv_page_bounds", "nvfp4_kv_select_pages", "nvfp4_paged_sparse_decode_workspace_size",
+    "nvfp4_paged_sparse_decode_attention",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20   # NVFP4KV_NOALLOC_SCRATCH_BYTES
 
 BF16, FP16, FP8_E4M3 = 0, 1, 2
 PACK_DIM_PAIRS, PACK_TOKEN_PAIRS = 0, 1   # nvfp4kv_packing: K pools, V pools of the decode call
 STATUS_PAGE_OOB, STATUS_BAD_SEQ_LEN, STATUS_TIMEOUT = 0x1, 0x2, 0x4
+STATUS_BAD_POSITION = 0x8
 _STATUS_NAMES = {1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "CUDA"}
 
 
@@ -78,6 +82,23 @@ class ColdBlockLayout(ctypes.Structure):
     def __repr__(self):
         return "ColdBlockLayout(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in
                                               self._fields_) + ")"
+
+
+ROTARY_HALVES, ROTARY_PAIRS = 0, 1   # nvfp4kv_rotary_style
+
+
+class Rotary(ctypes.Structure):
+    """The rotated head dims [first_dim, first_dim + dims) of q and k, how they pair up, and the
+    table of the rotation: `cos_sin` [positions, dims] float32 CUDA tensor, dims/2 cosines then
+    dims/2 sines of each position (``nvfp4kv_rotary``). Keeps the tensor alive."""
+    _fields_ = [("style", ctypes.c_int32), ("first_dim", ctypes.c_int32), ("dims", ctypes.c_int32),
+                ("max_positions", ctypes.c_int32), ("cos_sin", ctypes.c_void_p)]
+
+    def __init__(self, style: int, first_dim: int, dims: int, cos_sin: torch.Tensor):
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != dims:
+            raise ValueError("cos_sin must be a float32 tensor [positions, dims]")
+        super().__init__(int(style), int(first_dim), int(dims), cos_sin.shape[0], _ptr(cos_sin))
+        self.table = cos_sin
 
 
 class ExtendTensor(ctypes.Structure):
@@ -144,6 +165,15 @@ def load():
             "nvfp4_kv_host_device_pointer": (I32, [P, ctypes.POINTER(ctypes.c_void_p)]),
             "nvfp4_paged_decode_attention_noalloc": (I32, [LP, I32, I32, P, P, P, P, P, P, P,
                                                            I32, P, I32, P, F, I32, P, P, P, P]),
+            "nvfp4_kv_append": (I32, [LP, I32, I32, I32, P, I64, P, I64, P, I64, P,
+                                      ctypes.POINTER(Rotary), P, P, P, P, P, P, P, I32, I32, P, I64,
+                                      P, P, P, P]),
+            "nvfp4_kv_page_bounds": (I32, [LP, P, P, I32, P, P, I32, P, P, P, P]),
+            "nvfp4_kv_select_pages": (I32, [LP, I32, I32, P, P, P, I32, P, I32, P, I32, I32, I32, P,
+                                            P, P, P, P, P]),
+            "nvfp4_paged_sparse_decode_workspace_size": (SZ, [LP, I32, I32, I32]),
+            "nvfp4_paged_sparse_decode_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, P, I32, P,
+                                                          I32, P, F, P, SZ, P, P, P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -509,3 +539,172 @@ def nvfp4_kv_onboard_pages(layout: Layout, cold: torch.Tensor, hot_k: torch.Tens
             s)
     _check("nvfp4_kv_onboard_pages", code)
 
+
+# ------------------------------------------------------------------------------ decode steps
+
+def _expect(t: Optional[torch.Tensor], name: str, dtype, numel: Optional[int] = None):
+    """Type and size of a tensor argument whose size follows from the others."""
+    if t is not None and (t.dtype != dtype or (numel is not None and t.numel() != numel)):
+        raise ValueError(f"{name} must be {dtype}" + ("" if numel is None else f" with {numel} values")
+                         + f", got {t.dtype} with {t.numel()}")
+
+
+def _pool_pages(layout: Layout, data: torch.Tensor, scales: torch.Tensor, name: str) -> int:
+    """Pages of an NVFP4 pool, after a check that both of its tensors have them whole."""
+    per = layout.num_kv_heads * layout.page_size * layout.head_dim
+    pages = data.shape[0]
+    if (data.element_size() != 1 or scales.element_size() != 1 or data.numel() * 2 != pages * per
+            or scales.numel() * 16 != pages * per):
+        raise ValueError(f"{name}_data and {name}_scales must be byte tensors of {pages} whole pages")
+    return pages
+
+
+def _rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int):
+    """Pointer and row stride of a [rows, heads, dim] CUDA tensor whose rows are each contiguous
+    (rows may be slices of a wider projection)."""
+    if not t.is_cuda or t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must be a CUDA tensor [{rows}, {heads}, {dim}]")
+    sr, sh, sd = t.stride()
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+        raise ValueError(f"each row of {name} must be contiguous")
+    return t.data_ptr(), sr if rows > 1 else -(-heads * dim // 8) * 8
+
+
+def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    k_data: torch.Tensor, k_scales: torch.Tensor, v_data: torch.Tensor,
+                    v_scales: torch.Tensor, *, q=None, q_out=None, k_out=None, v_out=None,
+                    rotary: Optional[Rotary] = None, positions=None, k_global_scale=None,
+                    v_global_scale=None, status=None, stream=None):
+    """Append rows `k`, `v` ([rows, H, D] BF16 / FP16, rows may be strided) to the cache at token
+    slots `slots` (int64 [rows], page * T + token, -1 = padding row), rotating `k` and `q`
+    ([rows, Hq, D]) by `rotary` at `positions` (int32 [rows]). `q_out` [rows, Hq, D] gets the rotated
+    queries; `k_out`, `v_out` [rows, H, D] (optional) the rows as the cache now holds them."""
+    lib = load()
+    H, D = layout.num_kv_heads, layout.head_dim
+    rows, hq = k.shape[0], 0 if q is None else q.shape[1]
+    pages = _pool_pages(layout, k_data, k_scales, "k")
+    if _pool_pages(layout, v_data, v_scales, "v") != pages:
+        raise ValueError("the K and V pools must have the same number of pages")
+    if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have one dtype")
+    _expect(slots, "slots", torch.int64, rows)
+    _expect(positions, "positions", torch.int32, rows)
+    if rotary is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    kp, ks = _rows(k, "k", rows, H, D)
+    vp, vs = _rows(v, "v", rows, H, D)
+    qp, qs = (None, 0) if q is None else _rows(q, "q", rows, hq, D)
+    op, os_ = (None, 0) if q is None else _rows(q_out, "q_out", rows, hq, D)
+    outs = [t for t in (q_out, k_out, v_out) if t is not None]
+    if any(t.dtype != outs[0].dtype for t in outs):
+        raise TypeError("q_out, k_out and v_out must have one dtype")
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None and t.numel() != rows * H * D:
+            raise ValueError(f"{name} must be [{rows}, {H}, {D}]")
+    with _on_device((k, v, slots, k_data, k_scales, v_data, v_scales, q, q_out, k_out, v_out,
+                     positions, None if rotary is None else rotary.table, k_global_scale,
+                     v_global_scale, status), stream) as s:
+        code = lib.nvfp4_kv_append(
+            layout, _dtype_code(k, None), rows, hq, qp, qs, kp, ks, vp, vs, _ptr(slots), rotary,
+            _ptr(positions), _ptr(k_global_scale), _ptr(v_global_scale), _ptr(k_data), _ptr(k_scales),
+            _ptr(v_data), _ptr(v_scales), pages, _dtype_code(outs[0], None) if outs else BF16, op, os_,
+            _ptr(k_out), _ptr(v_out), _ptr(status), s)
+    _check("nvfp4_kv_append", code)
+
+
+def nvfp4_kv_page_bounds(layout: Layout, k_data: torch.Tensor, k_scales: torch.Tensor,
+                         bounds: torch.Tensor, bound_scales: torch.Tensor, *, page_ids=None,
+                         page_tokens=None, status=None, stream=None):
+    """Int8 bounds of the keys of the listed pages (all of the pool when `page_ids` is None): `bounds`
+    [pages, H, 2, D] int8 (upper, lower) in steps of `bound_scales` [pages, H] float32. `page_tokens`
+    (int32, one per listed page) counts the page's valid tokens (None: full pages)."""
+    lib = load()
+    H, D = layout.num_kv_heads, layout.head_dim
+    pages = _pool_pages(layout, k_data, k_scales, "k")
+    num = pages if page_ids is None else page_ids.numel()
+    _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
+    _expect(bound_scales, "bound_scales", torch.float32, pages * H)
+    _expect(page_tokens, "page_tokens", torch.int32, num)
+    with _on_device((k_data, k_scales, bounds, bound_scales, page_ids, page_tokens, status),
+                    stream) as s:
+        code = lib.nvfp4_kv_page_bounds(layout, _ptr(k_data), _ptr(k_scales), pages, _ids(page_ids),
+                                        _ptr(page_tokens), num, _ptr(bounds), _ptr(bound_scales),
+                                        _ptr(status), s)
+    _check("nvfp4_kv_page_bounds", code)
+
+
+def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
+                          bound_scales: torch.Tensor, page_table: torch.Tensor,
+                          seq_lens: torch.Tensor, sel_page_table: torch.Tensor,
+                          sel_lens: torch.Tensor, *, sink_pages: int = 1, recent_pages: int = 1,
+                          sel_index=None, scores=None, status=None, stream=None):
+    """Take up to sel_page_table.shape[2] pages for each (sequence, KV head): the first `sink_pages`,
+    the last `recent_pages`, and those whose bounds allow the largest product with `q` ([B, Hq, D]
+    BF16). Writes `sel_page_table` [B, H, budget] int32 (page ids in sequence order, then -1) and
+    `sel_lens` [B, H] int32 (their tokens), which nvfp4_paged_sparse_decode_attention takes;
+    optionally `sel_index` (positions in the page table) and `scores` [B, H, max pages] float32."""
+    lib = load()
+    H, D = layout.num_kv_heads, layout.head_dim
+    B, hq, dq = q.shape
+    maxp, budget, pages = page_table.shape[1], sel_page_table.shape[-1], bounds.shape[0]
+    if dq != D:
+        raise ValueError(f"q must have head_dim {D}")
+    _expect(q, "q", torch.bfloat16)
+    _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
+    _expect(bound_scales, "bound_scales", torch.float32, pages * H)
+    _expect(page_table, "page_table", torch.int32, B * maxp)
+    _expect(seq_lens, "seq_lens", torch.int32, B)
+    _expect(sel_page_table, "sel_page_table", torch.int32, B * H * budget)
+    _expect(sel_lens, "sel_lens", torch.int32, B * H)
+    _expect(sel_index, "sel_index", torch.int32, B * H * budget)
+    _expect(scores, "scores", torch.float32, B * H * maxp)
+    with _on_device((q, bounds, bound_scales, page_table, seq_lens, sel_page_table, sel_lens,
+                     sel_index, scores, status), stream) as s:
+        code = lib.nvfp4_kv_select_pages(
+            layout, B, hq, _ptr(q), _ptr(bounds), _ptr(bound_scales), pages, _ptr(page_table), maxp,
+            _ptr(seq_lens), budget, int(sink_pages), int(recent_pages), _ptr(sel_page_table),
+            _ptr(sel_lens), _ptr(sel_index), _ptr(scores), _ptr(status), s)
+    _check("nvfp4_kv_select_pages", code)
+
+
+def nvfp4_paged_sparse_decode_workspace_size(layout: Layout, batch: int, num_q_heads: int,
+                                             max_sel_pages: int) -> int:
+    return int(load().nvfp4_paged_sparse_decode_workspace_size(
+        ctypes.byref(layout), int(batch), int(num_q_heads), int(max_sel_pages)))
+
+
+def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data, k_scales,
+                                        k_global_scale, v_data, v_scales, v_global_scale,
+                                        sel_page_table: torch.Tensor, sel_lens: torch.Tensor,
+                                        sm_scale: float, out: torch.Tensor, *, lse=None,
+                                        workspace=None, status=None, stream=None):
+    """The decode attention with a page table (`sel_page_table` [B, H, pages] int32) and a length
+    (`sel_lens` [B, H] int32) for each (sequence, KV head), as nvfp4_kv_select_pages writes them."""
+    lib = load()
+    H, D = layout.num_kv_heads, layout.head_dim
+    B, hq, dq = q.shape
+    max_sel = sel_page_table.shape[-1]
+    pages = _pool_pages(layout, k_data, k_scales, "k")
+    if _pool_pages(layout, v_data, v_scales, "v") != pages:
+        raise ValueError("the K and V pools must have the same number of pages")
+    if dq != D:
+        raise ValueError(f"q must have head_dim {D}")
+    _expect(q, "q", torch.bfloat16)
+    _expect(out, "out", torch.bfloat16, B * hq * D)
+    _expect(lse, "lse", torch.float32, B * hq)
+    _expect(sel_page_table, "sel_page_table", torch.int32, B * H * max_sel)
+    _expect(sel_lens, "sel_lens", torch.int32, B * H)
+    if workspace is None:
+        need = nvfp4_paged_sparse_decode_workspace_size(layout, B, hq, max_sel)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    with _on_device((q, k_data, k_scales, k_global_scale, v_data, v_scales, v_global_scale,
+                     sel_page_table, sel_lens, out, lse, workspace, status), stream) as s:
+        code = lib.nvfp4_paged_sparse_decode_attention(
+            layout, B, hq, _ptr(q), _ptr(k_data), _ptr(k_scales), _ptr(k_global_scale),
+            _ptr(v_data), _ptr(v_scales), _ptr(v_global_scale), pages, _ptr(sel_page_table), max_sel,
+            _ptr(sel_lens), float(sm_scale), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status), s)
+    _check("nvfp4_paged_sparse_decode_attention", code)
+    return out
