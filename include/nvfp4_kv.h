@@ -408,7 +408,7 @@ nvfp4kv_status nvfp4_kv_append(
  *   bounds         int8 [pool_pages][H][2][D]: hi, then lo; only the listed pages are written
  *   bound_scales   float [pool_pages][H]
  * A page id outside the pool (PAGE_OOB) or a token count outside 0 .. T (BAD_SEQ_LEN) skips the
- * page. Supported: head_dim 64, 128 or 256.
+ * page. Supported: head_dim 64, 128 or 256; page_size % 16 == 0.
  * ------------------------------------------------------------------------------------------ */
 nvfp4kv_status nvfp4_kv_page_bounds(
     const nvfp4kv_layout* layout, const uint8_t* k_data, const uint8_t* k_scales,
@@ -440,7 +440,7 @@ nvfp4kv_status nvfp4_kv_page_bounds(
  *                  left as they were
  * sel_page_table and sel_lens are what nvfp4_paged_sparse_decode_attention takes. Supported:
  * head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; batch * num_kv_heads <= 65535;
- * max_pages_per_seq <= 393216.
+ * max_pages_per_seq <= 49152.
  * ------------------------------------------------------------------------------------------ */
 nvfp4kv_status nvfp4_kv_select_pages(
     const nvfp4kv_layout* layout, int32_t batch, int32_t num_q_heads, const void* q,

@@ -542,32 +542,79 @@ def nvfp4_kv_onboard_pages(layout: Layout, cold: torch.Tensor, hot_k: torch.Tens
 
 # ------------------------------------------------------------------------------ decode steps
 
-def _expect(t: Optional[torch.Tensor], name: str, dtype, numel: Optional[int] = None):
+_CODES = {torch.bfloat16: BF16, torch.float16: FP16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _pointers(*tensors):
+    """Pointers of contiguous CUDA tensors (None stays None) and the index of their one device."""
+    dev, out = -2, []  # (a CPU tensor has device -1)
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("tensors passed to the NVFP4 KV library must be CUDA tensors")
+            if dev >= 0:
+                raise ValueError(f"all CUDA tensors of one call must be on one device, got cuda:{dev} "
+                                 f"and cuda:{d}")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the NVFP4 KV library must be contiguous")
+        out.append(t.data_ptr())
+    return out, dev
+
+
+def _run(name: str, dev: int, stream, *args):
+    """Call a library function with `args` and the stream on device `dev`, as _on_device does."""
+    if stream is None:
+        s = _raw_stream(dev)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"stream is on {stream.device} but the tensors are on cuda:{dev}")
+        s = stream.cuda_stream
+    else:
+        s = int(stream)
+    fn = getattr(_lib, name)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, s)
+    if code:
+        _check(name, code)
+
+
+def _expect(t: Optional[torch.Tensor], name: str, dtype, numel: int):
     """Type and size of a tensor argument whose size follows from the others."""
-    if t is not None and (t.dtype != dtype or (numel is not None and t.numel() != numel)):
-        raise ValueError(f"{name} must be {dtype}" + ("" if numel is None else f" with {numel} values")
-                         + f", got {t.dtype} with {t.numel()}")
+    if t is not None and (t.dtype != dtype or t.numel() != numel):
+        raise ValueError(f"{name} must be {dtype} with {numel} values, got {t.dtype} with {t.numel()}")
 
 
 def _pool_pages(layout: Layout, data: torch.Tensor, scales: torch.Tensor, name: str) -> int:
     """Pages of an NVFP4 pool, after a check that both of its tensors have them whole."""
-    per = layout.num_kv_heads * layout.page_size * layout.head_dim
     pages = data.shape[0]
-    if (data.element_size() != 1 or scales.element_size() != 1 or data.numel() * 2 != pages * per
-            or scales.numel() * 16 != pages * per):
+    values = pages * layout.num_kv_heads * layout.page_size * layout.head_dim
+    if (data.numel() * 2 != values or scales.numel() * 16 != values or data.element_size() != 1
+            or scales.element_size() != 1):
         raise ValueError(f"{name}_data and {name}_scales must be byte tensors of {pages} whole pages")
     return pages
 
 
-def _rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int):
-    """Pointer and row stride of a [rows, heads, dim] CUDA tensor whose rows are each contiguous
-    (rows may be slices of a wider projection)."""
-    if not t.is_cuda or t.shape != (rows, heads, dim):
-        raise ValueError(f"{name} must be a CUDA tensor [{rows}, {heads}, {dim}]")
+def _rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dev: int):
+    """Pointer and row stride of a [rows, heads, dim] tensor of device `dev` whose rows are each
+    contiguous (rows may be slices of a wider projection)."""
+    if t.shape != (rows, heads, dim):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {list(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     sr, sh, sd = t.stride()
-    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
+    if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"each row of {name} must be contiguous")
-    return t.data_ptr(), sr if rows > 1 else -(-heads * dim // 8) * 8
+    return t.data_ptr(), sr if rows > 1 else heads * dim
 
 
 def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -579,7 +626,7 @@ def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: tor
     slots `slots` (int64 [rows], page * T + token, -1 = padding row), rotating `k` and `q`
     ([rows, Hq, D]) by `rotary` at `positions` (int32 [rows]). `q_out` [rows, Hq, D] gets the rotated
     queries; `k_out`, `v_out` [rows, H, D] (optional) the rows as the cache now holds them."""
-    lib = load()
+    load()
     H, D = layout.num_kv_heads, layout.head_dim
     rows, hq = k.shape[0], 0 if q is None else q.shape[1]
     pages = _pool_pages(layout, k_data, k_scales, "k")
@@ -587,31 +634,32 @@ def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: tor
         raise ValueError("the K and V pools must have the same number of pages")
     if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
         raise TypeError("q, k and v must have one dtype")
-    _expect(slots, "slots", torch.int64, rows)
-    _expect(positions, "positions", torch.int32, rows)
-    if rotary is not None and positions is None:
-        raise ValueError("a rotation needs positions")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
-    kp, ks = _rows(k, "k", rows, H, D)
-    vp, vs = _rows(v, "v", rows, H, D)
-    qp, qs = (None, 0) if q is None else _rows(q, "q", rows, hq, D)
-    op, os_ = (None, 0) if q is None else _rows(q_out, "q_out", rows, hq, D)
-    outs = [t for t in (q_out, k_out, v_out) if t is not None]
-    if any(t.dtype != outs[0].dtype for t in outs):
-        raise TypeError("q_out, k_out and v_out must have one dtype")
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None and t.numel() != rows * H * D:
-            raise ValueError(f"{name} must be [{rows}, {H}, {D}]")
-    with _on_device((k, v, slots, k_data, k_scales, v_data, v_scales, q, q_out, k_out, v_out,
-                     positions, None if rotary is None else rotary.table, k_global_scale,
-                     v_global_scale, status), stream) as s:
-        code = lib.nvfp4_kv_append(
-            layout, _dtype_code(k, None), rows, hq, qp, qs, kp, ks, vp, vs, _ptr(slots), rotary,
-            _ptr(positions), _ptr(k_global_scale), _ptr(v_global_scale), _ptr(k_data), _ptr(k_scales),
-            _ptr(v_data), _ptr(v_scales), pages, _dtype_code(outs[0], None) if outs else BF16, op, os_,
-            _ptr(k_out), _ptr(v_out), _ptr(status), s)
-    _check("nvfp4_kv_append", code)
+    if rotary is not None and positions is None:
+        raise ValueError("a rotation needs positions")
+    _expect(slots, "slots", torch.int64, rows)
+    _expect(positions, "positions", torch.int32, rows)
+    out_dtype = None
+    for t, name, heads in ((q_out, "q_out", hq), (k_out, "k_out", H), (v_out, "v_out", H)):
+        if t is not None:
+            out_dtype = out_dtype or t.dtype
+            if t.dtype != out_dtype:
+                raise TypeError("q_out, k_out and v_out must have one dtype")
+            if t.numel() != rows * heads * D:
+                raise ValueError(f"{name} must be [{rows}, {heads}, {D}]")
+    (sp, pp, gk, gv, kd, ksc, vd, vsc, ko, vo, st, _), dev = _pointers(
+        slots, positions, k_global_scale, v_global_scale, k_data, k_scales, v_data, v_scales, k_out,
+        v_out, status, None if rotary is None else rotary.table)
+    kp, ks = _rows(k, "k", rows, H, D, dev)
+    vp, vs = _rows(v, "v", rows, H, D, dev)
+    qp = qs = op = os_ = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", rows, hq, D, dev)
+        op, os_ = _rows(q_out, "q_out", rows, hq, D, dev)
+    _run("nvfp4_kv_append", dev, stream, layout, _CODES.get(k.dtype, -1), rows, hq, qp, qs, kp, ks, vp, vs,
+         sp, rotary, pp, gk, gv, kd, ksc, vd, vsc, pages,
+         BF16 if out_dtype is None else _CODES.get(out_dtype, -1), op, os_, ko, vo, st)
 
 
 def nvfp4_kv_page_bounds(layout: Layout, k_data: torch.Tensor, k_scales: torch.Tensor,
@@ -620,19 +668,17 @@ def nvfp4_kv_page_bounds(layout: Layout, k_data: torch.Tensor, k_scales: torch.T
     """Int8 bounds of the keys of the listed pages (all of the pool when `page_ids` is None): `bounds`
     [pages, H, 2, D] int8 (upper, lower) in steps of `bound_scales` [pages, H] float32. `page_tokens`
     (int32, one per listed page) counts the page's valid tokens (None: full pages)."""
-    lib = load()
+    load()
     H, D = layout.num_kv_heads, layout.head_dim
     pages = _pool_pages(layout, k_data, k_scales, "k")
     num = pages if page_ids is None else page_ids.numel()
+    _expect(page_ids, "page_ids", torch.int32, num)
+    _expect(page_tokens, "page_tokens", torch.int32, num)
     _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
     _expect(bound_scales, "bound_scales", torch.float32, pages * H)
-    _expect(page_tokens, "page_tokens", torch.int32, num)
-    with _on_device((k_data, k_scales, bounds, bound_scales, page_ids, page_tokens, status),
-                    stream) as s:
-        code = lib.nvfp4_kv_page_bounds(layout, _ptr(k_data), _ptr(k_scales), pages, _ids(page_ids),
-                                        _ptr(page_tokens), num, _ptr(bounds), _ptr(bound_scales),
-                                        _ptr(status), s)
-    _check("nvfp4_kv_page_bounds", code)
+    (kd, ks, ip, tp, bp, bs, st), dev = _pointers(k_data, k_scales, page_ids, page_tokens, bounds,
+                                                  bound_scales, status)
+    _run("nvfp4_kv_page_bounds", dev, stream, layout, kd, ks, pages, ip, tp, num, bp, bs, st)
 
 
 def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
@@ -645,13 +691,11 @@ def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
     BF16). Writes `sel_page_table` [B, H, budget] int32 (page ids in sequence order, then -1) and
     `sel_lens` [B, H] int32 (their tokens), which nvfp4_paged_sparse_decode_attention takes;
     optionally `sel_index` (positions in the page table) and `scores` [B, H, max pages] float32."""
-    lib = load()
+    load()
     H, D = layout.num_kv_heads, layout.head_dim
-    B, hq, dq = q.shape
+    B, hq = q.shape[0], q.shape[1]
     maxp, budget, pages = page_table.shape[1], sel_page_table.shape[-1], bounds.shape[0]
-    if dq != D:
-        raise ValueError(f"q must have head_dim {D}")
-    _expect(q, "q", torch.bfloat16)
+    _expect(q, "q", torch.bfloat16, B * hq * D)
     _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
     _expect(bound_scales, "bound_scales", torch.float32, pages * H)
     _expect(page_table, "page_table", torch.int32, B * maxp)
@@ -660,13 +704,10 @@ def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
     _expect(sel_lens, "sel_lens", torch.int32, B * H)
     _expect(sel_index, "sel_index", torch.int32, B * H * budget)
     _expect(scores, "scores", torch.float32, B * H * maxp)
-    with _on_device((q, bounds, bound_scales, page_table, seq_lens, sel_page_table, sel_lens,
-                     sel_index, scores, status), stream) as s:
-        code = lib.nvfp4_kv_select_pages(
-            layout, B, hq, _ptr(q), _ptr(bounds), _ptr(bound_scales), pages, _ptr(page_table), maxp,
-            _ptr(seq_lens), budget, int(sink_pages), int(recent_pages), _ptr(sel_page_table),
-            _ptr(sel_lens), _ptr(sel_index), _ptr(scores), _ptr(status), s)
-    _check("nvfp4_kv_select_pages", code)
+    (qp, bp, bs, tp, lp, op, ol, oi, sc, st), dev = _pointers(
+        q, bounds, bound_scales, page_table, seq_lens, sel_page_table, sel_lens, sel_index, scores, status)
+    _run("nvfp4_kv_select_pages", dev, stream, layout, B, hq, qp, bp, bs, pages, tp, maxp, lp, budget,
+         int(sink_pages), int(recent_pages), op, ol, oi, sc, st)
 
 
 def nvfp4_paged_sparse_decode_workspace_size(layout: Layout, batch: int, num_q_heads: int,
@@ -682,16 +723,14 @@ def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data,
                                         workspace=None, status=None, stream=None):
     """The decode attention with a page table (`sel_page_table` [B, H, pages] int32) and a length
     (`sel_lens` [B, H] int32) for each (sequence, KV head), as nvfp4_kv_select_pages writes them."""
-    lib = load()
+    load()
     H, D = layout.num_kv_heads, layout.head_dim
-    B, hq, dq = q.shape
+    B, hq = q.shape[0], q.shape[1]
     max_sel = sel_page_table.shape[-1]
     pages = _pool_pages(layout, k_data, k_scales, "k")
     if _pool_pages(layout, v_data, v_scales, "v") != pages:
         raise ValueError("the K and V pools must have the same number of pages")
-    if dq != D:
-        raise ValueError(f"q must have head_dim {D}")
-    _expect(q, "q", torch.bfloat16)
+    _expect(q, "q", torch.bfloat16, B * hq * D)
     _expect(out, "out", torch.bfloat16, B * hq * D)
     _expect(lse, "lse", torch.float32, B * hq)
     _expect(sel_page_table, "sel_page_table", torch.int32, B * H * max_sel)
@@ -699,12 +738,10 @@ def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data,
     if workspace is None:
         need = nvfp4_paged_sparse_decode_workspace_size(layout, B, hq, max_sel)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    with _on_device((q, k_data, k_scales, k_global_scale, v_data, v_scales, v_global_scale,
-                     sel_page_table, sel_lens, out, lse, workspace, status), stream) as s:
-        code = lib.nvfp4_paged_sparse_decode_attention(
-            layout, B, hq, _ptr(q), _ptr(k_data), _ptr(k_scales), _ptr(k_global_scale),
-            _ptr(v_data), _ptr(v_scales), _ptr(v_global_scale), pages, _ptr(sel_page_table), max_sel,
-            _ptr(sel_lens), float(sm_scale), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _ptr(out), _ptr(lse), _ptr(status), s)
-    _check("nvfp4_paged_sparse_decode_attention", code)
+    (qp, kd, ks, gk, vd, vs, gv, tp, lp, wp, op, ol, st), dev = _pointers(
+        q, k_data, k_scales, k_global_scale, v_data, v_scales, v_global_scale, sel_page_table, sel_lens,
+        workspace, out, lse, status)
+    _run("nvfp4_paged_sparse_decode_attention", dev, stream, layout, B, hq, qp, kd, ks, gk, vd, vs, gv,
+         pages, tp, max_sel, lp, float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol,
+         st)
     return out

@@ -66,17 +66,11 @@ struct AppendParams {
     int64_t tasks;
 };
 
-// 16 values of a source row as exact fp32.
-template <int SRC>
-__device__ __forceinline__ void load_block(const uint8_t* a, bool wide, float (&x)[16]) {
-    U8x32 raw;
-    if (wide) {
-        raw = ld_stream_32B(a);
-    } else {
-        const uint4 lo = ld_stream_16B(a), hi = ld_stream_16B(a + 16);
-        raw = U8x32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
-    }
-    widen<SRC>(raw, 1.0f, x);
+// 16 values of a source row.
+__device__ __forceinline__ U8x32 load_block(const uint8_t* a, bool wide) {
+    if (wide) return ld_stream_32B(a);
+    const uint4 lo = ld_stream_16B(a), hi = ld_stream_16B(a + 16);
+    return U8x32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
 }
 
 // 16 values rounded to the 16-bit output type (round to nearest even).
@@ -97,7 +91,7 @@ __device__ __forceinline__ void rotate(float& x1, float& x2, float c, float s) {
 }
 
 template <int SRC, int D, int STYLE>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
     pdl_enter();
     constexpr int U = D / 32;   // threads of a head
     constexpr int HW = 32 / U;  // heads of a warp
@@ -156,17 +150,35 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             }
         }
 
-        // ---- q and K heads
-        for (int seg = seg0; seg < min(seg1, p.segs_rot); ++seg) {
+        // ---- q and K heads; a head group's values are loaded while the one before is worked on
+        const int rot1 = min(seg1, p.segs_rot);
+        auto source = [&](int seg) -> const uint8_t* {  // null: no head for this thread
             const int head = seg * HW + hl;
+            if (seg >= rot1 || head >= p.Hq + p.H) return nullptr;
+            return head < p.Hq ? p.q + row * p.q_stride + static_cast<int64_t>(head) * D * 2
+                               : p.k + row * p.k_stride + static_cast<int64_t>(head - p.Hq) * D * 2;
+        };
+        U8x32 n0, n1;
+        {
+            const uint8_t* src = source(seg0);
+            if (src) {
+                n0 = load_block(src + 32 * b0, wide);
+                n1 = load_block(src + 32 * b1, wide);
+            }
+        }
+        for (int seg = seg0; seg < rot1; ++seg) {
+            const int head = seg * HW + hl;
+            float x0[16], x1[16];
+            widen<SRC>(n0, 1.0f, x0);
+            widen<SRC>(n1, 1.0f, x1);
+            const uint8_t* src = source(seg + 1);
+            if (src) {
+                n0 = load_block(src + 32 * b0, wide);
+                n1 = load_block(src + 32 * b1, wide);
+            }
             if (head >= p.Hq + p.H) continue;
             const bool is_q = head < p.Hq;
             const int kh = head - p.Hq;
-            const uint8_t* src = is_q ? p.q + row * p.q_stride + static_cast<int64_t>(head) * D * 2
-                                      : p.k + row * p.k_stride + static_cast<int64_t>(kh) * D * 2;
-            float x0[16], x1[16];
-            load_block<SRC>(src + 32 * b0, wide, x0);
-            load_block<SRC>(src + 32 * b1, wide, x1);
             if (turns) {
                 if constexpr (STYLE == NVFP4KV_ROTARY_HALVES) {
 #pragma unroll
@@ -224,12 +236,18 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
             const uint8_t* src = p.v + row * p.v_stride + static_cast<int64_t>(h) * D * 2;
             const int64_t vrow = (page * p.H + h) * half_T + (t >> 1);
             const float d = __fmul_rn(6.0f, gv);
+            U8x32 v0[2], v1[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v0[u] = load_block(src + 32 * (2 * i + u), wide);
+                if (both) v1[u] = load_block(src + p.v_stride + 32 * (2 * i + u), wide);
+            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int b = 2 * i + u;
-                float x0[16], x1[16];  // first and second token of the pair; an absent one is 0
-                load_block<SRC>(src + 32 * b, wide, x0);
-                if (both) load_block<SRC>(src + p.v_stride + 32 * b, wide, x1);
+                float x0[16], x1[16];  // first and second token of the pair
+                widen<SRC>(v0[u], 1.0f, x0);
+                if (both) widen<SRC>(v1[u], 1.0f, x1);
                 uint32_t s0, s1 = 0u;
                 float r0, r1 = 0.0f;
                 pick_scale(x0, gv, d, s0, r0);
@@ -381,10 +399,11 @@ extern "C" nvfp4kv_status nvfp4_kv_append(
     const int HW = 32 / (D / 32);
     p.segs_rot = (num_q_heads + H + HW - 1) / HW;
     p.segs = p.segs_rot + (H + HW - 1) / HW;
-    // few rows: a warp per head group, for latency; many: a warp per row, which reads the position's
-    // table row once
+    // a warp takes as many head groups of a row as leave 16 warps to an SM: few rows are spread over
+    // the GPU, and with many rows the position's table row is read once for all heads
     const int64_t spread = static_cast<int64_t>(num_rows) * p.segs;
-    p.segs_per_task = spread <= static_cast<int64_t>(num_sms()) * 32 ? 1 : p.segs;
+    const int64_t each = (spread + num_sms() * 16 - 1) / (num_sms() * 16);
+    p.segs_per_task = static_cast<int>(each < p.segs ? each : p.segs);
     p.tasks_per_row = (p.segs + p.segs_per_task - 1) / p.segs_per_task;
     p.tasks = static_cast<int64_t>(num_rows) * p.tasks_per_row;
     const int64_t ctas = (p.tasks + kAppendThreads / 32 - 1) / (kAppendThreads / 32);

@@ -32,14 +32,37 @@ namespace {
 
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit_group() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+    uint32_t o;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    return o;
+}
+__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b) {
+    uint32_t o;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+    return o;
+}
 
 // ------------------------------------------------------------------------------------------
-// Page bounds. One warp per (page, head): a lane owns 32 dims (16 code bytes) of every
-// (32 / (D / 32))-th token, and keeps max v and max -v of its dims in FP16 pairs; the lanes that
-// hold the same dims then exchange halves of what they have (a reduce-scatter), so each ends with
-// a few finished dims to round and store.
+// Page bounds. One warp per (page, head), in chunks of 4608 bytes (128, 64 or 32 tokens of head_dim
+// 64, 128 or 256) that it copies ahead into a ring of two shared-memory slots, so that the next
+// chunk or page is on its way while this one is reduced. A lane owns 32 dims (16 code bytes) of every
+// (32 / (D / 32))-th token and keeps the maxima and minima of its dims in FP16 pairs; the lanes that
+// hold the same dims then exchange halves of what they have (a reduce-scatter), so each ends with a
+// few finished dims to round and store.
 // ------------------------------------------------------------------------------------------
-constexpr int kBoundsThreads = 256;
+constexpr int kBoundsThreads = 128;
+constexpr int kBoundsChunk = 4608;  // bytes of a slot: codes, then scales
 
 struct BoundsParams {
     const uint8_t* kd;
@@ -53,6 +76,25 @@ struct BoundsParams {
     int64_t items;
 };
 
+// Maxima over the lanes that differ in the bits OFF, OFF / 2, .. LAST: with each bit a lane gives half of
+// its CNT pairs away and keeps the other half, in m[0 ..]. Returns where the kept pairs began in m.
+template <int CNT, int OFF, int LAST>
+__device__ __forceinline__ int reduce_scatter(uint32_t (&m)[32], int lane) {
+    if constexpr (OFF >= LAST) {
+        constexpr int half = CNT / 2;
+        const bool up = (lane & OFF) != 0;
+#pragma unroll
+        for (int k = 0; k < half; ++k) {
+            const uint32_t give = up ? m[k] : m[k + half];
+            const uint32_t keep = up ? m[k + half] : m[k];
+            m[k] = max_f16x2(keep, __shfl_xor_sync(0xFFFFFFFFu, give, OFF));
+        }
+        return (up ? half : 0) + reduce_scatter<half, OFF / 2, LAST>(m, lane);
+    } else {
+        return 0;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const BoundsParams p) {
     pdl_enter();
@@ -60,74 +102,126 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     constexpr int RPP = 32 / LPR;  // token rows of a pass
     constexpr int NB = D / 16;
     constexpr int KEEP = 32 / RPP; // FP16 pairs a lane ends with
+    constexpr int CH = 8 * RPP;    // token rows of a chunk
+    static_assert(CH * (D / 2 + NB) == kBoundsChunk, "chunk size");
+    __shared__ __align__(16) uint8_t ring[kBoundsThreads / 32][2][kBoundsChunk];
     const int lane = threadIdx.x & 31;
     const int l = lane % LPR, rr = lane / LPR;
     const int64_t step = static_cast<int64_t>(gridDim.x) * (kBoundsThreads / 32);
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (kBoundsThreads / 32) + (threadIdx.x >> 5);
-         item < p.items; item += step) {
-        const int i = static_cast<int>(item / p.H);
-        const int h = static_cast<int>(item - static_cast<int64_t>(i) * p.H);
-        const int page = p.page_ids ? __ldg(p.page_ids + i) : i;
-        if (page == -1) continue;
-        const int n = p.page_tokens ? __ldg(p.page_tokens + i) : p.T;
-        if (page < 0 || page >= p.pool_pages || n < 0 || n > p.T) {
-            if (lane == 0)
-                flag_status(p.status, (page < 0 || page >= p.pool_pages) ? NVFP4KV_STATUS_PAGE_OOB
-                                                                         : NVFP4KV_STATUS_BAD_SEQ_LEN);
-            continue;
+    uint8_t(*slots)[kBoundsChunk] = ring[threadIdx.x >> 5];
+
+    // the walk over the warp's chunks, one ahead of the reduction; the ids of the item after are
+    // loaded while an item is walked
+    int64_t item = static_cast<int64_t>(blockIdx.x) * (kBoundsThreads / 32) + (threadIdx.x >> 5) - step;
+    int64_t ph = 0;                    // page * H + head of the item
+    int n = 0, t0 = 0;                 // its tokens, first token of the chunk
+    int id_page = -1, id_n = 0;        // of the item after
+    auto load_ids = [&](int64_t it) {
+        if (it >= p.items) return;
+        const int i = static_cast<int>(it / p.H);
+        id_page = p.page_ids ? __ldg(p.page_ids + i) : i;
+        id_n = p.page_tokens ? __ldg(p.page_tokens + i) : p.T;
+    };
+    load_ids(item + step);
+    auto advance = [&]() -> bool {  // to the next chunk; false: none left
+        t0 += CH;
+        if (t0 < n) return true;
+        for (;;) {
+            item += step;
+            if (item >= p.items) return false;
+            const int page = id_page;
+            n = id_n;
+            load_ids(item + step);
+            if (page == -1) continue;
+            if (page < 0 || page >= p.pool_pages || n < 0 || n > p.T) {
+                if (lane == 0)
+                    flag_status(p.status, (page < 0 || page >= p.pool_pages) ? NVFP4KV_STATUS_PAGE_OOB
+                                                                             : NVFP4KV_STATUS_BAD_SEQ_LEN);
+                continue;
+            }
+            ph = static_cast<int64_t>(page) * p.H + item % p.H;
+            t0 = 0;
+            return true;
         }
-        const int64_t ph = static_cast<int64_t>(page) * p.H + h;
-        const uint8_t* kd = p.kd + ph * p.T * (D / 2) + 16 * l;
-        const uint8_t* ks = p.ks + ph * p.T * NB + 2 * l;
-        __half2 m[32];  // max of dims (2j, 2j+1) in m[j], of their negatives in m[16 + j]
+    };
+    // rows [t0, t0 + CH) of the page, as far as it has them
+    auto copy = [&](uint8_t* slot) {
+        const int rows = min(CH, p.T - t0);
+        const int64_t r0 = ph * p.T + t0;
+        const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot)) + 16 * lane;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) m[j] = as_h2(0xFC00FC00u);
-#pragma unroll 4
-        for (int t = rr; t < n; t += RPP) {
-            const uint4 w = ld_stream_16B(kd + static_cast<int64_t>(t) * (D / 2));
-            const uint32_t sc = *reinterpret_cast<const uint16_t*>(ks + static_cast<int64_t>(t) * NB);
-            const uint32_t sa = e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u);
-            const uint32_t sb = e4m3x2_to_f16x2((sc >> 8) * 0x0101u);
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int k = 0; k < 8; ++k)
+            if (32 * k + lane < rows * (D / 32)) cp_async_16(dst + 512 * k, p.kd + r0 * (D / 2) + 512 * k + 16 * lane);
+        if (16 * lane < rows * NB) cp_async_16(dst + CH * (D / 2), p.ks + r0 * NB + 16 * lane);
+    };
+
+    n = 0;
+    bool more = advance();
+    if (more) copy(slots[0]);
+    cp_async_commit_group();
+    // maxima of dims (2j, 2j+1) in m[j], minima in m[16 + j]
+    uint32_t m[32];
+    for (int turn = 0; more; turn ^= 1) {
+        const int64_t my_ph = ph;
+        const int my_n = n, my_t0 = t0;
+        more = advance();
+        if (more) copy(slots[turn ^ 1]);
+        cp_async_commit_group();
+        cp_async_wait_group<1>();
+        __syncwarp();
+        if (my_t0 == 0) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t v[4];
-                e2m1x8_to_f16x2x4(ww[k], v);
+            for (int j = 0; j < 32; ++j) m[j] = j < 16 ? 0xFC00FC00u : 0x7C007C00u;
+        }
+        const uint8_t* codes = slots[turn] + 16 * l;
+        const uint8_t* scales = slots[turn] + CH * (D / 2) + 2 * l;
+        const int rows = min(CH, my_n - my_t0);
+        // passes two at a time, so that their values meet in one three-way maximum; a row past the end
+        // repeats the last one
+        for (int r0 = rr; r0 - rr < rows; r0 += 2 * RPP) {
+            uint4 w[2];
+            uint32_t sa[2], sb[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int t = min(r0 + k * RPP, rows - 1);
+                w[k] = *reinterpret_cast<const uint4*>(codes + t * (D / 2));
+                const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + t * NB);
+                sa[k] = e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u);
+                sb[k] = e4m3x2_to_f16x2((sc >> 8) * 0x0101u);
+            }
+            const uint32_t ww[2][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w}};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t v0[4], v1[4];
+                e2m1x8_to_f16x2x4(ww[0][e], v0);
+                e2m1x8_to_f16x2x4(ww[1][e], v1);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t x = hmul2_u32(v[j], k < 2 ? sa : sb);
-                    m[4 * k + j] = __hmax2(m[4 * k + j], as_h2(x));
-                    m[16 + 4 * k + j] = __hmax2(m[16 + 4 * k + j], as_h2(x ^ 0x80008000u));
+                    const uint32_t x0 = hmul2_u32(v0[j], e < 2 ? sa[0] : sb[0]);
+                    const uint32_t x1 = hmul2_u32(v1[j], e < 2 ? sa[1] : sb[1]);
+                    m[4 * e + j] = max_f16x2(max_f16x2(m[4 * e + j], x0), x1);
+                    m[16 + 4 * e + j] = min_f16x2(min_f16x2(m[16 + 4 * e + j], x0), x1);
                 }
             }
         }
-        int base = 0, cnt = 32;
+        __syncwarp();  // every lane is done with the slot before it refills
+        if (my_t0 + CH < my_n) continue;
+        // from here on the negated minima, so that both halves are maxima
 #pragma unroll
-        for (int off = 16; off >= LPR; off >>= 1) {
-            cnt >>= 1;
-            const bool up = (lane & off) != 0;
-            if (up) base += cnt;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                if (k >= cnt) break;
-                const uint32_t give = as_u32(up ? m[k] : m[k + cnt]);
-                const __half2 keep = up ? m[k + cnt] : m[k];
-                m[k] = __hmax2(keep, as_h2(__shfl_xor_sync(0xFFFFFFFFu, give, off)));
-            }
-        }
+        for (int j = 16; j < 32; ++j) m[j] ^= 0x80008000u;
+        const int base = reduce_scatter<32, 16, LPR>(m, lane);
         float a = 0.0f;
         float y[2 * KEEP];
 #pragma unroll
         for (int k = 0; k < KEEP; ++k) {
-            const float2 f = __half22float2(m[k]);
-            y[2 * k] = n > 0 ? f.x : 0.0f;
-            y[2 * k + 1] = n > 0 ? f.y : 0.0f;
+            y[2 * k] = my_n > 0 ? f16_lo(m[k]) : 0.0f;
+            y[2 * k + 1] = my_n > 0 ? f16_hi(m[k]) : 0.0f;
             a = fmaxf(a, fmaxf(fabsf(y[2 * k]), fabsf(y[2 * k + 1])));
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, off));
         const float s = __fdiv_rn(a, 127.0f);
-        if (lane == 0) p.scales[ph] = s;
+        if (lane == 0) p.scales[my_ph] = s;
         const bool neg = base >= 16;
         uint32_t w[(2 * KEEP + 3) / 4];
 #pragma unroll
@@ -138,7 +232,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             const int c = s > 0.0f ? static_cast<int>(fminf(127.0f, ceilf(__fdiv_rn(y[k], s)))) : 0;
             w[k / 4] |= static_cast<uint32_t>((neg ? -c : c) & 0xFF) << (8 * (k % 4));
         }
-        int8_t* dst = p.bounds + (ph * 2 + (neg ? 1 : 0)) * D + 32 * l + 2 * (base & 15);
+        int8_t* dst = p.bounds + (my_ph * 2 + (neg ? 1 : 0)) * D + 32 * l + 2 * (base & 15);
         if constexpr (KEEP == 2) {
             *reinterpret_cast<uint32_t*>(dst) = w[0];
         } else if constexpr (KEEP == 4) {
@@ -150,18 +244,19 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
 }
 
 // ------------------------------------------------------------------------------------------
-// Selection. One thread-block cluster per (sequence, KV head) pair; every CTA scores a contiguous
-// share of the sequence's pages on the tensor cores (16 pages as M, the query group as N, the 2 D
-// bounds as K) and keeps the scores as sortable keys in shared memory. The smallest selected key is
-// found by a radix selection over the cluster's keys (8 bits a pass, histograms summed through
-// distributed shared memory), and the selected pages are written in ascending order, equal keys
-// from the lowest page on.
+// Selection. One thread-block cluster per (sequence, KV head) pair. Its warps score tiles of 16
+// pages on the tensor cores (FP16, whose mma.sync runs 8 times as often per clock as the int8 one on
+// this GPU; pages as M, the query group as N, head dims as K, once with the upper bounds and the
+// positive queries, once with the lower and the negative) and put the scores as sortable keys into the shared memory of the cluster's first CTA, which then finds the
+// smallest selected key: by counting ranks when the pages are as few as its threads, else by a radix
+// selection that starts at the highest bit in which the keys differ and stops when a bin is taken
+// whole. The selected pages are written in ascending order, equal keys from the lowest page on.
 // ------------------------------------------------------------------------------------------
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxGroup = 8;
 constexpr int kSelMaxCluster = 8;
-constexpr int kSelMaxKeys = 49152;  // keys of a CTA: 192 KiB of shared memory
+constexpr int kSelMaxPages = 49152;  // keys of a pair: 192 KiB of shared memory
+constexpr int kSelBins = 1024;
+constexpr int kSelRankKeys = 160;    // up to here ranks are counted, see below
 
 struct SelectParams {
     const uint16_t* q;
@@ -177,277 +272,409 @@ struct SelectParams {
     int32_t B, H, G, T, pool_pages, max_pages, budget, sink, recent;
 };
 
-// Order-preserving map of a score to an unsigned key; NaN (a page whose bounds were never written)
-// below everything, 0 and -0 equal.
+// Order-preserving map of a score to a key above 0; NaN (a page whose bounds were never written) below
+// everything, 0 and -0 equal.
 __device__ __forceinline__ uint32_t key_of(float x) {
-    if (!(x == x)) return 0u;
+    if (!(x == x)) return 1u;
     const uint32_t u = __float_as_uint(x + 0.0f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The four int8 of w as FP16 pairs (exact): v + 128 placed in the mantissa of 1024 + (v + 128).
+// The four int8 of w plus 128, as FP16 pairs of the value times 2^-24: a byte in the low half of an
+// FP16 mantissa is that subnormal, and the tensor cores take subnormals exactly.
 __device__ __forceinline__ void s8x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
     const uint32_t x = w ^ 0x80808080u;
-    const __half2 bias = as_h2(0x64806480u);  // 1152
-    lo = as_u32(__hsub2(as_h2(__byte_perm(x, 0x64646464u, 0x4140)), bias));
-    hi = as_u32(__hsub2(as_h2(__byte_perm(x, 0x64646464u, 0x4342)), bias));
+    lo = __byte_perm(x, 0u, 0x4140);
+    hi = __byte_perm(x, 0u, 0x4342);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) select_pages_kernel(const SelectParams p) {
+// What the kernel has to know of one radix pass: the bin that holds the wanted key, how many keys
+// are wanted from it and how many it has.
+struct RadixBin {
+    uint32_t bin, want, have;
+};
+
+// Inclusive sum over the CTA's threads (every thread calls); sums: one word per warp.
+template <int NT>
+__device__ __forceinline__ uint32_t cta_inclusive(uint32_t v, uint32_t* sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
+    }
+    if (lane == 31) sums[warp] = v;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NT / 32; ++k)
+        if (k < warp) v += sums[k];
+    return v;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const SelectParams p) {
     pdl_enter();
-    extern __shared__ uint32_t keys[];
-    __shared__ uint32_t hist[4][256];
-    __shared__ uint32_t warp_sum[kSelWarps][2];
-    __shared__ uint32_t found[2];    // bin of the pass, keys still wanted from it
-    __shared__ uint32_t cta_sum[2];  // this CTA's keys above and at the threshold
+    constexpr int NW = NT / 32;
+    constexpr int QROW = D + 8;  // FP16 of a query row in shared memory
+    extern __shared__ __align__(16) uint32_t keys[];  // [max_pages rounded up to 32], then two masks of as many bits
+    __shared__ __align__(16) uint32_t hist[kSelBins];
+    __shared__ __align__(16) uint16_t q_s[kSelMaxGroup * QROW];
+    __shared__ float f_s[kSelMaxGroup];   // step of each head's integers
+    __shared__ float bias_s[kSelMaxGroup];  // 128 times their sum
+    __shared__ uint32_t sums[2][NW];
+    __shared__ RadixBin found;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
+    if (C > 1) cluster.barrier_arrive();  // waited for before the first remote store
     const int pair = blockIdx.x / C;
     const int b = pair / p.H, h = pair - b * p.H;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
 
+    // loads that do not wait for one another: the length, the first page ids, the queries (a warp per
+    // head of the group)
+    const int32_t* row = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    auto id_at = [&](int i) { return i < p.max_pages ? __ldg(row + i) : -1; };
+    const int first = (rank * NW + warp) * 16, stride = C * NW * 16;
+    int id0 = id_at(first + r), id1 = id_at(first + r + 8);
     const int len = __ldg(p.seq_lens + b);
+    uint32_t qw[D / 64];  // BF16 pairs: dims [lane D/32, lane D/32 + D/32) of head `warp`
+    if (warp < p.G) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            p.q + (static_cast<int64_t>(pair) * p.G + warp) * D) + lane * (D / 64);
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) qw[k] = __ldg(src + k);
+    }
+
     const bool len_ok = len >= 0 && len <= static_cast<int64_t>(p.max_pages) * p.T;
     if (!len_ok && h == 0 && rank == 0 && tid == 0) flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
     const int n = len_ok ? static_cast<int>((static_cast<int64_t>(len) + p.T - 1) / p.T) : 0;
     const int count = min(n, p.budget);
-    const int per = ((n + C - 1) / C + 15) & ~15;
-    const int lo = min(n, rank * per), hi = min(n, lo + per), m = hi - lo;
-    const int32_t* row = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+    const bool choose = n > p.budget;
     int32_t* out_table = p.sel_table + static_cast<int64_t>(pair) * p.budget;
     int32_t* out_index = p.sel_index ? p.sel_index + static_cast<int64_t>(pair) * p.budget : nullptr;
-    if (rank == 0) {
-        for (int i = count + tid; i < p.budget; i += kSelThreads) {
-            out_table[i] = -1;
-            if (out_index) out_index[i] = -1;
-        }
-        // the last page is always taken, and it alone can be cut short
-        if (tid == 0) p.sel_lens[pair] = n > 0 ? (count - 1) * p.T + (len - (n - 1) * p.T) : 0;
-    }
-    const bool choose = n > p.budget;
 
     if (choose || p.scores) {
-        // ---- the group's queries as integers: lane (r, c) holds head r, dims [c D/4, c D/4 + D/4);
-        // fragments of the positive parts (against hi) and of the negative parts (against lo)
-        uint32_t qp[D / 16][2], qn[D / 16][2];
-        float f = 0.0f;
-        {
-            uint32_t w[D / 8];
-            float amax = 0.0f;
-            if (r < p.G) {
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + (static_cast<int64_t>(pair) * p.G + r) * D + c * (D / 4));
+        // tiles of 16 pages; lane (r, c) holds quarter c of the bounds of pages r and r + 8
+        struct Tile {
+            uint32_t hi0[D / 16], hi1[D / 16], lo0[D / 16], lo1[D / 16];
+            float s0, s1;
+            int a0, a1;  // page ids; -1: not scored, -2: outside the pool
+        };
+        auto load_tile = [&](int t, Tile& x) {  // with the ids of tile t; leaves those of the next one
+            auto checked = [&](int i, int id) {
+                if (i >= n || i < p.sink || i >= n - p.recent) return -1;
+                return id >= 0 && id < p.pool_pages ? id : -2;
+            };
+            x.a0 = checked(t + r, id0);
+            x.a1 = checked(t + r + 8, id1);
+            const int64_t ph0 = static_cast<int64_t>(max(x.a0, 0)) * p.H + h;
+            const int64_t ph1 = static_cast<int64_t>(max(x.a1, 0)) * p.H + h;
+            auto fetch = [&](bool there, const int8_t* a, uint32_t(&w)[D / 16]) {
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
-                    const uint4 v = __ldg(src + k);
+                for (int k = 0; k < D / 64; ++k) {
+                    const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(a) + k) : make_uint4(0u, 0u, 0u, 0u);
                     w[4 * k] = v.x;
                     w[4 * k + 1] = v.y;
                     w[4 * k + 2] = v.z;
                     w[4 * k + 3] = v.w;
                 }
-            } else {
-#pragma unroll
-                for (int k = 0; k < D / 8; ++k) w[k] = 0u;
-            }
+            };
+            const int8_t* src0 = p.bounds + ph0 * 2 * D + c * (D / 4);
+            const int8_t* src1 = p.bounds + ph1 * 2 * D + c * (D / 4);
+            fetch(x.a0 >= 0, src0, x.hi0);
+            fetch(x.a1 >= 0, src1, x.hi1);
+            fetch(x.a0 >= 0, src0 + D, x.lo0);
+            fetch(x.a1 >= 0, src1 + D, x.lo1);
+            x.s0 = x.a0 >= 0 ? __ldg(p.bscales + ph0) : 0.0f;
+            x.s1 = x.a1 >= 0 ? __ldg(p.bscales + ph1) : 0.0f;
+            id0 = id_at(t + r + stride);
+            id1 = id_at(t + r + 8 + stride);
+        };
+        Tile cur;
+        if (first < n) load_tile(first, cur);
+
+        // ---- the group's queries as integers, exact in FP16
+        for (int g = warp; g < kSelMaxGroup; g += NW) {  // (one round: there are at least 8 warps)
+            float amax = 0.0f, x[D / 32];
             bool finite = true;
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                const float x0 = fabsf(bf16_lo(w[k])), x1 = fabsf(bf16_hi(w[k]));
-                finite = finite && x0 < INFINITY && x1 < INFINITY;
-                amax = fmaxf(amax, fmaxf(x0, x1));
+            for (int k = 0; k < D / 64; ++k) {
+                x[2 * k] = g < p.G ? bf16_lo(qw[k]) : 0.0f;
+                x[2 * k + 1] = g < p.G ? bf16_hi(qw[k]) : 0.0f;
             }
-            if (!finite) amax = INFINITY;
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-            f = amax < INFINITY ? __fdiv_rn(amax, 255.0f) : 0.0f;
-            auto whole = [&](float x) { return f > 0.0f ? rintf(__fdiv_rn(x, f)) : 0.0f; };
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
-                const float x0 = whole(bf16_lo(w[k])), x1 = whole(bf16_hi(w[k]));
-                qp[k / 2][k % 2] = pack_f16x2(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f));
-                qn[k / 2][k % 2] = pack_f16x2(fminf(x0, 0.0f), fminf(x1, 0.0f));
+            for (int k = 0; k < D / 32; ++k) {
+                finite = finite && fabsf(x[k]) < INFINITY;
+                amax = fmaxf(amax, fabsf(x[k]));
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            const float f = __all_sync(0xFFFFFFFFu, finite) ? __fdiv_rn(amax, 255.0f) : 0.0f;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                x[k] = f > 0.0f ? rintf(__fdiv_rn(x[k], f)) : 0.0f;
+                sum += x[k];
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(q_s + g * QROW + lane * (D / 32));
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) dst[k] = pack_f16x2(x[2 * k], x[2 * k + 1]);
+            if (lane == 0) {
+                f_s[g] = f;
+                bias_s[g] = 128.0f * sum;
             }
         }
-        const float f0 = __shfl_sync(0xFFFFFFFFu, f, 8 * c), f1 = __shfl_sync(0xFFFFFFFFu, f, 8 * c + 4);
+        __syncthreads();
+        uint32_t q[D / 8];  // head r, dims [c D/4, c D/4 + D/4), which meet the same quarter of the bounds
+        {
+            const uint4* src = reinterpret_cast<const uint4*>(q_s + r * QROW + c * (D / 4));
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const uint4 v = src[k];
+                q[4 * k] = v.x;
+                q[4 * k + 1] = v.y;
+                q[4 * k + 2] = v.z;
+                q[4 * k + 3] = v.w;
+            }
+        }
+        const float f0 = f_s[2 * c], f1 = f_s[2 * c + 1];
+        const float bias0 = bias_s[2 * c], bias1 = bias_s[2 * c + 1];
         const bool has0 = 2 * c < p.G, has1 = 2 * c + 1 < p.G;
+        uint32_t* pair_keys = keys;
+        if (C > 1) {
+            cluster.barrier_wait();
+            pair_keys = cluster.map_shared_rank(keys, 0);
+        }
 
-        // ---- scores of this CTA's pages, 16 to a warp tile; lane (r, c) loads quarter c of the
-        // bounds of pages r and r + 8
-        auto page_at = [&](int i) -> int {  // page id of page i; -1: not scored, -2: outside the pool
-            if (i >= hi || i < p.sink || i >= n - p.recent) return -1;
-            const int id = __ldg(row + i);
-            return id >= 0 && id < p.pool_pages ? id : -2;
-        };
-        for (int t = warp * 16; t < m; t += kSelWarps * 16) {
-            const int i0 = lo + t + r, i1 = i0 + 8;
-            const int id0 = page_at(i0), id1 = page_at(i1);
-            uint32_t w0[D / 8], w1[D / 8];  // quarter c of hi, then of lo
-            float s0 = 0.0f, s1 = 0.0f;
-            auto fetch = [&](int id, uint32_t(&w)[D / 8], float& s) {
-                const int64_t ph = static_cast<int64_t>(id) * p.H + h;
-                if (id >= 0) {
-                    const int8_t* a = p.bounds + ph * 2 * D + c * (D / 4);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int k = 0; k < D / 64; ++k) {
-                            const uint4 v = __ldg(reinterpret_cast<const uint4*>(a + half * D) + k);
-                            w[half * (D / 16) + 4 * k] = v.x;
-                            w[half * (D / 16) + 4 * k + 1] = v.y;
-                            w[half * (D / 16) + 4 * k + 2] = v.z;
-                            w[half * (D / 16) + 4 * k + 3] = v.w;
-                        }
-                    s = __ldg(p.bscales + ph);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < D / 8; ++k) w[k] = 0u;
-                }
-            };
-            fetch(id0, w0, s0);
-            fetch(id1, w1, s1);
-            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = first; t < n; t += stride) {
+            Tile next;
+            if constexpr (D <= 128) {  // (at 256 the registers hold one tile)
+                if (t + stride < n) load_tile(t + stride, next);
+            }
+            // the positive parts of the queries meet the upper bounds, the negative the lower
+            float up[4] = {0.0f, 0.0f, 0.0f, 0.0f}, down[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t a[4];
-                s8x4_to_f16x2x2(w0[k], a[0], a[2]);
-                s8x4_to_f16x2x2(w1[k], a[1], a[3]);
-                mma_f16_16816(acc, a, qp[k][0], qp[k][1]);
-                s8x4_to_f16x2x2(w0[D / 16 + k], a[0], a[2]);
-                s8x4_to_f16x2x2(w1[D / 16 + k], a[1], a[3]);
-                mma_f16_16816(acc, a, qn[k][0], qn[k][1]);
+                s8x4_to_f16x2x2(cur.hi0[k], a[0], a[2]);
+                s8x4_to_f16x2x2(cur.hi1[k], a[1], a[3]);
+                mma_f16_16816(up, a, max_f16x2(q[2 * k], 0u), max_f16x2(q[2 * k + 1], 0u));
+                s8x4_to_f16x2x2(cur.lo0[k], a[0], a[2]);
+                s8x4_to_f16x2x2(cur.lo1[k], a[1], a[3]);
+                mma_f16_16816(down, a, min_f16x2(q[2 * k], 0u), min_f16x2(q[2 * k + 1], 0u));
             }
             auto score = [&](float x0, float x1, float s) {
                 float v = -INFINITY;
-                if (has0) v = __fmul_rn(__fmul_rn(x0, f0), s);
-                if (has1) v = fmaxf(v, __fmul_rn(__fmul_rn(x1, f1), s));
+                if (has0) v = __fmul_rn(__fmul_rn(x0 * 16777216.0f - bias0, f0), s);
+                if (has1) v = fmaxf(v, __fmul_rn(__fmul_rn(x1 * 16777216.0f - bias1, f1), s));
                 v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 1));
                 return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
             };
-            const float v0 = score(acc[0], acc[1], s0), v1 = score(acc[2], acc[3], s1);
+            const float v0 = score(up[0] + down[0], up[1] + down[1], cur.s0);
+            const float v1 = score(up[2] + down[2], up[3] + down[3], cur.s1);
             if (c < 2) {
-                const int i = c == 0 ? i0 : i1, id = c == 0 ? id0 : id1;
+                const int i = t + r + 8 * c, id = c == 0 ? cur.a0 : cur.a1;
                 float v = c == 0 ? v0 : v1;
-                if (i < hi) {
+                if (i < n) {
                     if (id == -1) v = INFINITY;
                     if (id == -2) {
                         v = -INFINITY;
                         flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
                     }
-                    if (choose) keys[i - lo] = id == -1 ? 0xFFFFFFFFu : key_of(v);
+                    if (choose) pair_keys[i] = id == -1 ? 0u : key_of(v);
                     if (p.scores) p.scores[static_cast<int64_t>(pair) * p.max_pages + i] = v;
                 }
             }
+            if constexpr (D <= 128) {
+                cur = next;
+            } else {
+                if (t + stride < n) load_tile(t + stride, cur);
+            }
         }
+    } else if (C > 1) {
+        cluster.barrier_wait();
     }
 
-    if (!choose) {  // every page is taken (the same for all CTAs of the cluster)
-        for (int i = lo + tid; i < hi; i += kSelThreads) {
+    if (choose) {  // (the same for all CTAs of the cluster) until every CTA's keys are written
+        if (C > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    }
+    if (rank != 0) return;
+    for (int i = count + tid; i < p.budget; i += NT) {
+        out_table[i] = -1;
+        if (out_index) out_index[i] = -1;
+    }
+    // the last page is always taken, and it alone can be cut short
+    if (tid == 0) p.sel_lens[pair] = n > 0 ? (count - 1) * p.T + (len - (n - 1) * p.T) : 0;
+    if (!choose) {  // every page is taken
+        for (int i = tid; i < n; i += NT) {
             out_table[i] = __ldg(row + i);
             if (out_index) out_index[i] = i;
         }
         return;
     }
 
-    // ---- the count-th largest key of the cluster
-    for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0u;
-    __syncthreads();
-    uint32_t prefix = 0u, mask = 0u, want = static_cast<uint32_t>(count);
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int i = tid; i < m; i += kSelThreads) {
+    // ---- the always-taken pages are [0, lo) and [hi, n); `want` of the keys in [lo, hi) are taken:
+    // those above `above`, and the first `equal` of those equal to it
+    const int lo = p.sink, hi = n - p.recent;
+    uint32_t want = static_cast<uint32_t>(count - p.sink - p.recent);
+    uint32_t above = 0xFFFFFFFFu, equal = 0u;
+    if (n <= kSelRankKeys) {
+        // one key a thread: its rank is how many keys come before it (those of always-taken pages are
+        // 0, below all others). At 128 pages this takes 0.6 us where the radix passes take 2; at 512
+        // it would take 4
+        if (tid >= n && tid < ((n + 3) & ~3)) keys[tid] = 0u;
+        __syncthreads();
+        if (tid < n) {
+            const uint32_t mine = keys[tid];
+            uint32_t before = 0u;
+            for (int j = 0; j < n; j += 4) {
+                const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
+                before += k.x > mine || (k.x == mine && j < tid);
+                before += k.y > mine || (k.y == mine && j + 1 < tid);
+                before += k.z > mine || (k.z == mine && j + 2 < tid);
+                before += k.w > mine || (k.w == mine && j + 3 < tid);
+            }
+            // the last one taken is the threshold
+            if (mine != 0u && before + 1 == want) found.bin = static_cast<uint32_t>(tid);
+        }
+        __syncthreads();
+        if (want > 0) {
+            const uint32_t last = found.bin;
+            above = keys[last];
+            // those equal to it up to its own place are taken
+            equal = static_cast<uint32_t>(__syncthreads_count(tid <= static_cast<int>(last) && keys[tid] == above));
+        }
+    } else if (want > 0) {
+        uint32_t top = 0u, low = 0xFFFFFFFFu;
+        for (int i = lo + tid; i < hi; i += NT) {
             const uint32_t k = keys[i];
-            if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255u], 1u);
+            top = max(top, k);
+            low = min(low, k);
         }
-        cluster.sync();
-        // thread t takes bin 255 - t: inclusive counts from the top bin down
-        uint32_t mine = 0u, incl = 0u;
-        if (tid < 256) {
-            for (int k = 0; k < C; ++k) mine += cluster.map_shared_rank(&hist[pass][0], k)[255 - tid];
-            incl = mine;
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        low = __reduce_min_sync(0xFFFFFFFFu, low);
+        if (lane == 0) {
+            sums[0][warp] = top;
+            sums[1][warp] = low;
+        }
+        __syncthreads();
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (lane == 31) warp_sum[warp][0] = incl;
+        for (int k = 0; k < NW; ++k) {
+            top = max(top, sums[0][k]);
+            low = min(low, sums[1][k]);
         }
-        __syncthreads();
-        if (tid < 256) {
-            for (int k = 0; k < warp; ++k) incl += warp_sum[k][0];
-            const uint32_t excl = incl - mine;
-            if (excl < want && want <= incl) {
-                found[0] = static_cast<uint32_t>(255 - tid);
-                found[1] = want - excl;
+        // keys agree above bit `bits`; a pass looks at the next 10 bits below
+        int bits = 32 - __clz(top ^ low);
+        uint32_t prefix = bits < 32 ? (top >> bits) << bits : 0u;
+        bool whole_bin = false;
+        while (bits > 0) {
+            const int shift = max(0, bits - 10);
+            const uint32_t mask = bits < 32 ? ~((1u << bits) - 1u) : 0u;
+#pragma unroll
+            for (int i = 0; i < kSelBins / NT; ++i) hist[tid + i * NT] = 0u;
+            __syncthreads();
+            for (int i = lo + tid; i < hi; i += NT) {
+                const uint32_t k = keys[i];
+                if ((k & mask) == prefix) atomicAdd(&hist[(k & ~mask) >> shift], 1u);
             }
+            __syncthreads();
+            // thread t sums the bins below 1024 - PER t, from the top
+            constexpr int PER = kSelBins / NT;
+            const int b0 = kSelBins - PER - PER * tid;
+            uint32_t mine = 0u;
+#pragma unroll
+            for (int k = 0; k < PER; ++k) mine += hist[b0 + k];
+            uint32_t at = cta_inclusive<NT>(mine, sums[0]) - mine;
+            if (at < want && want <= at + mine) {
+#pragma unroll
+                for (int k = PER - 1; k >= 0; --k) {
+                    const uint32_t have = hist[b0 + k];
+                    if (at < want && want <= at + have)
+                        found = RadixBin{static_cast<uint32_t>(b0 + k), want - at, have};
+                    at += have;
+                }
+            }
+            __syncthreads();
+            prefix |= found.bin << shift;
+            want = found.want;
+            bits = shift;
+            whole_bin = found.have == want;
+            if (whole_bin) break;
         }
-        __syncthreads();
-        prefix |= found[0] << shift;
-        mask |= 255u << shift;
-        want = found[1];
-        __syncthreads();  // found and warp_sum are free for the next pass
+        // a bin taken whole: every key from its lowest on (0 cannot be, it would be all the keys)
+        above = whole_bin ? prefix - 1u : prefix;
+        equal = whole_bin ? 0u : want;
     }
 
-    // ---- the selected pages in ascending order: thread t looks at a run of consecutive keys
-    const int run = (m + kSelThreads - 1) / kSelThreads;
-    const int j0 = min(m, tid * run), j1 = min(m, j0 + run);
-    uint32_t above = 0u, equal = 0u;
-    for (int j = j0; j < j1; ++j) {
-        above += keys[j] > prefix;
-        equal += keys[j] == prefix;
-    }
-    uint32_t ia = above, ie = equal;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t va = __shfl_up_sync(0xFFFFFFFFu, ia, o), ve = __shfl_up_sync(0xFFFFFFFFu, ie, o);
-        if (lane >= o) {
-            ia += va;
-            ie += ve;
+    // ---- the selected pages in ascending order: a warp takes consecutive keys, 32 at a time, and
+    // leaves one mask of those above the threshold and one of those at it
+    const int words = (n + 31) >> 5;
+    uint32_t* over = keys + ((p.max_pages + 31) & ~31);
+    uint32_t* same = over + ((p.max_pages + 31) >> 5);
+    const int share = (words + NW - 1) / NW;
+    const int w0 = min(words, warp * share), w1 = min(words, w0 + share);
+    uint32_t bo = 0u, bs = 0u;
+#pragma unroll 4
+    for (int w = w0; w < w1; ++w) {
+        const int i = 32 * w + lane;
+        const bool forced = i < lo || i >= hi;
+        const uint32_t k = i < n ? keys[i] : 0u;
+        const uint32_t mo = __ballot_sync(0xFFFFFFFFu, i < n && (forced || k > above));
+        const uint32_t ms = __ballot_sync(0xFFFFFFFFu, i < n && !forced && k == above);
+        if (lane == 0) {
+            over[w] = mo;
+            same[w] = ms;
         }
+        bo += __popc(mo);
+        bs += __popc(ms);
     }
-    if (lane == 31) {
-        warp_sum[warp][0] = ia;
-        warp_sum[warp][1] = ie;
+    __syncthreads();  // sums and keys are free, once every warp is here
+    if (lane == 0) {
+        sums[0][warp] = bo;
+        sums[1][warp] = bs;
     }
     __syncthreads();
-    uint32_t ba = ia - above, be = ie - equal;
-    for (int k = 0; k < warp; ++k) {
-        ba += warp_sum[k][0];
-        be += warp_sum[k][1];
-    }
-    if (tid == kSelThreads - 1) {
-        cta_sum[0] = ba + above;
-        cta_sum[1] = be + equal;
-    }
-    cluster.sync();
-    for (int k = 0; k < rank; ++k) {
-        const uint32_t* other = cluster.map_shared_rank(&cta_sum[0], k);
-        ba += other[0];
-        be += other[1];
-    }
-    for (int j = j0; j < j1; ++j) {
-        const uint32_t k = keys[j];
-        if (k > prefix || (k == prefix && be < want)) {
-            const uint32_t at = ba + min(be, want);
-            out_table[at] = __ldg(row + lo + j);
-            if (out_index) out_index[at] = lo + j;
+    bo = bs = 0u;
+#pragma unroll
+    for (int k = 0; k < NW; ++k)
+        if (k < warp) {
+            bo += sums[0][k];
+            bs += sums[1][k];
         }
-        ba += k > prefix;
-        be += k == prefix;
+#pragma unroll 4
+    for (int w = w0; w < w1; ++w) {
+        const uint32_t mo = over[w], ms = same[w], less = (1u << lane) - 1u;
+        const uint32_t es = bs + __popc(ms & less);
+        if (((mo >> lane) & 1u) || (((ms >> lane) & 1u) && es < equal))
+            keys[bo + __popc(mo & less) + min(es, equal)] = static_cast<uint32_t>(32 * w + lane);
+        bo += __popc(mo);
+        bs += __popc(ms);
     }
-    cluster.sync();  // no CTA leaves while another may still read its counts
+    __syncthreads();
+    for (int j = tid; j < count; j += NT) {
+        const int i = static_cast<int>(keys[j]);
+        out_table[j] = __ldg(row + i);
+        if (out_index) out_index[j] = i;
+    }
 }
 
-template <int D>
+template <int D, int NT>
 cudaError_t launch_select(const SelectParams& p, int cluster, size_t smem, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kSelMaxKeys * 4);
-    if (e != cudaSuccess) return e;
+    if (smem > 36 * 1024) {  // with the static arrays, past the 48 KiB a launch may use by default
+        const cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, NT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxPages / 32 * 136);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.B * p.H * cluster));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -459,7 +686,12 @@ cudaError_t launch_select(const SelectParams& p, int cluster, size_t smem, cudaS
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_pages_kernel<D>, p);
+    return cudaLaunchKernelEx(&cfg, select_pages_kernel<D, NT>, p);
+}
+
+template <int D>
+cudaError_t launch_select_for(const SelectParams& p, bool large, int cluster, size_t smem, cudaStream_t s) {
+    return large ? launch_select<D, 512>(p, cluster, smem, s) : launch_select<D, 256>(p, cluster, smem, s);
 }
 
 }  // namespace
@@ -473,7 +705,8 @@ extern "C" nvfp4kv_status nvfp4_kv_page_bounds(
     int8_t* bounds, float* bound_scales, int32_t* status, nvfp4kv_stream_t stream) {
     if (!layout_ok(layout) || num_pages < 0) return NVFP4KV_ERR_INVALID_ARG;
     const int D = layout->head_dim;
-    if (D != 64 && D != 128 && D != 256) return NVFP4KV_ERR_UNSUPPORTED;
+    if ((D != 64 && D != 128 && D != 256) || layout->page_size % 16 != 0)
+        return NVFP4KV_ERR_UNSUPPORTED;
     if (num_pages == 0) return NVFP4KV_OK;
     if (!k_data || !k_scales || !bounds || !bound_scales || pool_pages <= 0 ||
         !aligned16(k_data) || !aligned16(k_scales) || !aligned16(bounds) ||
@@ -524,17 +757,16 @@ extern "C" nvfp4kv_status nvfp4_kv_select_pages(
         !aligned16(q) || !aligned16(bounds))
         return NVFP4KV_ERR_INVALID_ARG;
     const int64_t pairs = static_cast<int64_t>(batch) * H;
-    if (pairs > 65535 || max_pages_per_seq > kSelMaxKeys * kSelMaxCluster ||
+    if (pairs > 65535 || max_pages_per_seq > kSelMaxPages ||
         static_cast<int64_t>(max_pages_per_seq) * layout->page_size > INT32_MAX ||
         static_cast<int64_t>(budget) * layout->page_size > INT32_MAX)
         return NVFP4KV_ERR_UNSUPPORTED;
-    // CTAs per pair: enough to fill the GPU when there are few pairs, but at least 128 pages (one
-    // tile for every second warp) each, and no more keys than fit in shared memory
+    // CTAs per pair: while they fit the GPU at two CTAs of 256 threads per SM and each still has a tile
+    // for every warp. CTAs of 512 threads where even they fit at once
     int cluster = 1;
-    while (cluster < kSelMaxCluster &&
-           ((pairs * cluster < num_sms() && max_pages_per_seq > 128 * cluster) ||
-            max_pages_per_seq > kSelMaxKeys * cluster))
+    while (cluster < kSelMaxCluster && pairs * cluster <= num_sms() && max_pages_per_seq > 128 * cluster)
         cluster *= 2;
+    const bool large = pairs * cluster <= num_sms() && max_pages_per_seq > 128 * cluster;
     SelectParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.bounds = bounds;
@@ -555,13 +787,13 @@ extern "C" nvfp4kv_status nvfp4_kv_select_pages(
     p.budget = budget;
     p.sink = sink_pages;
     p.recent = recent_pages;
-    const size_t smem = static_cast<size_t>(((max_pages_per_seq + cluster - 1) / cluster + 15) & ~15) * 4;
+    const size_t smem = static_cast<size_t>((max_pages_per_seq + 31) / 32) * (32 * 4 + 2 * 4);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (D) {
-    case 64: e = launch_select<64>(p, cluster, smem, s); break;
-    case 128: e = launch_select<128>(p, cluster, smem, s); break;
-    default: e = launch_select<256>(p, cluster, smem, s); break;
+    case 64: e = launch_select_for<64>(p, large, cluster, smem, s); break;
+    case 128: e = launch_select_for<128>(p, large, cluster, smem, s); break;
+    default: e = launch_select_for<256>(p, large, cluster, smem, s); break;
     }
     return e == cudaSuccess ? launch_status() : NVFP4KV_ERR_CUDA;
 }

@@ -74,7 +74,7 @@ def test_no_rows_is_a_no_op(kv):
 def test_bounds_refuses(kv):
     f = kv.load().nvfp4_kv_page_bounds
     good = [kv.Layout(8, 128, 64), FAKE, FAKE, 8, None, None, 8, FAKE, FAKE, None, None]
-    for at, bad, code in ((0, kv.Layout(8, 96, 64), 2), (0, kv.Layout(8, 120, 64), 1), (1, None, 1), (1, MIS, 1),
+    for at, bad, code in ((0, kv.Layout(8, 96, 64), 2), (0, kv.Layout(8, 120, 64), 1), (0, kv.Layout(8, 128, 40), 2), (1, None, 1), (1, MIS, 1),
                           (2, MIS, 1), (3, 0, 1), (6, -1, 1), (6, 9, 1), (7, None, 1), (7, MIS, 1), (8, None, 1)):
         a = list(good)
         a[at] = bad
@@ -87,7 +87,7 @@ def test_select_refuses(kv):
             None, None]
     for at, bad, code in ((0, kv.Layout(8, 96, 64), 2), (1, -1, 1), (2, 0, 1), (2, 30, 2), (2, 72, 2), (3, MIS, 1),
                           (3, None, 1), (4, MIS, 1), (5, None, 1), (6, 0, 1), (7, None, 1), (8, 0, 1),
-                          (8, 8 * 49152 + 1, 2), (9, None, 1), (10, 0, 1), (10, 1, 1), (11, -1, 1), (11, 10, 1),
+                          (8, 49152 + 1, 2), (9, None, 1), (10, 0, 1), (10, 1, 1), (11, -1, 1), (11, 10, 1),
                           (12, 0, 1), (12, 11, 1), (13, None, 1), (14, None, 1), (1, 8192, 2),
                           (10, 1 << 30, 2), (0, kv.Layout(8, 128, 1 << 28), 2)):
         a = list(good)
@@ -119,7 +119,7 @@ def test_binding_refuses_tensors_on_the_host(kv):
     k = torch.zeros(2, 8, 128, dtype=torch.bfloat16)
     b = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     lay = kv.Layout(8, 128, 64)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="CUDA"):
         kv.nvfp4_kv_append(lay, k, k, torch.zeros(2, dtype=torch.int64), b(1, 8, 64, 64), b(1, 8, 64, 8),
                            b(1, 8, 64, 64), b(1, 8, 64, 8))
     with pytest.raises(ValueError):   # the pool's scales are short
@@ -128,6 +128,27 @@ def test_binding_refuses_tensors_on_the_host(kv):
     with pytest.raises(ValueError):   # slots of another type
         kv.nvfp4_kv_append(lay, k, k, torch.zeros(2, dtype=torch.int32), b(1, 8, 64, 64), b(1, 8, 64, 8),
                            b(1, 8, 64, 64), b(1, 8, 64, 8))
+    f = lambda *s: torch.zeros(s)  # noqa: E731
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    i8 = lambda *s: torch.zeros(s, dtype=torch.int8)  # noqa: E731
+    for kd, bo, sc, kw in ((b(2, 8, 64, 64), i8(2, 8, 2, 64), f(2, 8), {}), (b(2, 8, 64, 64), i8(2, 8, 2, 128), f(2, 7), {}),
+                           (b(2, 8, 64, 64), b(2, 8, 2, 128), f(2, 8), {}),
+                           (b(2, 8, 64, 64), i8(2, 8, 2, 128), f(2, 8), dict(page_ids=i(3), page_tokens=i(2)))):
+        with pytest.raises(ValueError, match="must be"):
+            kv.nvfp4_kv_page_bounds(lay, kd, b(2, 8, 64, 8), bo, sc, **kw)
+    q = torch.zeros(3, 16, 128, dtype=torch.bfloat16)
+    good = dict(q=q, bounds=i8(2, 8, 2, 128), bound_scales=f(2, 8), page_table=i(3, 5), seq_lens=i(3),
+                sel_page_table=i(3, 8, 2), sel_lens=i(3, 8))
+    for bad in (dict(q=q[..., :64]), dict(q=q.float()), dict(seq_lens=i(2)), dict(sel_lens=i(8)),
+                dict(sel_page_table=i(3, 7, 2)), dict(page_table=i(3, 5).long()), dict(scores=f(3, 8, 4)),
+                dict(sel_index=i(3, 8, 3))):
+        with pytest.raises(ValueError, match="must be"):
+            kv.nvfp4_kv_select_pages(lay, **{**good, **bad})
+    pool = [b(2, 8, 64, 64), b(2, 8, 64, 8), None, b(2, 8, 64, 64), b(2, 8, 64, 8), None]
+    for tab, ln, out, lse in ((i(3, 8, 2), i(3, 7), q, None), (i(3, 7, 2), i(3, 8), q, None),
+                              (i(3, 8, 2), i(3, 8), q.half(), None), (i(3, 8, 2), i(3, 8), q, f(3, 15))):
+        with pytest.raises(ValueError, match="must be"):
+            kv.nvfp4_paged_sparse_decode_attention(lay, q, *pool, tab, ln, 0.1, out, lse=lse)
     with pytest.raises(ValueError):
         kv.Rotary(kv.ROTARY_HALVES, 0, 64, torch.zeros(4, 32))
 
