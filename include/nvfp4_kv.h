@@ -353,7 +353,7 @@ nvfp4kv_status nvfp4_paged_decode_attention_noalloc(
  *   q, k, v        row n of q at q + n * q_row_stride elements, [heads][D] contiguous in a row (so
  *                  the three may be slices of one projection); 16-byte aligned, strides multiples
  *                  of 8 and at least heads * D
- *   slots          int64 [num_rows]; -1 marks a padding row: nothing of it is read or written. Two
+ *   slots          int64 [num_rows]; -1 marks a padding row, of which nothing is written. Two
  *                  rows of a call with the same slot race (the slot then holds bytes of either)
  *   rotary         host pointer, NULL = no rotation (positions is not read then)
  *   positions      int32 [num_rows], 0 <= position < rotary->max_positions

@@ -13,10 +13,12 @@
 // position (at most 4 D bytes) is read once per warp task into registers and reused for every head
 // of the task.
 //
-// A thread owns 32 dims of one head: two 16-value blocks that rotate with one another (block i of
-// the first half with block i of the second, or two neighbouring blocks when adjacent dims pair
-// up), so the rotation, the block maximum and the packing need no other thread. A warp covers
-// 32 / (D / 32) heads at a time.
+// A thread owns 8 dims of each of two 16-value blocks of one head that rotate with one another (block i
+// of the first half with block i of the second, or two neighbouring blocks when adjacent dims pair
+// up), so the rotation needs no other thread, and two neighbouring lanes hold the two blocks: they
+// share the block maximum by a shuffle and each picks the scale of one block. (With whole blocks in a
+// thread the kernel needed 157 registers, and 128 with spills kept 16 warps on an SM: 46.6 us for
+// 8192 rows of 32 + 8 + 8 heads of 128; the halves take 64.)
 //
 // K bytes belong to one token each. A V byte holds two tokens (token pairs): when the next row of
 // the call is the second token of the pair, one thread encodes both and stores whole bytes; a token
@@ -60,27 +62,57 @@ struct AppendParams {
     int32_t rot_units;         // rotated dims / 32
     int32_t max_pos;
     int32_t out_f16;           // the 16-bit outputs are FP16 (else BF16)
-    int32_t wide;              // every source row is 32-byte aligned
     int32_t segs_rot, segs;    // warp-wide head groups of a row: q and K heads, then V heads
     int32_t segs_per_task, tasks_per_row;
     int64_t tasks;
 };
 
-// 16 values of a source row.
-__device__ __forceinline__ U8x32 load_block(const uint8_t* a, bool wide) {
-    if (wide) return ld_stream_32B(a);
-    const uint4 lo = ld_stream_16B(a), hi = ld_stream_16B(a + 16);
-    return U8x32{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
+// 8 values of a source row as exact fp32.
+template <int SRC>
+__device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = SRC == NVFP4KV_BF16 ? bf16_lo(w[j]) : f16_lo(w[j]);
+        x[2 * j + 1] = SRC == NVFP4KV_BF16 ? bf16_hi(w[j]) : f16_hi(w[j]);
+    }
 }
 
-// 16 values rounded to the 16-bit output type (round to nearest even).
-__device__ __forceinline__ void store_block(uint8_t* a, const float (&x)[16], bool f16) {
-    uint32_t w[8];
+// 8 values rounded to the 16-bit output type (round to nearest even).
+__device__ __forceinline__ void store8(uint8_t* a, const float (&x)[8], bool f16) {
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int j = 0; j < 4; ++j)
         w[j] = f16 ? pack_f16x2(x[2 * j], x[2 * j + 1]) : pack_bf16x2(x[2 * j], x[2 * j + 1]);
-    *reinterpret_cast<uint4*>(a) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(a + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    st_cs(a, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(x[j]));
+    return a;
+}
+
+// The scale picks of two blocks whose halves lie in lanes 2j and 2j + 1: a0, a1 are this lane's
+// maxima of block 0 and 1; the even lane picks for block 0, the odd one for block 1 (the arithmetic of
+// pick_scale), and both get scale bytes and reciprocals of both. Both lanes of a pair call.
+__device__ __forceinline__ void pick_two(float a0, float a1, float g, float d, uint32_t& s0, uint32_t& s1,
+                                         float& r0, float& r1) {
+    const bool odd = (threadIdx.x & 1) != 0;
+    const uint32_t lanes = 3u << (threadIdx.x & 30);
+    // the other lane's maximum of the block that this lane picks for
+    const float other = __shfl_xor_sync(lanes, odd ? a0 : a1, 1);
+    const float a = fmaxf(odd ? a1 : a0, other);
+    const uint32_t sb = f32x2_to_e4m3x2(__fdiv_rn(a, d), 0.0f) & 0xFFu;
+    const float sg = __fmul_rn(e4m3_to_f32(sb), g);
+    const float r = (sg == 0.0f) ? 0.0f : __frcp_rn(sg);
+    const uint32_t so = __shfl_xor_sync(lanes, sb, 1);
+    const float ro = __shfl_xor_sync(lanes, r, 1);
+    s0 = odd ? so : sb;
+    s1 = odd ? sb : so;
+    r0 = odd ? ro : r;
+    r1 = odd ? r : ro;
 }
 
 // (x1, x2) -> (x1 c - x2 s, x2 c + x1 s), every product and sum rounded to fp32.
@@ -91,17 +123,17 @@ __device__ __forceinline__ void rotate(float& x1, float& x2, float c, float s) {
 }
 
 template <int SRC, int D, int STYLE>
-__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendParams p) {
     pdl_enter();
-    constexpr int U = D / 32;   // threads of a head
-    constexpr int HW = 32 / U;  // heads of a warp
+    constexpr int L = D / 16;   // lanes of a head
+    constexpr int HW = 32 / L;  // heads of a warp
     constexpr int NB = D / 16;
     const int lane = threadIdx.x & 31;
-    const int i = lane % U, hl = lane / U;
+    const int i = (lane % L) >> 1, half = lane & 1, hl = lane / L;
     const int warps = static_cast<int>(gridDim.x) * (kAppendThreads / 32);
     const int half_T = p.T / 2;
     const float gk = p.gk ? __ldg(p.gk) : 1.0f, gv = p.gv ? __ldg(p.gv) : 1.0f;
-    const bool wide = p.wide != 0, f16 = p.out_f16 != 0;
+    const bool f16 = p.out_f16 != 0;
 
     // the thread's two blocks: a rotated pair, or two of the blocks outside the rotated dims
     const bool turns = i < p.rot_units;
@@ -114,6 +146,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
         b0 = e < p.first_blk ? e : e + 2 * p.rot_units;
         b1 = e + 1 < p.first_blk ? e + 1 : e + 1 + 2 * p.rot_units;
     }
+    const int o0 = 32 * b0 + 16 * half, o1 = 32 * b1 + 16 * half;  // bytes of its values within a head
 
     for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
          task < p.tasks; task += warps) {
@@ -121,8 +154,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
         const int seg0 = static_cast<int>(task - static_cast<int64_t>(row) * p.tasks_per_row) * p.segs_per_task;
         const int seg1 = min(seg0 + p.segs_per_task, p.segs);
         const int64_t slot = __ldg(p.slots + row);
-        if (slot == -1) continue;  // a padding row
         const int pos = p.positions ? __ldg(p.positions + row) : 0;
+
+        if (slot == -1) continue;  // a padding row
         const bool pos_ok = !p.positions || (pos >= 0 && pos < p.max_pos);
         if (slot < 0 || slot >= p.num_slots || !pos_ok) {
             if (lane == 0)
@@ -132,13 +166,31 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
         const int64_t page = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(slot), p.t_magic));
         const int t = static_cast<int>(slot - page * p.T);
 
-        float cs[16], sn[16];
+        // a head group's q and K values are loaded while the one before is worked on (two groups ahead took
+        // 48 us for 8192 rows against 43, the first group's loads before the slot is known 45)
+        const int rot1 = min(seg1, p.segs_rot);
+        auto source = [&](int seg) -> const uint8_t* {  // null: no head for this thread
+            const int head = seg * HW + hl;
+            if (seg >= rot1 || head >= p.Hq + p.H) return nullptr;
+            return head < p.Hq ? p.q + row * p.q_stride + head * (D * 2)
+                               : p.k + row * p.k_stride + (head - p.Hq) * (D * 2);
+        };
+        uint4 n0, n1;
+        if (const uint8_t* src = source(seg0)) {
+            n0 = ld_stream_16B(src + o0);
+            n1 = ld_stream_16B(src + o1);
+        }
+        // halves: the cosines and sines of dims 8 half .. +7 of the block; adjacent pairs: those of the
+        // four pairs in each of the two blocks
+        float cs[8], sn[8];
         if (seg0 < p.segs_rot && turns) {
-            const float* row_cs = p.table + static_cast<int64_t>(pos) * 32 * p.rot_units + 16 * i;
+            const float* row_cs = p.table + static_cast<int64_t>(pos) * 32 * p.rot_units + 16 * i +
+                                  (STYLE == NVFP4KV_ROTARY_HALVES ? 8 : 4) * half;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4 c4 = __ldg(reinterpret_cast<const float4*>(row_cs) + j);
-                const float4 s4 = __ldg(reinterpret_cast<const float4*>(row_cs + 16 * p.rot_units) + j);
+            for (int j = 0; j < 2; ++j) {
+                const float* at = row_cs + (STYLE == NVFP4KV_ROTARY_HALVES ? 4 : 8) * j;
+                const float4 c4 = __ldg(reinterpret_cast<const float4*>(at));
+                const float4 s4 = __ldg(reinterpret_cast<const float4*>(at + 16 * p.rot_units));
                 cs[4 * j] = c4.x;
                 cs[4 * j + 1] = c4.y;
                 cs[4 * j + 2] = c4.z;
@@ -149,72 +201,62 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
                 sn[4 * j + 3] = s4.w;
             }
         }
-
-        // ---- q and K heads; a head group's values are loaded while the one before is worked on
-        const int rot1 = min(seg1, p.segs_rot);
-        auto source = [&](int seg) -> const uint8_t* {  // null: no head for this thread
-            const int head = seg * HW + hl;
-            if (seg >= rot1 || head >= p.Hq + p.H) return nullptr;
-            return head < p.Hq ? p.q + row * p.q_stride + static_cast<int64_t>(head) * D * 2
-                               : p.k + row * p.k_stride + static_cast<int64_t>(head - p.Hq) * D * 2;
-        };
-        U8x32 n0, n1;
-        {
-            const uint8_t* src = source(seg0);
-            if (src) {
-                n0 = load_block(src + 32 * b0, wide);
-                n1 = load_block(src + 32 * b1, wide);
-            }
-        }
+        // ---- q and K heads
         for (int seg = seg0; seg < rot1; ++seg) {
             const int head = seg * HW + hl;
-            float x0[16], x1[16];
-            widen<SRC>(n0, 1.0f, x0);
-            widen<SRC>(n1, 1.0f, x1);
-            const uint8_t* src = source(seg + 1);
-            if (src) {
-                n0 = load_block(src + 32 * b0, wide);
-                n1 = load_block(src + 32 * b1, wide);
+            float x0[8], x1[8];
+            widen8<SRC>(n0, x0);
+            widen8<SRC>(n1, x1);
+            if (const uint8_t* src = source(seg + 1)) {
+                n0 = ld_stream_16B(src + o0);
+                n1 = ld_stream_16B(src + o1);
             }
             if (head >= p.Hq + p.H) continue;
-            const bool is_q = head < p.Hq;
-            const int kh = head - p.Hq;
             if (turns) {
                 if constexpr (STYLE == NVFP4KV_ROTARY_HALVES) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) rotate(x0[j], x1[j], cs[j], sn[j]);
+                    for (int j = 0; j < 8; ++j) rotate(x0[j], x1[j], cs[j], sn[j]);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         rotate(x0[2 * j], x0[2 * j + 1], cs[j], sn[j]);
-                        rotate(x1[2 * j], x1[2 * j + 1], cs[8 + j], sn[8 + j]);
+                        rotate(x1[2 * j], x1[2 * j + 1], cs[4 + j], sn[4 + j]);
                     }
                 }
             }
-            if (is_q) {
-                uint8_t* dst = p.q_out + row * p.q_out_stride + static_cast<int64_t>(head) * D * 2;
-                store_block(dst + 32 * b0, x0, f16);
-                store_block(dst + 32 * b1, x1, f16);
+            if (head < p.Hq) {
+                uint8_t* dst = p.q_out + row * p.q_out_stride + head * (D * 2);
+                store8(dst + o0, x0, f16);
+                store8(dst + o1, x1, f16);
             } else {
+                const int kh = head - p.Hq;
                 const int64_t krow = (page * p.H + kh) * p.T + t;
-                const float d = __fmul_rn(6.0f, gk);
-                auto put = [&](const float(&x)[16], int b) {
-                    uint32_t sb;
-                    float r;
-                    pick_scale(x, gk, d, sb, r);
-                    const uint2 code = pack_e2m1_block(x, r);
-                    *reinterpret_cast<uint2*>(p.kd + krow * (D / 2) + 8 * b) = code;
-                    p.ks[krow * NB + b] = static_cast<uint8_t>(sb);
-                    if (p.k_out) {
-                        float y[16];
-                        block_values(code, sb, y);
+                uint32_t s0, s1;
+                float r0, r1;
+                pick_two(amax8(x0), amax8(x1), gk, __fmul_rn(6.0f, gk), s0, s1, r0, r1);
+                auto put = [&](const float(&x)[8], uint32_t sb, float rr, int b) {
+                    uint32_t code = 0u;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] = __fmul_rn(y[j], gk);
-                        store_block(p.k_out + ((static_cast<int64_t>(row) * p.H + kh) * D + 16 * b) * 2, y, f16);
+                    for (int j = 0; j < 4; ++j)
+                        code |= f32x2_to_e2m1x2(__fmul_rn(x[2 * j], rr), __fmul_rn(x[2 * j + 1], rr)) << (8 * j);
+                    *reinterpret_cast<uint32_t*>(p.kd + krow * (D / 2) + 8 * b + 4 * half) = code;
+                    if (p.k_out) {
+                        uint32_t v[4];
+                        e2m1x8_to_f16x2x4(code, v);
+                        const uint32_t s2 = e4m3x2_to_f16x2(sb * 0x0101u);
+                        float y[8];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t e = hmul2_u32(v[j], s2);
+                            y[2 * j] = __fmul_rn(f16_lo(e), gk);
+                            y[2 * j + 1] = __fmul_rn(f16_hi(e), gk);
+                        }
+                        store8(p.k_out + ((static_cast<int64_t>(row) * p.H + kh) * D + 16 * b + 8 * half) * 2, y, f16);
                     }
                 };
-                put(x0, b0);
-                put(x1, b1);
+                put(x0, s0, r0, b0);
+                put(x1, s1, r1, b1);
+                p.ks[krow * NB + (half ? b1 : b0)] = static_cast<uint8_t>(half ? s1 : s0);
             }
         }
         if (seg1 <= p.segs_rot) continue;
@@ -233,57 +275,56 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
         for (int seg = max(seg0, p.segs_rot); seg < seg1; ++seg) {
             const int h = (seg - p.segs_rot) * HW + hl;
             if (h >= p.H) continue;
-            const uint8_t* src = p.v + row * p.v_stride + static_cast<int64_t>(h) * D * 2;
+            const uint8_t* src = p.v + row * p.v_stride + h * (D * 2) + 64 * i + 16 * half;
             const int64_t vrow = (page * p.H + h) * half_T + (t >> 1);
             const float d = __fmul_rn(6.0f, gv);
-            U8x32 v0[2], v1[2];
+            uint4 w0[2], w1[2];  // blocks 2i and 2i + 1 of this row and the next
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                v0[u] = load_block(src + 32 * (2 * i + u), wide);
-                if (both) v1[u] = load_block(src + p.v_stride + 32 * (2 * i + u), wide);
+                w0[u] = ld_stream_16B(src + 32 * u);
+                w1[u] = both ? ld_stream_16B(src + p.v_stride + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int b = 2 * i + u;
-                float x0[16], x1[16];  // first and second token of the pair
-                widen<SRC>(v0[u], 1.0f, x0);
-                if (both) widen<SRC>(v1[u], 1.0f, x1);
-                uint32_t s0, s1 = 0u;
-                float r0, r1 = 0.0f;
-                pick_scale(x0, gv, d, s0, r0);
-                if (both) pick_scale(x1, gv, d, s1, r1);
-                uint32_t w[4];
+                float x0[8], x1[8];  // first and second token of the pair
+                widen8<SRC>(w0[u], x0);
+                widen8<SRC>(w1[u], x1);
+                uint32_t s0, s1;
+                float r0, r1;
+                pick_two(amax8(x0), amax8(x1), gv, d, s0, s1, r0, r1);
+                uint32_t w[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
+                for (int e = 0; e < 2; ++e) {
                     w[e] = 0u;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float y0 = __fmul_rn(x0[4 * e + j], r0);
-                        const float y1 = both ? __fmul_rn(x1[4 * e + j], r1) : 0.0f;
-                        w[e] |= f32x2_to_e2m1x2(y0, y1) << (8 * j);
+                        const int k = 4 * e + j;
+                        w[e] |= f32x2_to_e2m1x2(__fmul_rn(x0[k], r0), __fmul_rn(x1[k], r1)) << (8 * j);
                     }
                 }
-                uint8_t* vd = p.vd + vrow * D + 16 * b;
+                uint8_t* vd = p.vd + vrow * D + 16 * b + 8 * half;
                 uint8_t* vs = p.vs + vrow * (2 * NB) + 2 * b;
                 if (both) {
-                    *reinterpret_cast<uint4*>(vd) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint16_t*>(vs) = static_cast<uint16_t>(s0 | (s1 << 8));
+                    *reinterpret_cast<uint2*>(vd) = make_uint2(w[0], w[1]);
+                    if (!half) *reinterpret_cast<uint16_t*>(vs) = static_cast<uint16_t>(s0 | (s1 << 8));
                 } else {
                     unsigned int* words = reinterpret_cast<unsigned int*>(vd);
                     const uint32_t keep = odd ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t code = w[e] & 0x0F0F0F0Fu;
                         atomicAnd(words + e, keep);
-                        atomicOr(words + e, odd ? w[e] << 4 : w[e]);
+                        atomicOr(words + e, odd ? code << 4 : code);
                     }
-                    vs[odd ? 1 : 0] = static_cast<uint8_t>(s0);
+                    if (!half) vs[odd ? 1 : 0] = static_cast<uint8_t>(s0);
                 }
                 if (p.v_out) {
                     // a byte's two codes times the two tokens' scales, exact in FP16
                     const uint32_t s2 = e4m3x2_to_f16x2(s0 | (s1 << 8));
-                    float y0[16], y1[16];
+                    float y0[8], y1[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2; ++e) {
                         uint32_t c[4];
                         e2m1x8_to_f16x2x4(w[e], c);
 #pragma unroll
@@ -293,9 +334,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
                             y1[4 * e + j] = __fmul_rn(f16_hi(v2), gv);
                         }
                     }
-                    uint8_t* dst = p.v_out + ((static_cast<int64_t>(row) * p.H + h) * D + 16 * b) * 2;
-                    store_block(dst, y0, f16);
-                    if (both) store_block(dst + static_cast<int64_t>(p.H) * D * 2, y1, f16);
+                    uint8_t* dst = p.v_out + ((static_cast<int64_t>(row) * p.H + h) * D + 16 * b + 8 * half) * 2;
+                    store8(dst, y0, f16);
+                    if (both) store8(dst + static_cast<int64_t>(p.H) * D * 2, y1, f16);
                 }
             }
         }
@@ -392,17 +433,13 @@ extern "C" nvfp4kv_status nvfp4_kv_append(
         p.max_pos = rotary->max_positions;
     }
     p.out_f16 = out_dtype == NVFP4KV_FP16;
-    auto wide = [](const void* a, int64_t stride) {
-        return reinterpret_cast<uintptr_t>(a) % 32 == 0 && stride % 32 == 0;
-    };
-    p.wide = wide(k, p.k_stride) && wide(v, p.v_stride) && (num_q_heads == 0 || wide(q, p.q_stride));
-    const int HW = 32 / (D / 32);
+    const int HW = 32 / (D / 16);
     p.segs_rot = (num_q_heads + H + HW - 1) / HW;
     p.segs = p.segs_rot + (H + HW - 1) / HW;
-    // a warp takes as many head groups of a row as leave 16 warps to an SM: few rows are spread over
+    // a warp takes as many head groups of a row as leave 32 warps to an SM: few rows are spread over
     // the GPU, and with many rows the position's table row is read once for all heads
     const int64_t spread = static_cast<int64_t>(num_rows) * p.segs;
-    const int64_t each = (spread + num_sms() * 16 - 1) / (num_sms() * 16);
+    const int64_t each = (spread + num_sms() * 32 - 1) / (num_sms() * 32);
     p.segs_per_task = static_cast<int>(each < p.segs ? each : p.segs);
     p.tasks_per_row = (p.segs + p.segs_per_task - 1) / p.segs_per_task;
     p.tasks = static_cast<int64_t>(num_rows) * p.tasks_per_row;

@@ -32,8 +32,10 @@ namespace {
 
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes of a lane, 512 K bytes (K whole warps) behind both addresses.
+template <int K>
+__device__ __forceinline__ void cp_async_512(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%2], 16;" ::"r"(dst), "l"(src), "n"(512 * K) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit_group() {
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -149,10 +151,23 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
         const int rows = min(CH, p.T - t0);
         const int64_t r0 = ph * p.T + t0;
         const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(slot)) + 16 * lane;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (32 * k + lane < rows * (D / 32)) cp_async_16(dst + 512 * k, p.kd + r0 * (D / 2) + 512 * k + 16 * lane);
-        if (16 * lane < rows * NB) cp_async_16(dst + CH * (D / 2), p.ks + r0 * NB + 16 * lane);
+        const uint8_t* codes = p.kd + r0 * (D / 2) + 16 * lane;
+        const uint8_t* scales = p.ks + r0 * NB + 16 * lane;
+        if (rows == CH) {
+            cp_async_512<0>(dst, codes);
+            cp_async_512<1>(dst, codes);
+            cp_async_512<2>(dst, codes);
+            cp_async_512<3>(dst, codes);
+            cp_async_512<4>(dst, codes);
+            cp_async_512<5>(dst, codes);
+            cp_async_512<6>(dst, codes);
+            cp_async_512<7>(dst, codes);
+            cp_async_512<0>(dst + CH * (D / 2), scales);
+        } else {
+#pragma unroll 1
+            for (int k = 0; 32 * k + lane < rows * (D / 32); ++k) cp_async_512<0>(dst + 512 * k, codes + 512 * k);
+            if (16 * lane < rows * NB) cp_async_512<0>(dst + CH * (D / 2), scales);
+        }
     };
 
     n = 0;
@@ -186,8 +201,8 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
                 const int t = min(r0 + k * RPP, rows - 1);
                 w[k] = *reinterpret_cast<const uint4*>(codes + t * (D / 2));
                 const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + t * NB);
-                sa[k] = e4m3x2_to_f16x2((sc & 0xFFu) * 0x0101u);
-                sb[k] = e4m3x2_to_f16x2((sc >> 8) * 0x0101u);
+                sa[k] = e4m3x2_to_f16x2(__byte_perm(sc, 0u, 0x0000));
+                sb[k] = e4m3x2_to_f16x2(__byte_perm(sc, 0u, 0x1111));
             }
             const uint32_t ww[2][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[1].x, w[1].y, w[1].z, w[1].w}};
 #pragma unroll
@@ -226,11 +241,27 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
         uint32_t w[(2 * KEEP + 3) / 4];
 #pragma unroll
         for (int k = 0; k < (2 * KEEP + 3) / 4; ++k) w[k] = 0u;
+        // ceil(fp32(y / s)) by a product with 1 / s, off by less than 2^-15 at 127; next to a whole number by
+        // the division itself, but for those past 126, which end at 127 either way (the largest value of
+        // the page always lies there). A non-zero s is at least 2^-17 (a at least 2^-10), so 1 / s is finite
+        const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        bool open = false;
 #pragma unroll
         for (int k = 0; k < 2 * KEEP; ++k) {
+            const float x = y[k] * inv;
+            open = open || (fabsf(x - rintf(x)) < 1e-4f && x < 126.5f && y[k] != 0.0f);
             // floor of a negated value is the negated ceil
-            const int c = s > 0.0f ? static_cast<int>(fminf(127.0f, ceilf(__fdiv_rn(y[k], s)))) : 0;
+            const int c = static_cast<int>(fminf(127.0f, ceilf(x)));
             w[k / 4] |= static_cast<uint32_t>((neg ? -c : c) & 0xFF) << (8 * (k % 4));
+        }
+        if (open) {
+#pragma unroll
+            for (int k = 0; k < (2 * KEEP + 3) / 4; ++k) w[k] = 0u;
+#pragma unroll
+            for (int k = 0; k < 2 * KEEP; ++k) {
+                const int c = static_cast<int>(fminf(127.0f, ceilf(__fdiv_rn(y[k], s))));
+                w[k / 4] |= static_cast<uint32_t>((neg ? -c : c) & 0xFF) << (8 * (k % 4));
+            }
         }
         int8_t* dst = p.bounds + (my_ph * 2 + (neg ? 1 : 0)) * D + 32 * l + 2 * (base & 15);
         if constexpr (KEEP == 2) {
