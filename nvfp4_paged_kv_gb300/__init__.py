@@ -542,30 +542,50 @@ def nvfp4_kv_onboard_pages(layout: Layout, cold: torch.Tensor, hot_k: torch.Tens
 
 # ------------------------------------------------------------------------------ decode steps
 
+# The calls of a decode step run once per layer and step, often on a few rows: their marshalling looks at
+# each tensor once.
 _CODES = {torch.bfloat16: BF16, torch.float16: FP16}
+_U8, _I8, _I32, _I64 = torch.uint8, torch.int8, torch.int32, torch.int64
+_F32, _BF16 = torch.float32, torch.bfloat16
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _pointers(*tensors):
-    """Pointers of contiguous CUDA tensors (None stays None) and the index of their one device."""
-    dev, out = -2, []  # (a CPU tensor has device -1)
-    for t in tensors:
+def _refuse(t, name, dtype, numel, dev):
+    """Why a tensor argument is refused."""
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: tensors passed to the NVFP4 KV library must be CUDA tensors")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"all CUDA tensors of one call must be on one device, got {name} on {t.device} "
+                         f"beside cuda:{dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must be of {numel} values, got {t.numel()}")
+    raise ValueError(f"{name}: tensors passed to the NVFP4 KV library must be contiguous")
+
+
+def _pointers(dev, *specs):
+    """Pointers of the contiguous tensors of device `dev` in `specs`: (tensor or None, name, dtype or
+    None, number of values or None)."""
+    out = []
+    for t, name, dtype, numel in specs:
         if t is None:
             out.append(None)
             continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("tensors passed to the NVFP4 KV library must be CUDA tensors")
-            if dev >= 0:
-                raise ValueError(f"all CUDA tensors of one call must be on one device, got cuda:{dev} "
-                                 f"and cuda:{d}")
-            dev = d
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to the NVFP4 KV library must be contiguous")
+        if (t.get_device() != dev or (dtype is not None and t.dtype != dtype)
+                or (numel is not None and t.numel() != numel) or not t.is_contiguous()):
+            _refuse(t, name, dtype, numel, dev)
         out.append(t.data_ptr())
-    return out, dev
+    return out
+
+
+def _first_device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        _refuse(t, name, None, None, None)
+    return dev
 
 
 def _run(name: str, dev: int, stream, *args):
@@ -578,8 +598,8 @@ def _run(name: str, dev: int, stream, *args):
         s = stream.cuda_stream
     else:
         s = int(stream)
-    fn = getattr(_lib, name)
-    if torch.cuda.current_device() == dev:
+    fn = getattr(_lib or load(), name)
+    if _device() == dev:
         code = fn(*args, s)
     else:
         with torch.cuda.device(dev):
@@ -588,29 +608,13 @@ def _run(name: str, dev: int, stream, *args):
         _check(name, code)
 
 
-def _expect(t: Optional[torch.Tensor], name: str, dtype, numel: int):
-    """Type and size of a tensor argument whose size follows from the others."""
-    if t is not None and (t.dtype != dtype or t.numel() != numel):
-        raise ValueError(f"{name} must be {dtype} with {numel} values, got {t.dtype} with {t.numel()}")
-
-
-def _pool_pages(layout: Layout, data: torch.Tensor, scales: torch.Tensor, name: str) -> int:
-    """Pages of an NVFP4 pool, after a check that both of its tensors have them whole."""
-    pages = data.shape[0]
-    values = pages * layout.num_kv_heads * layout.page_size * layout.head_dim
-    if (data.numel() * 2 != values or scales.numel() * 16 != values or data.element_size() != 1
-            or scales.element_size() != 1):
-        raise ValueError(f"{name}_data and {name}_scales must be byte tensors of {pages} whole pages")
-    return pages
-
-
 def _rows(t: torch.Tensor, name: str, rows: int, heads: int, dim: int, dev: int):
     """Pointer and row stride of a [rows, heads, dim] tensor of device `dev` whose rows are each
     contiguous (rows may be slices of a wider projection)."""
     if t.shape != (rows, heads, dim):
         raise ValueError(f"{name} must be [{rows}, {heads}, {dim}], got {list(t.shape)}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+        _refuse(t, name, None, None, dev)
     sr, sh, sd = t.stride()
     if sd != 1 or (sh != dim and heads > 1):
         raise ValueError(f"each row of {name} must be contiguous")
@@ -626,31 +630,29 @@ def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: tor
     slots `slots` (int64 [rows], page * T + token, -1 = padding row), rotating `k` and `q`
     ([rows, Hq, D]) by `rotary` at `positions` (int32 [rows]). `q_out` [rows, Hq, D] gets the rotated
     queries; `k_out`, `v_out` [rows, H, D] (optional) the rows as the cache now holds them."""
-    load()
     H, D = layout.num_kv_heads, layout.head_dim
     rows, hq = k.shape[0], 0 if q is None else q.shape[1]
-    pages = _pool_pages(layout, k_data, k_scales, "k")
-    if _pool_pages(layout, v_data, v_scales, "v") != pages:
-        raise ValueError("the K and V pools must have the same number of pages")
+    pages = k_data.shape[0]
+    codes = pages * H * D * layout.page_size // 2
     if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
         raise TypeError("q, k and v must have one dtype")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if rotary is not None and positions is None:
         raise ValueError("a rotation needs positions")
-    _expect(slots, "slots", torch.int64, rows)
-    _expect(positions, "positions", torch.int32, rows)
-    out_dtype = None
-    for t, name, heads in ((q_out, "q_out", hq), (k_out, "k_out", H), (v_out, "v_out", H)):
-        if t is not None:
-            out_dtype = out_dtype or t.dtype
-            if t.dtype != out_dtype:
-                raise TypeError("q_out, k_out and v_out must have one dtype")
-            if t.numel() != rows * heads * D:
-                raise ValueError(f"{name} must be [{rows}, {heads}, {D}]")
-    (sp, pp, gk, gv, kd, ksc, vd, vsc, ko, vo, st, _), dev = _pointers(
-        slots, positions, k_global_scale, v_global_scale, k_data, k_scales, v_data, v_scales, k_out,
-        v_out, status, None if rotary is None else rotary.table)
+    out = q_out if q_out is not None else (k_out if k_out is not None else v_out)
+    out = None if out is None else out.dtype
+    for t in (k_out, v_out):
+        if t is not None and t.dtype != out:
+            raise TypeError("q_out, k_out and v_out must have one dtype")
+    dev = _first_device(k, "k")
+    sp, pp, gk, gv, kd, ksc, vd, vsc, ko, vo, st, _ = _pointers(
+        dev, (slots, "slots", _I64, rows), (positions, "positions", _I32, rows),
+        (k_global_scale, "k_global_scale", _F32, None), (v_global_scale, "v_global_scale", _F32, None),
+        (k_data, "k_data", _U8, codes), (k_scales, "k_scales", _U8, codes // 8),
+        (v_data, "v_data", _U8, codes), (v_scales, "v_scales", _U8, codes // 8),
+        (k_out, "k_out", None, rows * H * D), (v_out, "v_out", None, rows * H * D),
+        (status, "status", _I32, None), (None if rotary is None else rotary.table, "cos_sin", None, None))
     kp, ks = _rows(k, "k", rows, H, D, dev)
     vp, vs = _rows(v, "v", rows, H, D, dev)
     qp = qs = op = os_ = 0
@@ -659,7 +661,7 @@ def nvfp4_kv_append(layout: Layout, k: torch.Tensor, v: torch.Tensor, slots: tor
         op, os_ = _rows(q_out, "q_out", rows, hq, D, dev)
     _run("nvfp4_kv_append", dev, stream, layout, _CODES.get(k.dtype, -1), rows, hq, qp, qs, kp, ks, vp, vs,
          sp, rotary, pp, gk, gv, kd, ksc, vd, vsc, pages,
-         BF16 if out_dtype is None else _CODES.get(out_dtype, -1), op, os_, ko, vo, st)
+         BF16 if out is None else _CODES.get(out, -1), op, os_, ko, vo, st)
 
 
 def nvfp4_kv_page_bounds(layout: Layout, k_data: torch.Tensor, k_scales: torch.Tensor,
@@ -668,16 +670,16 @@ def nvfp4_kv_page_bounds(layout: Layout, k_data: torch.Tensor, k_scales: torch.T
     """Int8 bounds of the keys of the listed pages (all of the pool when `page_ids` is None): `bounds`
     [pages, H, 2, D] int8 (upper, lower) in steps of `bound_scales` [pages, H] float32. `page_tokens`
     (int32, one per listed page) counts the page's valid tokens (None: full pages)."""
-    load()
     H, D = layout.num_kv_heads, layout.head_dim
-    pages = _pool_pages(layout, k_data, k_scales, "k")
+    pages = k_data.shape[0]
+    codes = pages * H * D * layout.page_size // 2
     num = pages if page_ids is None else page_ids.numel()
-    _expect(page_ids, "page_ids", torch.int32, num)
-    _expect(page_tokens, "page_tokens", torch.int32, num)
-    _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
-    _expect(bound_scales, "bound_scales", torch.float32, pages * H)
-    (kd, ks, ip, tp, bp, bs, st), dev = _pointers(k_data, k_scales, page_ids, page_tokens, bounds,
-                                                  bound_scales, status)
+    dev = _first_device(k_data, "k_data")
+    kd, ks, ip, tp, bp, bs, st = _pointers(
+        dev, (k_data, "k_data", _U8, codes), (k_scales, "k_scales", _U8, codes // 8),
+        (page_ids, "page_ids", _I32, num), (page_tokens, "page_tokens", _I32, num),
+        (bounds, "bounds", _I8, pages * H * 2 * D), (bound_scales, "bound_scales", _F32, pages * H),
+        (status, "status", _I32, None))
     _run("nvfp4_kv_page_bounds", dev, stream, layout, kd, ks, pages, ip, tp, num, bp, bs, st)
 
 
@@ -691,21 +693,17 @@ def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
     BF16). Writes `sel_page_table` [B, H, budget] int32 (page ids in sequence order, then -1) and
     `sel_lens` [B, H] int32 (their tokens), which nvfp4_paged_sparse_decode_attention takes;
     optionally `sel_index` (positions in the page table) and `scores` [B, H, max pages] float32."""
-    load()
     H, D = layout.num_kv_heads, layout.head_dim
     B, hq = q.shape[0], q.shape[1]
     maxp, budget, pages = page_table.shape[1], sel_page_table.shape[-1], bounds.shape[0]
-    _expect(q, "q", torch.bfloat16, B * hq * D)
-    _expect(bounds, "bounds", torch.int8, pages * H * 2 * D)
-    _expect(bound_scales, "bound_scales", torch.float32, pages * H)
-    _expect(page_table, "page_table", torch.int32, B * maxp)
-    _expect(seq_lens, "seq_lens", torch.int32, B)
-    _expect(sel_page_table, "sel_page_table", torch.int32, B * H * budget)
-    _expect(sel_lens, "sel_lens", torch.int32, B * H)
-    _expect(sel_index, "sel_index", torch.int32, B * H * budget)
-    _expect(scores, "scores", torch.float32, B * H * maxp)
-    (qp, bp, bs, tp, lp, op, ol, oi, sc, st), dev = _pointers(
-        q, bounds, bound_scales, page_table, seq_lens, sel_page_table, sel_lens, sel_index, scores, status)
+    kept = B * H * budget
+    dev = _first_device(q, "q")
+    qp, bp, bs, tp, lp, op, ol, oi, sc, st = _pointers(
+        dev, (q, "q", _BF16, B * hq * D), (bounds, "bounds", _I8, pages * H * 2 * D),
+        (bound_scales, "bound_scales", _F32, pages * H), (page_table, "page_table", _I32, B * maxp),
+        (seq_lens, "seq_lens", _I32, B), (sel_page_table, "sel_page_table", _I32, kept),
+        (sel_lens, "sel_lens", _I32, B * H), (sel_index, "sel_index", _I32, kept),
+        (scores, "scores", _F32, B * H * maxp), (status, "status", _I32, None))
     _run("nvfp4_kv_select_pages", dev, stream, layout, B, hq, qp, bp, bs, pages, tp, maxp, lp, budget,
          int(sink_pages), int(recent_pages), op, ol, oi, sc, st)
 
@@ -723,24 +721,21 @@ def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data,
                                         workspace=None, status=None, stream=None):
     """The decode attention with a page table (`sel_page_table` [B, H, pages] int32) and a length
     (`sel_lens` [B, H] int32) for each (sequence, KV head), as nvfp4_kv_select_pages writes them."""
-    load()
     H, D = layout.num_kv_heads, layout.head_dim
     B, hq = q.shape[0], q.shape[1]
-    max_sel = sel_page_table.shape[-1]
-    pages = _pool_pages(layout, k_data, k_scales, "k")
-    if _pool_pages(layout, v_data, v_scales, "v") != pages:
-        raise ValueError("the K and V pools must have the same number of pages")
-    _expect(q, "q", torch.bfloat16, B * hq * D)
-    _expect(out, "out", torch.bfloat16, B * hq * D)
-    _expect(lse, "lse", torch.float32, B * hq)
-    _expect(sel_page_table, "sel_page_table", torch.int32, B * H * max_sel)
-    _expect(sel_lens, "sel_lens", torch.int32, B * H)
+    pages, max_sel = k_data.shape[0], sel_page_table.shape[-1]
+    codes = pages * H * D * layout.page_size // 2
+    dev = _first_device(q, "q")
+    qp, kd, ks, gk, vd, vs, gv, tp, lp, op, ol, st = _pointers(
+        dev, (q, "q", _BF16, B * hq * D), (k_data, "k_data", _U8, codes), (k_scales, "k_scales", _U8, codes // 8),
+        (k_global_scale, "k_global_scale", _F32, None), (v_data, "v_data", _U8, codes),
+        (v_scales, "v_scales", _U8, codes // 8), (v_global_scale, "v_global_scale", _F32, None),
+        (sel_page_table, "sel_page_table", _I32, B * H * max_sel), (sel_lens, "sel_lens", _I32, B * H),
+        (out, "out", _BF16, B * hq * D), (lse, "lse", _F32, B * hq), (status, "status", _I32, None))
     if workspace is None:
         need = nvfp4_paged_sparse_decode_workspace_size(layout, B, hq, max_sel)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    (qp, kd, ks, gk, vd, vs, gv, tp, lp, wp, op, ol, st), dev = _pointers(
-        q, k_data, k_scales, k_global_scale, v_data, v_scales, v_global_scale, sel_page_table, sel_lens,
-        workspace, out, lse, status)
+        workspace = torch.empty(max(need, 16), dtype=_U8, device=q.device)
+    wp, = _pointers(dev, (workspace, "workspace", None, None))
     _run("nvfp4_paged_sparse_decode_attention", dev, stream, layout, B, hq, qp, kd, ks, gk, vd, vs, gv,
          pages, tp, max_sel, lp, float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol,
          st)

@@ -30,8 +30,6 @@ namespace cg = cooperative_groups;
 namespace nvfp4kv {
 namespace {
 
-__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 // 16 bytes of a lane, 512 K bytes (K whole warps) behind both addresses.
 template <int K>
 __device__ __forceinline__ void cp_async_512(uint32_t dst, const void* src) {
@@ -278,16 +276,16 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
 // Selection. One thread-block cluster per (sequence, KV head) pair. Its warps score tiles of 16
 // pages on the tensor cores (FP16, whose mma.sync runs 8 times as often per clock as the int8 one on
 // this GPU; pages as M, the query group as N, head dims as K, once with the upper bounds and the
-// positive queries, once with the lower and the negative) and put the scores as sortable keys into the shared memory of the cluster's first CTA, which then finds the
-// smallest selected key: by counting ranks when the pages are as few as its threads, else by a radix
-// selection that starts at the highest bit in which the keys differ and stops when a bin is taken
-// whole. The selected pages are written in ascending order, equal keys from the lowest page on.
+// positive queries, once with the lower and the negative) and put the scores as sortable keys into the
+// shared memory of the cluster's first CTA, which then finds the smallest selected key by a radix selection that starts at the highest bit in which the keys differ and
+// stops when a bin is taken whole. (Counting ranks was no faster for few pages, 6.1 against 6.0 us for 256
+// pairs of 128, nor among the keys of the last bin, 12.9 against 12.3 us for 64 pairs of up to 2048: code
+// that runs once costs its fetch.) The selected pages are written in ascending order, equal keys from the lowest page on.
 // ------------------------------------------------------------------------------------------
 constexpr int kSelMaxGroup = 8;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelMaxPages = 49152;  // keys of a pair: 192 KiB of shared memory
 constexpr int kSelBins = 1024;
-constexpr int kSelRankKeys = 160;    // up to here ranks are counted, see below
 
 struct SelectParams {
     const uint16_t* q;
@@ -556,33 +554,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
     const int lo = p.sink, hi = n - p.recent;
     uint32_t want = static_cast<uint32_t>(count - p.sink - p.recent);
     uint32_t above = 0xFFFFFFFFu, equal = 0u;
-    if (n <= kSelRankKeys) {
-        // one key a thread: its rank is how many keys come before it (those of always-taken pages are
-        // 0, below all others). At 128 pages this takes 0.6 us where the radix passes take 2; at 512
-        // it would take 4
-        if (tid >= n && tid < ((n + 3) & ~3)) keys[tid] = 0u;
-        __syncthreads();
-        if (tid < n) {
-            const uint32_t mine = keys[tid];
-            uint32_t before = 0u;
-            for (int j = 0; j < n; j += 4) {
-                const uint4 k = *reinterpret_cast<const uint4*>(keys + j);
-                before += k.x > mine || (k.x == mine && j < tid);
-                before += k.y > mine || (k.y == mine && j + 1 < tid);
-                before += k.z > mine || (k.z == mine && j + 2 < tid);
-                before += k.w > mine || (k.w == mine && j + 3 < tid);
-            }
-            // the last one taken is the threshold
-            if (mine != 0u && before + 1 == want) found.bin = static_cast<uint32_t>(tid);
-        }
-        __syncthreads();
-        if (want > 0) {
-            const uint32_t last = found.bin;
-            above = keys[last];
-            // those equal to it up to its own place are taken
-            equal = static_cast<uint32_t>(__syncthreads_count(tid <= static_cast<int>(last) && keys[tid] == above));
-        }
-    } else if (want > 0) {
+    if (want > 0) {
         uint32_t top = 0u, low = 0xFFFFFFFFu;
         for (int i = lo + tid; i < hi; i += NT) {
             const uint32_t k = keys[i];
@@ -611,6 +583,7 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
 #pragma unroll
             for (int i = 0; i < kSelBins / NT; ++i) hist[tid + i * NT] = 0u;
             __syncthreads();
+#pragma unroll 1
             for (int i = lo + tid; i < hi; i += NT) {
                 const uint32_t k = keys[i];
                 if ((k & mask) == prefix) atomicAdd(&hist[(k & ~mask) >> shift], 1u);
@@ -792,12 +765,13 @@ extern "C" nvfp4kv_status nvfp4_kv_select_pages(
         static_cast<int64_t>(max_pages_per_seq) * layout->page_size > INT32_MAX ||
         static_cast<int64_t>(budget) * layout->page_size > INT32_MAX)
         return NVFP4KV_ERR_UNSUPPORTED;
-    // CTAs per pair: while they fit the GPU at two CTAs of 256 threads per SM and each still has a tile
-    // for every warp. CTAs of 512 threads where even they fit at once
+    // CTAs per pair: as many as the SMs allow while each still has a tile for every warp (64 pairs of up to
+    // 2048 pages: 12.3 us with 2 CTAs, 12.8 with 4, 16.7 with 8). CTAs of 512 threads for the few pairs
+    // that leave more than half of the SMs free even so (2 pairs of 6251 pages: 11.4 us against 13.0)
     int cluster = 1;
-    while (cluster < kSelMaxCluster && pairs * cluster <= num_sms() && max_pages_per_seq > 128 * cluster)
+    while (cluster < kSelMaxCluster && pairs * cluster * 2 <= num_sms() && max_pages_per_seq > 128 * cluster)
         cluster *= 2;
-    const bool large = pairs * cluster <= num_sms() && max_pages_per_seq > 128 * cluster;
+    const bool large = pairs * cluster * 2 <= num_sms() && max_pages_per_seq > 128 * cluster;
     SelectParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.bounds = bounds;

@@ -271,5 +271,10 @@ def test_binding_refuses_on_the_gpu(kv, cuda):
     with pytest.raises(ValueError, match="positions"):
         kv.nvfp4_kv_append(lay, c.k, c.v, slots, *pool,
                            rotary=kv.Rotary(kv.ROTARY_HALVES, 0, 64, table_of(9, 64).to(cuda)))
-    with pytest.raises(ValueError, match="pages"):
-        kv.nvfp4_kv_append(lay, c.k, c.v, slots, pool[0], pool[1], pool[2][:2], pool[3][:2])
+    for bad in ((pool[0], pool[1], pool[2][:2], pool[3][:2]), (pool[0], pool[1][..., :1], pool[2], pool[3]),
+                (pool[0].to(torch.int8), pool[1], pool[2], pool[3]), (pool[0].cpu(), *pool[1:])):
+        with pytest.raises(ValueError):
+            kv.nvfp4_kv_append(lay, c.k, c.v, slots, *bad)
+    for bad in (slots[:3], slots.int(), slots.cpu(), slots.repeat(2)[::2]):
+        with pytest.raises(ValueError, match="slots"):
+            kv.nvfp4_kv_append(lay, c.k, c.v, bad, *pool)

@@ -286,10 +286,12 @@ def test_attention_of_ragged_pairs(kv, cuda, D, T, H, G):
     assert status.item() == 0
 
 
-@pytest.mark.parametrize("B,H,most,low", [(1, 1, 1, 16), (1, 1, 400, 6400), (1, 8, 64, 900), (300, 4, 3, 0), (2, 2, 150, 0)])
+@pytest.mark.parametrize("B,H,most,low", [(1, 1, 1, 16), (1, 1, 400, 6400), (1, 8, 64, 900), (300, 4, 3, 0), (2, 2, 150, 0),
+                                            (500, 8, 9, 0), (240, 8, 6, 90), (61, 7, 40, 500), (60, 8, 33, 0)])
 def test_attention_of_few_and_many_pairs(kv, cuda, B, H, most, low):
-    """One pair over one page or split over every SM, 1200 short pairs."""
-    T, D, G = 16, 128, 4
+    """One pair over one page or split over every SM, 1200 short pairs; more pairs than the 1824 warps, and
+    pairs whose runs of their own would be more than the warps (runs then cross pairs)."""
+    T, D, G = 16, 128, 4 if B < 100 else 1
     c = Cache(cuda, 90, H, T, D, B + H)
     lens = torch.randint(low, most * T + 1, (B, H), generator=c.g, dtype=torch.int32)
     q, table = queries(c, B, G), c.tables(B, most, lens)
@@ -588,3 +590,38 @@ def test_two_calls_at_once_on_two_streams(kv, cuda):
         torch.cuda.synchronize()
         for o, a in zip(outs, alone):
             assert np.array_equal(o.float().cpu().numpy(), a[0])
+
+
+def test_binding_refuses_on_the_gpu(kv, cuda):
+    lay = kv.Layout(8, 128, 64)
+    z = lambda dt, *s: torch.zeros(s, dtype=dt, device=cuda)  # noqa: E731
+    u8, i8, i32, f32, bf = torch.uint8, torch.int8, torch.int32, torch.float32, torch.bfloat16
+    kd, ks, bo, sc = z(u8, 2, 8, 64, 64), z(u8, 2, 8, 64, 8), z(i8, 2, 8, 2, 128), z(f32, 2, 8)
+    for bad in ((kd[..., :32], ks, bo, sc, {}), (kd, ks[..., :4].contiguous(), bo, sc, {}), (kd, ks, bo[:1], sc, {}),
+                (kd, ks, bo.to(u8), sc, {}), (kd, ks, bo, sc[:, :7], {}), (kd, ks, bo, sc.double(), {}),
+                (kd, ks, bo, sc, dict(page_ids=z(i32, 3), page_tokens=z(i32, 2))), (kd, ks, bo, sc, dict(page_ids=z(torch.int64, 3))),
+                (kd, ks, bo.cpu(), sc, {})):
+        with pytest.raises(ValueError):
+            kv.nvfp4_kv_page_bounds(lay, *bad[:4], **bad[4])
+    q = z(bf, 3, 16, 128)
+    good = dict(q=q, bounds=bo, bound_scales=sc, page_table=z(i32, 3, 5), seq_lens=z(i32, 3), sel_page_table=z(i32, 3, 8, 2),
+                sel_lens=z(i32, 3, 8))
+    kv.nvfp4_kv_select_pages(lay, **good)
+    for bad in (dict(q=q[..., :64]), dict(q=q.float()), dict(seq_lens=z(i32, 2)), dict(sel_lens=z(i32, 8)),
+                dict(sel_page_table=z(i32, 3, 7, 2)), dict(page_table=z(torch.int64, 3, 5)), dict(scores=z(f32, 3, 8, 4)),
+                dict(sel_index=z(i32, 3, 8, 3)), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)), dict(bounds=bo[:1])):
+        with pytest.raises(ValueError):
+            kv.nvfp4_kv_select_pages(lay, **{**good, **bad})
+    with pytest.raises(kv.NVFP4KVError, match="INVALID"):
+        kv.nvfp4_kv_select_pages(lay, **good, sink_pages=2)
+    g = z(f32, 1)
+    pool = [kd, ks, g, z(u8, 2, 8, 32, 128), z(u8, 2, 8, 32, 8, 2), g]
+    kv.nvfp4_paged_sparse_decode_attention(lay, q, *pool, z(i32, 3, 8, 2), z(i32, 3, 8), 0.1, torch.zeros_like(q))
+    for tab, ln, out, kw in ((z(i32, 3, 8, 2), z(i32, 3, 7), q, {}), (z(i32, 3, 7, 2), z(i32, 3, 8), q, {}),
+                             (z(i32, 3, 8, 2), z(i32, 3, 8), q.half(), {}), (z(i32, 3, 8, 2), z(i32, 3, 8), q, dict(lse=z(f32, 3, 15))),
+                             (z(i32, 3, 8, 2), z(i32, 3, 8), q, dict(workspace=torch.zeros(1 << 20, dtype=u8)))):
+        with pytest.raises(ValueError):
+            kv.nvfp4_paged_sparse_decode_attention(lay, q, *pool, tab, ln, 0.1, out, **kw)
+    with pytest.raises(kv.NVFP4KVError, match="WORKSPACE"):
+        kv.nvfp4_paged_sparse_decode_attention(lay, q, *pool, z(i32, 3, 8, 2), z(i32, 3, 8), 0.1, torch.zeros_like(q),
+                                               workspace=z(u8, 64))
