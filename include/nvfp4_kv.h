@@ -353,8 +353,9 @@ nvfp4kv_status nvfp4_paged_decode_attention_noalloc(
  *   q, k, v        row n of q at q + n * q_row_stride elements, [heads][D] contiguous in a row (so
  *                  the three may be slices of one projection); 16-byte aligned, strides multiples
  *                  of 8 and at least heads * D
- *   slots          int64 [num_rows]; -1 marks a padding row, of which nothing is written. Two
- *                  rows of a call with the same slot race (the slot then holds bytes of either)
+ *   slots          int64 [num_rows]; -1 marks a padding row, of which nothing is written. If two rows
+ *                  of a call have the same slot, the values of that token are unspecified (no other
+ *                  token is touched)
  *   rotary         host pointer, NULL = no rotation (positions is not read then)
  *   positions      int32 [num_rows], 0 <= position < rotary->max_positions
  *   k_global_scale, v_global_scale   device scalars g (NULL = 1)
@@ -403,7 +404,8 @@ nvfp4kv_status nvfp4_kv_append(
  *   hi = min(127, ceil(fp32(max_t v / s))),  lo = max(-127, floor(fp32(min_t v / s)))
  * and 0 everywhere when a is 0 or the page has no tokens.
  *   k_data, k_scales, pool_pages   NVFP4 K pool in NVFP4KV_PACK_DIM_PAIRS
- *   page_ids       [num_pages] pages to do (NULL = 0 .. num_pages-1); -1 = no page (padding)
+ *   page_ids       [num_pages] pages to do (NULL = 0 .. num_pages-1); -1 = no page (padding). A page
+ *                  listed twice with different token counts gets bounds of either, mixed
  *   page_tokens    [num_pages], 0 .. T (NULL = T for all)
  *   bounds         int8 [pool_pages][H][2][D]: hi, then lo; only the listed pages are written
  *   bound_scales   float [pool_pages][H]
@@ -438,7 +440,11 @@ nvfp4kv_status nvfp4_kv_page_bounds(
  *   scores         optional float [batch][H][max_pages_per_seq]: the scores (+inf for the
  *                  always-taken pages, -inf for a page id outside the pool); entries past n are
  *                  left as they were
- * sel_page_table and sel_lens are what nvfp4_paged_sparse_decode_attention takes. Supported:
+ * sel_page_table and sel_lens are what nvfp4_paged_sparse_decode_attention takes. A page id outside
+ * the pool among the scored pages sets PAGE_OOB (its score is -inf, so it is taken only when the
+ * budget has room); ids of pages that are not scored are passed on unchecked. A sequence length
+ * outside [0, max_pages_per_seq * T] sets BAD_SEQ_LEN and takes no page. Bounds that were never
+ * written give their page an unspecified score, and nothing else. Supported:
  * head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; batch * num_kv_heads <= 65535;
  * max_pages_per_seq <= 49152.
  * ------------------------------------------------------------------------------------------ */

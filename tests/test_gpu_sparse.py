@@ -223,6 +223,56 @@ def test_selection_bad_lengths_and_page_ids(kv, cuda):
                     kv.STATUS_PAGE_OOB)
 
 
+@pytest.mark.parametrize("B,H,maxp", [(1, 1, 2000), (2, 3, 600), (9, 8, 300)])
+def test_selection_captured_and_replayed(kv, cuda, B, H, maxp):
+    """Clusters of several CTAs in a CUDA graph on a side stream; lengths and queries change between
+    replays, down to sequences that fit the budget."""
+    D, T, G, budget = 128, 16, 4, 24
+    bounds, scales, g = some_pages(400, H, D, maxp)
+    table = torch.randint(0, 400, (B, maxp), generator=g, dtype=torch.int32)
+    io = {"q": torch.zeros((B, H * G, D), dtype=torch.bfloat16, device=cuda), "lens": torch.zeros(B, dtype=torch.int32, device=cuda),
+          "sel": torch.zeros((B, H, budget), dtype=torch.int32, device=cuda), "sl": torch.zeros((B, H), dtype=torch.int32, device=cuda)}
+    db, ds, dt = bounds.to(cuda), scales.to(cuda), table.to(cuda)
+
+    def call(stream=None):
+        kv.nvfp4_kv_select_pages(kv.Layout(H, D, T), io["q"], db, ds, dt, io["lens"], io["sel"], io["sl"], sink_pages=1,
+                                 recent_pages=2, stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for high in (maxp * T, 20 * T, 1, maxp * T):
+        lens = torch.randint(0, high + 1, (B,), generator=g, dtype=torch.int32)
+        q = torch.randn((B, H * G, D), generator=g).to(torch.bfloat16)
+        io["lens"].copy_(lens), io["q"].copy_(q)
+        graph.replay()
+        want = plain_steps.select(q.double().numpy(), bounds.numpy(), scales.double().numpy(), table.numpy(), lens.numpy(), T,
+                                  budget, 1, 2)
+        assert np.array_equal(io["sel"].cpu().numpy(), want[1]) and np.array_equal(io["sl"].cpu().numpy(), want[2])
+
+
+def test_unwritten_bounds_only_cost_their_page(kv, cuda):
+    """Bounds and scales of NaN and infinity (never written): every id selected is still one of the
+    sequence's pages, in order, and the pages with finite bounds keep their order among themselves."""
+    D, T, H = 64, 16, 1
+    bounds, scales, g = some_pages(60, H, D, 31)
+    table = torch.randperm(60, generator=g).to(torch.int32)[None]
+    bad = torch.tensor([5, 17, 40])
+    scales[table[0, bad].long()] = torch.tensor([float("nan"), float("inf"), float("-inf")])[:, None]
+    bounds[table[0, bad].long()] = -128
+    q = torch.randn((1, 2, D), generator=g).to(torch.bfloat16)
+    index, sel, sl, scores = selection(kv, cuda, q, bounds, scales, table, torch.tensor([960], dtype=torch.int32), H, T, 12, 1, 1)
+    assert (np.diff(index[0, 0]) > 0).all() and index[0, 0, 0] == 0 and index[0, 0, -1] == 59
+    assert np.array_equal(sel[0, 0], table[0].numpy()[index[0, 0]]) and sl[0, 0] == 12 * T
+    kept = [i for i in index[0, 0] if i not in bad]
+    left = [i for i in range(1, 59) if i not in kept and i not in bad]
+    assert min(scores[0, 0, kept]) >= max(scores[0, 0, left])
+
+
 # ------------------------------------------------------------------------------------ attention
 
 class Cache:
