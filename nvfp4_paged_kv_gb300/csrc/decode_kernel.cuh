@@ -127,6 +127,7 @@ struct DecodeParams {
     uint32_t nonce;     // tag of this call
     int32_t B, Hq, H, G, T, pool_pages, max_pages, num_runs;
     int32_t pool_heads;  // KV heads of a page in the pools (PER_HEAD: H is 1)
+    int32_t full_stages, full_run;  // PER_HEAD: stages when every pair has all its pages, and W then
     float sm_scale;
 };
 
@@ -517,11 +518,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
         total += scan_warp[w];
     }
     // warp run gw takes [gw W, gw W + W) of the stage list. PER_HEAD, where a call often has few stages
-    // per warp and then fewer runs than warps: the R runs are spread over the CTAs (512 stages on 43 of
-    // the 152 SMs took 14.8 us, spread over all 11.8; runs of unequal length that use every warp were
-    // slower than equal ones by their additional records, 33.0 against 31.4 us at 8192 stages)
+    // per warp:
+    //  * fewer runs than warps are spread over the CTAs (512 stages on 43 of the 152 SMs took 14.8 us,
+    //    spread over all 11.4; runs of unequal length that use every warp were slower than equal ones by
+    //    their additional records, 31.1 against 29.2 us at 8192 stages);
+    //  * when every pair has all its pages, W may be a little larger, so that runs end with pairs
+    //    (aligned_run).
     const int num_runs = p.num_runs;
-    const int W = max(1, (total + num_runs - 1) / num_runs);
+    const int W = PER_HEAD && total == p.full_stages ? p.full_run : max(1, (total + num_runs - 1) / num_runs);
     const int R = (total + W - 1) / W;
     if (blockIdx.x == 0) {
         // sequences without stages (length 0 or invalid): output 0, LSE -inf, a warp per sequence
@@ -1121,6 +1125,16 @@ int warps_per_cta(int D) { return D == 64 ? 16 : (D == 128 ? 12 : 8); }
 int64_t decode_runs(int batch, int H, int D, int max_num_splits) {
     if (max_num_splits > 0) return static_cast<int64_t>(max_num_splits) * batch * H;
     return static_cast<int64_t>(num_sms()) * warps_per_cta(D);
+}
+
+// PER_HEAD: the stages of a run, at least W, for pairs of S stages each. A run that crosses pairs leaves
+// two records and starts a second piece, so W becomes a divisor or a multiple of S when one is at most a
+// third larger, and S up to 3, where a merge takes as long as the additional stages (256 pairs: of 16
+// stages 19.5 us with W = 3, 18.2 with 4; of 2 stages 10.1 with 1, 8.3 with 2).
+int aligned_run(int64_t W, int64_t S) {
+    const int64_t up = (W + S - 1) / S * S;
+    if (S <= 3 || (W >= S && 3 * up <= 4 * W)) return static_cast<int>(up);
+    return static_cast<int>(W >= 3 && S % W != 0 && S % (W + 1) == 0 ? W + 1 : W);
 }
 
 struct WsLayout {

@@ -78,6 +78,9 @@ extern "C" nvfp4kv_status nvfp4_paged_sparse_decode_attention(
     p.max_pages = max_sel_pages;
     p.num_runs = static_cast<int32_t>(runs);
     p.pool_heads = H;
+    const int64_t each = (static_cast<int64_t>(max_sel_pages) * T + stage_tokens(D) - 1) / stage_tokens(D);
+    p.full_stages = static_cast<int32_t>(pairs * each);  // (bounded by decode_size_ok)
+    p.full_run = aligned_run((pairs * each + runs - 1) / runs, each);
     p.sm_scale = sm_scale;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
