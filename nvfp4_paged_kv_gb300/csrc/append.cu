@@ -9,16 +9,19 @@
 // rotation and the encoder. The rotation rounds each product and each sum (no fused multiply-add),
 // so that the stored codes do not depend on how a compiler contracts them.
 //
-// Bound: HBM. Every source value is read once and every output written once; the table row of a
-// position (at most 4 D bytes) is read once per warp task into registers and reused for every head
-// of the task.
+// Bound: HBM for a chunk, latency for a decode step. Every source value is read once and every output
+// written once; the table row of a position (at most 4 D bytes) is read once per warp task into registers
+// and reused for every head of the task. Measured: 8192 rows of 32 + 8 + 8 heads of 128 with all outputs
+// (215 MB) 39.4 us, 5.5 TB/s; 32 such rows 3.4 us.
 //
+// A warp task is a row's q and K heads, or its V heads, as many head groups of it as leave 32 warps to an
+// SM.
 // A thread owns 8 dims of each of two 16-value blocks of one head that rotate with one another (block i
 // of the first half with block i of the second, or two neighbouring blocks when adjacent dims pair
 // up), so the rotation needs no other thread, and two neighbouring lanes hold the two blocks: they
 // share the block maximum by a shuffle and each picks the scale of one block. (With whole blocks in a
-// thread the kernel needed 157 registers, and 128 with spills kept 16 warps on an SM: 46.6 us for
-// 8192 rows of 32 + 8 + 8 heads of 128; the halves take 64.)
+// thread the kernel needed 157 registers, and 128 with spills kept 16 warps on an SM: 46.6 us; the halves
+// take 64, 32 warps.)
 //
 // K bytes belong to one token each. A V byte holds two tokens (token pairs): when the next row of
 // the call is the second token of the pair, one thread encodes both and stores whole bytes; a token
@@ -62,9 +65,9 @@ struct AppendParams {
     int32_t rot_units;         // rotated dims / 32
     int32_t max_pos;
     int32_t out_f16;           // the 16-bit outputs are FP16 (else BF16)
-    int32_t segs_rot, segs;    // warp-wide head groups of a row: q and K heads, then V heads
-    int32_t segs_per_task, tasks_per_row;
-    int64_t tasks;
+    int32_t segs_rot, segs_v;  // warp-wide head groups of a row: q and K heads; V heads
+    int32_t rot_each, rot_tasks, v_each, v_tasks;  // head groups of a warp's task, tasks of a row
+    int64_t rot_total, tasks;  // tasks of q and K, tasks of all
 };
 
 // 8 values of a source row as exact fp32.
@@ -78,13 +81,16 @@ __device__ __forceinline__ void widen8(uint4 v, float (&x)[8]) {
     }
 }
 
-// 8 values rounded to the 16-bit output type (round to nearest even).
+// 8 values rounded to the 16-bit output type (round to nearest even), stored past L1, which they would
+// only fill (8192 rows 42.4 -> 39.4 us), but left in L2 for the attention that reads them next.
 __device__ __forceinline__ void store8(uint8_t* a, const float (&x)[8], bool f16) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         w[j] = f16 ? pack_f16x2(x[2 * j], x[2 * j + 1]) : pack_bf16x2(x[2 * j], x[2 * j + 1]);
-    st_cs(a, make_uint4(w[0], w[1], w[2], w[3]));
+    asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3])
+                 : "memory");
 }
 
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
@@ -122,8 +128,97 @@ __device__ __forceinline__ void rotate(float& x1, float& x2, float c, float s) {
     x1 = a;
 }
 
+// The V heads of groups seg0 .. seg1 - 1 of a row, alone or with the next row as the other token of its
+// pair.
+template <int SRC, int D>
+__device__ __forceinline__ void append_v(const AppendParams& p, int row, int seg0, int seg1, int64_t slot,
+                                         int64_t page, int t, float gv, bool f16) {
+    constexpr int L = D / 16, HW = 32 / L, NB = D / 16;
+    const int lane = threadIdx.x & 31;
+    const int i = (lane % L) >> 1, half = lane & 1, hl = lane / L;
+    const int half_T = p.T / 2;
+    const bool odd = (t & 1) != 0;
+    bool both = false;
+    {
+        const int other = odd ? row - 1 : row + 1;
+        if (other >= 0 && other < p.rows && __ldg(p.slots + other) == (odd ? slot - 1 : slot + 1)) {
+            const int opos = p.positions ? __ldg(p.positions + other) : 0;
+            both = !p.positions || (opos >= 0 && opos < p.max_pos);
+        }
+    }
+    if (both && odd) return;  // written with the row before
+    for (int seg = seg0; seg < seg1; ++seg) {
+        const int h = seg * HW + hl;
+        if (h >= p.H) continue;
+        const uint8_t* src = p.v + row * p.v_stride + h * (D * 2) + 64 * i + 16 * half;
+        const int64_t vrow = (page * p.H + h) * half_T + (t >> 1);
+        const float d = __fmul_rn(6.0f, gv);
+        uint4 w0[2], w1[2];  // blocks 2i and 2i + 1 of this row and the next
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w0[u] = ld_stream_16B(src + 32 * u);
+            w1[u] = both ? ld_stream_16B(src + p.v_stride + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int b = 2 * i + u;
+            float x0[8], x1[8];  // first and second token of the pair
+            widen8<SRC>(w0[u], x0);
+            widen8<SRC>(w1[u], x1);
+            uint32_t s0, s1;
+            float r0, r1;
+            pick_two(amax8(x0), amax8(x1), gv, d, s0, s1, r0, r1);
+            uint32_t w[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[e] = 0u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = 4 * e + j;
+                    w[e] |= f32x2_to_e2m1x2(__fmul_rn(x0[k], r0), __fmul_rn(x1[k], r1)) << (8 * j);
+                }
+            }
+            uint8_t* vd = p.vd + vrow * D + 16 * b + 8 * half;
+            uint8_t* vs = p.vs + vrow * (2 * NB) + 2 * b;
+            if (both) {
+                *reinterpret_cast<uint2*>(vd) = make_uint2(w[0], w[1]);
+                if (!half) *reinterpret_cast<uint16_t*>(vs) = static_cast<uint16_t>(s0 | (s1 << 8));
+            } else {
+                unsigned int* words = reinterpret_cast<unsigned int*>(vd);
+                const uint32_t keep = odd ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t code = w[e] & 0x0F0F0F0Fu;
+                    atomicAnd(words + e, keep);
+                    atomicOr(words + e, odd ? code << 4 : code);
+                }
+                if (!half) vs[odd ? 1 : 0] = static_cast<uint8_t>(s0);
+            }
+            if (p.v_out) {
+                // a byte's two codes times the two tokens' scales, exact in FP16
+                const uint32_t s2 = e4m3x2_to_f16x2(s0 | (s1 << 8));
+                float y0[8], y1[8];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t c[4];
+                    e2m1x8_to_f16x2x4(w[e], c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t v2 = hmul2_u32(c[j], s2);
+                        y0[4 * e + j] = __fmul_rn(f16_lo(v2), gv);
+                        y1[4 * e + j] = __fmul_rn(f16_hi(v2), gv);
+                    }
+                }
+                uint8_t* dst = p.v_out + ((static_cast<int64_t>(row) * p.H + h) * D + 16 * b + 8 * half) * 2;
+                store8(dst, y0, f16);
+                if (both) store8(dst + static_cast<int64_t>(p.H) * D * 2, y1, f16);
+            }
+        }
+    }
+}
+
 template <int SRC, int D, int STYLE>
-__global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) append_kernel(const AppendParams p) {
     pdl_enter();
     constexpr int L = D / 16;   // lanes of a head
     constexpr int HW = 32 / L;  // heads of a warp
@@ -131,7 +226,6 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendP
     const int lane = threadIdx.x & 31;
     const int i = (lane % L) >> 1, half = lane & 1, hl = lane / L;
     const int warps = static_cast<int>(gridDim.x) * (kAppendThreads / 32);
-    const int half_T = p.T / 2;
     const float gk = p.gk ? __ldg(p.gk) : 1.0f, gv = p.gv ? __ldg(p.gv) : 1.0f;
     const bool f16 = p.out_f16 != 0;
 
@@ -150,9 +244,10 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendP
 
     for (int64_t task = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / 32) + (threadIdx.x >> 5);
          task < p.tasks; task += warps) {
-        const int row = static_cast<int>(task / p.tasks_per_row);
-        const int seg0 = static_cast<int>(task - static_cast<int64_t>(row) * p.tasks_per_row) * p.segs_per_task;
-        const int seg1 = min(seg0 + p.segs_per_task, p.segs);
+        const bool is_v = task >= p.rot_total;
+        const int64_t at = is_v ? task - p.rot_total : task;
+        const int row = static_cast<int>(at / (is_v ? p.v_tasks : p.rot_tasks));
+        const int part = static_cast<int>(at - static_cast<int64_t>(row) * (is_v ? p.v_tasks : p.rot_tasks));
         const int64_t slot = __ldg(p.slots + row);
         const int pos = p.positions ? __ldg(p.positions + row) : 0;
 
@@ -166,9 +261,14 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendP
         const int64_t page = static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(slot), p.t_magic));
         const int t = static_cast<int>(slot - page * p.T);
 
-        // a head group's q and K values are loaded while the one before is worked on (two groups ahead took
-        // 48 us for 8192 rows against 43, the first group's loads before the slot is known 45)
-        const int rot1 = min(seg1, p.segs_rot);
+        if (is_v) {
+            append_v<SRC, D>(p, row, part * p.v_each, min((part + 1) * p.v_each, p.segs_v), slot, page, t, gv, f16);
+            continue;
+        }
+
+        // a head group's q and K values are loaded while the one before is worked on (two groups ahead was
+        // 5 us slower for 8192 rows, the first group's loads before the slot is known 2 us)
+        const int seg0 = part * p.rot_each, rot1 = min(seg0 + p.rot_each, p.segs_rot);
         auto source = [&](int seg) -> const uint8_t* {  // null: no head for this thread
             const int head = seg * HW + hl;
             if (seg >= rot1 || head >= p.Hq + p.H) return nullptr;
@@ -183,7 +283,7 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendP
         // halves: the cosines and sines of dims 8 half .. +7 of the block; adjacent pairs: those of the
         // four pairs in each of the two blocks
         float cs[8], sn[8];
-        if (seg0 < p.segs_rot && turns) {
+        if (turns) {
             const float* row_cs = p.table + static_cast<int64_t>(pos) * 32 * p.rot_units + 16 * i +
                                   (STYLE == NVFP4KV_ROTARY_HALVES ? 8 : 4) * half;
 #pragma unroll
@@ -257,87 +357,6 @@ __global__ void __launch_bounds__(kAppendThreads, 7) append_kernel(const AppendP
                 put(x0, s0, r0, b0);
                 put(x1, s1, r1, b1);
                 p.ks[krow * NB + (half ? b1 : b0)] = static_cast<uint8_t>(half ? s1 : s0);
-            }
-        }
-        if (seg1 <= p.segs_rot) continue;
-
-        // ---- V heads: this row alone, or with the next one as the other token of its pair
-        const bool odd = (t & 1) != 0;
-        bool both = false;
-        {
-            const int other = odd ? row - 1 : row + 1;
-            if (other >= 0 && other < p.rows && __ldg(p.slots + other) == (odd ? slot - 1 : slot + 1)) {
-                const int opos = p.positions ? __ldg(p.positions + other) : 0;
-                both = !p.positions || (opos >= 0 && opos < p.max_pos);
-            }
-        }
-        if (both && odd) continue;  // written with the row before
-        for (int seg = max(seg0, p.segs_rot); seg < seg1; ++seg) {
-            const int h = (seg - p.segs_rot) * HW + hl;
-            if (h >= p.H) continue;
-            const uint8_t* src = p.v + row * p.v_stride + h * (D * 2) + 64 * i + 16 * half;
-            const int64_t vrow = (page * p.H + h) * half_T + (t >> 1);
-            const float d = __fmul_rn(6.0f, gv);
-            uint4 w0[2], w1[2];  // blocks 2i and 2i + 1 of this row and the next
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                w0[u] = ld_stream_16B(src + 32 * u);
-                w1[u] = both ? ld_stream_16B(src + p.v_stride + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int b = 2 * i + u;
-                float x0[8], x1[8];  // first and second token of the pair
-                widen8<SRC>(w0[u], x0);
-                widen8<SRC>(w1[u], x1);
-                uint32_t s0, s1;
-                float r0, r1;
-                pick_two(amax8(x0), amax8(x1), gv, d, s0, s1, r0, r1);
-                uint32_t w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    w[e] = 0u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = 4 * e + j;
-                        w[e] |= f32x2_to_e2m1x2(__fmul_rn(x0[k], r0), __fmul_rn(x1[k], r1)) << (8 * j);
-                    }
-                }
-                uint8_t* vd = p.vd + vrow * D + 16 * b + 8 * half;
-                uint8_t* vs = p.vs + vrow * (2 * NB) + 2 * b;
-                if (both) {
-                    *reinterpret_cast<uint2*>(vd) = make_uint2(w[0], w[1]);
-                    if (!half) *reinterpret_cast<uint16_t*>(vs) = static_cast<uint16_t>(s0 | (s1 << 8));
-                } else {
-                    unsigned int* words = reinterpret_cast<unsigned int*>(vd);
-                    const uint32_t keep = odd ? 0x0F0F0F0Fu : 0xF0F0F0F0u;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t code = w[e] & 0x0F0F0F0Fu;
-                        atomicAnd(words + e, keep);
-                        atomicOr(words + e, odd ? code << 4 : code);
-                    }
-                    if (!half) vs[odd ? 1 : 0] = static_cast<uint8_t>(s0);
-                }
-                if (p.v_out) {
-                    // a byte's two codes times the two tokens' scales, exact in FP16
-                    const uint32_t s2 = e4m3x2_to_f16x2(s0 | (s1 << 8));
-                    float y0[8], y1[8];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t c[4];
-                        e2m1x8_to_f16x2x4(w[e], c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t v2 = hmul2_u32(c[j], s2);
-                            y0[4 * e + j] = __fmul_rn(f16_lo(v2), gv);
-                            y1[4 * e + j] = __fmul_rn(f16_hi(v2), gv);
-                        }
-                    }
-                    uint8_t* dst = p.v_out + ((static_cast<int64_t>(row) * p.H + h) * D + 16 * b + 8 * half) * 2;
-                    store8(dst, y0, f16);
-                    if (both) store8(dst + static_cast<int64_t>(p.H) * D * 2, y1, f16);
-                }
             }
         }
     }
@@ -435,14 +454,17 @@ extern "C" nvfp4kv_status nvfp4_kv_append(
     p.out_f16 = out_dtype == NVFP4KV_FP16;
     const int HW = 32 / (D / 16);
     p.segs_rot = (num_q_heads + H + HW - 1) / HW;
-    p.segs = p.segs_rot + (H + HW - 1) / HW;
-    // a warp takes as many head groups of a row as leave 32 warps to an SM: few rows are spread over
-    // the GPU, and with many rows the position's table row is read once for all heads
-    const int64_t spread = static_cast<int64_t>(num_rows) * p.segs;
+    p.segs_v = (H + HW - 1) / HW;
+    // few rows are spread over the GPU, and with many rows the position's table row is read once for all
+    // heads (1237 rows of 24 + 4 heads of 256: 12.7 us so, 14.9 with 16 warps to an SM)
+    const int64_t spread = static_cast<int64_t>(num_rows) * (p.segs_rot + p.segs_v);
     const int64_t each = (spread + num_sms() * 32 - 1) / (num_sms() * 32);
-    p.segs_per_task = static_cast<int>(each < p.segs ? each : p.segs);
-    p.tasks_per_row = (p.segs + p.segs_per_task - 1) / p.segs_per_task;
-    p.tasks = static_cast<int64_t>(num_rows) * p.tasks_per_row;
+    p.rot_each = static_cast<int>(each < p.segs_rot ? each : p.segs_rot);
+    p.rot_tasks = (p.segs_rot + p.rot_each - 1) / p.rot_each;
+    p.v_each = static_cast<int>(each < p.segs_v ? each : p.segs_v);
+    p.v_tasks = (p.segs_v + p.v_each - 1) / p.v_each;
+    p.rot_total = static_cast<int64_t>(num_rows) * p.rot_tasks;
+    p.tasks = p.rot_total + static_cast<int64_t>(num_rows) * p.v_tasks;
     const int64_t ctas = (p.tasks + kAppendThreads / 32 - 1) / (kAppendThreads / 32);
     const int64_t most = static_cast<int64_t>(num_sms()) * 32;
     const int grid = static_cast<int>(ctas < most ? ctas : most);

@@ -1,6 +1,15 @@
 // Paged decode attention over selected pages: C entry points. Every (sequence, KV head) pair reads
 // the pages of its own table, so the decode kernel runs with the pairs in the place of the
 // sequences (decode_kernel.cuh, PER_HEAD).
+//
+// Bound: HBM in the steady state (6.45 TB/s from 32 to 128 pages per pair), but the calls are short: of
+// 25.7 us for 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) the lengths, the stage prefix, the
+// page ids and the first stage take 5.6 us, the end of the last runs and the merge of their records 5 us.
+// 64 pairs of 8192 tokens with 8 query heads each take 28.9 us (28 records of 4 KB per pair to merge), 8
+// pairs of 4096 tokens 11.3 us. Measured against it and slower: one combined record per CTA and pair, runs
+// that never cross pairs, runs of unequal length on every warp, 32-token stages (14 to 16 warps, or more
+// slots), tiles of a stage worked on two or one at a time, and the scores of a stage interleaved with P V
+// of the one before (one more iteration per run: 28.6 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
