@@ -70,7 +70,6 @@ extern "C" nvfp4kv_status nvfp4_paged_decode_attention(
     p.B = batch;
     p.Hq = num_q_heads;
     p.H = H;
-    p.pool_heads = H;
     p.G = num_q_heads / H;
     p.T = T;
     p.pool_pages = pool_pages;
@@ -81,9 +80,9 @@ extern "C" nvfp4kv_status nvfp4_paged_decode_attention(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (D) {
-    case 64: e = launch_decode<64, false>(p, runs, s); break;
-    case 128: e = launch_decode<128, false>(p, runs, s); break;
-    default: e = launch_decode<256, false>(p, runs, s); break;
+    case 64: e = launch_decode<64>(p, runs, s); break;
+    case 128: e = launch_decode<128>(p, runs, s); break;
+    default: e = launch_decode<256>(p, runs, s); break;
     }
     if (e != cudaSuccess) return NVFP4KV_ERR_CUDA;
 

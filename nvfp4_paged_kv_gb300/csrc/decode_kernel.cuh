@@ -47,10 +47,6 @@
 //    takes float4 output columns and forms its head's weights from the staged maxima itself.
 //    A pair with more records than fit at once is merged by chunks.
 // Bytes per (token, KV head) at head_dim 128: 64 + 8 (K) + 64 + 8 (V) = 144.
-//
-// PER_HEAD is the decode over selected pages: every (sequence, KV head) pair has a page table and
-// a length of its own. The pairs then take the place of the sequences (B = pairs, H = 1), and only
-// the pool address still needs the pair's KV head.
 #pragma once
 #include <cstdint>
 #include <utility>
@@ -64,7 +60,6 @@ namespace {
 
 constexpr int kMaxGroup = 8;
 constexpr int kMaxSplits = 64;     // bound of the caller-forced split count
-constexpr int kMaxSparsePairs = 65535;  // (sequence, KV head) pairs of a call over selected pages
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kFirst = 1u, kLast = 2u;  // slot header flags: first / last stage of a piece
@@ -126,8 +121,6 @@ struct DecodeParams {
     uint64_t t_magic;   // ceil(2^64 / T)
     uint32_t nonce;     // tag of this call
     int32_t B, Hq, H, G, T, pool_pages, max_pages, num_runs;
-    int32_t pool_heads;  // KV heads of a page in the pools (PER_HEAD: H is 1)
-    int32_t full_stages, full_run;  // PER_HEAD: stages when every pair has all its pages, and W then
     float sm_scale;
 };
 
@@ -461,7 +454,7 @@ __device__ __forceinline__ int merge_batch(const DecodeParams& p, const int (*pe
     return cnt;
 }
 
-template <int D, bool PER_HEAD>
+template <int D>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const DecodeParams p) {
     pdl_enter();
     using G_ = Geo<D>;
@@ -517,41 +510,24 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
         if (w < warp) excl += scan_warp[w];
         total += scan_warp[w];
     }
-    // warp run gw takes [gw W, gw W + W) of the stage list. PER_HEAD, where a call often has few stages
-    // per warp:
-    //  * fewer runs than warps are spread over the CTAs (512 stages on 43 of the 152 SMs took 14.8 us,
-    //    spread over all 11.4; runs of unequal length that use every warp were slower than equal ones by
-    //    their additional records, 31.1 against 29.2 us at 8192 stages);
-    //  * when every pair has all its pages, W may be a little larger, so that runs end with pairs
-    //    (aligned_run).
+    // warp run gw takes [gw W, gw W + W) of the stage list
     const int num_runs = p.num_runs;
-    const int W = PER_HEAD && total == p.full_stages ? p.full_run : max(1, (total + num_runs - 1) / num_runs);
-    const int R = (total + W - 1) / W;
+    const int W = max(1, (total + num_runs - 1) / num_runs);
     if (blockIdx.x == 0) {
-        // sequences without stages (length 0 or invalid): output 0, LSE -inf, a warp per sequence
-        for (int j = 0; j < C; ++j) {
-            const int b = b_lo + j;
-            const bool none = b < b_hi && seq_stages(len_of(b), max_tokens, TOK) == 0;
-            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, none); todo != 0u; todo &= todo - 1u) {
-                const int64_t bz = __shfl_sync(0xFFFFFFFFu, b, __ffs(todo) - 1);
-                uint4* ob = reinterpret_cast<uint4*>(p.out + bz * p.Hq * D);
-                for (int i = lane; i < p.Hq * (D / 8); i += 32) ob[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (p.lse)
-                    for (int i = lane; i < p.Hq; i += 32) p.lse[bz * p.Hq + i] = -INFINITY;
-            }
+        // sequences without stages (length 0 or invalid): output 0, LSE -inf
+        for (int b = b_lo; b < b_hi; ++b) {
+            if (seq_stages(__ldg(p.seq_lens + b), max_tokens, TOK) != 0) continue;
+            uint16_t* ob = p.out + static_cast<int64_t>(b) * p.Hq * D;
+            for (int i = 0; i < p.Hq * D; ++i) ob[i] = 0;
+            if (p.lse)
+                for (int i = 0; i < p.Hq; ++i) p.lse[static_cast<int64_t>(b) * p.Hq + i] = -INFINITY;
         }
     }
     // One walk over this thread's sequences finds the sequence holding each of the CTA's run
     // starts and its two span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
-    int gw0 = blockIdx.x * NW;
-    int n_runs_cta = max(0, min(num_runs - gw0, NW));
-    if constexpr (PER_HEAD) {
-        // the runs k whose place k num_runs / R is one of this CTA's
-        const int k_end = min(R, ((gw0 + n_runs_cta) * R + num_runs - 1) / num_runs);
-        gw0 = min(k_end, (gw0 * R + num_runs - 1) / num_runs);
-        n_runs_cta = k_end - gw0;
-    }
-    const int span_lo = (n_runs_cta > 0 && gw0 < R) ? gw0 * W : total;
+    const int gw0 = blockIdx.x * NW;
+    const int n_runs_cta = max(0, min(num_runs - gw0, NW));
+    const int span_lo = (n_runs_cta > 0 && gw0 < (total + W - 1) / W) ? gw0 * W : total;
     const int span_hi = min(total, (gw0 + n_runs_cta) * W);
     if (local > 0 && span_lo < span_hi && span_lo < excl + local && span_hi > excl) {
         int acc = excl;
@@ -593,7 +569,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
 
     const int gw = gw0 + warp;
     const int64_t s_begin64 = static_cast<int64_t>(gw) * W;
-    const bool has_run = (PER_HEAD ? warp < n_runs_cta : gw < num_runs) && s_begin64 < total;
+    const bool has_run = gw < num_runs && s_begin64 < total;
     const int s_begin = has_run ? static_cast<int>(s_begin64) : 0;
     const int n_st = has_run ? min(total - s_begin, W) : 0;
 
@@ -654,16 +630,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
         return (pg >= 0 && pg < p.pool_pages) ? pg : -1;
     };
 
-    const int64_t page_rows = static_cast<int64_t>(PER_HEAD ? p.pool_heads : H) * T;
-    // PER_HEAD: the KV head of pair ib
-    int ipool_h = PER_HEAD ? ib % p.pool_heads : 0;
+    const int64_t page_rows = static_cast<int64_t>(H) * T;
     const bool page_aligned = (T % TOK) == 0;
     // issue the next stage of the walk into `slot`, then advance the walk
     auto issue_next = [&](uint32_t slot) {
         const uint64_t kv_pol = l2_policy_evict_first();
         const int t0 = ij * TOK;
         const int nval = min(TOK, ilen - t0);
-        const int64_t head_rows = static_cast<int64_t>(PER_HEAD ? ipool_h : ih) * T;
+        const int64_t head_rows = static_cast<int64_t>(ih) * T;
         int64_t row0[G_::SUB];  // token row of each sub-tile in its pool, -1: not real
         if (page_aligned) {
             const int pidx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t0), p.t_magic));
@@ -751,12 +725,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
             if (issued < n_st && ++ih == H) {
                 ih = 0;
                 ++ib;
-                if constexpr (PER_HEAD) ipool_h = ib % p.pool_heads;
                 ilen = nlen;
                 iS = seq_stages(ilen, max_tokens, TOK);
                 while (iS == 0) {  // sequences without stages are not in the list
                     ++ib;
-                    if constexpr (PER_HEAD) ipool_h = ib % p.pool_heads;
                     ilen = __ldg(p.seq_lens + ib);
                     iS = seq_stages(ilen, max_tokens, TOK);
                 }
@@ -1127,16 +1099,6 @@ int64_t decode_runs(int batch, int H, int D, int max_num_splits) {
     return static_cast<int64_t>(num_sms()) * warps_per_cta(D);
 }
 
-// PER_HEAD: the stages of a run, at least W, for pairs of S stages each. A run that crosses pairs leaves
-// two records and starts a second piece, so W becomes a divisor or a multiple of S when one is at most a
-// third larger, and S up to 3, where a merge takes as long as the additional stages (256 pairs: of 16
-// stages 19.5 us with W = 3, 18.2 with 4; of 2 stages 10.1 with 1, 8.3 with 2).
-int aligned_run(int64_t W, int64_t S) {
-    const int64_t up = (W + S - 1) / S * S;
-    if (S <= 3 || (W >= S && 3 * up <= 4 * W)) return static_cast<int>(up);
-    return static_cast<int>(W >= 3 && S % W != 0 && S % (W + 1) == 0 ? W + 1 : W);
-}
-
 struct WsLayout {
     size_t done, ml, o, total;
 };
@@ -1174,14 +1136,14 @@ bool decode_size_ok(int batch, int H, int D, int max_pages, int T, int64_t runs)
            runs + static_cast<int64_t>(batch) * H < lim;
 }
 
-template <int D, bool PER_HEAD>
+template <int D>
 cudaError_t launch_decode(const DecodeParams& p, int64_t runs, cudaStream_t s) {
     using G_ = Geo<D>;
-    cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D, PER_HEAD>,
+    cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
-    e = launch_pdl(decode_split_kernel<D, PER_HEAD>, static_cast<unsigned>(ctas), G_::THREADS,
+    e = launch_pdl(decode_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS,
                    static_cast<size_t>(G_::SMEM), s, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();

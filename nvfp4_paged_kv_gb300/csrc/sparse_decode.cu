@@ -1,19 +1,8 @@
-// Paged decode attention over selected pages: C entry points. Every (sequence, KV head) pair reads
-// the pages of its own table, so the decode kernel runs with the pairs in the place of the
-// sequences (decode_kernel.cuh, PER_HEAD).
-//
-// Bound: HBM in the steady state (6.45 TB/s from 32 to 128 pages per pair), but the calls are short: of
-// 25.7 us for 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) the lengths, the stage prefix, the
-// page ids and the first stage take 5.6 us, the end of the last runs and the merge of their records 5 us.
-// 64 pairs of 8192 tokens with 8 query heads each take 28.9 us (28 records of 4 KB per pair to merge), 8
-// pairs of 4096 tokens 11.3 us. Measured against it and slower: one combined record per CTA and pair, runs
-// that never cross pairs, runs of unequal length on every warp, 32-token stages (14 to 16 warps, or more
-// slots), tiles of a stage worked on two or one at a time, and the scores of a stage interleaved with P V
-// of the one before (one more iteration per run: 28.6 us).
+// C entry points of the paged decode attention over selected pages; the kernel is in sparse_kernel.cuh.
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "decode_kernel.cuh"
+#include "sparse_kernel.cuh"
 
 using namespace nvfp4kv;
 
@@ -60,7 +49,7 @@ extern "C" nvfp4kv_status nvfp4_paged_sparse_decode_attention(
         return NVFP4KV_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
 
-    DecodeParams p{};
+    SparseParams p{};
     p.q = static_cast<const uint16_t*>(q);
     p.kd = k_data;
     p.ks = k_scales;
@@ -89,15 +78,16 @@ extern "C" nvfp4kv_status nvfp4_paged_sparse_decode_attention(
     p.pool_heads = H;
     const int64_t each = (static_cast<int64_t>(max_sel_pages) * T + stage_tokens(D) - 1) / stage_tokens(D);
     p.full_stages = static_cast<int32_t>(pairs * each);  // (bounded by decode_size_ok)
-    p.full_run = aligned_run((pairs * each + runs - 1) / runs, each);
+    p.full_each = static_cast<int32_t>(each);
+    p.full_runs = even_runs(pairs, each, runs);
     p.sm_scale = sm_scale;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (D) {
-    case 64: e = launch_decode<64, true>(p, runs, s); break;
-    case 128: e = launch_decode<128, true>(p, runs, s); break;
-    default: e = launch_decode<256, true>(p, runs, s); break;
+    case 64: e = launch_sparse<64>(p, runs, s); break;
+    case 128: e = launch_sparse<128>(p, runs, s); break;
+    default: e = launch_sparse<256>(p, runs, s); break;
     }
     return e == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
 }

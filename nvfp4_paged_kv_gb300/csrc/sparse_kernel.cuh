@@ -1,0 +1,712 @@
+// Split-KV decode attention over selected pages: every (sequence, KV head) pair has a page table and a length
+// of its own. The mathematics, packings, per-warp pipeline, records and merge are those of the dense decode
+// (decode_kernel.cuh, whose helpers this file uses); what differs is how the list of stages is cut into runs
+// and that the pairs stand where the dense decode has sequences. It is a kernel of its own because the dense
+// one loses 1 to 2 % to the additional cases, of its 60 and 120 us.
+//
+// Bound: HBM in the steady state (6.45 TB/s from 32 to 128 pages per pair), but the calls are short: of 24.7 us
+// for 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) the lengths, the stage prefix, the page ids
+// and the first stage take 5.6 us, the end of the last runs and the merge of their records 4 us. 64 pairs of
+// 8192 tokens with 8 query heads each take 27.6 us (26 records of 4 KB per pair to merge), 8 pairs of 4096
+// tokens 11.3 us. Measured against it and slower: one combined record per CTA and pair, runs of unequal length
+// on every warp, 32-token stages (14 to 16 warps, or more slots), tiles of a stage worked on two or one at a
+// time, and the scores of a stage interleaved with P V of the one before (one more iteration per run: 28.6 us).
+#pragma once
+#include "decode_kernel.cuh"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int kMaxSparsePairs = 65535;  // (sequence, KV head) pairs of a call
+
+// B: pairs, H: 1, Hq: query heads of a pair; seq_lens and page_table are those of the pairs.
+struct SparseParams : DecodeParams {
+    int32_t pool_heads;  // KV heads of a page in the pools
+    // when every pair has all its pages: stages of all pairs, and of one, and its runs (0: runs cross pairs)
+    int32_t full_stages, full_each, full_runs;
+};
+
+template <int D>
+__global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const SparseParams p) {
+    pdl_enter();
+    using G_ = Geo<D>;
+    constexpr int TOK = G_::TOK;
+    constexpr int NW = G_::WARPS;
+    constexpr int NT = G_::THREADS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int scan_warp[NW];
+    __shared__ int start_bp[NW][3];  // run start of each warp: pair, its first stage, length
+    __shared__ int span_pair[2];     // first and last pair the CTA's runs touch
+    __shared__ int pend_n;           // pairs whose last piece finished in this CTA ...
+    __shared__ int pend[2 * NW][4];  // ... (b, h, first record, records): merged at the end
+
+    const int tid = threadIdx.x;
+    const int warp = tid >> 5;
+    const int lane = tid & 31;
+    const int r = lane >> 2;  // row group of the MMA fragments
+    const int c = lane & 3;   // column pair of the MMA fragments
+    const int G = p.G, T = p.T;
+    const int max_tokens = p.max_pages * T;
+
+    // ------------------------------------------------ stage prefix over the pairs
+    // Thread t owns pairs [t C, t C + C); PS_b = sum_{b' < b} stages(b').
+    // The first two lengths stay in registers for the walk below (a second load of the same
+    // words would cost another round trip at the start).
+    const int C = (p.B + NT - 1) / NT;
+    const int b_lo = min(p.B, tid * C), b_hi = min(p.B, b_lo + C);
+    const int kept0 = (b_lo < b_hi) ? __ldg(p.seq_lens + b_lo) : 0;
+    const int kept1 = (b_lo + 1 < b_hi) ? __ldg(p.seq_lens + b_lo + 1) : 0;
+    auto len_of = [&](int b) {
+        return b == b_lo ? kept0 : (b == b_lo + 1 ? kept1 : __ldg(p.seq_lens + b));
+    };
+    int local = 0;
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int L = len_of(b);
+        if (blockIdx.x == 0 && (L < 0 || L > max_tokens))
+            flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
+        local += seq_stages(L, max_tokens, TOK);
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) scan_warp[warp] = incl;
+    if (tid < 2) span_pair[tid] = 0;
+    if (tid == 0) pend_n = 0;
+    __syncthreads();
+    int excl = incl - local, total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) excl += scan_warp[w];
+        total += scan_warp[w];
+    }
+    // warp run gw takes [gw W, gw W + W) of the stage list, or, when every pair has all its pages, each pair
+    // is cut into full_runs runs of its own (`even`). Fewer runs than warps are spread over the CTAs (512
+    // stages on 43 of the 152 SMs took 14.8 us, spread over all 11.4).
+    const int num_runs = p.num_runs;
+    const int W = max(1, (total + num_runs - 1) / num_runs);
+    const bool even = total == p.full_stages && p.full_runs > 0;
+    const int Wr = even ? 1 : W;
+    const int R = even ? p.B * p.full_runs : (total + W - 1) / W;
+    if (blockIdx.x == 0) {
+        // pairs without stages (length 0 or invalid): output 0, LSE -inf, a warp per pair
+        for (int j = 0; j < C; ++j) {
+            const int b = b_lo + j;
+            const bool none = b < b_hi && seq_stages(len_of(b), max_tokens, TOK) == 0;
+            for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, none); todo != 0u; todo &= todo - 1u) {
+                const int64_t bz = __shfl_sync(0xFFFFFFFFu, b, __ffs(todo) - 1);
+                uint4* ob = reinterpret_cast<uint4*>(p.out + bz * G * D);
+                for (int i = lane; i < G * (D / 8); i += 32) ob[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (p.lse)
+                    for (int i = lane; i < G; i += 32) p.lse[bz * G + i] = -INFINITY;
+            }
+        }
+    }
+    // One walk over this thread's pairs finds the pair holding each of the CTA's run
+    // starts and its two span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
+    int gw0 = blockIdx.x * NW;
+    int n_runs_cta = max(0, min(num_runs - gw0, NW));
+    {
+        // the runs k whose place k num_runs / R is one of this CTA's
+        const int k_end = min(R, ((gw0 + n_runs_cta) * R + num_runs - 1) / num_runs);
+        gw0 = min(k_end, (gw0 * R + num_runs - 1) / num_runs);
+        n_runs_cta = k_end - gw0;
+    }
+    const int span_lo = (n_runs_cta > 0 && gw0 < R) ? gw0 * W : total;
+    const int span_hi = min(total, (gw0 + n_runs_cta) * W);
+    if (even) {
+        if (tid == 0 && n_runs_cta > 0) {
+            span_pair[0] = gw0 / p.full_runs;
+            span_pair[1] = (gw0 + n_runs_cta - 1) / p.full_runs;
+        }
+    } else if (local > 0 && span_lo < span_hi && span_lo < excl + local && span_hi > excl) {
+        int acc = excl;
+        for (int b = b_lo; b < b_hi && acc < span_hi; ++b) {
+            const int L = len_of(b);
+            const int S = seq_stages(L, max_tokens, TOK);
+            const int n = S;
+            if (n > 0 && acc + n > span_lo) {
+                // runs of this CTA starting in [acc, acc + n): w in [w_a, w_b)
+                const int w_a = max(0, (acc - gw0 * W + W - 1) / W);
+                const int w_b = min(n_runs_cta, (acc + n - gw0 * W + W - 1) / W);
+                for (int w = w_a; w < w_b; ++w) {
+                    start_bp[w][0] = b;
+                    start_bp[w][1] = acc;
+                    start_bp[w][2] = L;
+                }
+                if (span_lo >= acc && span_lo < acc + n) span_pair[0] = b;
+                if (span_hi - 1 >= acc && span_hi - 1 < acc + n)
+                    span_pair[1] = b;
+            }
+            acc += n;
+        }
+    }
+    __syncthreads();
+
+    // ------------------------------------------------ queries of the CTA's pairs
+    const uint32_t smem_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const uint32_t qcache = smem_base + G_::Q_OFF;
+    const int q_first = span_pair[0];
+    const int q_cached = (even ? n_runs_cta > 0 : span_lo < span_hi)
+                             ? min(span_pair[1] - span_pair[0] + 1, G_::QCACHE / (G * D * 2))
+                             : 0;
+    {
+        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
+        const int nq = q_cached * G * D * 2 / 16;
+        for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
+        cp_async_commit();
+    }
+
+    const int gw = gw0 + warp;
+    const int64_t s_begin64 = static_cast<int64_t>(gw) * W;
+    const bool has_run = warp < n_runs_cta && (even || s_begin64 < total);
+    const int s_begin = has_run ? static_cast<int>(s_begin64) : 0;
+    // even: the run's pair, its first run, its place among the pair's runs, its first stage and the one after
+    const int e_pair = even && has_run ? gw / p.full_runs : 0;
+    const int e_run0 = e_pair * p.full_runs, e_at = gw - e_run0;
+    const int e_lo = even && has_run ? e_at * p.full_each / p.full_runs : 0;
+    const int e_hi = even && has_run ? (e_at + 1) * p.full_each / p.full_runs : 0;
+    const int n_st = has_run ? (even ? e_hi - e_lo : min(total - s_begin, W)) : 0;
+
+    // ------------------------------------------------ per-lane constants
+    const uint32_t ring = smem_base + warp * G_::RING;
+    // V chunk j = lane + 32 i of a stage lands XOR-swizzled by its pair row
+    uint32_t v_dst[G_::DCH];
+#pragma unroll
+    for (int i = 0; i < G_::DCH; ++i) {
+        const int j = lane + 32 * i;
+        const int pr = j / G_::VCH, cj = j - pr * G_::VCH;
+        v_dst[i] = G_::V_OFF + pr * D + 16 * (cj ^ (pr & G_::SWZ));
+    }
+    const int rho = (r >> 1) | ((r & 1) << 2);  // V rows of this lane: chunk rho of a pair row
+
+    // ------------------------------------------------ issue side: the walk over the run
+    int ib = has_run ? (even ? e_pair : start_bp[warp][0]) : 0;
+    int ilen = has_run ? (even ? __ldg(p.seq_lens + e_pair) : start_bp[warp][2]) : 0;
+    int iS = has_run ? seq_stages(ilen, max_tokens, TOK) : 1;
+    int ij = has_run ? (even ? e_lo : s_begin - start_bp[warp][1]) : 0;
+    // flat index of stage 0 of pair ib; even: the pair's first run
+    int ips = has_run ? (even ? e_run0 : start_bp[warp][1]) : 0;
+    bool ifirst = true;                     // the next stage to issue starts a piece
+    int issued = 0;
+    int nlen = (has_run && !even && ib + 1 < p.B) ? __ldg(p.seq_lens + ib + 1) : 0;  // next pair
+    // page-id windows: lane l holds the id of page base + l of a pair's page-table row; the
+    // window after the current one (in issue order) is loaded when the current one is taken
+    int wrow = -1, wbase = 0, win = 0;
+    int prow = -1, pbase = 0, pwin = 0;
+    auto load_window = [&](int b_, int base) -> int {
+        const int i = base + lane;
+        return (i < p.max_pages) ? __ldg(p.page_table + static_cast<int64_t>(b_) * p.max_pages + i)
+                                 : -1;
+    };
+    // make the window holding page pidx of pair ib current (its loads are only issued) and
+    // start loading the one after it
+    auto set_window = [&](int pidx) {
+        const int nbase = pidx & ~31;
+        win = (ib == prow && nbase == pbase) ? pwin : load_window(ib, nbase);
+        wrow = ib;
+        wbase = nbase;
+        const int npg = (ilen + T - 1) / T;
+        if (nbase + 32 < npg) {
+            prow = ib;
+            pbase = nbase + 32;
+        } else {
+            prow = ib + 1;  // an empty next pair makes this a miss
+            pbase = 0;
+        }
+        if (prow < p.B && !(prow == wrow && pbase == wbase))
+            pwin = load_window(prow, pbase);
+        else
+            prow = -1;
+    };
+    auto page_of = [&](int pidx) -> int {  // warp-uniform pidx of pair ib; every lane calls
+        if (ib != wrow || pidx < wbase || pidx >= wbase + 32) set_window(pidx);
+        const int pg = __shfl_sync(0xFFFFFFFFu, win, pidx - wbase);
+        return (pg >= 0 && pg < p.pool_pages) ? pg : -1;
+    };
+
+    const int64_t page_rows = static_cast<int64_t>(p.pool_heads) * T;
+    int ih = ib % p.pool_heads;  // KV head of pair ib
+    const bool page_aligned = (T % TOK) == 0;
+    // issue the next stage of the walk into `slot`, then advance the walk
+    auto issue_next = [&](uint32_t slot) {
+        const uint64_t kv_pol = l2_policy_evict_first();
+        const int t0 = ij * TOK;
+        const int nval = min(TOK, ilen - t0);
+        const int64_t head_rows = static_cast<int64_t>(ih) * T;
+        int64_t row0[G_::SUB];  // token row of each sub-tile in its pool, -1: not real
+        if (page_aligned) {
+            const int pidx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t0), p.t_magic));
+            const int pg = page_of(pidx);
+            const int64_t r0 = pg * page_rows + head_rows + (t0 - pidx * T);
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u)
+                row0[u] = (pg >= 0 && 16 * u < nval) ? r0 + 16 * u : -1;
+        } else {
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u) {
+                const int t = t0 + 16 * u;
+                const int pidx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t), p.t_magic));
+                const int pg = page_of(min(pidx, max(0, (ilen - 1) / T)));
+                row0[u] = (pg >= 0 && 16 * u < nval) ? pg * page_rows + head_rows + (t - pidx * T)
+                                                      : -1;
+            }
+        }
+        uint32_t okbits = 0;
+#pragma unroll
+        for (int u = 0; u < G_::SUB; ++u) okbits |= (row0[u] >= 0 ? 1u : 0u) << u;
+        const uint32_t want = (1u << ((nval + 15) / 16)) - 1u;
+        if (okbits != want && lane == 0) flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
+        if (page_aligned && okbits == (1u << G_::SUB) - 1) {
+            // the whole stage is one run of each pool: offsets are compile-time constants
+            const int64_t doff = row0[0] * (D / 2) + 16 * lane;
+            const uint8_t* ksrc = p.kd + doff;
+            const uint8_t* vsrc = p.vd + doff;
+            static_for<G_::DCH>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                cp_async16<G_::K_OFF + 512 * i, 512 * i>(slot + 16 * lane, ksrc, kv_pol);
+                cp_async16<0, 512 * i>(slot + v_dst[i], vsrc, kv_pol);
+            });
+            const int64_t soff = row0[0] * G_::NB;
+#pragma unroll
+            for (int k = 0; k < G_::SC_PER_LANE; ++k) {
+                const int jc = lane + 32 * k;
+                const bool kpool = jc < G_::SCH;
+                const int jj = kpool ? jc : jc - G_::SCH;
+                cp_async16<0, 0>(slot + (kpool ? G_::KS_OFF : G_::VS_OFF) + 16 * jj,
+                                 (kpool ? p.ks : p.vs) + soff + 16 * jj, kv_pol);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < G_::DCH; ++i) {
+                const int u = i / G_::SUB_DIV;
+                const int jj = lane + 32 * i - u * (D / 2);  // chunk within the sub-tile
+                const bool ok = row0[u] >= 0;
+                const int64_t off = ok ? row0[u] * (D / 2) + 16 * jj : 0;
+                cp_async16_zfill(slot + G_::K_OFF + 16 * (lane + 32 * i), p.kd + off,
+                                 ok ? 16u : 0u, kv_pol);
+                cp_async16_zfill(slot + v_dst[i], p.vd + off, ok ? 16u : 0u, kv_pol);
+            }
+#pragma unroll
+            for (int k = 0; k < G_::SC_PER_LANE; ++k) {
+                const int jc = lane + 32 * k;
+                const bool kpool = jc < G_::SCH;
+                const int jj = kpool ? jc : jc - G_::SCH;
+                const int u = jj / (D / 16);
+                int64_t ru = row0[0];  // row0[u] without a dynamically indexed array
+#pragma unroll
+                for (int uu = 1; uu < G_::SUB; ++uu)
+                    if (u == uu) ru = row0[uu];
+                const bool ok = ru >= 0;
+                const int64_t off = ok ? ru * G_::NB + 16 * (jj - u * (D / 16)) : 0;
+                cp_async16_zfill(slot + (kpool ? G_::KS_OFF : G_::VS_OFF) + 16 * jj,
+                                 (kpool ? p.ks : p.vs) + off, ok ? 16u : 0u, kv_pol);
+            }
+        }
+        const bool last = (ij == iS - 1) || (issued == n_st - 1);
+        const uint32_t flags = (ifirst ? kFirst : 0u) | (last ? kLast : 0u);
+        if (lane == 0) {
+            sts_v4(slot + G_::HDR_OFF, okbits | (static_cast<uint32_t>(nval) << 8), flags,
+                   static_cast<uint32_t>(ib), 0u);
+            sts_v4(slot + G_::HDR_OFF + 16, static_cast<uint32_t>(ips),
+                   static_cast<uint32_t>(even ? p.full_runs : iS), 0u, 0u);
+        }
+        // advance the walk
+        ++issued;
+        ifirst = false;
+        if (last) {
+            ij = 0;
+            ips += iS;
+            ifirst = true;
+            if (issued < n_st) {
+                ++ib;
+                ilen = nlen;
+                iS = seq_stages(ilen, max_tokens, TOK);
+                while (iS == 0) {  // pairs without stages are not in the list
+                    ++ib;
+                    ilen = __ldg(p.seq_lens + ib);
+                    iS = seq_stages(ilen, max_tokens, TOK);
+                }
+                nlen = (ib + 1 < p.B) ? __ldg(p.seq_lens + ib + 1) : 0;
+                ih = ib % p.pool_heads;
+            }
+        } else {
+            ++ij;
+        }
+    };
+
+    // ------------------------------------------------ start: stage 0, then the query cache
+    // The first page-id window is loaded while the query cache fills; the first copies go out
+    // as soon as the page ids are in, and the queries are waited for behind them.
+    if (n_st > 0) issue_next(ring);
+    cp_async_commit();
+    cp_async_wait<1>();  // this thread's query chunks have landed ...
+    __syncthreads();     // ... and every thread's: from here on warps run alone until the merge
+
+    // ------------------------------------------------ compute side
+    uint32_t qf[G_::KSTEPS][2];
+    float cs0 = 0.0f, cs1 = 0.0f;
+    float o[G_::KSTEPS][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    const float gvs = __ldg(p.gv);
+
+#pragma unroll 1
+    for (int i = 0; i < n_st; ++i) {
+        // the next stage goes into the slot computed at iteration i - 1
+        if (i + 1 < n_st) issue_next(ring + ((i + 1) % G_::SLOTS) * G_::SLOT);
+        cp_async_commit();
+        cp_async_wait<1>();  // this lane's copies of stage i are done ...
+        __syncwarp();        // ... and so are the other lanes'
+        const uint32_t st = ring + (i % G_::SLOTS) * G_::SLOT;
+        uint32_t hdr[4];
+        lds_words(hdr, st + G_::HDR_OFF);
+        const uint32_t okbits = hdr[0] & 0xFFu;
+        const int nval = static_cast<int>(hdr[0] >> 8);
+        const uint32_t flags = hdr[1];
+        if (flags & kFirst) {
+            // ---- Q fragments of the piece: lane (r, c) holds head r of the group; k-step kk
+            // covers head dims c*D/4 + 4kk + {0..3} (the same permutation is used for K), as
+            // FP16 q * 2^kq. From the query cache, or from global memory for a pair beyond it.
+            const int qpair = static_cast<int>(hdr[2]);
+            float qv[D / 4];
+            float qmax = 0.0f;
+            if (r < G) {
+                uint32_t qw[D / 8];
+                const int qi = qpair - q_first;
+                if (qi >= 0 && qi < q_cached) {
+                    lds_words(qw, qcache + ((qi * G + r) * D + c * (D / 4)) * 2);
+                } else {
+                    const uint4* qsrc = reinterpret_cast<const uint4*>(
+                        p.q + (static_cast<int64_t>(qpair) * G + r) * D + c * (D / 4));
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        const uint4 v = __ldg(qsrc + k);
+                        qw[4 * k] = v.x;
+                        qw[4 * k + 1] = v.y;
+                        qw[4 * k + 2] = v.z;
+                        qw[4 * k + 3] = v.w;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) {
+                    qv[2 * k] = bf16_lo(qw[k]);
+                    qv[2 * k + 1] = bf16_hi(qw[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < D / 4; ++k) qmax = fmaxf(qmax, fabsf(qv[k]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < D / 4; ++k) qv[k] = 0.0f;
+            }
+            qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, 1));
+            qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, 2));
+            // qmax * 2^kq in [2^14, 2^15): every BF16 value of the head is exact in FP16 down
+            // to 2^-18 of the head maximum.
+            int kq = (qmax > 0.0f) ? (14 - ilogbf(qmax)) : 0;
+            kq = max(-120, min(kq, 120));
+            const float up = ldexpf(1.0f, kq);
+#pragma unroll
+            for (int kk = 0; kk < G_::KSTEPS; ++kk) {
+                qf[kk][0] = pack_f16x2(qv[4 * kk] * up, qv[4 * kk + 1] * up);
+                qf[kk][1] = pack_f16x2(qv[4 * kk + 2] * up, qv[4 * kk + 3] * up);
+            }
+            const float cs_row = (r < G) ? p.sm_scale * __ldg(p.gk) * kLog2e * ldexpf(1.0f, -kq)
+                                         : 0.0f;
+            // score scale of this lane's two S^T columns (query heads 2c, 2c+1)
+            cs0 = __shfl_sync(0xFFFFFFFFu, cs_row, 8 * c);
+            cs1 = __shfl_sync(0xFFFFFFFFu, cs_row, 8 * c + 4);
+#pragma unroll
+            for (int m = 0; m < G_::KSTEPS; ++m)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[m][k] = 0.0f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.0f;
+        }
+
+        if (okbits != 0u) {
+            const bool full = (okbits == (1u << G_::SUB) - 1) && nval >= TOK;
+            // valid-token bits of each sub-tile (only read when !full)
+            uint32_t tmask[G_::SUB];
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u) {
+                const int nv = min(16, max(0, nval - 16 * u));
+                tmask[u] = ((okbits >> u) & 1u) ? ((nv >= 16) ? 0xFFFFu : ((1u << nv) - 1u)) : 0u;
+            }
+
+            // ---- S^T = K^ Q^T for the SUB sub-tiles
+            float x[G_::SUB][4];
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u) {
+                const int row0 = 16 * u + r;
+                const int row1 = row0 + 8;
+                uint32_t kw0[G_::CW], kw1[G_::CW];
+                lds_words(kw0, st + G_::K_OFF + row0 * (D / 2) + c * G_::CHUNK);
+                lds_words(kw1, st + G_::K_OFF + row1 * (D / 2) + c * G_::CHUNK);
+                // FP16 (s, s) of the lane's D/64 blocks in rows row0 / row1: the scale byte
+                // is duplicated by an integer multiply, then converted as an E4M3 pair
+                uint32_t ks0[D / 64], ks1[D / 64];
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    ks0[q] = e4m3x2_to_f16x2(
+                        lds_u8(st + G_::KS_OFF + row0 * G_::NB + c * (D / 64) + q) * 0x0101u);
+                    ks1[q] = e4m3x2_to_f16x2(
+                        lds_u8(st + G_::KS_OFF + row1 * G_::NB + c * (D / 64) + q) * 0x0101u);
+                }
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < G_::CW; ++q) {
+                    uint32_t c0[4], c1[4];
+                    e2m1x8_to_f16x2x4(kw0[q], c0);
+                    e2m1x8_to_f16x2x4(kw1[q], c1);
+#pragma unroll
+                    for (int hk = 0; hk < 2; ++hk) {
+                        const int kk = 2 * q + hk;  // k-step: bytes 2kk, 2kk+1 of the chunk
+                        const int blk = kk / 4;     // block of the lane's chunk
+                        uint32_t a[4];
+                        a[0] = h2_mul(c0[2 * hk], ks0[blk]);
+                        a[1] = h2_mul(c1[2 * hk], ks1[blk]);
+                        a[2] = h2_mul(c0[2 * hk + 1], ks0[blk]);
+                        a[3] = h2_mul(c1[2 * hk + 1], ks1[blk]);
+                        mma_f16_16816(acc, a, qf[kk][0], qf[kk][1]);
+                    }
+                }
+                x[u][0] = acc[0] * cs0;
+                x[u][1] = acc[1] * cs1;
+                x[u][2] = acc[2] * cs0;
+                x[u][3] = acc[3] * cs1;
+            }
+
+            // ---- online softmax over the stage, columns = query heads 2c, 2c+1
+            if (!full) {
+#pragma unroll
+                for (int u = 0; u < G_::SUB; ++u) {
+                    if (!((tmask[u] >> r) & 1u)) x[u][0] = x[u][1] = -INFINITY;
+                    if (!((tmask[u] >> (r + 8)) & 1u)) x[u][2] = x[u][3] = -INFINITY;
+                }
+            }
+            float lm0 = fmaxf(x[0][0], x[0][2]), lm1 = fmaxf(x[0][1], x[0][3]);
+#pragma unroll
+            for (int u = 1; u < G_::SUB; ++u) {
+                lm0 = fmaxf(lm0, fmaxf(x[u][0], x[u][2]));
+                lm1 = fmaxf(lm1, fmaxf(x[u][1], x[u][3]));
+            }
+            // column maxima over the stage, both columns in one FP16 pair (the running
+            // maximum only has to be close to the true one: p = 2^(x - m) stays below 2^8)
+            __half2 hm = __floats2half2_rn(lm0, lm1);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                const uint32_t uu =
+                    __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&hm), off);
+                hm = __hmax2(hm, *reinterpret_cast<const __half2*>(&uu));
+            }
+            float mx0 = __low2float(hm), mx1 = __high2float(hm);
+            if (__any_sync(0xFFFFFFFFu, fmaxf(mx0, mx1) > 65000.0f)) {
+                // scores beyond the FP16 range: reduce in fp32 instead
+                mx0 = lm0;
+                mx1 = lm1;
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
+                }
+            }
+            const bool grow = (mx0 > m0 + kRescaleThreshold) || (mx1 > m1 + kRescaleThreshold);
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+                const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+                const float a0 = ex2_approx(m0 - n0), a1 = ex2_approx(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= a0;
+                l1 *= a1;
+#pragma unroll
+                for (int m = 0; m < G_::KSTEPS; ++m) {
+                    o[m][0] *= a0;
+                    o[m][1] *= a1;
+                    o[m][2] *= a0;
+                    o[m][3] *= a1;
+                }
+            }
+            uint32_t pb[G_::SUB][2];
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u) {
+                const float p0 = ex2_approx(x[u][0] - m0), p1 = ex2_approx(x[u][1] - m1);
+                const float p2 = ex2_approx(x[u][2] - m0), p3 = ex2_approx(x[u][3] - m1);
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                // P^T (tokens x heads) -> B operand (k = tokens, n = heads)
+                pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
+                pb[u][1] = movmatrix_trans(pack_f16x2(p2, p3));
+            }
+
+            // ---- O^T += V^^T P^T. Lane pairs: pr0 (tokens 2c, 2c+1), pr1 (tokens 2c+8, 2c+9)
+#pragma unroll
+            for (int u = 0; u < G_::SUB; ++u) {
+                const int pr0 = 8 * u + c, pr1 = pr0 + 4;
+                // the lane's chunk covers head dims rho*D/8 .. +D/8-1: blocks (rho*D/8)/16 ...
+                constexpr int kBlkPerChunk = (D / 8 + 15) / 16;
+                uint32_t vsc0[kBlkPerChunk], vsc1[kBlkPerChunk];
+#pragma unroll
+                for (int q = 0; q < kBlkPerChunk; ++q) {
+                    const int blk = (rho * (D / 8)) / 16 + q;
+                    vsc0[q] = e4m3x2_to_f16x2(lds_u16(st + G_::VS_OFF + pr0 * 2 * G_::NB + 2 * blk));
+                    vsc1[q] = e4m3x2_to_f16x2(lds_u16(st + G_::VS_OFF + pr1 * 2 * G_::NB + 2 * blk));
+                }
+                if (!full && tmask[u] != 0xFFFFu) {
+                    // tokens past the pair end in a real page: their V scales may be
+                    // anything, so they are zeroed (P is 0 there already)
+                    const uint32_t tm = tmask[u];
+                    const uint32_t keep0 = (((tm >> (2 * c)) & 1u) ? 0x0000FFFFu : 0u) |
+                                           (((tm >> (2 * c + 1)) & 1u) ? 0xFFFF0000u : 0u);
+                    const uint32_t keep1 = (((tm >> (2 * c + 8)) & 1u) ? 0x0000FFFFu : 0u) |
+                                           (((tm >> (2 * c + 9)) & 1u) ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int q = 0; q < kBlkPerChunk; ++q) {
+                        vsc0[q] &= keep0;
+                        vsc1[q] &= keep1;
+                    }
+                }
+                uint32_t vw0[G_::CW], vw1[G_::CW];
+#pragma unroll
+                for (int q = 0; q < G_::CW; q += (G_::CW >= 4 ? 4 : G_::CW)) {
+                    const int xb = rho * G_::CHUNK + 4 * q;  // logical byte of the chunk piece
+                    uint32_t t0w[G_::CW >= 4 ? 4 : G_::CW], t1w[G_::CW >= 4 ? 4 : G_::CW];
+                    lds_words(t0w, st + G_::V_OFF + v_swz<D>(pr0, xb));
+                    lds_words(t1w, st + G_::V_OFF + v_swz<D>(pr1, xb));
+#pragma unroll
+                    for (int e = 0; e < (G_::CW >= 4 ? 4 : G_::CW); ++e) {
+                        vw0[q + e] = t0w[e];
+                        vw1[q + e] = t1w[e];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < G_::CW; ++q) {
+                    uint32_t c0[4], c1[4];
+                    e2m1x8_to_f16x2x4(vw0[q], c0);
+                    e2m1x8_to_f16x2x4(vw1[q], c1);
+#pragma unroll
+                    for (int hm2 = 0; hm2 < 2; ++hm2) {
+                        const int m = 2 * q + hm2;   // M-tile: bytes 2m, 2m+1 of the chunk
+                        const int sq = (2 * m) / 16; // block of that byte within the chunk
+                        uint32_t a[4];
+                        a[0] = h2_mul(c0[2 * hm2], vsc0[sq]);
+                        a[1] = h2_mul(c0[2 * hm2 + 1], vsc0[sq]);
+                        a[2] = h2_mul(c1[2 * hm2], vsc1[sq]);
+                        a[3] = h2_mul(c1[2 * hm2 + 1], vsc1[sq]);
+                        mma_f16_16816(o[m], a, pb[u][0], pb[u][1]);
+                    }
+                }
+            }
+        }
+
+        if (flags & kLast) {
+            // ---- end of a piece: the whole pair (outputs) or a record
+            uint32_t h2[4];
+            lds_words(h2, st + G_::HDR_OFF + 16);
+            const int pair = static_cast<int>(hdr[2]);
+            const int pps = static_cast<int>(h2[0]), pS = static_cast<int>(h2[1]);
+            float ls0 = l0, ls1 = l1;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                ls0 += __shfl_xor_sync(0xFFFFFFFFu, ls0, off);
+                ls1 += __shfl_xor_sync(0xFFFFFFFFu, ls1, off);
+            }
+            const int g0 = 2 * c, g1 = 2 * c + 1;
+            const int gf = pps / Wr, gl = (pps + pS - 1) / Wr;  // the pair's first and last run
+            const int64_t bh = pair;
+            if (gf == gl) {
+                // the whole pair is this piece: normalise and write the output directly
+                uint16_t* ob = p.out + bh * G * D;
+                const float f0 = ls0 > 0.0f ? gvs / ls0 : 0.0f;
+                const float f1 = ls1 > 0.0f ? gvs / ls1 : 0.0f;
+#pragma unroll
+                for (int m = 0; m < G_::KSTEPS; ++m) {
+                    const int d0 = rho * (D / 8) + 2 * m;
+                    if (g0 < G)
+                        *reinterpret_cast<uint32_t*>(ob + g0 * D + d0) =
+                            pack_bf16x2(o[m][0] * f0, o[m][2] * f0);
+                    if (g1 < G)
+                        *reinterpret_cast<uint32_t*>(ob + g1 * D + d0) =
+                            pack_bf16x2(o[m][1] * f1, o[m][3] * f1);
+                }
+                if (r == 0 && p.lse) {
+                    float* lb = p.lse + bh * G;
+                    if (g0 < G) lb[g0] = ls0 > 0.0f ? (m0 + log2f(ls0)) * 0.6931471805599453f : -INFINITY;
+                    if (g1 < G) lb[g1] = ls1 > 0.0f ? (m1 + log2f(ls1)) * 0.6931471805599453f : -INFINITY;
+                }
+            } else {
+                const int64_t rec = gw + bh;
+                float* ro = p.rec_o + rec * G * D;
+#pragma unroll
+                for (int m = 0; m < G_::KSTEPS; ++m) {
+                    const int d0 = rho * (D / 8) + 2 * m;
+                    if (g0 < G) *reinterpret_cast<float2*>(ro + g0 * D + d0) = make_float2(o[m][0], o[m][2]);
+                    if (g1 < G) *reinterpret_cast<float2*>(ro + g1 * D + d0) = make_float2(o[m][1], o[m][3]);
+                }
+                if (r == 0) {
+                    if (g0 < G) *reinterpret_cast<float2*>(p.rec_ml + (rec * G + g0) * 2) = make_float2(m0, ls0);
+                    if (g1 < G) *reinterpret_cast<float2*>(p.rec_ml + (rec * G + g1) * 2) = make_float2(m1, ls1);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    fence_acq_rel_gpu();  // release: the record is visible before the count says so
+                    unsigned long long* cnt = p.done + bh;
+                    const uint32_t k = tagged_finish(cnt, atomicAdd(cnt, 1ull), p.nonce, 1);
+                    if (k == kTagGiveUp) flag_status(p.status, NVFP4KV_STATUS_TIMEOUT);
+                    if (k == static_cast<uint32_t>(gl - gf)) {  // every piece is in: merge here
+                        // acquire: the other pieces' records are read after their counts (the
+                        // CTA barrier before the merge carries this to every thread)
+                        fence_acq_rel_gpu();
+                        const int slot = atomicAdd(&pend_n, 1);
+                        pend[slot][0] = pair;
+                        pend[slot][1] = 0;
+                        pend[slot][2] = static_cast<int>(gf + bh);
+                        pend[slot][3] = gl - gf + 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();  // every lane is done reading the slot before it refills
+    }
+    cp_async_wait<0>();
+    __syncthreads();  // every warp's run is done: the rings are free for the merge
+    const int n_pend = pend_n;
+    for (int k = 0; k < n_pend;) {
+        const int m = merge_batch<D>(p, pend, k, n_pend, smem);
+        if (m == 0) {  // a pair whose records do not fit at once: by chunks
+            merge_pair<D>(p, pend[k][0], pend[k][1], pend[k][2], pend[k][3], smem);
+            ++k;
+        }
+        k += m;
+    }
+}
+
+// The runs of its own that every pair of S stages is cut into when there are `pairs` of them, or 0:
+// runs that cross pairs, as in the dense decode. A run that crosses pairs leaves two records, one of them in
+// the middle of its stream, so runs of a pair's own are taken wherever they are no longer (256 pairs of 32
+// stages 24.5 us against 25.7, of 16 stages 17.6 against 19.5, but of 128 stages 62.2 with one stage more
+// against 60.2). Pairs of up to 3 stages stay whole: a merge takes as long as the additional stages (of 2
+// stages 8.1 us, as two runs each 10.1).
+int even_runs(int64_t pairs, int64_t S, int64_t runs) {
+    if (pairs > runs) return 0;
+    if (S <= 3) return 1;
+    const int64_t W = (pairs * S + runs - 1) / runs;
+    const int64_t n = (S + W - 1) / W;
+    return n * pairs <= runs ? static_cast<int>(n) : 0;
+}
+
+template <int D>
+cudaError_t launch_sparse(const SparseParams& p, int64_t runs, cudaStream_t s) {
+    using G_ = Geo<D>;
+    cudaError_t e = cudaFuncSetAttribute(sparse_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         G_::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
+    e = launch_pdl(sparse_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS, static_cast<size_t>(G_::SMEM),
+                   s, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace nvfp4kv
