@@ -461,7 +461,7 @@ nvfp4kv_status nvfp4_kv_select_pages(
  * page table and a length for each (sequence, KV head) pair, shared by the pair's query heads.
  *   sel_page_table int32 [batch][H][max_sel_pages]
  *   sel_lens       int32 [batch][H] tokens of the pair's pages, 0 <= len <= max_sel_pages * T; every
- *                  page but the last is full. Table entries past ceil(len / T) are not read. A length
+ *                  page but the last is full. Table entries past ceil(len / T) do not matter. A length
  *                  of 0 gives out = 0 and lse = -inf, as does one outside the range (BAD_SEQ_LEN)
  *   workspace      device scratch of nvfp4_paged_sparse_decode_workspace_size(...) bytes; needs no
  *                  clearing, and calls that can overlap on the GPU must not share it

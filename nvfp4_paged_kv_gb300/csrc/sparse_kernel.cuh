@@ -59,6 +59,55 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     auto len_of = [&](int b) {
         return b == b_lo ? kept0 : (b == b_lo + 1 ? kept1 : __ldg(p.seq_lens + b));
     };
+
+    // ------------------------------------------------ the even partition, while the lengths are on their way
+    // When every pair has all its pages, each is cut into full_runs runs of its own, whatever the lengths
+    // say beyond that. So every warp starts on that run, with the loads of its pair's length and page ids and
+    // its CTA's queries, and drops it if a pair turns out shorter.
+    const int num_runs = p.num_runs;
+    const int cta0 = blockIdx.x * NW, cta_runs = max(0, min(num_runs - cta0, NW));
+    // this CTA's runs of R: those k whose place k num_runs / R is one of its warps (fewer runs than warps are
+    // spread over the CTAs: 512 stages on 43 of the 152 SMs took 14.8 us, spread over all 11.4)
+    auto first_run = [&](int R) { return min(R, (cta0 * R + num_runs - 1) / num_runs); };
+    auto end_run = [&](int R) { return min(R, ((cta0 + cta_runs) * R + num_runs - 1) / num_runs); };
+    const uint32_t smem_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    const uint32_t qcache = smem_base + G_::Q_OFF;
+    auto load_window = [&](int b_, int base) -> int {
+        const int i = base + lane;
+        return (i < p.max_pages) ? __ldg(p.page_table + static_cast<int64_t>(b_) * p.max_pages + i)
+                                 : -1;
+    };
+    int gw0 = 0, n_runs_cta = 0;
+    int q_first = 0, q_cached = 0;
+    auto copy_queries = [&]() {
+        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
+        const int nq = q_cached * G * D * 2 / 16;
+        for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
+        cp_async_commit();
+    };
+    int e_pair = 0, e_run0 = 0, e_lo = 0, e_hi = 0, e_len = 0;
+    int prow = -1, pbase = 0, pwin = 0;  // page-id window loaded ahead, see below
+    if (p.full_runs > 0) {
+        gw0 = first_run(p.B * p.full_runs);
+        n_runs_cta = end_run(p.B * p.full_runs) - gw0;
+        if (n_runs_cta > 0) {
+            q_first = gw0 / p.full_runs;
+            q_cached = min((gw0 + n_runs_cta - 1) / p.full_runs - q_first + 1, G_::QCACHE / (G * D * 2));
+        }
+        if (warp < n_runs_cta) {
+            e_pair = (gw0 + warp) / p.full_runs;
+            e_run0 = e_pair * p.full_runs;
+            const int at = gw0 + warp - e_run0;
+            e_lo = at * p.full_each / p.full_runs;
+            e_hi = (at + 1) * p.full_each / p.full_runs;
+            e_len = __ldg(p.seq_lens + e_pair);
+            prow = e_pair;
+            pbase = static_cast<int>(__umul64hi(static_cast<uint64_t>(e_lo) * TOK, p.t_magic)) & ~31;
+            pwin = load_window(prow, pbase);
+        }
+        copy_queries();
+    }
+
     int local = 0;
     for (int b = b_lo; b < b_hi; ++b) {
         const int L = len_of(b);
@@ -82,14 +131,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         if (w < warp) excl += scan_warp[w];
         total += scan_warp[w];
     }
-    // warp run gw takes [gw W, gw W + W) of the stage list, or, when every pair has all its pages, each pair
-    // is cut into full_runs runs of its own (`even`). Fewer runs than warps are spread over the CTAs (512
-    // stages on 43 of the 152 SMs took 14.8 us, spread over all 11.4).
-    const int num_runs = p.num_runs;
+    // otherwise warp run gw takes [gw W, gw W + W) of the stage list
     const int W = max(1, (total + num_runs - 1) / num_runs);
     const bool even = total == p.full_stages && p.full_runs > 0;
     const int Wr = even ? 1 : W;
-    const int R = even ? p.B * p.full_runs : (total + W - 1) / W;
     if (blockIdx.x == 0) {
         // pairs without stages (length 0 or invalid): output 0, LSE -inf, a warp per pair
         for (int j = 0; j < C; ++j) {
@@ -104,70 +149,47 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
             }
         }
     }
-    // One walk over this thread's pairs finds the pair holding each of the CTA's run
-    // starts and its two span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
-    int gw0 = blockIdx.x * NW;
-    int n_runs_cta = max(0, min(num_runs - gw0, NW));
-    {
-        // the runs k whose place k num_runs / R is one of this CTA's
-        const int k_end = min(R, ((gw0 + n_runs_cta) * R + num_runs - 1) / num_runs);
-        gw0 = min(k_end, (gw0 * R + num_runs - 1) / num_runs);
-        n_runs_cta = k_end - gw0;
-    }
-    const int span_lo = (n_runs_cta > 0 && gw0 < R) ? gw0 * W : total;
-    const int span_hi = min(total, (gw0 + n_runs_cta) * W);
-    if (even) {
-        if (tid == 0 && n_runs_cta > 0) {
-            span_pair[0] = gw0 / p.full_runs;
-            span_pair[1] = (gw0 + n_runs_cta - 1) / p.full_runs;
-        }
-    } else if (local > 0 && span_lo < span_hi && span_lo < excl + local && span_hi > excl) {
-        int acc = excl;
-        for (int b = b_lo; b < b_hi && acc < span_hi; ++b) {
-            const int L = len_of(b);
-            const int S = seq_stages(L, max_tokens, TOK);
-            const int n = S;
-            if (n > 0 && acc + n > span_lo) {
-                // runs of this CTA starting in [acc, acc + n): w in [w_a, w_b)
-                const int w_a = max(0, (acc - gw0 * W + W - 1) / W);
-                const int w_b = min(n_runs_cta, (acc + n - gw0 * W + W - 1) / W);
-                for (int w = w_a; w < w_b; ++w) {
-                    start_bp[w][0] = b;
-                    start_bp[w][1] = acc;
-                    start_bp[w][2] = L;
+    if (!even) {
+        // One walk over this thread's pairs finds the pair holding each of the CTA's run starts and its two
+        // span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
+        const int R = (total + W - 1) / W;
+        gw0 = first_run(R);
+        n_runs_cta = end_run(R) - gw0;
+        const int span_lo = (n_runs_cta > 0 && gw0 < R) ? gw0 * W : total;
+        const int span_hi = min(total, (gw0 + n_runs_cta) * W);
+        if (local > 0 && span_lo < span_hi && span_lo < excl + local && span_hi > excl) {
+            int acc = excl;
+            for (int b = b_lo; b < b_hi && acc < span_hi; ++b) {
+                const int L = len_of(b);
+                const int n = seq_stages(L, max_tokens, TOK);
+                if (n > 0 && acc + n > span_lo) {
+                    // runs of this CTA starting in [acc, acc + n): w in [w_a, w_b)
+                    const int w_a = max(0, (acc - gw0 * W + W - 1) / W);
+                    const int w_b = min(n_runs_cta, (acc + n - gw0 * W + W - 1) / W);
+                    for (int w = w_a; w < w_b; ++w) {
+                        start_bp[w][0] = b;
+                        start_bp[w][1] = acc;
+                        start_bp[w][2] = L;
+                    }
+                    if (span_lo >= acc && span_lo < acc + n) span_pair[0] = b;
+                    if (span_hi - 1 >= acc && span_hi - 1 < acc + n)
+                        span_pair[1] = b;
                 }
-                if (span_lo >= acc && span_lo < acc + n) span_pair[0] = b;
-                if (span_hi - 1 >= acc && span_hi - 1 < acc + n)
-                    span_pair[1] = b;
+                acc += n;
             }
-            acc += n;
         }
-    }
-    __syncthreads();
-
-    // ------------------------------------------------ queries of the CTA's pairs
-    const uint32_t smem_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    const uint32_t qcache = smem_base + G_::Q_OFF;
-    const int q_first = span_pair[0];
-    const int q_cached = (even ? n_runs_cta > 0 : span_lo < span_hi)
-                             ? min(span_pair[1] - span_pair[0] + 1, G_::QCACHE / (G * D * 2))
-                             : 0;
-    {
-        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
-        const int nq = q_cached * G * D * 2 / 16;
-        for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
-        cp_async_commit();
+        cp_async_wait<0>();  // the queries copied ahead, before others take their place
+        __syncthreads();
+        q_first = span_pair[0];
+        q_cached = span_lo < span_hi ? min(span_pair[1] - span_pair[0] + 1, G_::QCACHE / (G * D * 2)) : 0;
+        prow = -1;
+        copy_queries();
     }
 
     const int gw = gw0 + warp;
     const int64_t s_begin64 = static_cast<int64_t>(gw) * W;
     const bool has_run = warp < n_runs_cta && (even || s_begin64 < total);
     const int s_begin = has_run ? static_cast<int>(s_begin64) : 0;
-    // even: the run's pair, its first run, its place among the pair's runs, its first stage and the one after
-    const int e_pair = even && has_run ? gw / p.full_runs : 0;
-    const int e_run0 = e_pair * p.full_runs, e_at = gw - e_run0;
-    const int e_lo = even && has_run ? e_at * p.full_each / p.full_runs : 0;
-    const int e_hi = even && has_run ? (e_at + 1) * p.full_each / p.full_runs : 0;
     const int n_st = has_run ? (even ? e_hi - e_lo : min(total - s_begin, W)) : 0;
 
     // ------------------------------------------------ per-lane constants
@@ -184,7 +206,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
 
     // ------------------------------------------------ issue side: the walk over the run
     int ib = has_run ? (even ? e_pair : start_bp[warp][0]) : 0;
-    int ilen = has_run ? (even ? __ldg(p.seq_lens + e_pair) : start_bp[warp][2]) : 0;
+    int ilen = has_run ? (even ? e_len : start_bp[warp][2]) : 0;
     int iS = has_run ? seq_stages(ilen, max_tokens, TOK) : 1;
     int ij = has_run ? (even ? e_lo : s_begin - start_bp[warp][1]) : 0;
     // flat index of stage 0 of pair ib; even: the pair's first run
@@ -195,12 +217,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     // page-id windows: lane l holds the id of page base + l of a pair's page-table row; the
     // window after the current one (in issue order) is loaded when the current one is taken
     int wrow = -1, wbase = 0, win = 0;
-    int prow = -1, pbase = 0, pwin = 0;
-    auto load_window = [&](int b_, int base) -> int {
-        const int i = base + lane;
-        return (i < p.max_pages) ? __ldg(p.page_table + static_cast<int64_t>(b_) * p.max_pages + i)
-                                 : -1;
-    };
     // make the window holding page pidx of pair ib current (its loads are only issued) and
     // start loading the one after it
     auto set_window = [&](int pidx) {
@@ -689,7 +705,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
 // against 60.2). Pairs of up to 3 stages stay whole: a merge takes as long as the additional stages (of 2
 // stages 8.1 us, as two runs each 10.1).
 int even_runs(int64_t pairs, int64_t S, int64_t runs) {
-    if (pairs > runs) return 0;
+    if (pairs > runs || S * runs > INT32_MAX) return 0;
     if (S <= 3) return 1;
     const int64_t W = (pairs * S + runs - 1) / runs;
     const int64_t n = (S + W - 1) / W;
