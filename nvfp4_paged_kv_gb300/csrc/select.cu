@@ -16,9 +16,11 @@
 // selection is the same bit for bit whatever the split of the work: the reason for integer bounds
 // and integer queries, which also halve the bytes of 16-bit bounds.
 //
-// Bounds kernel: 4096 pages of 64 tokens x 8 heads x 128 (160 MB) take 38.9 us, 4.1 TB/s, bound by the
-// ALU pipe (conversions of two codes each and the maxima: 71 % busy), which has 3.3 operations per pair
-// of values where HBM would leave time for 3.5. The selection's bytes are few (2 D + 4 per scored page
+// Bounds kernel: 4096 pages of 64 tokens x 8 heads x 128 (160 MB) take 37.0 us, 4.3 TB/s, bound by the
+// conversions of two codes each, the products and the maxima: without any one of the three kinds it would be
+// 2 to 3 us less (with the walk's 64-bit divisions and a ceil by conversions it was 38.9). Halves as large in
+// flight for 32 warps an SM took 39 to 40, three slots 40, a grid of one wave 39.3.
+// Selection kernel: its bytes are few (2 D + 4 per scored page
 // and head) and its time is latency: 256 pairs of 128 pages (9 MB) 6.0 us, 64 pairs of up to 2048 pages
 // (22 MB) 12.4 us, of which 2 us until the queries are integers, 3 to 5 us of scores, 3 us of radix passes
 // and 1.5 us of writing the tables.
@@ -78,7 +80,6 @@ struct BoundsParams {
     float* scales;
     int32_t* status;
     int32_t pool_pages, num_pages, H, T;
-    int64_t items;
 };
 
 // Maxima over the lanes that differ in the bits OFF, OFF / 2, .. LAST: with each bit a lane gives half of
@@ -112,31 +113,41 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
     __shared__ __align__(16) uint8_t ring[kBoundsThreads / 32][2][kBoundsChunk];
     const int lane = threadIdx.x & 31;
     const int l = lane % LPR, rr = lane / LPR;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (kBoundsThreads / 32);
     uint8_t(*slots)[kBoundsChunk] = ring[threadIdx.x >> 5];
 
     // the walk over the warp's chunks, one ahead of the reduction; the ids of the item after are
-    // loaded while an item is walked
-    int64_t item = static_cast<int64_t>(blockIdx.x) * (kBoundsThreads / 32) + (threadIdx.x >> 5) - step;
+    // loaded while an item is walked. An item is a place in the list and a head, kept apart: one 64-bit
+    // division for each item's place would cost as much as a quarter of its values
+    const uint32_t H = static_cast<uint32_t>(p.H);
+    const uint32_t first = blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t step = gridDim.x * (kBoundsThreads / 32), step_i = step / H, step_h = step % H;
+    uint32_t next_i = first / H, next_h = first % H;  // of the item after
+    int id_page = -1, id_n = 0;
     int64_t ph = 0;                    // page * H + head of the item
     int n = 0, t0 = 0;                 // its tokens, first token of the chunk
-    int id_page = -1, id_n = 0;        // of the item after
-    auto load_ids = [&](int64_t it) {
-        if (it >= p.items) return;
-        const int i = static_cast<int>(it / p.H);
-        id_page = p.page_ids ? __ldg(p.page_ids + i) : i;
-        id_n = p.page_tokens ? __ldg(p.page_tokens + i) : p.T;
+    auto load_ids = [&]() {
+        if (next_i >= static_cast<uint32_t>(p.num_pages)) return;
+        id_page = p.page_ids ? __ldg(p.page_ids + next_i) : static_cast<int>(next_i);
+        id_n = p.page_tokens ? __ldg(p.page_tokens + next_i) : p.T;
     };
-    load_ids(item + step);
+    load_ids();
     auto advance = [&]() -> bool {  // to the next chunk; false: none left
-        t0 += CH;
-        if (t0 < n) return true;
+        if (n - t0 > CH) {
+            t0 += CH;
+            return true;
+        }
         for (;;) {
-            item += step;
-            if (item >= p.items) return false;
+            if (next_i >= static_cast<uint32_t>(p.num_pages)) return false;
             const int page = id_page;
+            const uint32_t head = next_h;
             n = id_n;
-            load_ids(item + step);
+            next_i += step_i;
+            next_h += step_h;
+            if (next_h >= H) {
+                next_h -= H;
+                ++next_i;
+            }
+            load_ids();
             if (page == -1) continue;
             if (page < 0 || page >= p.pool_pages || n < 0 || n > p.T) {
                 if (lane == 0)
@@ -144,7 +155,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
                                                                              : NVFP4KV_STATUS_BAD_SEQ_LEN);
                 continue;
             }
-            ph = static_cast<int64_t>(page) * p.H + item % p.H;
+            ph = static_cast<int64_t>(page) * p.H + head;
             t0 = 0;
             return true;
         }
@@ -173,7 +184,6 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
         }
     };
 
-    n = 0;
     bool more = advance();
     if (more) copy(slots[0]);
     cp_async_commit_group();
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
             }
         }
         __syncwarp();  // every lane is done with the slot before it refills
-        if (my_t0 + CH < my_n) continue;
+        if (my_n - my_t0 > CH) continue;
         // from here on the negated minima, so that both halves are maxima
 #pragma unroll
         for (int j = 16; j < 32; ++j) m[j] ^= 0x80008000u;
@@ -244,18 +254,22 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
         uint32_t w[(2 * KEEP + 3) / 4];
 #pragma unroll
         for (int k = 0; k < (2 * KEEP + 3) / 4; ++k) w[k] = 0u;
-        // ceil(fp32(y / s)) by a product with 1 / s, off by less than 2^-15 at 127; next to a whole number by
-        // the division itself, but for those past 126, which end at 127 either way (the largest value of
-        // the page always lies there). A non-zero s is at least 2^-17 (a at least 2^-10), so 1 / s is finite
+        // ceil(fp32(y / s)) by a product with 1 / s, off by less than 2^-15 at 127, as the whole number next to
+        // x + 1/2; where x is next to a whole number itself by the division, but for those past 126, which end
+        // at 127 either way (the largest value of the page always lies there). A non-zero s is at least 2^-17
+        // (a at least 2^-10), so 1 / s is finite. Sums with 1.5 2^23 leave the whole number in the low bits
         const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
+        const float sign = neg ? -1.0f : 1.0f;  // floor of a negated value is the negated ceil
+        constexpr float kWhole = 12582912.0f;
         bool open = false;
 #pragma unroll
         for (int k = 0; k < 2 * KEEP; ++k) {
-            const float x = y[k] * inv;
-            open = open || (fabsf(x - rintf(x)) < 1e-4f && x < 126.5f && y[k] != 0.0f);
-            // floor of a negated value is the negated ceil
-            const int c = static_cast<int>(fminf(127.0f, ceilf(x)));
-            w[k / 4] |= static_cast<uint32_t>((neg ? -c : c) & 0xFF) << (8 * (k % 4));
+            const float u = fminf(fmaf(y[k], inv, 0.5f), 127.4f);
+            const float t = fmaf(u, sign, kWhole);
+            const float d = fmaf(-sign, t - kWhole, u);
+            open = open || (fabsf(d) > 0.4999f && y[k] != 0.0f);
+            w[k / 4] = __byte_perm(w[k / 4], __float_as_uint(t), k % 4 == 0 ? 0x3214 : k % 4 == 1 ? 0x3240
+                                                                 : k % 4 == 2 ? 0x3410 : 0x4210);
         }
         if (open) {
 #pragma unroll
@@ -733,8 +747,8 @@ extern "C" nvfp4kv_status nvfp4_kv_page_bounds(
     p.num_pages = num_pages;
     p.H = layout->num_kv_heads;
     p.T = layout->page_size;
-    p.items = static_cast<int64_t>(num_pages) * p.H;
-    const int64_t ctas = (p.items + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
+    const int64_t items = static_cast<int64_t>(num_pages) * p.H;
+    const int64_t ctas = (items + kBoundsThreads / 32 - 1) / (kBoundsThreads / 32);
     const int64_t most = static_cast<int64_t>(num_sms()) * 32;
     const int grid = static_cast<int>(ctas < most ? ctas : most);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
