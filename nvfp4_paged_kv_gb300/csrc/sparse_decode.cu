@@ -74,20 +74,17 @@ extern "C" nvfp4kv_status nvfp4_paged_sparse_decode_attention(
     p.T = T;
     p.pool_pages = pool_pages;
     p.max_pages = max_sel_pages;
-    p.num_runs = static_cast<int32_t>(runs);
     p.pool_heads = H;
     const int64_t each = (static_cast<int64_t>(max_sel_pages) * T + stage_tokens(D) - 1) / stage_tokens(D);
-    p.full_stages = static_cast<int32_t>(pairs * each);  // (bounded by decode_size_ok)
-    p.full_each = static_cast<int32_t>(each);
-    p.full_runs = even_runs(pairs, each, runs);
+    p.full_each = static_cast<int32_t>(each);  // (pairs * each is bounded by decode_size_ok)
     p.sm_scale = sm_scale;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (D) {
-    case 64: e = launch_sparse<64>(p, runs, s); break;
-    case 128: e = launch_sparse<128>(p, runs, s); break;
-    default: e = launch_sparse<256>(p, runs, s); break;
+    case 64: e = launch_sparse<64>(p, s); break;
+    case 128: e = launch_sparse<128>(p, s); break;
+    default: e = launch_sparse<256>(p, s); break;
     }
     return e == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
 }

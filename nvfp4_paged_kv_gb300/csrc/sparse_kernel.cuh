@@ -12,18 +12,44 @@
 // on every warp, 32-token stages (14 to 16 warps, or more slots), tiles of a stage worked on two or one at a
 // time, and the scores of a stage interleaved with P V of the one before (one more iteration per run: 28.6 us).
 #pragma once
+#include <algorithm>
+#include <atomic>
+#include <cooperative_groups.h>
+
 #include "decode_kernel.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace nvfp4kv {
 namespace {
 
+constexpr int kMaxCluster = 8;
 constexpr int kMaxSparsePairs = 65535;  // (sequence, KV head) pairs of a call
+
+// Microseconds of a call, of both ways to cut it, from measurements at head_dim 64 to 256, 1 to 8 query heads a
+// pair, 8 to 1024 pairs of 1 to 128 pages of 64. Runs over all pairs: the stages of an SM, the records of the pair
+// that has most, and those that the SMs write. Pairs by clusters: rounds of a stage for each warp of the longest
+// pair. The sooner way was chosen in all but one in eight of the 420 cases, where it took up to XX % longer.
+struct Times {
+    float all_base, record;            // runs over all pairs: base, and for each record of a pair
+    float own_base, own_round, share;  // pairs by clusters: base, for each round, rounds for each stage
+    __host__ __device__ float all(float sm_stages, float records) const {
+        return all_base + fminf(9.2f + 0.37f * sm_stages, 13.0f + 0.237f * sm_stages) + record * records;
+    }
+    __host__ __device__ float own(int stages) const {
+        const float rounds = stages * share;
+        return own_base + own_round * (0.5f * (rounds + ceilf(rounds)));
+    }
+};
 
 // B: pairs, H: 1, Hq: query heads of a pair; seq_lens and page_table are those of the pairs.
 struct SparseParams : DecodeParams {
     int32_t pool_heads;  // KV heads of a page in the pools
-    // when every pair has all its pages: stages of all pairs, and of one, and its runs (0: runs cross pairs)
-    int32_t full_stages, full_each, full_runs;
+    // pairs by clusters of CTAs, where that is no longer than runs over all pairs: clusters with pairs (0:
+    // never) and the stages of a pair that has all its pages
+    int32_t clusters, full_each;
+    float per_cta;  // 1 / CTAs
+    Times times;
 };
 
 template <int D>
@@ -39,6 +65,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     __shared__ int span_pair[2];     // first and last pair the CTA's runs touch
     __shared__ int pend_n;           // pairs whose last piece finished in this CTA ...
     __shared__ int pend[2 * NW][4];  // ... (b, h, first record, records): merged at the end
+    __shared__ int most_warp[NW];    // stages of the longest pair of each warp's lengths
+    __shared__ int pair_len[NW];     // lengths of the cluster's pairs
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -48,10 +76,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     const int G = p.G, T = p.T;
     const int max_tokens = p.max_pages * T;
 
-    // ------------------------------------------------ stage prefix over the pairs
-    // Thread t owns pairs [t C, t C + C); PS_b = sum_{b' < b} stages(b').
-    // The first two lengths stay in registers for the walk below (a second load of the same
-    // words would cost another round trip at the start).
+    // ------------------------------------------------ lengths
+    // Thread t owns pairs [t C, t C + C). The first two lengths stay in registers for the walk below (a second
+    // load of the same words would cost another round trip at the start).
     const int C = (p.B + NT - 1) / NT;
     const int b_lo = min(p.B, tid * C), b_hi = min(p.B, b_lo + C);
     const int kept0 = (b_lo < b_hi) ? __ldg(p.seq_lens + b_lo) : 0;
@@ -60,14 +87,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         return b == b_lo ? kept0 : (b == b_lo + 1 ? kept1 : __ldg(p.seq_lens + b));
     };
 
-    // ------------------------------------------------ the even partition, while the lengths are on their way
-    // When every pair has all its pages, each is cut into full_runs runs of its own, whatever the lengths
-    // say beyond that. So every warp starts on that run, with the loads of its pair's length and page ids and
-    // its CTA's queries, and drops it if a pair turns out shorter.
+    // ------------------------------------------------ pairs by clusters, while the lengths are on their way
+    // A cluster of CTAs holds pairs of its own, and each of its warps a run of one pair; the runs are merged
+    // through shared memory. Every warp starts on that run, with the loads of its pair's length and page ids
+    // and its CTA's queries, and drops it if the lengths ask for runs over all pairs.
     const int num_runs = p.num_runs;
     const int cta0 = blockIdx.x * NW, cta_runs = max(0, min(num_runs - cta0, NW));
-    // this CTA's runs of R: those k whose place k num_runs / R is one of its warps (fewer runs than warps are
-    // spread over the CTAs: 512 stages on 43 of the 152 SMs took 14.8 us, spread over all 11.4)
+    // this CTA's runs of R over all pairs: those k whose place k num_runs / R is one of its warps (fewer runs
+    // than warps are spread over the CTAs: 512 stages on 43 of the 152 SMs took 14.8 us, spread over all 11.4)
     auto first_run = [&](int R) { return min(R, (cta0 * R + num_runs - 1) / num_runs); };
     auto end_run = [&](int R) { return min(R, ((cta0 + cta_runs) * R + num_runs - 1) / num_runs); };
     const uint32_t smem_base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
@@ -77,7 +104,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         return (i < p.max_pages) ? __ldg(p.page_table + static_cast<int64_t>(b_) * p.max_pages + i)
                                  : -1;
     };
-    int gw0 = 0, n_runs_cta = 0;
     int q_first = 0, q_cached = 0;
     auto copy_queries = [&]() {
         const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
@@ -85,43 +111,62 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
         cp_async_commit();
     };
-    int e_pair = 0, e_run0 = 0, e_lo = 0, e_hi = 0, e_len = 0;
-    int prow = -1, pbase = 0, pwin = 0;  // page-id window loaded ahead, see below
-    if (p.full_runs > 0) {
-        gw0 = first_run(p.B * p.full_runs);
-        n_runs_cta = end_run(p.B * p.full_runs) - gw0;
-        if (n_runs_cta > 0) {
-            q_first = gw0 / p.full_runs;
-            q_cached = min((gw0 + n_runs_cta - 1) / p.full_runs - q_first + 1, G_::QCACHE / (G * D * 2));
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = static_cast<int>(cluster.num_blocks());
+    const int rank = static_cast<int>(cluster.block_rank());
+    // pairs [c_lo, c_lo + c_pairs), several only in a cluster of one CTA, with c_warps warps each. Warps are dealt
+    // to the pairs in turn, counted across the CTAs of a cluster first, so that few runs lie in different CTAs and
+    // quarters of an SM (dealt in blocks, 3 or 4 pairs of one page an SM took 7.8 to 8 us, so 6.6 to 7)
+    int c_lo = 0, c_pairs = 0, c_warps = 0;
+    int e_pair = 0, e_at = 0, e_len = 0;  // the warp's pair, its place there, the pair's length
+    int prow = -1, pbase = 0, pwin = 0;   // page-id window loaded ahead, see below
+    if (p.clusters > 0) {
+        const int cl = blockIdx.x / CS;
+        if (cl < p.clusters) {
+            c_lo = cl * p.B / p.clusters;
+            c_pairs = (cl + 1) * p.B / p.clusters - c_lo;
         }
-        if (warp < n_runs_cta) {
-            e_pair = (gw0 + warp) / p.full_runs;
-            e_run0 = e_pair * p.full_runs;
-            const int at = gw0 + warp - e_run0;
-            e_lo = at * p.full_each / p.full_runs;
-            e_hi = (at + 1) * p.full_each / p.full_runs;
+        if (c_pairs > 0) {
+            const int at = warp * CS + rank;
+            e_at = at / c_pairs;
+            e_pair = c_lo + at - e_at * c_pairs;
+            c_warps = CS * NW / c_pairs;
             e_len = __ldg(p.seq_lens + e_pair);
-            prow = e_pair;
-            pbase = static_cast<int>(__umul64hi(static_cast<uint64_t>(e_lo) * TOK, p.t_magic)) & ~31;
-            pwin = load_window(prow, pbase);
+            const int n = min(c_warps, p.full_each);
+            if (e_at < n) {
+                prow = e_pair;
+                pbase = static_cast<int>(__umul64hi(static_cast<uint64_t>(e_at * p.full_each / n) * TOK,
+                                                    p.t_magic)) & ~31;
+                pwin = load_window(prow, pbase);
+            }
+            q_first = c_lo;
+            q_cached = min(c_pairs, G_::QCACHE / (G * D * 2));
         }
+        if (tid < c_pairs) pair_len[tid] = __ldg(p.seq_lens + c_lo + tid);
         copy_queries();
     }
 
-    int local = 0;
+    // ------------------------------------------------ stage prefix over the pairs
+    int local = 0, most = 0;  // stages of this thread's pairs, and of the longest
     for (int b = b_lo; b < b_hi; ++b) {
         const int L = len_of(b);
         if (blockIdx.x == 0 && (L < 0 || L > max_tokens))
             flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
-        local += seq_stages(L, max_tokens, TOK);
+        const int n = seq_stages(L, max_tokens, TOK);
+        local += n;
+        most = max(most, n);
     }
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= o) incl += v;
     }
-    if (lane == 31) scan_warp[warp] = incl;
+    if (lane == 31) {
+        scan_warp[warp] = incl;
+        most_warp[warp] = most;
+    }
     if (tid < 2) span_pair[tid] = 0;
     if (tid == 0) pend_n = 0;
     __syncthreads();
@@ -130,11 +175,13 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     for (int w = 0; w < NW; ++w) {
         if (w < warp) excl += scan_warp[w];
         total += scan_warp[w];
+        most = max(most, most_warp[w]);
     }
-    // otherwise warp run gw takes [gw W, gw W + W) of the stage list
+    // pairs by clusters, or runs over all pairs: warp run gw takes [gw W, gw W + W) of the stage list
     const int W = max(1, (total + num_runs - 1) / num_runs);
-    const bool even = total == p.full_stages && p.full_runs > 0;
-    const int Wr = even ? 1 : W;
+    const bool own = p.clusters > 0 &&
+                     p.times.own(most) <= p.times.all(total * p.per_cta, __fdividef(most, W));
+    int gw0 = 0, n_runs_cta = 0;
     if (blockIdx.x == 0) {
         // pairs without stages (length 0 or invalid): output 0, LSE -inf, a warp per pair
         for (int j = 0; j < C; ++j) {
@@ -149,7 +196,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
             }
         }
     }
-    if (!even) {
+    if (!own) {
         // One walk over this thread's pairs finds the pair holding each of the CTA's run starts and its two
         // span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
         const int R = (total + W - 1) / W;
@@ -187,10 +234,29 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     }
 
     const int gw = gw0 + warp;
-    const int64_t s_begin64 = static_cast<int64_t>(gw) * W;
-    const bool has_run = warp < n_runs_cta && (even || s_begin64 < total);
-    const int s_begin = has_run ? static_cast<int>(s_begin64) : 0;
-    const int n_st = has_run ? (even ? e_hi - e_lo : min(total - s_begin, W)) : 0;
+    int ib = 0, ilen = 0, iS = 1, ij = 0;  // pair of the next stage to issue, its length and stages; the stage
+    int ips = 0, nlen = 0;                 // flat index of stage 0 of pair ib, length of the next (unless own)
+    int n_st = 0;                          // stages of the run
+    bool whole = false;                    // the run is its pair
+    if (own) {
+        const int S = seq_stages(e_len, max_tokens, TOK), n = min(c_warps, S);
+        if (e_at < n) {
+            ib = e_pair;
+            ilen = e_len;
+            iS = S;
+            ij = e_at * S / n;
+            n_st = (e_at + 1) * S / n - ij;
+            whole = n == 1;
+        }
+    } else if (warp < n_runs_cta && static_cast<int64_t>(gw) * W < total) {
+        ib = start_bp[warp][0];
+        ilen = start_bp[warp][2];
+        iS = seq_stages(ilen, max_tokens, TOK);
+        ips = start_bp[warp][1];
+        ij = gw * W - ips;
+        n_st = min(total - gw * W, W);
+        nlen = ib + 1 < p.B ? __ldg(p.seq_lens + ib + 1) : 0;
+    }
 
     // ------------------------------------------------ per-lane constants
     const uint32_t ring = smem_base + warp * G_::RING;
@@ -205,15 +271,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     const int rho = (r >> 1) | ((r & 1) << 2);  // V rows of this lane: chunk rho of a pair row
 
     // ------------------------------------------------ issue side: the walk over the run
-    int ib = has_run ? (even ? e_pair : start_bp[warp][0]) : 0;
-    int ilen = has_run ? (even ? e_len : start_bp[warp][2]) : 0;
-    int iS = has_run ? seq_stages(ilen, max_tokens, TOK) : 1;
-    int ij = has_run ? (even ? e_lo : s_begin - start_bp[warp][1]) : 0;
-    // flat index of stage 0 of pair ib; even: the pair's first run
-    int ips = has_run ? (even ? e_run0 : start_bp[warp][1]) : 0;
     bool ifirst = true;                     // the next stage to issue starts a piece
     int issued = 0;
-    int nlen = (has_run && !even && ib + 1 < p.B) ? __ldg(p.seq_lens + ib + 1) : 0;  // next pair
     // page-id windows: lane l holds the id of page base + l of a pair's page-table row; the
     // window after the current one (in issue order) is loaded when the current one is taken
     int wrow = -1, wbase = 0, win = 0;
@@ -326,8 +385,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         if (lane == 0) {
             sts_v4(slot + G_::HDR_OFF, okbits | (static_cast<uint32_t>(nval) << 8), flags,
                    static_cast<uint32_t>(ib), 0u);
-            sts_v4(slot + G_::HDR_OFF + 16, static_cast<uint32_t>(ips),
-                   static_cast<uint32_t>(even ? p.full_runs : iS), 0u, 0u);
+            sts_v4(slot + G_::HDR_OFF + 16, static_cast<uint32_t>(ips), static_cast<uint32_t>(iS), 0u, 0u);
         }
         // advance the walk
         ++issued;
@@ -616,7 +674,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
             }
         }
 
-        if (flags & kLast) {
+        if ((flags & kLast) && (!own || whole)) {
             // ---- end of a piece: the whole pair (outputs) or a record
             uint32_t h2[4];
             lds_words(h2, st + G_::HDR_OFF + 16);
@@ -629,9 +687,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
                 ls1 += __shfl_xor_sync(0xFFFFFFFFu, ls1, off);
             }
             const int g0 = 2 * c, g1 = 2 * c + 1;
-            const int gf = pps / Wr, gl = (pps + pS - 1) / Wr;  // the pair's first and last run
+            const int gf = pps / W, gl = (pps + pS - 1) / W;  // the pair's first and last run
             const int64_t bh = pair;
-            if (gf == gl) {
+            if (whole || gf == gl) {
                 // the whole pair is this piece: normalise and write the output directly
                 uint16_t* ob = p.out + bh * G * D;
                 const float f0 = ls0 > 0.0f ? gvs / ls0 : 0.0f;
@@ -686,6 +744,114 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         __syncwarp();  // every lane is done reading the slot before it refills
     }
     cp_async_wait<0>();
+    if (own) {
+        // ---- merge of a cluster's pairs. A warp leaves its run in its own ring, as its lanes have it: four outputs
+        // (heads 2c, 2c + 1 of two dims) per lane and 16 dims, behind them (max, sum) of heads 2c, 2c + 1. The runs
+        // of a pair in this CTA become the output, or, in a cluster of several CTAs, one record like theirs in the
+        // second slot of the first ring, joined with those of the other CTAs. (As [G][D] the lanes of a store would
+        // share a bank: 8 pairs of 64 pages 10.4 us against 9.2, of 8 heads of 256 24.6 against about 12.)
+        //
+        // Runs of the cluster's pair j to be merged: one alone has written the outputs itself, and a pair without
+        // any is the first CTA's.
+        auto runs_of = [&](int j) {
+            const int n = min(c_warps, seq_stages(pair_len[j], max_tokens, TOK));
+            return n > 1 ? n : 0;
+        };
+        int any = 0;
+        for (int j = 0; j < c_pairs; ++j) any |= runs_of(j);
+        if (any == 0) return;  // (the same in all CTAs of the cluster)
+        constexpr int ML = G_::KSTEPS * 32;  // float4 of a record before the maxima and sums
+        static_assert(16 * (ML + 4) <= G_::SLOT, "a record in a slot");
+        auto record = [&](int w, int slot) {
+            return reinterpret_cast<float4*>(smem + w * G_::RING + slot * G_::SLOT);
+        };
+        if (n_st > 0 && !whole) {
+            float ls0 = l0, ls1 = l1;
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+                ls0 += __shfl_xor_sync(0xFFFFFFFFu, ls0, off);
+                ls1 += __shfl_xor_sync(0xFFFFFFFFu, ls1, off);
+            }
+            float4* rec = record(warp, 0);
+#pragma unroll
+            for (int m = 0; m < G_::KSTEPS; ++m) rec[32 * m + lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
+            if (r == 0) rec[ML + c] = make_float4(m0, ls0, m1, ls1);
+        }
+        __syncthreads();
+        // a column: the lane and 16 dims whose four outputs are joined
+        struct Column {
+            int m, r, c;
+            float m0, m1, l0, l1;
+            float4 o;
+        };
+        const int CC = (G + 1) / 2, columns = G_::KSTEPS * 8 * CC;
+        auto column = [&](int i) {
+            Column k;
+            k.m = i / (8 * CC);
+            const int at = i - k.m * 8 * CC;
+            k.r = at / CC;
+            k.c = at - k.r * CC;
+            k.m0 = k.m1 = -INFINITY;
+            k.l0 = k.l1 = 0.0f;
+            k.o = make_float4(0.f, 0.f, 0.f, 0.f);
+            return k;
+        };
+        auto raise = [](Column& k, const float4* rec) {
+            k.m0 = fmaxf(k.m0, rec[ML + k.c].x);
+            k.m1 = fmaxf(k.m1, rec[ML + k.c].z);
+        };
+        auto join = [](Column& k, const float4* rec) {
+            const float4 ml = rec[ML + k.c], v = rec[32 * k.m + 4 * k.r + k.c];
+            const float w0 = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - k.m0);
+            const float w1 = ml.z == -INFINITY ? 0.0f : exp2f(ml.z - k.m1);
+            k.l0 += w0 * ml.y;
+            k.l1 += w1 * ml.w;
+            k.o.x += w0 * v.x;
+            k.o.y += w1 * v.y;
+            k.o.z += w0 * v.z;
+            k.o.w += w1 * v.w;
+        };
+        const float gvs = __ldg(p.gv);
+        auto finish = [&](int j, const Column& k) {
+            const int64_t row = static_cast<int64_t>(c_lo + j) * G + 2 * k.c;
+            const int d0 = ((k.r >> 1) | ((k.r & 1) << 2)) * (D / 8) + 2 * k.m;
+            const float f0 = k.l0 > 0.0f ? gvs / k.l0 : 0.0f, f1 = k.l1 > 0.0f ? gvs / k.l1 : 0.0f;
+            *reinterpret_cast<uint32_t*>(p.out + row * D + d0) = pack_bf16x2(k.o.x * f0, k.o.z * f0);
+            if (2 * k.c + 1 < G)
+                *reinterpret_cast<uint32_t*>(p.out + (row + 1) * D + d0) = pack_bf16x2(k.o.y * f1, k.o.w * f1);
+            if (p.lse && k.m == 0 && k.r == 0) {
+                p.lse[row] = k.l0 > 0.0f ? (k.m0 + log2f(k.l0)) * 0.6931471805599453f : -INFINITY;
+                if (2 * k.c + 1 < G)
+                    p.lse[row + 1] = k.l1 > 0.0f ? (k.m1 + log2f(k.l1)) * 0.6931471805599453f : -INFINITY;
+            }
+        };
+        for (int it = tid; it < c_pairs * columns; it += NT) {
+            const int j = it / columns;
+            Column k = column(it - j * columns);
+            // in this CTA every (rank + i CS)-th run, of its warps j, j + c_pairs, ..
+            const int n = (runs_of(j) - rank + CS - 1) / CS;
+            if (n <= 0) continue;
+            for (int i = 0; i < n; ++i) raise(k, record(j + i * c_pairs, 0));
+            for (int i = 0; i < n; ++i) join(k, record(j + i * c_pairs, 0));
+            if (CS == 1) {
+                finish(j, k);
+            } else {
+                record(0, 1)[32 * k.m + 4 * k.r + k.c] = k.o;
+                if (k.m == 0 && k.r == 0) record(0, 1)[ML + k.c] = make_float4(k.m0, k.l0, k.m1, k.l1);
+            }
+        }
+        if (CS == 1) return;
+        cluster.sync();
+        const int n = min(CS, any);  // CTAs with a record of the cluster's one pair
+        for (int it = rank * NT + tid; it < columns; it += CS * NT) {
+            Column k = column(it);
+            for (int q = 0; q < n; ++q) raise(k, cluster.map_shared_rank(record(0, 1), q));
+            for (int q = 0; q < n; ++q) join(k, cluster.map_shared_rank(record(0, 1), q));
+            finish(0, k);
+        }
+        cluster.sync();  // the records stay until every CTA has read them
+        return;
+    }
     __syncthreads();  // every warp's run is done: the rings are free for the merge
     const int n_pend = pend_n;
     for (int k = 0; k < n_pend;) {
@@ -698,29 +864,103 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     }
 }
 
-// The runs of its own that every pair of S stages is cut into when there are `pairs` of them, or 0:
-// runs that cross pairs, as in the dense decode. A run that crosses pairs leaves two records, one of them in
-// the middle of its stream, so runs of a pair's own are taken wherever they are no longer (256 pairs of 32
-// stages 24.5 us against 25.7, of 16 stages 17.6 against 19.5, but of 128 stages 62.2 with one stage more
-// against 60.2). Pairs of up to 3 stages stay whole: a merge takes as long as the additional stages (of 2
-// stages 8.1 us, as two runs each 10.1).
-int even_runs(int64_t pairs, int64_t S, int64_t runs) {
-    if (pairs > runs || S * runs > INT32_MAX) return 0;
-    if (S <= 3) return 1;
-    const int64_t W = (pairs * S + runs - 1) / runs;
-    const int64_t n = (S + W - 1) / W;
-    return n * pairs <= runs ? static_cast<int>(n) : 0;
+// Pairs by clusters (see the kernel): CTAs of a cluster, clusters with pairs, clusters of the grid.
+struct ClusterPlan {
+    int size, with_pairs, grid;
+    Times times;
+};
+
+template <int D>
+int max_clusters(int size) {  // clusters that run at once
+    if (size == 1) return num_sms();
+    static std::atomic<int> known[64][3];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int>& n = known[dev][size == 2 ? 0 : size == 4 ? 1 : 2];
+    if (n.load() == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(num_sms() / size * size));
+        cfg.blockDim = dim3(Geo<D>::THREADS);
+        cfg.dynamicSmemBytes = Geo<D>::SMEM;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int v = 0;
+        if (cudaOccupancyMaxActiveClusters(&v, sparse_split_kernel<D>, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            v = -1;
+        }
+        n.store(v > 0 ? std::min(v, num_sms() / size) : -1);
+    }
+    return std::max(0, n.load());
+}
+
+// The clusters that take the least time when every pair has all its pages; single CTAs where runs over all pairs
+// take less, for calls whose pairs turn out shorter.
+template <int D>
+ClusterPlan choose_clusters(int64_t pairs, int64_t each, int G) {
+    constexpr int NW = Geo<D>::WARPS;
+    const int sms = num_sms();
+    const float record_kb = G * D * 4 / 1024.0f;
+    auto plan = [&](int size, int64_t with_pairs, int grid) {
+        const int64_t held = (pairs + with_pairs - 1) / with_pairs, warps = std::max<int64_t>(1, NW * size / held);
+        Times t;
+        t.all_base = std::max(0.0f, 0.15f * (NW * record_kb - 24.0f));
+        t.record = 0.012f + 0.016f * record_kb;
+        t.own_base = size == 1 ? 6.5f : size == 2 ? 7.2f : size == 4 ? 7.6f : 7.9f;
+        t.own_round = 1.35f + 0.13f * static_cast<float>(warps * held / size);
+        t.share = 1.0f / static_cast<float>(warps);
+        return ClusterPlan{size, held <= NW ? static_cast<int>(with_pairs) : 0, grid, t};
+    };
+    ClusterPlan best = plan(1, std::min<int64_t>(pairs, sms), sms);
+    if (each * NW * kMaxCluster > INT32_MAX) best.with_pairs = 0;  // (places of stages are 32-bit products)
+    if (best.with_pairs == 0) return best;
+    const int64_t runs = static_cast<int64_t>(sms) * NW, W = (pairs * each + runs - 1) / runs;
+    const float all = best.times.all(static_cast<float>(pairs * each) / sms, static_cast<float>(each) / W);
+    float least = std::min(all, best.times.own(static_cast<int>(each)));
+    for (int size = 2; size <= kMaxCluster && pairs * size <= sms; size *= 2) {
+        ClusterPlan c = plan(size, pairs, 0);
+        const float t = c.times.own(static_cast<int>(each));
+        if (t >= least) continue;
+        c.grid = max_clusters<D>(size);
+        if (pairs > c.grid) continue;
+        best = c;
+        least = t;
+    }
+    return best;
 }
 
 template <int D>
-cudaError_t launch_sparse(const SparseParams& p, int64_t runs, cudaStream_t s) {
+cudaError_t launch_sparse(SparseParams& p, cudaStream_t s) {
     using G_ = Geo<D>;
     cudaError_t e = cudaFuncSetAttribute(sparse_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          G_::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
-    e = launch_pdl(sparse_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS, static_cast<size_t>(G_::SMEM),
-                   s, p);
+    const ClusterPlan plan = choose_clusters<D>(p.B, p.full_each, p.G);
+    p.clusters = plan.with_pairs;
+    p.times = plan.times;
+    const int ctas = plan.grid * plan.size;
+    p.num_runs = ctas * G_::WARPS;
+    p.per_cta = 1.0f / ctas;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(G_::THREADS);
+    cfg.dynamicSmemBytes = G_::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.size);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = plan.size > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, sparse_split_kernel<D>, static_cast<const SparseParams&>(p));
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -348,6 +348,38 @@ def test_attention_of_few_and_many_pairs(kv, cuda, B, H, most, low):
     c.check(c.run(kv, q, table, lens), c.want(q, table, lens))
 
 
+@pytest.mark.parametrize("B,H,G,D,T,pages", [
+    (1, 8, 4, 128, 64, 64), (2, 4, 8, 256, 16, 70), (1, 5, 1, 64, 32, 300),   # clusters of 8 CTAs a pair
+    (4, 5, 3, 128, 16, 150), (8, 4, 8, 64, 64, 40),                            # of 4
+    (8, 8, 2, 128, 64, 30), (12, 5, 7, 256, 32, 33),                           # of 2
+    (40, 3, 5, 128, 16, 70), (40, 8, 4, 128, 64, 9), (110, 8, 1, 64, 16, 21),  # one CTA for 1, 2 or 3, and 6 pairs
+    (20, 8, 1, 64, 64, 64), (19, 8, 8, 128, 16, 90), (290, 8, 2, 256, 16, 3),  # runs over all pairs
+])
+@pytest.mark.parametrize("lengths", ["full", "ragged", "one long"])
+def test_attention_however_it_is_cut(kv, cuda, B, H, G, D, T, pages, lengths):
+    """The same result for every way to cut the pairs: all of full length, ragged with empty pairs, and one long
+    among short ones, each with some pages outside the pool."""
+    c = Cache(cuda, 50, H, T, D, B + pages)
+    full = torch.full((B, H), pages * T, dtype=torch.int32)
+    lens = full.clone()
+    if lengths != "full":
+        lens = torch.randint(0, pages * T + 1 if lengths == "ragged" else T + 2, (B, H), generator=c.g, dtype=torch.int32)
+        lens[B // 2, 0] = pages * T
+        lens[0, H - 1] = 0
+    q, table = queries(c, B, G), c.tables(B, pages, lens)
+    bad = torch.rand(table.shape, generator=c.g) < 0.02
+    table = torch.where(bad, 50, table)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    n = kv.nvfp4_paged_sparse_decode_workspace_size(kv.Layout(H, D, T), B, H * G, pages)
+    w = torch.full((n,), 0xFF, dtype=torch.uint8, device=cuda)
+    got = c.run(kv, q, table, lens, status, w)
+    c.check(got, c.want(q, table, lens))
+    read = bad & (torch.arange(pages) * T < lens[..., None])
+    assert status.item() == (kv.STATUS_PAGE_OOB if bool(read.any()) else 0)
+    again = c.run(kv, q, table, lens, status, w)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+
+
 def test_all_pairs_empty(kv, cuda):
     c = Cache(cuda, 4, 3, 16, 64, 0)
     lens = torch.zeros((2, 3), dtype=torch.int32)
