@@ -20,10 +20,9 @@
 // conversions of two codes each, the products and the maxima: without any one of the three kinds it would be
 // 2 to 3 us less (with the walk's 64-bit divisions and a ceil by conversions it was 38.9). Halves as large in
 // flight for 32 warps an SM took 39 to 40, three slots 40, a grid of one wave 39.3.
-// Selection kernel: its bytes are few (2 D + 4 per scored page
-// and head) and its time is latency: 256 pairs of 128 pages (9 MB) 6.0 us, 64 pairs of up to 2048 pages
-// (22 MB) 12.4 us, of which 2 us until the queries are integers, 3 to 5 us of scores, 3 us of radix passes
-// and 1.5 us of writing the tables.
+// Selection kernel: its bytes are few (2 D + 4 per scored page and head) and its time is latency: 256 pairs of 128
+// pages (9 MB) 6.0 us, 64 pairs of up to 2048 pages (22 MB) 12.5 us, of which 2 us until the queries are integers,
+// 3 to 5 us of scores, 3 us of radix passes and 1.5 us of writing the tables.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -296,10 +295,11 @@ __global__ void __launch_bounds__(kBoundsThreads) page_bounds_kernel(const Bound
 // pages on the tensor cores (FP16, whose mma.sync runs 8 times as often per clock as the int8 one on
 // this GPU; pages as M, the query group as N, head dims as K, once with the upper bounds and the
 // positive queries, once with the lower and the negative) and put the scores as sortable keys into the
-// shared memory of the cluster's first CTA, which then finds the smallest selected key by a radix selection that starts at the highest bit in which the keys differ and
-// stops when a bin is taken whole. (Counting ranks was no faster for few pages, 6.1 against 6.0 us for 256
-// pairs of 128, nor among the keys of the last bin, 12.9 against 12.3 us for 64 pairs of up to 2048: code
-// that runs once costs its fetch.) The selected pages are written in ascending order, equal keys from the lowest page on.
+// shared memory of the cluster's first CTA, which then finds the smallest selected key by a radix selection
+// that starts at the highest bit in which the keys differ and stops when a bin is taken whole. (Counting ranks
+// was no faster for few pages, 6.1 against 6.0 us for 256 pairs of 128, nor among the keys of the last bin, 12.9
+// against 12.3 us for 64 pairs of up to 2048: code that runs once costs its fetch.) The selected pages are written
+// in ascending order, equal keys from the lowest page on.
 // ------------------------------------------------------------------------------------------
 constexpr int kSelMaxGroup = 8;
 constexpr int kSelMaxCluster = 8;
@@ -691,8 +691,8 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
 template <int D, int NT>
 cudaError_t launch_select(const SelectParams& p, int cluster, size_t smem, cudaStream_t s) {
     if (smem > 36 * 1024) {  // with the static arrays, past the 48 KiB a launch may use by default
-        const cudaError_t e = cudaFuncSetAttribute(select_pages_kernel<D, NT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxPages / 32 * 136);
+        const cudaError_t e = cudaFuncSetAttribute(
+            select_pages_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelMaxPages / 32 * 136);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

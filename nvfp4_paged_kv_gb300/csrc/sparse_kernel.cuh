@@ -1,16 +1,26 @@
 // Split-KV decode attention over selected pages: every (sequence, KV head) pair has a page table and a length
-// of its own. The mathematics, packings, per-warp pipeline, records and merge are those of the dense decode
-// (decode_kernel.cuh, whose helpers this file uses); what differs is how the list of stages is cut into runs
-// and that the pairs stand where the dense decode has sequences. It is a kernel of its own because the dense
-// one loses 1 to 2 % to the additional cases, of its 60 and 120 us.
+// of its own. The mathematics, packings and per-warp pipeline are those of the dense decode (decode_kernel.cuh,
+// whose helpers this file uses); what differs is how the pairs' stages are cut into warp runs. It is a kernel of
+// its own because the dense one loses 1 to 2 % to the additional cases, of its 60 and 120 us.
 //
-// Bound: HBM in the steady state (6.45 TB/s from 32 to 128 pages per pair), but the calls are short: of 24.7 us
-// for 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) the lengths, the stage prefix, the page ids
-// and the first stage take 5.6 us, the end of the last runs and the merge of their records 4 us. 64 pairs of
-// 8192 tokens with 8 query heads each take 27.6 us (26 records of 4 KB per pair to merge), 8 pairs of 4096
-// tokens 11.3 us. Measured against it and slower: one combined record per CTA and pair, runs of unequal length
-// on every warp, 32-token stages (14 to 16 warps, or more slots), tiles of a stage worked on two or one at a
-// time, and the scores of a stage interleaved with P V of the one before (one more iteration per run: 28.6 us).
+// The cut. The selection makes all pairs of about one length, and the calls are short, so the join of a pair's
+// runs counts: through records in global memory (a fence, a count, a last arrival that loads them all) it takes 4
+// to 5 us. Pairs by clusters avoid it: a cluster of 1, 2, 4 or 8 CTAs holds a few pairs, or one, and joins their
+// runs through its shared memory. But its SMs hold whole pairs (256 pairs are 2 on 104 of 152 SMs and 1 on the
+// others), so long pairs, and pairs of very different lengths, are cut as in the dense decode: runs of equal
+// length over all pairs and SMs. Both ways' times are estimated from the lengths (Times), on the host for the size
+// of the cluster, in the kernel for the cut. Against runs over all pairs (head_dim 128, 4 heads): 64 pairs of 32
+// pages 12.2 us, so 13.6; 256 pairs of 4 pages 7.7 and 11.1, of 16 pages 15.9 and 19.2, of 32 pages 24.2 and 26.3,
+// of 64 pages 39.4 and 37.7.
+//
+// Bound: an SM's rate. A stage (9216 bytes) takes it 0.24 us, with 12 warps at 293 instructions per 16-token tile
+// (39 GB/s each: 5.9 TB/s on all SMs, 0.87 of the copy peak), alone as well as with all others and with K and V in
+// L2. 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) take 24.2 us: 6 until the first stages are
+// computed, 64 stages on the fuller SMs, 1 for the join. 64 pairs of 8192 tokens with 8 heads, on clusters of 2,
+// 24.9 us; 8 pairs of 4096 tokens, on clusters of 8, 9.3 us; 95 ragged pairs with head_dim 256 24.2 us. Measured
+// and slower: one combined record per CTA and pair, runs of unequal length on every warp, 32-token stages (14 to 16
+// warps, or more slots), tiles of a stage worked on two or one at a time, the scores of a stage interleaved with
+// P V of the one before, and the first stage issued before the lengths are compared (no gain).
 #pragma once
 #include <algorithm>
 #include <atomic>
@@ -26,10 +36,10 @@ namespace {
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSparsePairs = 65535;  // (sequence, KV head) pairs of a call
 
-// Microseconds of a call, of both ways to cut it, from measurements at head_dim 64 to 256, 1 to 8 query heads a
-// pair, 8 to 1024 pairs of 1 to 128 pages of 64. Runs over all pairs: the stages of an SM, the records of the pair
-// that has most, and those that the SMs write. Pairs by clusters: rounds of a stage for each warp of the longest
-// pair. The sooner way was chosen in all but one in eight of the 420 cases, where it took up to XX % longer.
+// Microseconds of a call, of both ways to cut it, fitted to measurements of 539 calls (head_dim 64 to 256, 1 to 8
+// heads a pair, 8 to 1024 pairs of 1 to 128 pages of 64 tokens). Runs over all pairs: the stages of an SM, the
+// records of the pair that has most, and those that an SM's warps write. Pairs by clusters: rounds of one stage for
+// each warp of the longest pair. The cut chosen took over 5 % longer than the soonest in 8 of the calls, 13 % at most.
 struct Times {
     float all_base, record;            // runs over all pairs: base, and for each record of a pair
     float own_base, own_round, share;  // pairs by clusters: base, for each round, rounds for each stage
@@ -89,8 +99,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
 
     // ------------------------------------------------ pairs by clusters, while the lengths are on their way
     // A cluster of CTAs holds pairs of its own, and each of its warps a run of one pair; the runs are merged
-    // through shared memory. Every warp starts on that run, with the loads of its pair's length and page ids
-    // and its CTA's queries, and drops it if the lengths ask for runs over all pairs.
+    // through shared memory. Every warp starts on that run, with the loads of its pair's length and page ids,
+    // and drops it if the lengths ask for runs over all pairs.
     const int num_runs = p.num_runs;
     const int cta0 = blockIdx.x * NW, cta_runs = max(0, min(num_runs - cta0, NW));
     // this CTA's runs of R over all pairs: those k whose place k num_runs / R is one of its warps (fewer runs
@@ -103,13 +113,6 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         const int i = base + lane;
         return (i < p.max_pages) ? __ldg(p.page_table + static_cast<int64_t>(b_) * p.max_pages + i)
                                  : -1;
-    };
-    int q_first = 0, q_cached = 0;
-    auto copy_queries = [&]() {
-        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
-        const int nq = q_cached * G * D * 2 / 16;
-        for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
-        cp_async_commit();
     };
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = static_cast<int>(cluster.num_blocks());
@@ -139,11 +142,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
                                                     p.t_magic)) & ~31;
                 pwin = load_window(prow, pbase);
             }
-            q_first = c_lo;
-            q_cached = min(c_pairs, G_::QCACHE / (G * D * 2));
         }
         if (tid < c_pairs) pair_len[tid] = __ldg(p.seq_lens + c_lo + tid);
-        copy_queries();
     }
 
     // ------------------------------------------------ stage prefix over the pairs
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
     const bool own = p.clusters > 0 &&
                      p.times.own(most) <= p.times.all(total * p.per_cta, __fdividef(most, W));
     int gw0 = 0, n_runs_cta = 0;
+    int q_first = c_lo, q_pairs = c_pairs;  // pairs of the CTA, whose queries are cached as far as they fit
     if (blockIdx.x == 0) {
         // pairs without stages (length 0 or invalid): output 0, LSE -inf, a warp per pair
         for (int j = 0; j < C; ++j) {
@@ -225,12 +226,17 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
                 acc += n;
             }
         }
-        cp_async_wait<0>();  // the queries copied ahead, before others take their place
         __syncthreads();
         q_first = span_pair[0];
-        q_cached = span_lo < span_hi ? min(span_pair[1] - span_pair[0] + 1, G_::QCACHE / (G * D * 2)) : 0;
+        q_pairs = span_lo < span_hi ? span_pair[1] - span_pair[0] + 1 : 0;
         prow = -1;
-        copy_queries();
+    }
+    const int q_cached = min(q_pairs, G_::QCACHE / (G * D * 2));
+    {
+        const uint8_t* qsrc = reinterpret_cast<const uint8_t*>(p.q + static_cast<int64_t>(q_first) * G * D);
+        const int nq = q_cached * G * D * 2 / 16;
+        for (int ci = tid; ci < nq; ci += NT) cp_async16_plain(qcache + 16 * ci, qsrc + 16 * ci);
+        cp_async_commit();
     }
 
     const int gw = gw0 + warp;
