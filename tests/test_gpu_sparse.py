@@ -305,7 +305,10 @@ class Cache:
         a = np.abs(wout)
         half = np.where(a > 0, 2.0 ** (np.floor(np.log2(np.where(a > 0, a, 1.0))) - 8), 0.0)
         err = np.abs(out - wout)
-        assert (err <= MAX_ABS + half).all() and err.mean() <= MEAN_ABS, (err.max(), err.mean())
+        # out = bf16(x) with x within MAX_ABS of wout, MEAN_ABS in the mean: |out - wout| <= |bf16(x) - x| + |x - wout|, and
+        # the first term is at most half a step of each value, so its mean at most that of the half steps. (It counts
+        # where a pair has a single token: its output is a V value, not an average of many.)
+        assert (err <= MAX_ABS + half).all() and err.mean() <= MEAN_ABS + half.mean(), (err.max(), err.mean())
         fin = np.isfinite(wlse)
         assert np.array_equal(fin, np.isfinite(lse)) and (lse[~fin] == -np.inf).all()
         assert not fin.any() or np.abs(lse[fin] - wlse[fin]).max() <= LSE_ABS
@@ -378,6 +381,42 @@ def test_attention_however_it_is_cut(kv, cuda, B, H, G, D, T, pages, lengths):
     assert status.item() == (kv.STATUS_PAGE_OOB if bool(read.any()) else 0)
     again = c.run(kv, q, table, lens, status, w)
     assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+
+
+@pytest.mark.parametrize("B,H,G,D,T,pages", [(1, 8, 4, 128, 64, 64), (4, 5, 3, 128, 16, 150), (8, 8, 2, 128, 64, 30),
+                                             (40, 3, 5, 64, 16, 70), (20, 8, 1, 64, 64, 64)])
+def test_attention_captured_and_replayed(kv, cuda, B, H, G, D, T, pages):
+    """One graph of two calls that share a workspace, replayed while the lengths change what the pairs are cut into."""
+    c = Cache(cuda, 40, H, T, D, B * pages)
+    pool = [t.to(cuda) for t in (c.kd, c.ks, c.vd, c.vs)]
+    g = [torch.tensor([x], device=cuda) for x in (c.gk, c.gv)]
+    lay = kv.Layout(H, D, T)
+    full = torch.full((B, H), pages * T, dtype=torch.int32)
+    q = [queries(c, B, G) for _ in range(2)]
+    table = torch.randint(0, 40, (B, H, pages), generator=c.g, dtype=torch.int32)
+    dq, dt, dl = [x.to(cuda) for x in q], table.to(cuda), full.to(cuda)
+    out = [torch.zeros_like(x) for x in dq]
+    lse = [torch.zeros(x.shape[:2], device=cuda) for x in dq]
+    w = torch.empty(kv.nvfp4_paged_sparse_decode_workspace_size(lay, B, H * G, pages), dtype=torch.uint8, device=cuda)
+
+    def calls():
+        for i in range(2):
+            kv.nvfp4_paged_sparse_decode_attention(lay, dq[i], pool[0], pool[1], g[0], pool[2], pool[3], g[1], dt, dl, c.sm,
+                                                   out[i], lse=lse[i], workspace=w)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    short = torch.randint(0, T + 2, (B, H), generator=c.g, dtype=torch.int32)
+    short[B // 2, 0] = pages * T
+    for lens in (full, short, torch.zeros_like(full), torch.full_like(full, 1), short, full):
+        dl.copy_(lens)
+        for o, s in zip(out, lse):
+            o.fill_(float("nan"))
+            s.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            c.check((out[i].float().cpu().numpy(), lse[i].cpu().numpy()), c.want(q[i], table, lens))
 
 
 def test_all_pairs_empty(kv, cuda):
