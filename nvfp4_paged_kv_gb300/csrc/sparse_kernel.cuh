@@ -15,7 +15,8 @@
 //
 // Bound: an SM's rate. A stage (9216 bytes) takes it 0.24 us, with 12 warps at 293 instructions per 16-token tile
 // (39 GB/s each: 5.9 TB/s on all SMs, 0.87 of the copy peak), alone as well as with all others and with K and V in
-// L2. 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) take 24.2 us: 6 until the first stages are
+// L2. It is the instructions: of 128 pairs of 8192 tokens, 38.7 us, a throwaway copy without the products by the
+// scales took 31.4, without the E2M1 conversions 33.5, without both 30.2 (6.5 TB/s, HBM). 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) take 24.2 us: 6 until the first stages are
 // computed, 64 stages on the fuller SMs, 1 for the join. 64 pairs of 8192 tokens with 8 heads, on clusters of 2,
 // 24.9 us; 8 pairs of 4096 tokens, on clusters of 8, 9.3 us; 95 ragged pairs with head_dim 256 24.2 us. Measured
 // and slower: one combined record per CTA and pair, runs of unequal length on every warp, 32-token stages (14 to 16
