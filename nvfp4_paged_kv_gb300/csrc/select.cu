@@ -410,35 +410,37 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
             float s0, s1;
             int a0, a1;  // page ids; -1: not scored, -2: outside the pool
         };
-        auto load_tile = [&](int t, Tile& x) {  // with the ids of tile t; leaves those of the next one
+        auto load_ids = [&](int t, Tile& x) {  // those of tile t, loaded before; leaves the next one's
             auto checked = [&](int i, int id) {
                 if (i >= n || i < p.sink || i >= n - p.recent) return -1;
                 return id >= 0 && id < p.pool_pages ? id : -2;
             };
             x.a0 = checked(t + r, id0);
             x.a1 = checked(t + r + 8, id1);
-            const int64_t ph0 = static_cast<int64_t>(max(x.a0, 0)) * p.H + h;
-            const int64_t ph1 = static_cast<int64_t>(max(x.a1, 0)) * p.H + h;
-            auto fetch = [&](bool there, const int8_t* a, uint32_t(&w)[D / 16]) {
-#pragma unroll
-                for (int k = 0; k < D / 64; ++k) {
-                    const uint4 v = there ? __ldg(reinterpret_cast<const uint4*>(a) + k) : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * k] = v.x;
-                    w[4 * k + 1] = v.y;
-                    w[4 * k + 2] = v.z;
-                    w[4 * k + 3] = v.w;
-                }
-            };
-            const int8_t* src0 = p.bounds + ph0 * 2 * D + c * (D / 4);
-            const int8_t* src1 = p.bounds + ph1 * 2 * D + c * (D / 4);
-            fetch(x.a0 >= 0, src0, x.hi0);
-            fetch(x.a1 >= 0, src1, x.hi1);
-            fetch(x.a0 >= 0, src0 + D, x.lo0);
-            fetch(x.a1 >= 0, src1 + D, x.lo1);
-            x.s0 = x.a0 >= 0 ? __ldg(p.bscales + ph0) : 0.0f;
-            x.s1 = x.a1 >= 0 ? __ldg(p.bscales + ph1) : 0.0f;
+            x.s0 = x.a0 >= 0 ? __ldg(p.bscales + static_cast<int64_t>(x.a0) * p.H + h) : 0.0f;
+            x.s1 = x.a1 >= 0 ? __ldg(p.bscales + static_cast<int64_t>(x.a1) * p.H + h) : 0.0f;
             id0 = id_at(t + r + stride);
             id1 = id_at(t + r + 8 + stride);
+        };
+        // the upper (half 0) or lower (1) bounds of a page
+        auto fetch = [&](int id, int half, uint32_t(&w)[D / 16]) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.bounds + ((static_cast<int64_t>(max(id, 0)) * p.H + h) * 2 + half) * D + c * (D / 4));
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k) {
+                const uint4 v = id >= 0 ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * k] = v.x;
+                w[4 * k + 1] = v.y;
+                w[4 * k + 2] = v.z;
+                w[4 * k + 3] = v.w;
+            }
+        };
+        auto load_tile = [&](int t, Tile& x) {
+            load_ids(t, x);
+            fetch(x.a0, 0, x.hi0);
+            fetch(x.a1, 0, x.hi1);
+            fetch(x.a0, 1, x.lo0);
+            fetch(x.a1, 1, x.lo1);
         };
         Tile cur;
         if (first < n) load_tile(first, cur);
@@ -498,22 +500,45 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
             pair_keys = cluster.map_shared_rank(keys, 0);
         }
 
+        auto multiply = [](float(&sum)[4], uint32_t w0, uint32_t w1, uint32_t b0, uint32_t b1) {
+            uint32_t a[4];
+            s8x4_to_f16x2x2(w0, a[0], a[2]);
+            s8x4_to_f16x2x2(w1, a[1], a[3]);
+            mma_f16_16816(sum, a, b0, b1);
+        };
         for (int t = first; t < n; t += stride) {
             Tile next;
-            if constexpr (D <= 128) {  // (at 256 the registers hold one tile)
-                if (t + stride < n) load_tile(t + stride, next);
+            const bool more = t + stride < n;
+            if constexpr (D <= 128) {
+                if (more) load_tile(t + stride, next);
+            } else {
+                if (more) load_ids(t + stride, next);
             }
             // the positive parts of the queries meet the upper bounds, the negative the lower
             float up[4] = {0.0f, 0.0f, 0.0f, 0.0f}, down[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if constexpr (D <= 128) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t a[4];
-                s8x4_to_f16x2x2(cur.hi0[k], a[0], a[2]);
-                s8x4_to_f16x2x2(cur.hi1[k], a[1], a[3]);
-                mma_f16_16816(up, a, max_f16x2(q[2 * k], 0u), max_f16x2(q[2 * k + 1], 0u));
-                s8x4_to_f16x2x2(cur.lo0[k], a[0], a[2]);
-                s8x4_to_f16x2x2(cur.lo1[k], a[1], a[3]);
-                mma_f16_16816(down, a, min_f16x2(q[2 * k], 0u), min_f16x2(q[2 * k + 1], 0u));
+                for (int k = 0; k < D / 16; ++k) {
+                    multiply(up, cur.hi0[k], cur.hi1[k], max_f16x2(q[2 * k], 0u), max_f16x2(q[2 * k + 1], 0u));
+                    multiply(down, cur.lo0[k], cur.lo1[k], min_f16x2(q[2 * k], 0u), min_f16x2(q[2 * k + 1], 0u));
+                }
+            } else {
+                // at 256 the registers hold one tile, and each half of it makes room for the next one's (128 pairs
+                // of 512 pages 12.8 us; with the next tile loaded after this one 14.7)
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    multiply(up, cur.hi0[k], cur.hi1[k], max_f16x2(q[2 * k], 0u), max_f16x2(q[2 * k + 1], 0u));
+                if (more) {
+                    fetch(next.a0, 0, cur.hi0);
+                    fetch(next.a1, 0, cur.hi1);
+                }
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    multiply(down, cur.lo0[k], cur.lo1[k], min_f16x2(q[2 * k], 0u), min_f16x2(q[2 * k + 1], 0u));
+                if (more) {
+                    fetch(next.a0, 1, cur.lo0);
+                    fetch(next.a1, 1, cur.lo1);
+                }
             }
             auto score = [&](float x0, float x1, float s) {
                 float v = -INFINITY;
@@ -540,7 +565,10 @@ __global__ void __launch_bounds__(NT, 512 / NT) select_pages_kernel(const Select
             if constexpr (D <= 128) {
                 cur = next;
             } else {
-                if (t + stride < n) load_tile(t + stride, cur);
+                cur.a0 = next.a0;
+                cur.a1 = next.a1;
+                cur.s0 = next.s0;
+                cur.s1 = next.s1;
             }
         }
     } else if (C > 1) {
