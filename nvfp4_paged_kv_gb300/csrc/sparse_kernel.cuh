@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
         // (heads 2c, 2c + 1 of two dims) per lane and 16 dims, behind them (max, sum) of heads 2c, 2c + 1. The runs
         // of a pair in this CTA become the output, or, in a cluster of several CTAs, one record like theirs in the
         // second slot of the first ring, joined with those of the other CTAs. (As [G][D] the lanes of a store would
-        // share a bank: 8 pairs of 64 pages 10.4 us against 9.2, of 8 heads of 256 24.6 against about 12.)
+        // share a bank: 8 pairs of 64 pages 10.4 us against 9.2, of 8 heads of 256 24.6 against 14.3.)
         //
         // Runs of the cluster's pair j to be merged: one alone has written the outputs itself, and a pair without
         // any is the first CTA's.
