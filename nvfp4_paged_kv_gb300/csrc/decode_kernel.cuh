@@ -34,8 +34,9 @@
 //    token, exact in FP16, times its E4M3 block scale (exact). Q is brought into FP16 exactly by
 //    a per-head power of two; head dims inside a k-step are permuted identically in K and Q.
 //  * online softmax per stage in the log2 domain, column maxima by warp shuffles on packed
-//    FP16 pairs; the running maximum moves only when it grows by more than 2^8, so accumulator
-//    rescaling is rare. P^T moves to the B-operand layout with movmatrix.
+//    FP16 pairs (FP32 for scores past 2^12, see column_maxima); the running maximum moves only
+//    when it grows by more than 2^8, so accumulator rescaling is rare. P^T moves to the B-operand
+//    layout with movmatrix.
 //  * O^T += V^^T P^T with head dims as M: V is stored token-pair packed, so every converted byte
 //    is one A-register (one head dim of two adjacent tokens) times the pair's two block scales.
 //  * at the end of a piece the warp writes the BF16 output and the natural-log LSE directly
@@ -222,6 +223,34 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
+}
+
+// Maxima of a stage's scores (log2 units), a column's over the eight lanes that differ in bits 2 to
+// 4: lm0, lm1 are a lane's own maxima of its two columns. The running maximum m only has to be near
+// the true one, so both columns are reduced in one FP16 pair, whose step is at most 2 below 4096: the
+// result is off by at most 1, m by at most kRescaleThreshold more, and every p = 2^(x - m) stays within
+// 2^9, its largest at least 2^-1, well inside FP16. Past 4096 of either sign FP16 steps reach 32 (p
+// then overflows, or its FP16 rounding has few bits) and beyond 65504 an FP16 maximum is infinite (a
+// column whose scores all lie below that would keep m = -inf and get NaN), so there, and for infinities,
+// the reduction is in FP32. Every lane of the warp calls.
+__device__ __forceinline__ void column_maxima(float lm0, float lm1, float& mx0, float& mx1) {
+    __half2 hm = __floats2half2_rn(lm0, lm1);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+        const uint32_t u = __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&hm), off);
+        hm = __hmax2(hm, *reinterpret_cast<const __half2*>(&u));
+    }
+    mx0 = __low2float(hm);
+    mx1 = __high2float(hm);
+    if (__any_sync(0xFFFFFFFFu, fmaxf(fabsf(mx0), fabsf(mx1)) >= 4096.0f)) {
+        mx0 = lm0;
+        mx1 = lm1;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
+        }
+    }
 }
 
 // Merge the records of pair (b, h) (pieces of runs gf .. gl, records gf + bh .. gl + bh, one
@@ -894,26 +923,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
                 lm0 = fmaxf(lm0, fmaxf(x[u][0], x[u][2]));
                 lm1 = fmaxf(lm1, fmaxf(x[u][1], x[u][3]));
             }
-            // column maxima over the stage, both columns in one FP16 pair (the running
-            // maximum only has to be close to the true one: p = 2^(x - m) stays below 2^8)
-            __half2 hm = __floats2half2_rn(lm0, lm1);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                const uint32_t uu =
-                    __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&hm), off);
-                hm = __hmax2(hm, *reinterpret_cast<const __half2*>(&uu));
-            }
-            float mx0 = __low2float(hm), mx1 = __high2float(hm);
-            if (__any_sync(0xFFFFFFFFu, fmaxf(mx0, mx1) > 65000.0f)) {
-                // scores beyond the FP16 range: reduce in fp32 instead
-                mx0 = lm0;
-                mx1 = lm1;
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
-                }
-            }
+            float mx0, mx1;
+            column_maxima(lm0, lm1, mx0, mx1);
             const bool grow = (mx0 > m0 + kRescaleThreshold) || (mx1 > m1 + kRescaleThreshold);
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);

@@ -573,26 +573,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) sparse_split_kernel(const 
                 lm0 = fmaxf(lm0, fmaxf(x[u][0], x[u][2]));
                 lm1 = fmaxf(lm1, fmaxf(x[u][1], x[u][3]));
             }
-            // column maxima over the stage, both columns in one FP16 pair (the running
-            // maximum only has to be close to the true one: p = 2^(x - m) stays below 2^8)
-            __half2 hm = __floats2half2_rn(lm0, lm1);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-                const uint32_t uu =
-                    __shfl_xor_sync(0xFFFFFFFFu, *reinterpret_cast<const uint32_t*>(&hm), off);
-                hm = __hmax2(hm, *reinterpret_cast<const __half2*>(&uu));
-            }
-            float mx0 = __low2float(hm), mx1 = __high2float(hm);
-            if (__any_sync(0xFFFFFFFFu, fmaxf(mx0, mx1) > 65000.0f)) {
-                // scores beyond the FP16 range: reduce in fp32 instead
-                mx0 = lm0;
-                mx1 = lm1;
-#pragma unroll
-                for (int off = 4; off < 32; off <<= 1) {
-                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
-                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
-                }
-            }
+            float mx0, mx1;
+            column_maxima(lm0, lm1, mx0, mx1);
             const bool grow = (mx0 > m0 + kRescaleThreshold) || (mx1 > m1 + kRescaleThreshold);
             if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
