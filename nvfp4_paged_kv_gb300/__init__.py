@@ -224,6 +224,24 @@ def _on_device(tensors, stream):
             yield int(stream)
 
 
+def _scratch(nbytes: int, device: torch.device, stream):
+    """Scratch of one call on `stream` (as the entry points take it) that the call does not keep. It is taken
+    from the allocator with the launch stream current: the allocator reuses a block only in the order of the stream
+    it was taken on, so neither the block's last user nor its next can overlap the call. (A block of another
+    stream would be handed on, and written, while the call still counts in it.)"""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        if handle == 2:   # cudaStreamPerThread: no stream the allocator knows
+            raise ValueError("a call on the per-thread default stream needs a workspace of the caller")
+        # 0 and 1 (cudaStreamLegacy) are the default stream
+        stream = (torch.cuda.default_stream(device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=device))
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _check(fn: str, code: int):
     if code != 0:
         msg = load().nvfp4kv_status_string(code).decode()
@@ -262,8 +280,7 @@ def nvfp4_kv_compute_global_scale(layout: Layout, src: torch.Tensor, out: torch.
     if num_pages is None:
         num_pages = src_page_ids.numel() if src_page_ids is not None else src.shape[0]
     if workspace is None:
-        workspace = torch.empty(nvfp4_kv_global_scale_workspace_size(), dtype=torch.uint8,
-                                device=src.device)
+        workspace = _scratch(nvfp4_kv_global_scale_workspace_size(), src.device, stream)
     with _on_device((src, out, src_page_ids, src_scale, workspace, status), stream) as s:
         code = lib.nvfp4_kv_compute_global_scale(
             ctypes.byref(layout), _dtype_code(src, src_dtype), _ptr(src), src.shape[0],
@@ -390,7 +407,7 @@ def nvfp4_paged_decode_attention(layout: Layout, q: torch.Tensor, k_data, k_scal
     maxp = page_table.shape[1]
     if workspace is None:
         need = nvfp4_paged_decode_workspace_size(layout, B, Hq, maxp, max_num_splits)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(max(need, 16), q.device, stream)
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("page_table and seq_lens must be int32")
     with _on_device((q, k_data, k_scales, k_global_scale, v_data, v_scales, v_global_scale,
@@ -734,7 +751,7 @@ def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data,
         (out, "out", _BF16, B * hq * D), (lse, "lse", _F32, B * hq), (status, "status", _I32, None))
     if workspace is None:
         need = nvfp4_paged_sparse_decode_workspace_size(layout, B, hq, max_sel)
-        workspace = torch.empty(max(need, 16), dtype=_U8, device=q.device)
+        workspace = _scratch(max(need, 16), q.device, stream)
     wp, = _pointers(dev, (workspace, "workspace", None, None))
     _run("nvfp4_paged_sparse_decode_attention", dev, stream, layout, B, hq, qp, kd, ks, gk, vd, vs, gv,
          pages, tp, max_sel, lp, float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol,
