@@ -424,9 +424,12 @@ nvfp4kv_status nvfp4_kv_page_bounds(
  * to integers q_i = rint(fp32(q / f)), f = fp32(max|q| / 255) (all 0 when max|q| is 0 or a value
  * is not finite), the score of a page is the largest over the group of
  *   fp32(fp32(S f) s),  S = sum_d (q_i[d] > 0 ? q_i[d] hi[d] : q_i[d] lo[d])
- * which bounds the product of the query with every key of the page from above (in units of g).
- * S is exact, so the result does not depend on how the work is split. When n <= budget every page
- * is taken.
+ * in units of g. S is exact, so the result does not depend on how the work is split. When
+ * n <= budget every page is taken. Up to the FP32 roundings the score is at least the product of
+ * the rounded query f q_i with any key of the page. The product of the query itself may lie above
+ * it, by at most f/2 sum_d max(|hi[d]|, |lo[d]|) s: a query dim below max|q| / 510 counts as 0, so
+ * one large dim hides small ones. The score ranks pages; that a page was not taken does not prove
+ * that its keys lie below those of the pages that were.
  *   q              BF16 [batch][num_q_heads][D]
  *   bounds, bound_scales   as written by nvfp4_kv_page_bounds; those of the always-taken pages are
  *                  not read, so the last, growing page needs none

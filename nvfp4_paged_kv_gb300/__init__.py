@@ -707,7 +707,7 @@ def nvfp4_kv_select_pages(layout: Layout, q: torch.Tensor, bounds: torch.Tensor,
                           sel_index=None, scores=None, status=None, stream=None):
     """Take up to sel_page_table.shape[2] pages for each (sequence, KV head): the first `sink_pages`,
     the last `recent_pages`, and those whose bounds allow the largest product with `q` ([B, Hq, D]
-    BF16). Writes `sel_page_table` [B, H, budget] int32 (page ids in sequence order, then -1) and
+    BF16), each head rounded to steps of max|q| / 255. Writes `sel_page_table` [B, H, budget] int32 (page ids in sequence order, then -1) and
     `sel_lens` [B, H] int32 (their tokens), which nvfp4_paged_sparse_decode_attention takes;
     optionally `sel_index` (positions in the page table) and `scores` [B, H, max pages] float32."""
     H, D = layout.num_kv_heads, layout.head_dim

@@ -5,13 +5,15 @@
 //   a = max_d max(|max_t v|, |min_t v|),  s = fp32(a / 127),
 //   hi_d = min(127, ceil(fp32(max_t v / s))),  lo_d = max(-127, floor(fp32(min_t v / s))),
 // all 0 when a is 0. Rounding away from the interval keeps  lo_d s <= v <= hi_d s  (up to the two
-// FP32 roundings), so a query's product with the nearer bound of each dim is at least its product
-// with any key of the page.
+// FP32 roundings), so the product of any vector with the nearer bound of each dim is at least its
+// product with any key of the page.
 //
 // Scores and selection. The queries of a KV head's group are brought to integers of 9 bits,
 //   q_i = rint(fp32(q / f)),  f = fp32(max|q| / 255)   (0 when max|q| is 0 or not finite),
 // and the score of a page is the largest over the group of
 //   fp32(fp32(S f) s),  S = sum_d (q_d > 0 ? q_d hi_d : q_d lo_d).
+// This bounds the product of the rounded query f q_i; that of the query itself may be larger by up to
+// f/2 sum_d max(|hi_d|, |lo_d|) s.
 // S is an integer below 2^23 in magnitude, exact in FP32 in every order of summation, so the
 // selection is the same bit for bit whatever the split of the work: the reason for integer bounds
 // and integer queries, which also halve the bytes of 16-bit bounds.
