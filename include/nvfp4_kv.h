@@ -266,6 +266,14 @@ nvfp4kv_status nvfp4_kv_extend_step(const nvfp4kv_extend_tensor* tensors, int32_
  *   lse[b][qh] = log(sum_t exp(sm_scale * q . k_t))              (natural log; optional)
  * A sequence of length 0 gives out = 0 and lse = -inf.
  *
+ * Numerics: scores, softmax statistics and sums in FP32 (ex2.approx for the weights). Two operands
+ * of the tensor-core products are held in FP16: q, brought to [2^14, 2^15) by a power of two per
+ * head (exact but for elements below 2^-31 of the head's largest), and the weights p before P V
+ * (2^-11 relative, 2^-25 of a weight of 1 at least; their sum takes them unrounded), where p is
+ * taken against a running maximum that is at most 1 above and 9 below the true one in log2 units.
+ * K and V are exact in FP16. Scores of any size that FP32 holds are handled; their differences are
+ * those of FP32, so weights lose bits where scores are large (2^-24 |score| each).
+ *
  * Split-KV: the (sequence, KV head) pairs are cut into 64-token stages (32 at head_dim 256), the
  * stages of all pairs form one list, and the list is cut into equal runs, one per warp (one CTA
  * per SM). Each (run, pair) piece of a pair split over several runs leaves a partial (max, sum,
@@ -460,8 +468,9 @@ nvfp4kv_status nvfp4_kv_select_pages(
     nvfp4kv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
- * nvfp4_paged_decode_attention over selected pages: the same formula, numerics and pools, with a
- * page table and a length for each (sequence, KV head) pair, shared by the pair's query heads.
+ * nvfp4_paged_decode_attention over selected pages: the same formula, numerics (weights in FP16
+ * before P V) and pools, with a page table and a length for each (sequence, KV head) pair, shared
+ * by the pair's query heads.
  *   sel_page_table int32 [batch][H][max_sel_pages]
  *   sel_lens       int32 [batch][H] tokens of the pair's pages, 0 <= len <= max_sel_pages * T; every
  *                  page but the last is full. Table entries past ceil(len / T) do not matter. A length

@@ -833,8 +833,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
             }
             qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, 1));
             qmax = fmaxf(qmax, __shfl_xor_sync(0xFFFFFFFFu, qmax, 2));
-            // qmax * 2^kq in [2^14, 2^15): every BF16 value of the head is exact in FP16 down
-            // to 2^-18 of the head maximum.
+            // qmax * 2^kq in [2^14, 2^15): every BF16 value (8 bits) of the head is exact in FP16,
+            // whose last bit is 2^-24, down to 2^-31 of the head maximum.
             int kq = (qmax > 0.0f) ? (14 - ilogbf(qmax)) : 0;
             kq = max(-120, min(kq, 120));
             const float up = ldexpf(1.0f, kq);
@@ -948,7 +948,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const 
                 const float p2 = ex2_approx(x[u][2] - m0), p3 = ex2_approx(x[u][3] - m1);
                 l0 += p0 + p2;
                 l1 += p1 + p3;
-                // P^T (tokens x heads) -> B operand (k = tokens, n = heads)
+                // P^T (tokens x heads) -> B operand (k = tokens, n = heads), rounded to FP16: 11 bits
+                // where the output has 8, and FP16 is what V is exact in; the sum takes p as it is
                 pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
                 pb[u][1] = movmatrix_trans(pack_f16x2(p2, p3));
             }
