@@ -74,9 +74,10 @@ class Pool:
         torch.cuda.synchronize()
         return out.double().cpu().numpy(), lse.double().cpu().numpy()
 
-    def check(self, got, q, table, lens, exact_sums=False):
+    def check(self, got, q, table, lens, exact_sums=False, run=None, records=0):
         """table [B, H, pages], lens [B, H]: every row of `got` within the bound at the top of this file, S left out
-        where the sums of products are exact."""
+        where the sums of products are exact. Pairs known to be cut into runs of at most `run` tokens, joined from
+        `records` of them, sum that many terms each (and a run's weights are held against a maximum of its own)."""
         out, lse = got
         B, Hq, D = q.shape
         G, T = Hq // self.H, self.T
@@ -106,13 +107,14 @@ class Pool:
                 big = np.abs(x).max(-1) * LOG2E
                 dist = (top[:, 0] - x.min(-1)) * LOG2E
                 dx = (np.log(2) * (2.0 ** -24 * (2 * big + 3 * dist) + 2 * 2.0 ** -23 * D * S))[:, None]
-                rel = 2.0 ** -11 + 2 * (2.0 ** -22 + dx + 2.0 ** -23 * n) + 2.0 ** -21
-                tol = A * rel + 2.0 ** -24 * n * np.abs(v).max() * self.gv
+                terms = n if run is None else min(n, run) + records
+                rel = 2.0 ** -11 + 2 * (2.0 ** -22 + dx + 2.0 ** -23 * terms) + 2.0 ** -21
+                tol = A * rel + 2.0 ** -24 * (n if run is None else min(n, run)) * np.abs(v).max() * self.gv
                 half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want) + tol, 2.0 ** -126))) - 8)
                 err = np.abs(out[b, rows] - want)
                 assert (err <= tol + half).all(), (b, h, n, float((err - tol - half).max()))
                 # the scale's three roundings, x's own, that of m + log2(l), and two of its product with ln 2
-                ltol = 2.0 ** -24 * (3 + 1 + 3) * np.maximum(big, np.abs(want_lse) * LOG2E) + dx[:, 0] + 2.0 ** -22 * n + 2.0 ** -20
+                ltol = 2.0 ** -24 * (3 + 1 + 3) * np.maximum(big, np.abs(want_lse) * LOG2E) + dx[:, 0] + 2.0 ** -22 * terms + 2.0 ** -20
                 assert (np.abs(lse[b, rows] - want_lse) <= ltol).all(), (b, h, n, lse[b, rows] - want_lse, ltol)
 
 
@@ -188,3 +190,67 @@ def test_negative_scores_over_many_pairs(kv, cuda, size):
     table = torch.randint(0, 20, (B, H, most), generator=c.g, dtype=torch.int32)
     q = queries_of_scores(c, B, 2, [-size, 0])
     c.check(c.sparse(kv, q, table, lens), q, table, lens, True)
+
+
+# ------------------------------------------------------------------------------------ pairs of every length and cut
+
+def touched(kv, c, q, table, lens, **kw):
+    """The outputs over a workspace of garbage, twice the same, and the bytes of it that the call wrote (0 where each
+    pair was cut within a cluster of CTAs)."""
+    B, Hq, D = q.shape
+    n = kv.nvfp4_paged_sparse_decode_workspace_size(kv.Layout(c.H, D, c.T), B, Hq, table.shape[2])
+    w = torch.full((n,), 0xA5, dtype=torch.uint8, device=c.dev)
+    got = c.sparse(kv, q, table, lens, workspace=w, **kw)
+    again = c.sparse(kv, q, table, lens, workspace=w, **kw)
+    assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
+    return got, int((w != 0xA5).sum())
+
+
+@pytest.mark.parametrize("B,H,G,D,T,pages,own", [
+    (1, 8, 4, 128, 64, 64, True), (2, 4, 8, 256, 16, 70, True), (1, 5, 1, 64, 32, 128, True),  # clusters of 8 CTAs
+    (8, 4, 8, 64, 64, 40, True), (8, 8, 2, 128, 64, 30, True),                                 # of 4 and 2
+    (19, 8, 4, 128, 64, 32, True), (75, 4, 2, 128, 64, 20, True),                              # one CTA a pair, and two
+    (20, 8, 1, 64, 64, 64, False), (19, 5, 3, 256, 16, 150, False), (40, 8, 4, 128, 64, 32, False),  # over all pairs
+])
+def test_long_pairs_within_the_bound_of_their_roundings(kv, cuda, B, H, G, D, T, pages, own):
+    """Averages of about 1000 to 4000 tokens, outputs of a few hundredths, against the derived bound (about
+    2^-10 of the mean |v|), cut within clusters (`own`: the workspace is left alone) or into runs over all pairs; the
+    dense kernel over the same pages."""
+    c = Pool(cuda, 60, H, T, D, B + pages).to_device()
+    lens = torch.randint(pages * T // 2, pages * T + 1, (B, H), generator=c.g, dtype=torch.int32)
+    table = torch.randint(0, 60, (B, H, pages), generator=c.g, dtype=torch.int32)
+    q = torch.randn((B, H * G, D), generator=c.g).to(torch.bfloat16)
+    got, wrote = touched(kv, c, q, table, lens)
+    assert (wrote == 0) == own
+    c.check(got, q, table, lens)
+    same, one = table[:, :1].expand(B, H, pages).contiguous(), lens[:, :1].expand(B, H).contiguous()
+    c.check(c.dense(kv, q, same[:, 0].contiguous(), one[:, 0].contiguous()), q, same, one)
+
+
+@pytest.mark.parametrize("D,G,T,n", [(128, 1, 128, 38400), (256, 3, 128, 50000), (64, 2, 64, 100000), (128, 8, 128, 150000),
+                                      (256, 1, 16, 30000)])
+def test_a_pair_of_more_records_than_shared_memory_holds(kv, cuda, D, G, T, n):
+    """One long pair beside a short and an empty one, cut into 600 to 1600 runs: their records are joined in chunks.
+    What the call writes of the workspace shows the records: G (D + 2) floats each."""
+    pages = -(-n // T)
+    c = Pool(cuda, 50, 1, T, D, n).to_device()
+    lens = torch.tensor([[n], [70], [0]], dtype=torch.int32)
+    table = torch.randint(0, 50, (3, 1, pages), generator=c.g, dtype=torch.int32)
+    q = torch.randn((3, G, D), generator=c.g).to(torch.bfloat16)
+    got, wrote = touched(kv, c, q, table, lens)
+    record = G * (D + 2) * 4
+    held = 227 * 1024 // record
+    assert wrote > 0.9 * record * (held + 1), (wrote, record)
+    # 1600 runs and more (8 warps an SM and up): at most 3 stages each
+    c.check(got, q, table, lens, run=4 * 64, records=2500)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_one_token_pairs_return_their_value_rows(kv, cuda, D):
+    """A single token's output is its V row, rounded to FP16 against its own weight and to BF16, whatever its score."""
+    B, H, G, T = 64, 4, 3, 16
+    c = Pool(cuda, 40, H, T, D, D, scale=(0x20, 0x50)).to_device()
+    lens = torch.ones((B, H), dtype=torch.int32)
+    table = torch.randint(0, 40, (B, H, 2), generator=c.g, dtype=torch.int32)
+    q = (torch.randn((B, H * G, D), generator=c.g) * 10.0 ** torch.randint(-3, 3, (B, H * G, 1), generator=c.g)).to(torch.bfloat16)
+    c.check(c.sparse(kv, q, table, lens), q, table, lens)
