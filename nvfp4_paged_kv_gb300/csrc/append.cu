@@ -484,6 +484,5 @@ extern "C" nvfp4kv_status nvfp4_kv_append(
         default: e = launch_append<NVFP4KV_FP16, 256>(p, style, grid, s); break;
         }
     }
-    if (e != cudaSuccess) return NVFP4KV_ERR_CUDA;
-    return launch_status();
+    return launched(e);
 }

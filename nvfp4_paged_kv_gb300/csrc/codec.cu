@@ -645,8 +645,7 @@ cudaError_t launch_extend_step(ExtendStepParams& p, const int64_t (&items)[4],
         acc += static_cast<int>(cj);
         p.cta_end[j] = acc;
     }
-    const cudaError_t e = launch_pdl(extend_step_kernel<SRC, A32>, acc, kThreads, 0, s, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_pdl(extend_step_kernel<SRC, A32>, acc, kThreads, 0, s, p);
 }
 
 // Host-side validation and parameters of an encode job (quantize, or the NVFP4 half of an
@@ -759,8 +758,7 @@ extern "C" nvfp4kv_status nvfp4_kv_compute_global_scale(
         return NVFP4KV_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (num_pages == 0) {
-        launch_pdl(write_one_kernel, 1, 1, 0, s, global_scale_out);
-        return launch_status();
+        return launched(launch_pdl(write_one_kernel, 1, 1, 0, s, global_scale_out));
     }
     if (!src || !aligned16(src)) return NVFP4KV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < nvfp4_kv_global_scale_workspace_size() ||
@@ -785,15 +783,16 @@ extern "C" nvfp4kv_status nvfp4_kv_compute_global_scale(
     // one wave of resident CTAs: each CTA reads its items and raises the maximum once (a CTA
     // that waited for a slot would read its whole share after the others have finished)
     const int64_t items = static_cast<int64_t>(num_pages) * p.items_per_page;
+    cudaError_t e;
 #define NVFP4KV_ALAUNCH(SRC) \
-    launch_pdl(amax_kernel<SRC>, wave_grid<amax_kernel<SRC>>(items, kAmaxThreads), kAmaxThreads, 0, s, p)
+    e = launch_pdl(amax_kernel<SRC>, wave_grid<amax_kernel<SRC>>(items, kAmaxThreads), kAmaxThreads, 0, s, p)
     switch (src_dtype) {
     case NVFP4KV_BF16: NVFP4KV_ALAUNCH(NVFP4KV_BF16); break;
     case NVFP4KV_FP16: NVFP4KV_ALAUNCH(NVFP4KV_FP16); break;
     default: NVFP4KV_ALAUNCH(NVFP4KV_FP8_E4M3); break;
     }
 #undef NVFP4KV_ALAUNCH
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_quantize_pages(
@@ -813,8 +812,9 @@ extern "C" nvfp4kv_status nvfp4_kv_quantize_pages(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = grid_for(static_cast<int64_t>(num_pages) * p.items_per_page, 8);
     const bool a32 = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;
+    cudaError_t e;
 #define NVFP4KV_QLAUNCH(SRC, A32, PK) \
-    launch_pdl(quantize_pages_kernel<SRC, A32, PK>, grid, kThreads, 0, s, p)
+    e = launch_pdl(quantize_pages_kernel<SRC, A32, PK>, grid, kThreads, 0, s, p)
 #define NVFP4KV_QPACK(SRC, A32)                                          \
     do {                                                                  \
         if (pack == NVFP4KV_PACK_TOKEN_PAIRS)                             \
@@ -835,7 +835,7 @@ extern "C" nvfp4kv_status nvfp4_kv_quantize_pages(
     }
 #undef NVFP4KV_QPACK
 #undef NVFP4KV_QLAUNCH
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_extend_write(
@@ -865,12 +865,13 @@ extern "C" nvfp4kv_status nvfp4_kv_extend_write(
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = grid_for(static_cast<int64_t>(num_pages) * p.items_per_page, 8);
     const bool a32 = (reinterpret_cast<uintptr_t>(src) & 31u) == 0;
+    cudaError_t e;
 #define NVFP4KV_XLAUNCH(SRC, A32)                                                             \
     do {                                                                                     \
         if (pack == NVFP4KV_PACK_TOKEN_PAIRS)                                                \
-            launch_pdl(quantize_pages_kernel<SRC, A32, NVFP4KV_PACK_TOKEN_PAIRS, true>, grid, kThreads, 0, s, p); \
+            e = launch_pdl(quantize_pages_kernel<SRC, A32, NVFP4KV_PACK_TOKEN_PAIRS, true>, grid, kThreads, 0, s, p); \
         else                                                                                 \
-            launch_pdl(quantize_pages_kernel<SRC, A32, NVFP4KV_PACK_DIM_PAIRS, true>, grid, kThreads, 0, s, p);   \
+            e = launch_pdl(quantize_pages_kernel<SRC, A32, NVFP4KV_PACK_DIM_PAIRS, true>, grid, kThreads, 0, s, p);   \
     } while (0)
     if (src_dtype == NVFP4KV_BF16) {
         if (a32) NVFP4KV_XLAUNCH(NVFP4KV_BF16, true);
@@ -882,7 +883,7 @@ extern "C" nvfp4kv_status nvfp4_kv_extend_write(
         NVFP4KV_XLAUNCH(NVFP4KV_FP8_E4M3, false);
     }
 #undef NVFP4KV_XLAUNCH
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_dequantize_pages(
@@ -906,12 +907,13 @@ extern "C" nvfp4kv_status nvfp4_kv_dequantize_pages(
     // evens out the SMs' different streaming rates (BF16 out 57.3 -> 53.2 us, FP8 out 34.8 ->
     // 32.8 us on 4096 pages against 8 CTAs per SM)
     const int grid = grid_for(static_cast<int64_t>(num_pages) * p.items_per_page, 32);
+    cudaError_t e;
 #define NVFP4KV_DQLAUNCH(DST)                                                                \
     do {                                                                                      \
         if (pack == NVFP4KV_PACK_TOKEN_PAIRS)                                                 \
-            launch_pdl(dequantize_pages_kernel<DST, NVFP4KV_PACK_TOKEN_PAIRS>, grid, kThreads, 0, s, p); \
+            e = launch_pdl(dequantize_pages_kernel<DST, NVFP4KV_PACK_TOKEN_PAIRS>, grid, kThreads, 0, s, p); \
         else                                                                                  \
-            launch_pdl(dequantize_pages_kernel<DST, NVFP4KV_PACK_DIM_PAIRS>, grid, kThreads, 0, s, p);   \
+            e = launch_pdl(dequantize_pages_kernel<DST, NVFP4KV_PACK_DIM_PAIRS>, grid, kThreads, 0, s, p);   \
     } while (0)
     switch (dst_dtype) {
     case NVFP4KV_BF16: NVFP4KV_DQLAUNCH(NVFP4KV_BF16); break;
@@ -919,7 +921,7 @@ extern "C" nvfp4kv_status nvfp4_kv_dequantize_pages(
     default: NVFP4KV_DQLAUNCH(NVFP4KV_FP8_E4M3); break;
     }
 #undef NVFP4KV_DQLAUNCH
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_extend_step(const nvfp4kv_extend_tensor* tensors,
@@ -986,8 +988,7 @@ extern "C" nvfp4kv_status nvfp4_kv_extend_step(const nvfp4kv_extend_tensor* tens
         e = a32 ? launch_extend_step<NVFP4KV_BF16, true>(p, items, bytes, s)
                 : launch_extend_step<NVFP4KV_BF16, false>(p, items, bytes, s);
     }
-    if (e != cudaSuccess) return NVFP4KV_ERR_CUDA;
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_round_f32(const float* x, size_t n, int32_t target,
@@ -995,7 +996,9 @@ extern "C" nvfp4kv_status nvfp4_kv_round_f32(const float* x, size_t n, int32_t t
     if ((target != 0 && target != 1) || (n > 0 && (!x || !out))) return NVFP4KV_ERR_INVALID_ARG;
     if (n == 0) return NVFP4KV_OK;
     const int64_t blocks = static_cast<int64_t>((n + 255) / 256);
-    round_f32_kernel<<<grid_for(blocks, 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        x, n, target, out);
-    return launch_status();
+    cudaLaunchConfig_t cfg = {};  // (in full stream order: the kernel does not wait by itself)
+    cfg.gridDim = dim3(grid_for(blocks, 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    return launched(cudaLaunchKernelEx(&cfg, round_f32_kernel, x, n, target, out));
 }

@@ -554,21 +554,22 @@ extern "C" nvfp4kv_status nvfp4_kv_offload_pages(
     if (st != NVFP4KV_OK || num_pages == 0) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = cold_grid(p);
+    cudaError_t e;
 #define NVFP4KV_OFF(SRC)                                                                      \
     do {                                                                                      \
         if (p.rope_mode == NVFP4KV_ROPE_SKIP)                                                 \
-            launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_SKIP>, grid, kColdThreads, 0, s, p);     \
+            e = launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_SKIP>, grid, kColdThreads, 0, s, p);     \
         else if (p.rope_mode == NVFP4KV_ROPE_2FP4)                                            \
-            launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_2FP4>, grid, kColdThreads, 0, s, p);     \
+            e = launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_2FP4>, grid, kColdThreads, 0, s, p);     \
         else                                                                                  \
-            launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_QUANTIZE>, grid, kColdThreads, 0, s, p); \
+            e = launch_pdl(cold_offload_kernel<SRC, NVFP4KV_ROPE_QUANTIZE>, grid, kColdThreads, 0, s, p); \
     } while (0)
     if (hot_dtype == NVFP4KV_BF16)
         NVFP4KV_OFF(NVFP4KV_BF16);
     else
         NVFP4KV_OFF(NVFP4KV_FP16);
 #undef NVFP4KV_OFF
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_onboard_pages(
@@ -586,21 +587,22 @@ extern "C" nvfp4kv_status nvfp4_kv_onboard_pages(
     if (st != NVFP4KV_OK || num_pages == 0) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int grid = cold_grid(p);
+    cudaError_t e;
 #define NVFP4KV_ON(DST)                                                                      \
     do {                                                                                     \
         if (p.rope_mode == NVFP4KV_ROPE_SKIP)                                                \
-            launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_SKIP>, grid, kColdThreads, 0, s, p);    \
+            e = launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_SKIP>, grid, kColdThreads, 0, s, p);    \
         else if (p.rope_mode == NVFP4KV_ROPE_2FP4)                                           \
-            launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_2FP4>, grid, kColdThreads, 0, s, p);    \
+            e = launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_2FP4>, grid, kColdThreads, 0, s, p);    \
         else                                                                                 \
-            launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_QUANTIZE>, grid, kColdThreads, 0, s, p); \
+            e = launch_pdl(cold_onboard_kernel<DST, NVFP4KV_ROPE_QUANTIZE>, grid, kColdThreads, 0, s, p); \
     } while (0)
     if (hot_dtype == NVFP4KV_BF16)
         NVFP4KV_ON(NVFP4KV_BF16);
     else
         NVFP4KV_ON(NVFP4KV_FP16);
 #undef NVFP4KV_ON
-    return launch_status();
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_host_device_pointer(void* host_ptr, void** device_ptr) {

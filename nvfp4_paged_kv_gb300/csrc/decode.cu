@@ -84,7 +84,5 @@ extern "C" nvfp4kv_status nvfp4_paged_decode_attention(
     case 128: e = launch_decode<128>(p, runs, s); break;
     default: e = launch_decode<256>(p, runs, s); break;
     }
-    if (e != cudaSuccess) return NVFP4KV_ERR_CUDA;
-
-    return NVFP4KV_OK;
+    return launched(e);
 }

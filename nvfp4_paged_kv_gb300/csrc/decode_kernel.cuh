@@ -1151,14 +1151,12 @@ bool decode_size_ok(int batch, int H, int D, int max_pages, int T, int64_t runs)
 template <int D>
 cudaError_t launch_decode(const DecodeParams& p, int64_t runs, cudaStream_t s) {
     using G_ = Geo<D>;
-    cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
-    e = launch_pdl(decode_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS,
-                   static_cast<size_t>(G_::SMEM), s, p);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return launch_pdl(decode_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS,
+                      static_cast<size_t>(G_::SMEM), s, p);
 }
 
 }  // namespace

@@ -82,7 +82,7 @@ inline int wave_grid(int64_t items, int threads, size_t smem = 0) {
 // grid (griddepcontrol.wait) before its first global memory access, so data dependencies on the
 // stream are kept.
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+[[nodiscard]] inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t s, Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
@@ -97,8 +97,14 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-inline nvfp4kv_status launch_status() {
-    return cudaGetLastError() == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
+// Status of a call from what its launch (or a runtime call before it) returned. The runtime's last
+// error is not asked: the library shares the runtime with its caller, so that may be an error of
+// someone else's from before the call, whose work was enqueued. A failure of this call is reported
+// by the status alone and not left there for the caller's next check.
+inline nvfp4kv_status launched(cudaError_t e) {
+    if (e == cudaSuccess) return NVFP4KV_OK;
+    (void)cudaGetLastError();
+    return NVFP4KV_ERR_CUDA;
 }
 
 }  // namespace nvfp4kv

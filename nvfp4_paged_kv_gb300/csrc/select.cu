@@ -788,7 +788,7 @@ extern "C" nvfp4kv_status nvfp4_kv_page_bounds(
     case 128: e = launch_pdl(page_bounds_kernel<128>, grid, kBoundsThreads, 0, s, p); break;
     default: e = launch_pdl(page_bounds_kernel<256>, grid, kBoundsThreads, 0, s, p); break;
     }
-    return e == cudaSuccess ? launch_status() : NVFP4KV_ERR_CUDA;
+    return launched(e);
 }
 
 extern "C" nvfp4kv_status nvfp4_kv_select_pages(
@@ -849,5 +849,5 @@ extern "C" nvfp4kv_status nvfp4_kv_select_pages(
     case 128: e = launch_select_for<128>(p, large, cluster, smem, s); break;
     default: e = launch_select_for<256>(p, large, cluster, smem, s); break;
     }
-    return e == cudaSuccess ? launch_status() : NVFP4KV_ERR_CUDA;
+    return launched(e);
 }

@@ -86,5 +86,5 @@ extern "C" nvfp4kv_status nvfp4_paged_sparse_decode_attention(
     case 128: e = launch_sparse<128>(p, s); break;
     default: e = launch_sparse<256>(p, s); break;
     }
-    return e == cudaSuccess ? NVFP4KV_OK : NVFP4KV_ERR_CUDA;
+    return launched(e);
 }

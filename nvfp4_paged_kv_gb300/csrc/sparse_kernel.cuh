@@ -927,7 +927,7 @@ ClusterPlan choose_clusters(int64_t pairs, int64_t each, int G) {
 template <int D>
 cudaError_t launch_sparse(SparseParams& p, cudaStream_t s) {
     using G_ = Geo<D>;
-    cudaError_t e = cudaFuncSetAttribute(sparse_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(sparse_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          G_::SMEM);
     if (e != cudaSuccess) return e;
     const ClusterPlan plan = choose_clusters<D>(p.B, p.full_each, p.G);
@@ -950,8 +950,7 @@ cudaError_t launch_sparse(SparseParams& p, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = plan.size > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, sparse_split_kernel<D>, static_cast<const SparseParams&>(p));
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, sparse_split_kernel<D>, static_cast<const SparseParams&>(p));
 }
 
 }  // namespace
