@@ -580,19 +580,22 @@ def _refuse(t, name, dtype, numel, dev):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must be of {numel} values, got {t.numel()}")
+    if t.numel() == 0:
+        raise ValueError(f"{name} must hold at least one value")
     raise ValueError(f"{name}: tensors passed to the NVFP4 KV library must be contiguous")
 
 
 def _pointers(dev, *specs):
     """Pointers of the contiguous tensors of device `dev` in `specs`: (tensor or None, name, dtype or
-    None, number of values or None)."""
+    None, number of values or None for one or more: an empty tensor's pointer is null, which the library would take
+    for an argument left out)."""
     out = []
     for t, name, dtype, numel in specs:
         if t is None:
             out.append(None)
             continue
         if (t.get_device() != dev or (dtype is not None and t.dtype != dtype)
-                or (numel is not None and t.numel() != numel) or not t.is_contiguous()):
+                or (t.numel() != numel if numel is not None else t.numel() == 0) or not t.is_contiguous()):
             _refuse(t, name, dtype, numel, dev)
         out.append(t.data_ptr())
     return out
