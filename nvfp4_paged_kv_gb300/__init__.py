@@ -5,7 +5,10 @@ tensors become device pointers, the current torch stream becomes the stream argu
 non-OK status becomes an exception. All arithmetic runs in the library's CUDA kernels; there is
 no CPU path, and importing a function whose library is not built raises.
 
-PyTorch is used for device memory and streams only.
+PyTorch is used for device memory and streams only. `stream` is a torch.cuda.Stream or a raw handle
+(None: the current stream). As with any work on a stream that is not the current one, the caller orders it
+behind what made the tensors, and keeps them until it has run (or calls Tensor.record_stream): a call does
+not extend their lives. Scratch that a call takes itself (workspace=None) needs neither.
 """
 from __future__ import annotations
 

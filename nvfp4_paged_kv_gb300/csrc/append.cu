@@ -14,8 +14,9 @@
 // and reused for every head of the task. Measured: 8192 rows of 32 + 8 + 8 heads of 128 with all outputs
 // (215 MB) 39.4 us, 5.5 TB/s; 32 such rows 3.4 us.
 //
-// A warp task is a row's q and K heads, or its V heads, as many head groups of it as leave 32 warps to an
-// SM.
+// A warp task is a row's q and K heads, or its V heads, as many head groups of it as make about 32 warps to an
+// SM. (q with K, and V, are rounded up to tasks apart, so there can be a few more: 1237 rows of 20 + 4 heads of 256
+// are 4948 tasks for 4864 warps, and 21 CTAs wait for a second wave.)
 // A thread owns 8 dims of each of two 16-value blocks of one head that rotate with one another (block i
 // of the first half with block i of the second, or two neighbouring blocks when adjacent dims pair
 // up), so the rotation needs no other thread, and two neighbouring lanes hold the two blocks: they

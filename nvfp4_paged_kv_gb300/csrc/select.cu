@@ -21,7 +21,9 @@
 // Bounds kernel: 4096 pages of 64 tokens x 8 heads x 128 (160 MB) take 37.0 us, 4.3 TB/s, bound by the
 // conversions of two codes each, the products and the maxima: without any one of the three kinds it would be
 // 2 to 3 us less (with the walk's 64-bit divisions and a ceil by conversions it was 38.9). Halves as large in
-// flight for 32 warps an SM took 39 to 40, three slots 40, a grid of one wave 39.3.
+// flight for 32 warps an SM took 39 to 40, three slots 40, a grid of one wave 39.3. A chunk is copied whole as far
+// as the page goes, whatever page_tokens says (one of few tokens costs the bytes of a chunk); what lies past the
+// tokens is not looked at.
 // Selection kernel: its bytes are few (2 D + 4 per scored page and head) and its time is latency: 256 pairs of 128
 // pages (9 MB) 6.0 us, 64 pairs of up to 2048 pages (22 MB) 12.5 us, of which 2 us until the queries are integers,
 // 3 to 5 us of scores, 3 us of radix passes and 1.5 us of writing the tables.

@@ -13,15 +13,21 @@
 // pages 12.2 us, so 13.6; 256 pairs of 4 pages 7.7 and 11.1, of 16 pages 15.9 and 19.2, of 32 pages 24.2 and 26.3,
 // of 64 pages 39.4 and 37.7.
 //
-// Bound: an SM's rate. A stage (9216 bytes) takes it 0.24 us, with 12 warps at 293 instructions per 16-token tile
-// (39 GB/s each: 5.9 TB/s on all SMs, 0.87 of the copy peak), alone as well as with all others and with K and V in
-// L2. It is the instructions: of 128 pairs of 8192 tokens, 38.7 us, a throwaway copy without the products by the
-// scales took 31.4, without the E2M1 conversions 33.5, without both 30.2 (6.5 TB/s, HBM). 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) take 24.2 us: 6 until the first stages are
+// Bound: an SM's rate. One more stage (9216 bytes) takes it 0.24 us, with 12 warps (39 GB/s each SM: 5.9 TB/s on
+// all of them, 0.87 of the copy peak), alone as well as with all others and with K and V in L2: it is the
+// instructions, 352 to a 16-token tile with start and join (293 in the dense decode's longer runs). Of 128 pairs of
+// 8192 tokens (151 MB in 38.7 us), a throwaway copy without the products by the scales took 31.4, without the E2M1
+// conversions 33.5, without both 30.2 (5.0 TB/s over the whole call).
+// 256 pairs of 2048 tokens (76 MB, 11.2 us at the copy peak) take 24.2 us: 6 until the first stages are
 // computed, 64 stages on the fuller SMs, 1 for the join. 64 pairs of 8192 tokens with 8 heads, on clusters of 2,
 // 24.9 us; 8 pairs of 4096 tokens, on clusters of 8, 9.3 us; 95 ragged pairs with head_dim 256 24.2 us. Measured
 // and slower: one combined record per CTA and pair, runs of unequal length on every warp, 32-token stages (14 to 16
 // warps, or more slots), tiles of a stage worked on two or one at a time, the scores of a stage interleaved with
 // P V of the one before, and the first stage issued before the lengths are compared (no gain).
+//
+// Weights go to P V in FP16, as in the dense decode. Against the same products in FP32, 8 to 9 % of the BF16 outputs
+// are the neighbouring BF16 value, and the root mean square error against 64 bits is 1 % larger (3.05e-4 for 3.02e-4
+// over 256 pairs of 2048 tokens): the output's own rounding is nearly all of it.
 #pragma once
 #include <algorithm>
 #include <atomic>
@@ -38,9 +44,10 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxSparsePairs = 65535;  // (sequence, KV head) pairs of a call
 
 // Microseconds of a call, of both ways to cut it, fitted to measurements of 539 calls (head_dim 64 to 256, 1 to 8
-// heads a pair, 8 to 1024 pairs of 1 to 128 pages of 64 tokens). Runs over all pairs: the stages of an SM, the
+// heads a pair, 8 to 1024 pairs of 1 to 128 pages of 64 tokens; profiles/sparse_cut_times.csv has 924 such calls with
+// every cut's time, taken again). Runs over all pairs: the stages of an SM, the
 // records of the pair that has most, and those that an SM's warps write. Pairs by clusters: rounds of one stage for
-// each warp of the longest pair. The cut chosen took over 5 % longer than the soonest in 8 of the calls, 13 % at most.
+// each warp of the longest pair. The cut chosen took over 5 % longer than the soonest in 13 of the 924, 14 % at most.
 struct Times {
     float all_base, record;            // runs over all pairs: base, and for each record of a pair
     float own_base, own_round, share;  // pairs by clusters: base, for each round, rounds for each stage
@@ -890,7 +897,12 @@ int max_clusters(int size) {  // clusters that run at once
 }
 
 // The clusters that take the least time when every pair has all its pages; single CTAs where runs over all pairs
-// take less, for calls whose pairs turn out shorter.
+// take less, for calls whose pairs turn out shorter. The host does not know the lengths: under a table wider than they
+// are, the clusters it chose can cost more than they save, their barriers on short pairs and the SMs that no cluster
+// covers on uneven ones. Of 84 calls each (8 to 72 pairs, 16 to 256 pages), that was over 5 % of what single CTAs or
+// runs over all SMs take in 50 at a tenth of the width (3.0 us at most, 9.4 for 6.4), 21 at half (2.3), 6 ragged
+// (1.4) and 24 with one long pair (1.7); in the mean of the last three kinds clusters save 0.9 to 1.3 us.
+// (profiles/sparse_cut_times_short.csv)
 template <int D>
 ClusterPlan choose_clusters(int64_t pairs, int64_t each, int G) {
     constexpr int NW = Geo<D>::WARPS;
