@@ -92,6 +92,7 @@ typedef enum nvfp4kv_status {
 #define NVFP4KV_STATUS_BAD_SEQ_LEN 0x2   /* seq_len < 0 or > max_pages_per_seq * T: seq skipped   */
 #define NVFP4KV_STATUS_TIMEOUT 0x4       /* a bounded retry loop on a workspace word gave up       */
 #define NVFP4KV_STATUS_BAD_POSITION 0x8  /* a row's position was outside its table: row skipped    */
+#define NVFP4KV_STATUS_NO_PAGES 0x10     /* too few free pages: a sequence of the step not served  */
 
 typedef enum nvfp4kv_packing {
     NVFP4KV_PACK_DIM_PAIRS = 0,   /* a byte holds two head dims of one token (K cache)          */
@@ -101,7 +102,8 @@ typedef enum nvfp4kv_packing {
 typedef enum nvfp4kv_dtype {
     NVFP4KV_BF16 = 0,
     NVFP4KV_FP16 = 1,
-    NVFP4KV_FP8_E4M3 = 2
+    NVFP4KV_FP8_E4M3 = 2,
+    NVFP4KV_NVFP4 = 3 /* packed codes with block scales: a source of nvfp4_kv_fp8_pages alone */
 } nvfp4kv_dtype;
 
 /* Geometry of one paged K or V tensor. head_dim % 16 == 0; the first three fields > 0. */
@@ -492,6 +494,148 @@ nvfp4kv_status nvfp4_paged_sparse_decode_attention(
     int32_t pool_pages, const int32_t* sel_page_table, int32_t max_sel_pages,
     const int32_t* sel_lens, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
     float* lse, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Page tables and token slots of a step, built on the GPU from the lengths of its requests. The
+ * source pages leave this to the serving framework's scheduler; here the arrays that the other calls
+ * of a step take (page tables, lengths, slots, positions, rows of a sequence, pages that became full)
+ * come from one call that needs no host round trip, so a step can be captured into a graph.
+ *
+ * Sequence b has past_lens[b] = p tokens in the cache and adds new_lens[b] = a of them (0: none; -1:
+ * it ended, its pages are given back and its length becomes 0). With ceil(p / T) pages in its row
+ * of the table it needs n = ceil((p + a) / T) - ceil(p / T) more. free_pages is a stack of page ids,
+ * the first free_count of them free.
+ *   1. The pages of the sequences that ended are pushed on it, in the order of the sequences and of
+ *      their tables (the table rows are left as they are).
+ *   2. Pages are popped from its top, in the order of the sequences, into their tables from entry
+ *      ceil(p / T) on. A sequence that needs pages is served when its needs and those of all sequences
+ *      before it fit into the pages that are left; if not (NO_PAGES) it gets none and keeps its length.
+ *   seq_lens       int32 [batch]: p + a (0 when ended, p when not served; may be past_lens)
+ *   row_starts     int32 [batch + 1]: the first of the step's rows of each sequence (max(a, 0) each, served
+ *                  or not), and their number
+ *   slots          int64 [num_rows]: page * T + token of each row, as nvfp4_kv_append takes them; -1 for the
+ *                  rows of a sequence that is not served and for those behind the last (padding)
+ *   positions      int32 [num_rows]: p, p + 1, ..; 0 where the slot is -1
+ *   full_pages     optional int32 [full_capacity >= batch + num_rows / T]: ids of the pages that became
+ *                  full, in order, then -1: the page_ids of nvfp4_kv_page_bounds
+ *   free_left      int32: free pages after the call (may be free_count)
+ *   free_capacity  entries of free_pages; page ids on it and in the tables are passed on unchecked, and
+ *                  a page must be in one place only. Pages given back past it are lost (PAGE_OOB), as is a
+ *                  free_count outside 0 .. free_capacity, which is taken as the nearer of the two
+ * A length or addition out of range (p < 0, a < -1, p + a > max_pages_per_seq * T) or rows past num_rows
+ * set BAD_SEQ_LEN: the sequence is not served (a bad p counts as 0). Only page_size of the layout is read.
+ * Supported: batch <= 8192.
+ * ------------------------------------------------------------------------------------------ */
+nvfp4kv_status nvfp4_kv_step_tables(
+    const nvfp4kv_layout* layout, int32_t batch, const int32_t* past_lens, const int32_t* new_lens,
+    int32_t* free_pages, int32_t free_capacity, const int32_t* free_count, int32_t* free_left,
+    int32_t* page_table, int32_t max_pages_per_seq, int32_t* seq_lens, int32_t* row_starts,
+    int64_t* slots, int32_t* positions, int32_t num_rows, int32_t* full_pages,
+    int32_t full_capacity, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Pages held in 8 bits with a scale for each page and KV head: the FP8 workspace of the extend path
+ * (LMSYS page, "Path 2") with scales that follow the data, or a cache of its own for layers that 4 bits
+ * do not serve. For every listed page and head, over the page's first page_tokens[i] tokens:
+ *   a = max |x|,  s = fp32(a / 448) (1 where that is below 2^-100),  r = fp32(1 / s)
+ *   code = E4M3_rne_satfinite(fp32(x r)); the codes of the other tokens are 0
+ * A page that grows is encoded again, as a whole, from its 16-bit copy.
+ *   src_dtype      NVFP4KV_BF16, NVFP4KV_FP16: pages [src_pool_pages][H][T][D]; NVFP4KV_NVFP4: packed codes
+ *                  in layout.packing with src_scales, x = fp32(v g) as nvfp4_kv_dequantize_pages has it
+ *   src_global_scale   NVFP4 sources: device scalar g (NULL = 1)
+ *   src_page_ids, dst_page_ids   [num_pages] (NULL = 0 .. num_pages-1); -1 = no page (padding). Two entries
+ *                  with the same destination page race
+ *   page_tokens    [num_pages], 0 .. T (NULL = T for all)
+ *   dst            E4M3 [dst_pool_pages][H][T][D]; must not overlap src
+ *   dst_scales     float [dst_pool_pages][H]: s
+ * A page id outside its pool (PAGE_OOB) or a token count outside 0 .. T (BAD_SEQ_LEN) skips the page.
+ * ------------------------------------------------------------------------------------------ */
+nvfp4kv_status nvfp4_kv_fp8_pages(
+    const nvfp4kv_layout* layout, nvfp4kv_dtype src_dtype, const void* src, const uint8_t* src_scales,
+    const float* src_global_scale, int32_t src_pool_pages, const int32_t* src_page_ids,
+    const int32_t* page_tokens, uint8_t* dst, float* dst_scales, int32_t dst_pool_pages,
+    const int32_t* dst_page_ids, int32_t num_pages, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Attention with a sliding window and first tokens that stay visible: a query at position p of its
+ * sequence sees the tokens t <= p with t > p - window or t < sink_tokens. Pages without a visible token
+ * may have been given back: their table entries are not used.
+ *
+ * nvfp4_paged_window_decode_attention is nvfp4_paged_decode_attention for layers with such a window:
+ * the query of sequence b is its last token, p = seq_lens[b] - 1. window >= 1, sink_tokens >= 0; the other
+ * arguments, numerics and limits are those of that call (max_num_splits: automatic).
+ * ------------------------------------------------------------------------------------------ */
+size_t nvfp4_paged_window_decode_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
+                                                int32_t num_q_heads, int32_t max_pages_per_seq);
+
+nvfp4kv_status nvfp4_paged_window_decode_attention(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_q_heads, const void* q,
+    const uint8_t* k_data, const uint8_t* k_scales, const float* k_global_scale,
+    const uint8_t* v_data, const uint8_t* v_scales, const float* v_global_scale,
+    int32_t pool_pages, const int32_t* page_table, int32_t max_pages_per_seq,
+    const int32_t* seq_lens, int32_t window, int32_t sink_tokens, float sm_scale, void* workspace,
+    size_t workspace_bytes, void* out, float* lse, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * nvfp4_paged_decode_attention over FP8 pages: k_t = e4m3 * k_block_scales[page][head] * k_scale, and v_t
+ * likewise. The same numerics: K and V are exact in FP16, scales are applied to the scores and the weights
+ * in FP32, and the weights are rounded to FP16 before P V.
+ *   k_pages, v_pages               E4M3 [pool_pages][H][T][D], as nvfp4_kv_fp8_pages, nvfp4_kv_extend_step and
+ *                                  nvfp4_kv_dequantize_pages write them
+ *   k_block_scales, v_block_scales float [pool_pages][H], each positive and finite, those of V that one
+ *                                  sequence reads within a factor of 2^90 (NULL = 1)
+ *   k_scale, v_scale               device scalars of the whole tensor, positive (NULL = 1)
+ *   window, sink_tokens            as above; window = 0: none, every token is visible
+ *   workspace      device scratch of nvfp4_paged_fp8_decode_workspace_size(...) bytes; needs no clearing, and
+ *                  calls that can overlap on the GPU must not share it
+ * The other arguments and limits are those of nvfp4_paged_decode_attention.
+ * ------------------------------------------------------------------------------------------ */
+size_t nvfp4_paged_fp8_decode_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
+                                             int32_t num_q_heads, int32_t max_pages_per_seq);
+
+nvfp4kv_status nvfp4_paged_fp8_decode_attention(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_q_heads, const void* q,
+    const uint8_t* k_pages, const float* k_block_scales, const float* k_scale,
+    const uint8_t* v_pages, const float* v_block_scales, const float* v_scale, int32_t pool_pages,
+    const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t window,
+    int32_t sink_tokens, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    float* lse, int32_t* status, nvfp4kv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Attention of an extend step (LMSYS page, "Path 2: Chunked prefill / Extend": the attention that reads the
+ * FP8 workspace of cached prefix and chunk): rows row_starts[b] .. row_starts[b + 1] - 1 of q are the last tokens
+ * of sequence b, so row i of its n has position seq_lens[b] - n + i, and sees the tokens up to its own, all of
+ * them or with a sliding window as above. Sequences of one row (decode) may stand beside others. The pages hold
+ * the chunk's own keys and values too, as nvfp4_kv_extend_step and nvfp4_kv_fp8_pages write them.
+ *   num_rows       rows of q, out and lse. Rows from row_starts[batch] on (padding) are left as they were
+ *   q              BF16, row n at q + n * q_row_stride elements, [heads][D] contiguous in a row; 16-byte
+ *                  aligned, strides multiples of 8 and at least num_q_heads * D
+ *   row_starts     int32 [batch + 1], ascending, as nvfp4_kv_step_tables writes them
+ *   seq_lens       int32 [batch], the chunk included
+ *   k_pages ..     the FP8 pools and their scales, as in nvfp4_paged_fp8_decode_attention, as are window and
+ *                  sink_tokens
+ *   out            BF16, rows as those of q at out_row_stride; must not overlap q
+ *   lse            float [num_rows][num_q_heads] or NULL (natural log)
+ *   workspace      device scratch of nvfp4_paged_extend_attention_workspace_size(...) bytes; needs no clearing,
+ *                  and calls that can overlap on the GPU must not share it
+ * Numerics as in nvfp4_paged_decode_attention: queries and weights in FP16, K and V exact, the rest in FP32.
+ * Rows outside 0 .. num_rows, a length outside [0, max_pages_per_seq * T] and more rows than tokens set BAD_SEQ_LEN:
+ * the sequence's rows, where they lie in range, get out = 0 and lse = -inf. A page id outside the pool sets PAGE_OOB and its
+ * tokens are left out; a row that sees no token gets the same. TIMEOUT: a wait inside the kernel gave up (a defect;
+ * the outputs are incomplete).
+ * Three launches. Supported: head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; page_size % 16 == 0;
+ * batch <= 65535.
+ * ------------------------------------------------------------------------------------------ */
+size_t nvfp4_paged_extend_attention_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
+                                                   int32_t num_q_heads);
+
+nvfp4kv_status nvfp4_paged_extend_attention(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_rows, int32_t num_q_heads, const void* q,
+    int64_t q_row_stride, const int32_t* row_starts, const uint8_t* k_pages, const float* k_block_scales,
+    const float* k_scale, const uint8_t* v_pages, const float* v_block_scales, const float* v_scale,
+    int32_t pool_pages, const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+    int32_t window, int32_t sink_tokens, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    int64_t out_row_stride, float* lse, int32_t* status, nvfp4kv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
  * Cold-page codec ("KV Cache Compression in TensorRT LLM", NVIDIA: "NVFP4 Cold-Page

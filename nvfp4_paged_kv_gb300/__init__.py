@@ -37,13 +37,18 @@ __all__ = [
     "STATUS_BAD_POSITION", "Rotary", "ROTARY_HALVES", "ROTARY_PAIRS", "nvfp4_kv_append",
     "nvfp4_kv_page_bounds", "nvfp4_kv_select_pages", "nvfp4_paged_sparse_decode_workspace_size",
     "nvfp4_paged_sparse_decode_attention",
+    "STATUS_NO_PAGES", "NVFP4", "nvfp4_kv_step_tables", "nvfp4_kv_fp8_pages",
+    "nvfp4_paged_window_decode_workspace_size", "nvfp4_paged_window_decode_attention",
+    "nvfp4_paged_fp8_decode_workspace_size", "nvfp4_paged_fp8_decode_attention",
+    "nvfp4_paged_extend_attention_workspace_size", "nvfp4_paged_extend_attention",
 ]
 NOALLOC_SCRATCH_BYTES = 32 << 20   # NVFP4KV_NOALLOC_SCRATCH_BYTES
 
 BF16, FP16, FP8_E4M3 = 0, 1, 2
+NVFP4 = 3                           # packed codes as a source of nvfp4_kv_fp8_pages
 PACK_DIM_PAIRS, PACK_TOKEN_PAIRS = 0, 1   # nvfp4kv_packing: K pools, V pools of the decode call
 STATUS_PAGE_OOB, STATUS_BAD_SEQ_LEN, STATUS_TIMEOUT = 0x1, 0x2, 0x4
-STATUS_BAD_POSITION = 0x8
+STATUS_BAD_POSITION, STATUS_NO_PAGES = 0x8, 0x10
 _STATUS_NAMES = {1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "CUDA"}
 
 
@@ -175,6 +180,17 @@ def load():
             "nvfp4_kv_select_pages": (I32, [LP, I32, I32, P, P, P, I32, P, I32, P, I32, I32, I32, P,
                                             P, P, P, P, P]),
             "nvfp4_paged_sparse_decode_workspace_size": (SZ, [LP, I32, I32, I32]),
+            "nvfp4_kv_step_tables": (I32, [LP, I32, P, P, P, I32, P, P, P, I32, P, P, P, P, I32, P, I32, P, P]),
+            "nvfp4_kv_fp8_pages": (I32, [LP, I32, P, P, P, I32, P, P, P, P, I32, P, I32, P, P]),
+            "nvfp4_paged_window_decode_workspace_size": (SZ, [LP, I32, I32, I32]),
+            "nvfp4_paged_window_decode_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, P, I32, P, I32, P, I32,
+                                                          I32, F, P, SZ, P, P, P, P]),
+            "nvfp4_paged_fp8_decode_workspace_size": (SZ, [LP, I32, I32, I32]),
+            "nvfp4_paged_fp8_decode_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, P, I32, P, I32, P, I32, I32,
+                                                       F, P, SZ, P, P, P, P]),
+            "nvfp4_paged_extend_attention_workspace_size": (SZ, [LP, I32, I32]),
+            "nvfp4_paged_extend_attention": (I32, [LP, I32, I32, I32, P, I64, P, P, P, P, P, P, P, I32, P, I32, P, I32, I32,
+                                                   F, P, SZ, P, I64, P, P, P]),
             "nvfp4_paged_sparse_decode_attention": (I32, [LP, I32, I32, P, P, P, P, P, P, P, I32, P,
                                                           I32, P, F, P, SZ, P, P, P, P]),
         }
@@ -762,4 +778,166 @@ def nvfp4_paged_sparse_decode_attention(layout: Layout, q: torch.Tensor, k_data,
     _run("nvfp4_paged_sparse_decode_attention", dev, stream, layout, B, hq, qp, kd, ks, gk, vd, vs, gv,
          pages, tp, max_sel, lp, float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol,
          st)
+    return out
+
+
+# ------------------------------------------------------------------------------ steps, 8-bit pages, windows
+
+def nvfp4_kv_step_tables(layout: Layout, past_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                         free_count: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                         row_starts: torch.Tensor, slots: torch.Tensor, positions: torch.Tensor, *, free_left=None,
+                         full_pages=None, status=None, stream=None):
+    """Page tables and token slots of a step from the lengths of its requests: `past_lens` (tokens cached) and `new_lens`
+    (to add; -1: ended) int32 [B]. `free_pages` int32 is a stack of page ids with `free_count` (int32, one value) of them
+    free; pages of sequences that ended are pushed on it, new ones popped into `page_table` [B, max pages] int32. Writes
+    `seq_lens` [B] (may be past_lens), `row_starts` [B + 1] int32, `slots` int64 and `positions` int32 of the step's rows
+    (-1 and 0: no row), `free_left` (None: free_count) and optionally `full_pages` int32, the pages that became full,
+    then -1, of B + rows // page_size entries or more."""
+    B, maxp, rows = past_lens.shape[0], page_table.shape[-1], slots.shape[0]
+    left = free_count if free_left is None else free_left
+    dev = _first_device(past_lens, "past_lens")
+    pp, np_, cp, lp, tp, sl, rs, st = _pointers(
+        dev, (past_lens, "past_lens", _I32, B), (new_lens, "new_lens", _I32, B), (free_count, "free_count", _I32, 1),
+        (left, "free_left", _I32, 1), (page_table, "page_table", _I32, B * maxp), (seq_lens, "seq_lens", _I32, B),
+        (row_starts, "row_starts", _I32, B + 1), (status, "status", _I32, None))
+    capacity, fulls = free_pages.numel(), 0 if full_pages is None else full_pages.numel()
+    fp, sp, op, up = _pointers(dev, (free_pages, "free_pages", _I32, capacity), (slots, "slots", _I64, rows),
+                               (positions, "positions", _I32, rows), (full_pages, "full_pages", _I32, fulls))
+    _run("nvfp4_kv_step_tables", dev, stream, layout, B, pp, np_, fp, capacity, cp, lp, tp, maxp, sl, rs, sp, op, rows, up,
+         fulls, st)
+
+
+def nvfp4_kv_fp8_pages(layout: Layout, src: torch.Tensor, dst: torch.Tensor, dst_scales: torch.Tensor, *,
+                       src_scales=None, global_scale=None, src_page_ids=None, dst_page_ids=None, page_tokens=None,
+                       num_pages=None, status=None, stream=None):
+    """Encode pages as FP8 E4M3 with a scale for each page and head: `src` [pool, H, T, D] BF16 / FP16, or NVFP4 codes
+    (uint8, packed as `layout` says) with `src_scales` and the tensor's `global_scale`. Writes `dst` [pool, H, T, D]
+    (float8_e4m3fn or uint8) and `dst_scales` [pool, H] float32. `page_tokens` (int32, one per listed page) counts the
+    page's valid tokens (None: all); the others become 0. A page id of -1 is padding."""
+    H, D, T = layout.num_kv_heads, layout.head_dim, layout.page_size
+    src_pages, dst_pages = src.shape[0], dst.shape[0]
+    if num_pages is None:
+        ids = dst_page_ids if src_page_ids is None else src_page_ids
+        num_pages = src_pages if ids is None else ids.numel()
+    num = int(num_pages)
+    values = src_pages * H * T * D
+    if src_scales is not None:
+        code, kind, count = NVFP4, _U8, values // 2
+    else:
+        code, kind, count = _CODES.get(src.dtype, -1), None, values
+    if dst.element_size() != 1:
+        raise TypeError(f"dst must be float8_e4m3fn or uint8, got {dst.dtype}")
+    dev = _first_device(src, "src")
+    sp, ss, gp, ip, tp, dp, ds, op, st = _pointers(
+        dev, (src, "src", kind, count), (src_scales, "src_scales", _U8, values // 16),
+        (global_scale, "global_scale", _F32, 1), (src_page_ids, "src_page_ids", _I32, num),
+        (page_tokens, "page_tokens", _I32, num), (dst, "dst", None, dst_pages * H * T * D),
+        (dst_scales, "dst_scales", _F32, dst_pages * H), (dst_page_ids, "dst_page_ids", _I32, num),
+        (status, "status", _I32, None))
+    _run("nvfp4_kv_fp8_pages", dev, stream, layout, code, sp, ss, gp, src_pages, ip, tp, dp, ds, dst_pages, op, num, st)
+
+
+def nvfp4_paged_window_decode_workspace_size(layout: Layout, batch: int, num_q_heads: int, max_pages_per_seq: int) -> int:
+    return int(load().nvfp4_paged_window_decode_workspace_size(
+        ctypes.byref(layout), int(batch), int(num_q_heads), int(max_pages_per_seq)))
+
+
+def nvfp4_paged_window_decode_attention(layout: Layout, q: torch.Tensor, k_data, k_scales, k_global_scale, v_data,
+                                        v_scales, v_global_scale, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                                        sm_scale: float, out: torch.Tensor, *, window: int, sink_tokens: int = 0,
+                                        lse=None, workspace=None, status=None, stream=None):
+    """The decode attention over the last `window` tokens of each sequence and its first `sink_tokens`. Table entries of
+    pages without such a token are not used."""
+    H, D = layout.num_kv_heads, layout.head_dim
+    B, hq = q.shape[0], q.shape[1]
+    pages, maxp = k_data.shape[0], page_table.shape[-1]
+    codes = pages * H * D * layout.page_size // 2
+    dev = _first_device(q, "q")
+    qp, kd, ks, gk, vd, vs, gv, tp, lp, op, ol, st = _pointers(
+        dev, (q, "q", _BF16, B * hq * D), (k_data, "k_data", _U8, codes), (k_scales, "k_scales", _U8, codes // 8),
+        (k_global_scale, "k_global_scale", _F32, None), (v_data, "v_data", _U8, codes),
+        (v_scales, "v_scales", _U8, codes // 8), (v_global_scale, "v_global_scale", _F32, None),
+        (page_table, "page_table", _I32, B * maxp), (seq_lens, "seq_lens", _I32, B), (out, "out", _BF16, B * hq * D),
+        (lse, "lse", _F32, B * hq), (status, "status", _I32, None))
+    if workspace is None:
+        need = nvfp4_paged_window_decode_workspace_size(layout, B, hq, maxp)
+        workspace = _scratch(max(need, 16), q.device, stream)
+    wp, = _pointers(dev, (workspace, "workspace", None, None))
+    _run("nvfp4_paged_window_decode_attention", dev, stream, layout, B, hq, qp, kd, ks, gk, vd, vs, gv, pages, tp, maxp, lp,
+         int(window), int(sink_tokens), float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol, st)
+    return out
+
+
+def _fp8_pools(layout, dev, k_pages, v_pages, k_block_scales, v_block_scales, k_scale, v_scale):
+    """Pointers of FP8 pools and their scales, and the pages in a pool."""
+    H, pages = layout.num_kv_heads, k_pages.shape[0]
+    if k_pages.element_size() != 1 or v_pages.element_size() != 1:
+        raise TypeError(f"FP8 pages must be float8_e4m3fn or uint8, got {k_pages.dtype} and {v_pages.dtype}")
+    values = pages * H * layout.page_size * layout.head_dim
+    return _pointers(
+        dev, (k_pages, "k_pages", None, values), (k_block_scales, "k_block_scales", _F32, pages * H),
+        (k_scale, "k_scale", _F32, 1), (v_pages, "v_pages", None, values),
+        (v_block_scales, "v_block_scales", _F32, pages * H), (v_scale, "v_scale", _F32, 1)), pages
+
+
+def nvfp4_paged_fp8_decode_workspace_size(layout: Layout, batch: int, num_q_heads: int, max_pages_per_seq: int) -> int:
+    return int(load().nvfp4_paged_fp8_decode_workspace_size(
+        ctypes.byref(layout), int(batch), int(num_q_heads), int(max_pages_per_seq)))
+
+
+def nvfp4_paged_fp8_decode_attention(layout: Layout, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                     page_table: torch.Tensor, seq_lens: torch.Tensor, sm_scale: float,
+                                     out: torch.Tensor, *, k_block_scales=None, v_block_scales=None, k_scale=None,
+                                     v_scale=None, window: int = 0, sink_tokens: int = 0, lse=None, workspace=None,
+                                     status=None, stream=None):
+    """The decode attention over FP8 E4M3 pages `k_pages`, `v_pages` [pool, H, T, D] with scales for each page and head
+    (`*_block_scales` [pool, H] float32) and for the tensor (`*_scale`, one float32). With `window` > 0 over the last
+    `window` tokens and the first `sink_tokens`."""
+    D = layout.head_dim
+    B, hq = q.shape[0], q.shape[1]
+    maxp = page_table.shape[-1]
+    dev = _first_device(q, "q")
+    (kp, kb, ks, vp, vb, vs), pages = _fp8_pools(layout, dev, k_pages, v_pages, k_block_scales, v_block_scales, k_scale, v_scale)
+    qp, tp, lp, op, ol, st = _pointers(
+        dev, (q, "q", _BF16, B * hq * D), (page_table, "page_table", _I32, B * maxp), (seq_lens, "seq_lens", _I32, B),
+        (out, "out", _BF16, B * hq * D), (lse, "lse", _F32, B * hq), (status, "status", _I32, None))
+    if workspace is None:
+        need = nvfp4_paged_fp8_decode_workspace_size(layout, B, hq, maxp)
+        workspace = _scratch(max(need, 16), q.device, stream)
+    wp, = _pointers(dev, (workspace, "workspace", None, None))
+    _run("nvfp4_paged_fp8_decode_attention", dev, stream, layout, B, hq, qp, kp, kb, ks, vp, vb, vs, pages, tp, maxp, lp,
+         int(window), int(sink_tokens), float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, ol, st)
+    return out
+
+
+def nvfp4_paged_extend_attention_workspace_size(layout: Layout, batch: int, num_q_heads: int) -> int:
+    return int(load().nvfp4_paged_extend_attention_workspace_size(ctypes.byref(layout), int(batch), int(num_q_heads)))
+
+
+def nvfp4_paged_extend_attention(layout: Layout, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                                 page_table: torch.Tensor, seq_lens: torch.Tensor, row_starts: torch.Tensor,
+                                 sm_scale: float, out: torch.Tensor, *, k_block_scales=None, v_block_scales=None,
+                                 k_scale=None, v_scale=None, window: int = 0, sink_tokens: int = 0, lse=None,
+                                 workspace=None, status=None, stream=None):
+    """Causal attention of a step's rows `q` [rows, Hq, D] BF16 (rows may be strided) over FP8 pages: rows
+    row_starts[b] .. row_starts[b + 1] (int32 [B + 1]) are the last tokens of sequence b, of `seq_lens` [B] tokens with
+    them. `out` [rows, Hq, D] BF16, `lse` [rows, Hq] float32; rows behind the last sequence are left as they were.
+    Pools, scales, `window` and `sink_tokens` as in nvfp4_paged_fp8_decode_attention."""
+    D = layout.head_dim
+    rows, hq = q.shape[0], q.shape[1]
+    B, maxp = seq_lens.shape[0], page_table.shape[-1]
+    if q.dtype != _BF16 or out.dtype != _BF16:
+        raise TypeError(f"q and out must be bfloat16, got {q.dtype} and {out.dtype}")
+    dev = _first_device(q, "q")
+    (kp, kb, ks, vp, vb, vs), pages = _fp8_pools(layout, dev, k_pages, v_pages, k_block_scales, v_block_scales, k_scale, v_scale)
+    tp, lp, rp, ol, st = _pointers(
+        dev, (page_table, "page_table", _I32, B * maxp), (seq_lens, "seq_lens", _I32, B),
+        (row_starts, "row_starts", _I32, B + 1), (lse, "lse", _F32, rows * hq), (status, "status", _I32, None))
+    qp, qs = _rows(q, "q", rows, hq, D, dev)
+    op, os_ = _rows(out, "out", rows, hq, D, dev)
+    if workspace is None:
+        workspace = _scratch(max(nvfp4_paged_extend_attention_workspace_size(layout, B, hq), 16), q.device, stream)
+    wp, = _pointers(dev, (workspace, "workspace", None, None))
+    _run("nvfp4_paged_extend_attention", dev, stream, layout, B, rows, hq, qp, qs, rp, kp, kb, ks, vp, vb, vs, pages, tp, maxp,
+         lp, int(window), int(sink_tokens), float(sm_scale), wp, workspace.numel() * workspace.element_size(), op, os_, ol, st)
     return out

@@ -1,0 +1,1008 @@
+// Attention of an extend step: the rows of each sequence's chunk over its FP8 pages, causal, with an optional sliding
+// window and first tokens that stay visible (LMSYS, "Accelerating Long-Context and Agentic Inference with NVFP4 KV
+// Cache": "Path 2: Chunked prefill / Extend", whose attention reads the FP8 workspace).
+//
+// Work. The query heads of a KV head share its keys, so a tile of M = 128 rows holds floor(128 / G) tokens times the G
+// heads of a group. A unit is a block of such rows (two tiles at head_dim 64 and 128, one at 256) of one sequence and KV
+// head; its work is the list of KV tiles (128 tokens, 64 at head_dim 256) that hold a token visible to a row of it. The
+// tiles of all units form one list, cut into equal parts, one per SM: a part that begins or ends inside a unit leaves a
+// partial result (row maxima, sums, unnormalised output) that a second kernel joins. Cuts close to a unit's border are
+// moved onto it. The cuts are made on the GPU, from the lengths, by a kernel before it (plan_kernel).
+//
+// A CTA per SM, with a role for each warp:
+//  * 4 loader warps bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so they are
+//    loaded there directly, one tile ahead of the conversion, and stored in the 128-byte-swizzled layout that tcgen05.mma
+//    reads: K with the head dims contiguous (K-major), V with the same store and read as MN-major.
+//  * 1 warp issues S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), P read from TMEM where it
+//    lies over the scores it came from.
+//  * 4 softmax warps per tile, one row a thread, so that row maxima and sums need no exchange. While one tile's weights are
+//    made the tensor core works on the other's products; at head_dim 256 the next KV tile's scores are under way instead.
+// The running maximum moves only when it grows by more than 2^8, so rescaling O in TMEM is rare.
+//
+// Scales. With a page's scales s_K, s_V, a score becomes x = S c s_K + log2(s_V) in log2 units, so that p = 2^(x - m) is the
+// weight times s_V, as the sum over V needs it, with one FMA and one 2^x an element; the sum of the weights takes p / s_V. Q is
+// brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest).
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "host_util.h"
+
+using namespace nvfp4kv;
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.0f;  // log2 units
+constexpr int kMaxGroup = 8;
+constexpr int kRowsM = 128;       // rows of a tile
+constexpr int kLoaderWarps = 4;
+constexpr int kUnitCost = 1;      // of a unit beside its tiles: queries in, outputs out (in tiles)
+constexpr long long kWaitClocks = 8000000000ll;  // a wait gives up after about 4 s (a defect: no wait depends on another CTA)
+
+template <int D>
+struct Shape {
+    static constexpr int MT = D == 256 ? 1 : 2;      // row tiles of a unit
+    static constexpr int TK = D == 256 ? 64 : 128;   // tokens of a KV tile
+    static constexpr int GRP = TK / 16;              // 16-token groups, each in one page
+    static constexpr int BLOCKS = D / 64;            // 128-byte columns of a 16-bit row
+    static constexpr int QB = kRowsM * D * 2;        // bytes of a tile's queries
+    static constexpr int KB = TK * D * 2;            // bytes of a tile of K or V
+    static constexpr int STAGES = 2;
+    static constexpr int K_OFF = MT * QB;
+    static constexpr int V_OFF = K_OFF + STAGES * KB;
+    static constexpr int SMEM = V_OFF + STAGES * KB + 1024;  // the base is rounded up to 1024
+    static constexpr int SOFT_WARPS = 4 * MT;
+    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 1;
+    static constexpr int THREADS = WARPS * 32;
+    // TMEM columns: two score slots, then the outputs
+    static constexpr int S_COL = TK;                 // columns of a slot
+    static constexpr int O_COL = 2 * S_COL;
+    static_assert(O_COL + MT * D <= 512, "TMEM");
+    static_assert(SMEM <= 232448 - 1024, "shared memory");
+};
+
+struct PlanEntry {
+    int64_t cut;     // first position of this CTA in the list of units and tiles
+    int64_t begin;   // of the unit that holds it: its first position ...
+    int64_t end;     // ... and its end
+    int32_t b, h, qb, tile;  // the unit, and the first tile
+};
+
+struct ExtendParams {
+    const uint16_t* q;
+    const uint8_t* k;
+    const uint8_t* v;
+    const float* kbs;
+    const float* vbs;
+    const float* gk;
+    const float* gv;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* starts;
+    uint16_t* out;
+    float* lse;
+    int32_t* status;
+    PlanEntry* plan;    // [ctas + 1]
+    int64_t* cost;      // [B + 1] first position of each sequence
+    float* rec_o;       // [2 ctas][MT * 128][D]
+    float2* rec_ml;     // [2 ctas][MT * 128]
+    int64_t q_stride, out_stride;
+    uint64_t t_magic;
+    int32_t B, rows, Hq, H, G, T, pool_pages, max_pages, window, sinks, ctas;
+    float sm_scale;
+};
+
+// ------------------------------------------------------------------------------------------ what a unit is
+
+// A sequence's rows [first, first + n) and length; n = 0 for one without rows or with lengths out of range.
+struct Seq {
+    int first, n, len;
+    bool bad;
+};
+__device__ __forceinline__ Seq sequence(const ExtendParams& p, int b) {
+    const int a = __ldg(p.starts + b), e = __ldg(p.starts + b + 1), len = __ldg(p.lens + b);
+    Seq s{a, e - a, len, false};
+    if (a < 0 || e < a || e > p.rows) return Seq{0, 0, 0, true};
+    if (len < 0 || len > p.max_pages * p.T || s.n > len) {
+        s.bad = true;
+        s.n = 0;
+    }
+    return s;
+}
+
+// Block qb of a sequence's rows: tokens [t0, t1) of the chunk, and its KV tiles: `sink` tiles of the first tokens, then
+// those from `first` on.
+struct Unit {
+    int t0, t1;    // tokens of the chunk
+    int lo, hi;    // tokens [lo, hi) of the sequence, and the first `sinks`, are visible to a row of it
+    int sink, first, tiles;
+};
+template <int D>
+__device__ __forceinline__ Unit unit_of(const ExtendParams& p, const Seq& s, int qb) {
+    using G_ = Shape<D>;
+    const int each = G_::MT * (kRowsM / p.G);
+    Unit u;
+    u.t0 = qb * each;
+    u.t1 = min(s.n, u.t0 + each);
+    const int p0 = s.len - s.n + u.t0;
+    u.hi = s.len - s.n + u.t1;
+    u.lo = p0 >= p.window ? p0 - p.window + 1 : 0;
+    u.sink = (min(p.sinks, u.lo) + G_::TK - 1) / G_::TK;
+    u.first = max(u.lo / G_::TK, u.sink);
+    u.tiles = u.sink + (u.hi + G_::TK - 1) / G_::TK - u.first;
+    return u;
+}
+template <int D>
+__device__ __forceinline__ int blocks_of(const ExtendParams& p, int n) {
+    const int each = Shape<D>::MT * (kRowsM / p.G);
+    return (n + each - 1) / each;
+}
+template <int D>
+__device__ __forceinline__ int tile_start(const Unit& u, int j) {
+    return (j < u.sink ? j : j - u.sink + u.first) * Shape<D>::TK;
+}
+
+// ------------------------------------------------------------------------------------------ the cuts
+
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// One CTA: positions of the sequences in the list, then the cut of each CTA of the attention, a warp each.
+template <int D>
+__global__ void __launch_bounds__(1024, 1) plan_kernel(const ExtendParams p) {
+    pdl_enter();
+    __shared__ int64_t part[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // positions of one sequence and one KV head, a warp per sequence
+    for (int b = warp; b < p.B; b += 32) {
+        const Seq s = sequence(p, b);
+        if (s.bad && lane == 0) flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
+        int64_t sum = 0;
+        const int nqb = blocks_of<D>(p, s.n);
+        for (int qb = lane; qb < nqb; qb += 32) sum += unit_of<D>(p, s, qb).tiles + kUnitCost;
+        sum = warp_sum64(sum);
+        if (lane == 0) p.cost[b] = sum;
+    }
+    __syncthreads();
+    const int each = (p.B + 1023) / 1024, b_lo = min(p.B, tid * each), b_hi = min(p.B, b_lo + each);
+    int64_t local = 0;
+    for (int b = b_lo; b < b_hi; ++b) local += p.cost[b] * p.H;
+    int64_t incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    int64_t at = incl - local, total = 0;
+    for (int w = 0; w < 32; ++w) {
+        if (w < warp) at += part[w];
+        total += part[w];
+    }
+    __syncthreads();
+    for (int b = b_lo; b < b_hi; ++b) {
+        const int64_t c = p.cost[b] * p.H;
+        p.cost[b] = at;
+        at += c;
+    }
+    if (tid == 0) p.cost[p.B] = total;
+    __threadfence_block();
+    __syncthreads();
+
+    // the unit at position x (< total), a warp together
+    auto find = [&](int64_t x) {
+        PlanEntry e{};
+        int lo = 0, hi = p.B;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.cost[mid] <= x) lo = mid; else hi = mid;
+        }
+        const Seq s = sequence(p, lo);
+        const int64_t per_head = (p.cost[lo + 1] - p.cost[lo]) / p.H;
+        e.b = lo;
+        e.h = static_cast<int>((x - p.cost[lo]) / per_head);
+        const int64_t head = p.cost[lo] + e.h * per_head;
+        const int nqb = blocks_of<D>(p, s.n);
+        int64_t base = head;
+        for (int q0 = 0; q0 < nqb; q0 += 32) {
+            const int64_t c = q0 + lane < nqb ? unit_of<D>(p, s, q0 + lane).tiles + kUnitCost : 0;
+            int64_t inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            const uint32_t in = __ballot_sync(0xFFFFFFFFu, c > 0 && x < base + inc);
+            if (in) {
+                const int l = __ffs(static_cast<int>(in)) - 1;
+                e.qb = q0 + l;
+                e.end = base + __shfl_sync(0xFFFFFFFFu, inc, l);
+                e.begin = e.end - __shfl_sync(0xFFFFFFFFu, c, l);
+                break;
+            }
+            base += __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        return e;
+    };
+    const int64_t share = (total + p.ctas - 1) / p.ctas, slack = share / 8;
+    for (int c = warp; c <= p.ctas; c += 32) {
+        int64_t x = min(total, share * c);
+        PlanEntry e{};
+        e.cut = e.begin = e.end = x;
+        if (x < total) {
+            e = find(x);
+            if (x - e.begin <= max(slack, static_cast<int64_t>(kUnitCost))) {
+                x = e.begin;
+            } else if (e.end - x <= slack) {
+                x = e.end;
+                if (x < total) e = find(x);
+                else e.begin = e.end = x;
+            }
+            e.cut = x;
+            e.tile = static_cast<int32_t>(max(static_cast<int64_t>(0), x - e.begin - kUnitCost));
+        }
+        if (lane == 0) p.plan[c] = e;
+    }
+}
+
+// The pieces of a CTA's part, in order: every role walks over the same ones.
+template <int D>
+struct Walk {
+    int64_t pos, end, unit_begin;
+    int b, h, qb, tile0, piece_tiles;
+    Seq s;
+    Unit u;
+    __device__ __forceinline__ void start(const ExtendParams& p) {
+        const PlanEntry* e = p.plan + blockIdx.x;
+        pos = e->cut;
+        end = e[1].cut;
+        unit_begin = e->begin;
+        b = e->b;
+        h = e->h;
+        qb = e->qb;
+        tile0 = e->tile;
+        if (pos < end) {
+            s = sequence(p, b);
+            measure(p);
+        }
+    }
+    __device__ __forceinline__ void measure(const ExtendParams& p) {
+        u = unit_of<D>(p, s, qb);
+        const int64_t unit_end = unit_begin + kUnitCost + u.tiles;
+        piece_tiles = unit_end <= end ? u.tiles - tile0 : static_cast<int>(end - unit_begin - kUnitCost) - tile0;
+    }
+    __device__ __forceinline__ bool more() const { return pos < end; }
+    __device__ __forceinline__ bool whole() const { return tile0 == 0 && piece_tiles == u.tiles; }
+    __device__ __forceinline__ void next(const ExtendParams& p) {
+        unit_begin += kUnitCost + u.tiles;
+        pos = unit_begin;
+        tile0 = 0;
+        if (pos >= end) return;
+        if (++qb >= blocks_of<D>(p, s.n)) {
+            qb = 0;
+            if (++h == p.H) {
+                h = 0;
+                do s = sequence(p, ++b);
+                while (s.n == 0);
+            }
+        }
+        measure(p);
+    }
+};
+
+// ------------------------------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("{\n\t.reg .b64 s;\n\tmbarrier.arrive.shared::cta.b64 s, [%0];\n\t}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Waits for the phase of this parity; false when the wait, or another role's, has given up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (*dead) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// The same for a whole warp: all lanes go on together, or none.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead));
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand of tcgen05.mma: 128-byte swizzle, start address and byte offsets in units of 16. For K-major
+// operands `stride` is the distance of 8-row groups; for MN-major ones `lead` that of 64-element columns and `stride`
+// that of groups of 8 along K.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
+           static_cast<uint64_t>(stride >> 4) << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
+}
+// Instruction descriptor: FP16 operands, FP32 accumulators, M = 128, N; B K-major or MN-major.
+__host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n) >> 3) << 17 | (128u >> 4) << 24;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+// 32 columns of this warp's lanes (with the wait: nothing may use the registers before it).
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ uint4 ldg16(const void* p) {
+    uint4 r;
+    asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ float scalar_or_1(const float* p) { return p ? __ldg(p) : 1.0f; }
+
+// ------------------------------------------------------------------------------------------ the attention
+
+struct Shared {
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
+    uint64_t qfull[2], sfull[2], pfull[2], ofull[2];
+    uint64_t drained;
+    float4 scales[4][8];  // (s_K, log2 s_V, 1 / s_V) of a KV tile's groups, in a ring of tiles
+    uint32_t tmem;
+    int dead;
+};
+
+// The loader's threads: warp w takes row groups of 8 tokens w, w + 4, ..; a lane one 16-byte chunk of one row of it, so
+// that the eight lanes of a store phase lie in rows 0, 1, 4, 5 (or 2, 3, 6, 7) and two neighbouring chunks and hit distinct banks.
+template <int D>
+__device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, uint32_t kbuf, uint32_t vbuf, int warp, int lane) {
+    using S_ = Shape<D>;
+    constexpr int RG = S_::TK / 8 / kLoaderWarps;  // row groups of a warp
+    constexpr int N = RG * S_::BLOCKS;             // chunks of a lane
+    const int r8 = ((lane >> 1) & 1) | ((lane >> 3) & 1) << 1 | ((lane >> 2) & 1) << 2;
+    const int ch = (lane & 1) | (lane >> 4) << 1;
+    const uint32_t at0 = static_cast<uint32_t>(r8 * 128 + (((2 * ch) ^ r8) << 4));
+    volatile int* dead = &sh.dead;
+    const int64_t head_stride = static_cast<int64_t>(p.T) * D;
+
+    Walk<D> w;
+    w.start(p);
+    if (!w.more()) return;
+    // the next tile's page ids are loaded before the current tile's values: lane l < GRP has the page of group l
+    struct Tile {
+        int t0, page;  // first token; page of group `lane`, -1: none, or none visible
+        int lo, hi, h;
+    };
+    int j = 0;  // tile within the piece
+    auto look = [&]() {
+        Tile t;
+        t.t0 = tile_start<D>(w.u, w.tile0 + j);
+        t.lo = w.u.lo;
+        t.hi = w.u.hi;
+        t.h = w.h;
+        t.page = -1;
+        const int a = t.t0 + 16 * lane;
+        if (lane < S_::GRP && a < t.hi && (a + 15 >= t.lo || a < p.sinks)) {
+            const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(a), p.t_magic));
+            t.page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + idx);
+            if (t.page < 0 || t.page >= p.pool_pages) {
+                flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
+                t.page = -1;
+            }
+        }
+        return t;
+    };
+    auto advance = [&]() {  // to the next tile; false at the end
+        if (++j < w.piece_tiles) return true;
+        j = 0;
+        w.next(p);
+        return w.more();
+    };
+    auto load = [&](const Tile& t, const uint8_t* pool, uint4 (&r)[N]) {
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            const int rg = warp + kLoaderWarps * g, row = rg * 8 + r8, tok = t.t0 + row;
+            const int pg = __shfl_sync(0xFFFFFFFFu, t.page, rg >> 1);
+            const bool ok = pg >= 0 && tok < t.hi && (tok >= t.lo || tok < p.sinks);
+            const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(tok), p.t_magic));
+            const uint8_t* src = pool + (static_cast<int64_t>(pg) * p.H + t.h) * head_stride + static_cast<int64_t>(tok - idx * p.T) * D + 16 * ch;
+#pragma unroll
+            for (int c = 0; c < S_::BLOCKS; ++c) r[g * S_::BLOCKS + c] = ok ? ldg16(src + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto store = [&](uint32_t buf, const uint4 (&r)[N]) {
+#pragma unroll
+        for (int g = 0; g < RG; ++g)
+#pragma unroll
+            for (int c = 0; c < S_::BLOCKS; ++c) {
+                const uint4 x = r[g * S_::BLOCKS + c];
+                const uint32_t at = buf + c * (S_::TK * 128) + (warp + kLoaderWarps * g) * 1024 + at0;
+                uint32_t a[2], b[2];
+                e4m3x4_to_f16x2x2(x.x, a);
+                e4m3x4_to_f16x2x2(x.y, b);
+                sts16(at, a[0], a[1], b[0], b[1]);
+                e4m3x4_to_f16x2x2(x.z, a);
+                e4m3x4_to_f16x2x2(x.w, b);
+                sts16(at ^ 16u, a[0], a[1], b[0], b[1]);
+            }
+    };
+
+    Tile now = look();
+    uint4 rk[N], rv[N];
+    load(now, p.k, rk);
+    for (uint32_t n = 0;; ++n) {
+        const uint32_t stage = n & 1u, phase = (n >> 1) & 1u;
+        load(now, p.v, rv);
+        float sk = 1.0f, sv = 1.0f;
+        if (warp == 0 && now.page >= 0) {
+            const int64_t at = static_cast<int64_t>(now.page) * p.H + now.h;
+            if (p.kbs) sk = __ldg(p.kbs + at);
+            if (p.vbs) sv = __ldg(p.vbs + at);
+        }
+        if (!warp_wait(smem_u32(&sh.kempty[stage]), phase ^ 1u, dead)) return;
+        // the groups' scales: the products of tile n - 2 are done, so the weights of tile n - 4 have been made
+        if (warp == 0 && lane < S_::GRP)
+            sh.scales[n & 3u][lane] = now.page >= 0 ? make_float4(sk, log2f(sv), 1.0f / sv, 0.0f)
+                                                    : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
+        store(kbuf + stage * S_::KB, rk);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.kfull[stage]));
+        const bool more = advance();
+        Tile then = now;
+        if (more) {
+            then = look();
+            load(then, p.k, rk);
+        }
+        if (!warp_wait(smem_u32(&sh.vempty[stage]), phase ^ 1u, dead)) return;
+        store(vbuf + stage * S_::KB, rv);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.vfull[stage]));
+        if (!more) return;
+        now = then;
+    }
+}
+
+// The thread that issues the products.
+template <int D>
+__device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem) {
+    using S_ = Shape<D>;
+    volatile int* dead = &sh.dead;
+    constexpr uint32_t qk = instruction(S_::TK, false), pv = instruction(D, true);
+    uint32_t kn = 0, vn = 0;        // K and V tiles taken
+    uint32_t units = 0, units1 = 0;  // units of row tile 0, 1
+    uint32_t pn[2] = {0, 0};        // weights taken of slot 0, 1
+    Walk<D> w;
+    w.start(p);
+    auto scores = [&](int tile, int slot, uint32_t kstage) {
+        const uint32_t a = qbuf + tile * S_::QB, b = kbuf + kstage * S_::KB;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+            mma_ss(tmem + slot * S_::S_COL, operand(a + (ks / 4) * (kRowsM * 128) + (ks % 4) * 32, 16, 1024),
+                   operand(b + (ks / 4) * (S_::TK * 128) + (ks % 4) * 32, 16, 1024), qk, ks > 0);
+        tc_commit(smem_u32(&sh.sfull[slot]));
+    };
+    auto weighted = [&](int tile, int slot, uint32_t vstage, bool first) {
+        const uint32_t b = vbuf + vstage * S_::KB;
+#pragma unroll
+        for (int ks = 0; ks < S_::TK / 16; ++ks)
+            mma_ts(tmem + S_::O_COL + tile * D, tmem + slot * S_::S_COL + 8 * ks, operand(b + ks * 2048, S_::TK * 128, 1024), pv,
+                   !first || ks > 0);
+        tc_commit(smem_u32(&sh.ofull[tile]));
+    };
+    for (; w.more(); w.next(p)) {
+        const int n = w.piece_tiles;
+        const int tiles = (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G) ? 2 : 1;
+        if (!mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
+        for (int x = 0; x < tiles; ++x) {
+            uint32_t& un = x ? units1 : units;
+            if (!mbar_wait(smem_u32(&sh.qfull[x]), un & 1u, dead)) return;
+            ++un;
+            tc_after();
+            scores(x, S_::MT == 2 ? x : static_cast<int>(kn & 1u), kn & 1u);
+        }
+        tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+        ++kn;
+        for (int j = 0; j < n; ++j) {
+            const bool again = j + 1 < n;
+            if (S_::MT == 1 && again) {
+                // the other slot's weights of tile j - 1 have been taken
+                if (!mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
+                tc_after();
+                scores(0, static_cast<int>(kn & 1u), kn & 1u);
+                tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+                ++kn;
+            }
+            for (int x = 0; x < tiles; ++x) {
+                const int slot = S_::MT == 2 ? x : static_cast<int>(vn & 1u);
+                if (!mbar_wait(smem_u32(&sh.pfull[slot]), pn[slot] & 1u, dead)) return;
+                ++pn[slot];
+                if (x == 0 && !mbar_wait(smem_u32(&sh.vfull[vn & 1u]), (vn >> 1) & 1u, dead)) return;
+                tc_after();
+                weighted(x, slot, vn & 1u, j == 0);
+                if (x == tiles - 1) tc_commit(smem_u32(&sh.vempty[vn & 1u]));
+                if (S_::MT == 2 && again) {
+                    if (x == 0 && !mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
+                    tc_after();
+                    scores(x, x, kn & 1u);
+                    if (x == tiles - 1) tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+                }
+            }
+            ++vn;
+            if (S_::MT == 2 && again) ++kn;
+        }
+    }
+}
+
+// A softmax warp: 32 rows of row tile x.
+template <int D>
+__device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t tmem, int x, int warp, int lane) {
+    using S_ = Shape<D>;
+    volatile int* dead = &sh.dead;
+    const int row = 32 * (warp & 3) + lane;       // of the tile
+    const int per = kRowsM / p.G;                 // tokens of a tile
+    const int tok = row / p.G, head = row - tok * p.G;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const uint32_t o_col = lanes + S_::O_COL + x * D;
+    const uint32_t qrow = qbuf + x * S_::QB + row * 128;
+    const float scale = p.sm_scale * scalar_or_1(p.gk);
+    const float gv = scalar_or_1(p.gv);
+    uint32_t tn = 0, on = 0;  // KV tiles seen (slots: MT 2: one; MT 1: two in turn), products with V done before
+    uint32_t scale_n = 0;     // tiles of the CTA so far: place in the ring of scales
+    Walk<D> w;
+    for (w.start(p); w.more(); w.next(p)) {
+        const int n = w.piece_tiles;
+        const int tiles = (S_::MT == 2 && w.u.t1 - w.u.t0 > per) ? 2 : 1;
+        if (x >= tiles) {
+            scale_n += n;
+            continue;
+        }
+        // ---- queries: this thread's row, to FP16 by a power of two
+        const int t = w.u.t0 + x * per + tok;  // token of the chunk
+        const bool real = tok < per && t < w.u.t1;
+        const int pos = w.s.len - w.s.n + (real ? t : w.u.t1 - 1);
+        const int64_t out_row = w.s.first + t;
+        float cs;
+        {
+            const uint16_t* src = p.q + out_row * p.q_stride + (w.h * p.G + head) * D;
+            float top = 0.0f;
+            if (real) {
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = ldg16(src + 8 * c);
+                    top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))), fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
+                                           fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))), fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w))))));
+                }
+            }
+            int kq = top > 0.0f ? 14 - ilogbf(top) : 0;
+            kq = max(-120, min(kq, 120));
+            const float up = copysignf(ldexpf(1.0f, kq), scale);  // a negative scale turns the queries: c is never negative
+            cs = fabsf(scale) * kLog2e * ldexpf(1.0f, -kq);
+#pragma unroll 4
+            for (int c = 0; c < D / 8; ++c) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (real) v = ldg16(src + 8 * c);
+                sts16(qrow + (c / 8) * (kRowsM * 128) + (((c & 7) ^ (row & 7)) << 4), pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
+                      pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up), pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
+                      pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[x]));
+        }
+        float m = -INFINITY, l = 0.0f;
+        const int first_pos = w.s.len - w.s.n + w.u.t0 + x * per, last_pos = w.s.len - w.s.n + min(w.u.t1, w.u.t0 + (x + 1) * per) - 1;
+        for (int j = 0; j < n; ++j) {
+            const int slot = S_::MT == 2 ? x : static_cast<int>(tn & 1u);
+            const uint32_t s_col = lanes + slot * S_::S_COL;
+            const int t0 = tile_start<D>(w.u, w.tile0 + j);
+            if (!warp_wait(smem_u32(&sh.sfull[slot]), (S_::MT == 2 ? tn : tn >> 1) & 1u, dead)) return;
+            ++tn;
+            tc_after();
+            const float4* sc = sh.scales[(scale_n + j) & 3u];
+            // columns [0, hi) of the tile are at or before the row, those below lo hidden by the window but for the first `sk`
+            const bool edge = t0 + S_::TK - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + S_::TK > p.sinks);
+            const int hi = pos - t0 + 1, lo = pos >= p.window ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
+            auto seen = [&](int c0) {  // bit i: column c0 + i is visible
+                auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
+                return below(hi - c0) & (~below(lo - c0) | below(sk - c0));
+            };
+            float mt = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < S_::TK / 32; ++c) {
+                uint32_t s[32];
+                tmem_ld32(s, s_col + 32 * c);
+                if (edge) {
+                    const uint32_t ok = seen(32 * c);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((ok >> i) & 1u)) s[i] = 0xFF800000u;
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float a = __uint_as_float(s[16 * g]);
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(s[16 * g + i]));
+                    const float4 f = sc[2 * c + g];
+                    // (a row without scale, c = 0, sees -inf only where a column is hidden)
+                    mt = fmaxf(mt, a == -INFINITY ? a : fmaf(a, cs * f.x, f.y));
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, mt > m + kRescale)) {
+                const float mn = fmaxf(m, mt);
+                const float a = mn == -INFINITY ? 1.0f : ex2_approx(m - mn);
+                m = mn;
+                l *= a;
+                if (j > 0) {
+                    if (!warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead)) return;
+                    tc_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_col + 32 * c);
+        #pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                        tmem_st32(o_col + 32 * c, o);
+                    }
+                }
+            }
+            const float mu = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int c = 0; c < S_::TK / 32; ++c) {
+                uint32_t s[32], pk[16];
+                tmem_ld32(s, s_col + 32 * c);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float4 f = sc[2 * c + g];
+                    const float cg = cs * f.x, off = f.y - mu;
+                    float sum = 0.0f;
+                    if (edge) {
+                        const uint32_t ok = seen(32 * c) >> (16 * g);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e = ((ok >> i) & 1u) ? ex2_approx(fmaf(__uint_as_float(s[16 * g + i]), cg, off)) : 0.0f;
+                            s[16 * g + i] = __float_as_uint(e);
+                            sum += e;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float e = ex2_approx(fmaf(__uint_as_float(s[16 * g + i]), cg, off));
+                            s[16 * g + i] = __float_as_uint(e);
+                            sum += e;
+                        }
+                    }
+                    l = fmaf(sum, f.z, l);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+                tmem_st16(s_col + 16 * c, pk);
+            }
+            tc_wait_st();
+            tc_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[slot]));
+        }
+        scale_n += n;
+        // ---- the piece's end: outputs, or a partial result
+        // (a parity tells only the last phase from the one before: the last tile's scores stand for all products with V
+        // before them, but at head_dim 256 they were issued before those of the last tile but one)
+        if (S_::MT == 1 && n > 1 && !warp_wait(smem_u32(&sh.ofull[x]), (on + n - 2) & 1u, dead)) return;
+        if (!warp_wait(smem_u32(&sh.ofull[x]), (on + n - 1) & 1u, dead)) return;
+        on += n;
+        tc_after();
+        const bool whole = w.whole();
+        const int64_t rec = (2 * static_cast<int64_t>(blockIdx.x) + (w.tile0 > 0 ? 0 : 1)) * (S_::MT * kRowsM) + x * kRowsM + row;
+        const float f = l > 0.0f ? gv / l : 0.0f;
+        uint16_t* dst = p.out + out_row * p.out_stride + (w.h * p.G + head) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o, o_col + 32 * c);
+            if (real && whole) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint4 v;
+                    v.x = pack_bf16x2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f);
+                    v.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f);
+                    v.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f);
+                    v.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f);
+                    *reinterpret_cast<uint4*>(dst + 32 * c + 8 * i) = v;
+                }
+            } else if (real) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(p.rec_o + rec * D + 32 * c + 4 * i) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+            __syncwarp();
+        }
+        if (real) {
+            if (!whole) p.rec_ml[rec] = make_float2(m, l);
+            else if (p.lse) p.lse[out_row * p.Hq + w.h * p.G + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+        tc_before();  // the next unit's products overwrite what was read here
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const ExtendParams p) {
+    using S_ = Shape<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.kfull[i]), kLoaderWarps);
+            mbar_init(smem_u32(&sh.vfull[i]), kLoaderWarps);
+            mbar_init(smem_u32(&sh.kempty[i]), 1);
+            mbar_init(smem_u32(&sh.vempty[i]), 1);
+            mbar_init(smem_u32(&sh.qfull[i]), 4);
+            mbar_init(smem_u32(&sh.sfull[i]), 1);
+            mbar_init(smem_u32(&sh.pfull[i]), 4);
+            mbar_init(smem_u32(&sh.ofull[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.drained), 1);
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    constexpr int kIssuer = S_::WARPS - 1;
+    if (warp == kIssuer) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_enter();
+    if (warp < S_::SOFT_WARPS) {
+        softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
+    } else if (warp < kIssuer) {
+        load_tiles<D>(p, sh, base + S_::K_OFF, base + S_::V_OFF, warp - S_::SOFT_WARPS, lane);
+    } else {
+        if (lane == 0) {
+            issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem);
+            // all products are done before TMEM is given back
+            tc_commit(smem_u32(&sh.drained));
+            volatile int alive = 0;
+            mbar_wait(smem_u32(&sh.drained), 0, &alive);
+        }
+        __syncwarp();
+    }
+    __syncwarp();
+    tc_before();
+    __syncthreads();
+    if (warp == kIssuer) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+    if (threadIdx.x == 0 && sh.dead) flag_status(p.status, NVFP4KV_STATUS_TIMEOUT);
+}
+
+// ------------------------------------------------------------------------------------------ the join
+
+// Block (c, y): the unit that CTA c begins and others go on with, rows y, y + gridDim.y, .. of it; and the rows of
+// sequences with lengths out of range.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
+    pdl_enter();
+    using S_ = Shape<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int worker = (blockIdx.x * gridDim.y + blockIdx.y) * 8 + warp, workers = gridDim.x * gridDim.y * 8;
+    for (int b = worker; b < p.B; b += workers) {
+        const Seq s = sequence(p, b);
+        if (!s.bad) continue;
+        const int a = __ldg(p.starts + b), e = __ldg(p.starts + b + 1);
+        if (a < 0 || e < a || e > p.rows) continue;
+        for (int64_t r = a; r < e; ++r) {
+            for (int i = lane; i < p.Hq * D / 8; i += 32)
+                *reinterpret_cast<uint4*>(p.out + r * p.out_stride + 8 * i) = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse)
+                for (int i = lane; i < p.Hq; i += 32) p.lse[r * p.Hq + i] = -INFINITY;
+        }
+    }
+    const int c = blockIdx.x;
+    const PlanEntry next = p.plan[c + 1];
+    if (!(next.cut > next.begin && next.cut < next.end) || next.begin < p.plan[c].cut) return;
+    int last = c + 1;  // the last CTA with a piece of the unit
+    while (last + 1 < p.ctas && p.plan[last + 1].cut < next.end) ++last;
+    const Seq s = sequence(p, next.b);
+    const Unit u = unit_of<D>(p, s, next.qb);
+    const int per = kRowsM / p.G;
+    const float gv = scalar_or_1(p.gv);
+    for (int row = blockIdx.y * 8 + warp; row < S_::MT * kRowsM; row += gridDim.y * 8) {
+        const int x = row / kRowsM, r = row - x * kRowsM, tok = r / p.G, head = r - tok * p.G;
+        const int t = u.t0 + x * per + tok;
+        if (tok >= per || t >= u.t1) continue;
+        auto rec = [&](int k) { return (2 * static_cast<int64_t>(k) + (k == c ? 1 : 0)) * (S_::MT * kRowsM) + row; };
+        float m = -INFINITY;
+        for (int k = c; k <= last; ++k) m = fmaxf(m, p.rec_ml[rec(k)].x);
+        float l = 0.0f, o[D / 32];
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
+        for (int k = c; k <= last; ++k) {
+            const float2 ml = p.rec_ml[rec(k)];
+            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m);
+            l = fmaf(w, ml.y, l);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const float2 v = *reinterpret_cast<const float2*>(p.rec_o + rec(k) * D + 64 * i + 2 * lane);
+                o[2 * i] = fmaf(w, v.x, o[2 * i]);
+                o[2 * i + 1] = fmaf(w, v.y, o[2 * i + 1]);
+            }
+        }
+        const float f = l > 0.0f ? gv / l : 0.0f;
+        const int64_t out_row = s.first + t;
+        const int hq = next.h * p.G + head;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+            *reinterpret_cast<uint32_t*>(p.out + out_row * p.out_stride + hq * D + 64 * i + 2 * lane) = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
+        if (lane == 0 && p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+// ------------------------------------------------------------------------------------------ host
+
+struct Carve {
+    size_t plan, cost, ml, o, total;
+};
+Carve carve(int B, int D, int ctas) {
+    auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+    const size_t records = static_cast<size_t>(2 * ctas) * (D == 256 ? 1 : 2) * kRowsM;
+    Carve c;
+    c.plan = 0;
+    c.cost = up(static_cast<size_t>(ctas + 1) * sizeof(PlanEntry));
+    c.ml = c.cost + up((static_cast<size_t>(B) + 1) * sizeof(int64_t));
+    c.o = c.ml + up(records * sizeof(float2));
+    c.total = c.o + records * D * sizeof(float);
+    return c;
+}
+
+bool shape_ok(const nvfp4kv_layout* l, int Hq) {
+    const int D = l->head_dim;
+    if ((D != 64 && D != 128 && D != 256) || l->page_size % 16 != 0 || Hq % l->num_kv_heads != 0) return false;
+    return Hq / l->num_kv_heads <= kMaxGroup;
+}
+
+template <int D>
+cudaError_t launch_extend(const ExtendParams& p, cudaStream_t s) {
+    using S_ = Shape<D>;
+    cudaError_t e = cudaFuncSetAttribute(extend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_::SMEM);
+    if (e == cudaSuccess) e = launch_pdl(plan_kernel<D>, dim3(1), dim3(1024), 0, s, p);
+    if (e == cudaSuccess) e = launch_pdl(extend_kernel<D>, dim3(p.ctas), dim3(S_::THREADS), S_::SMEM, s, p);
+    if (e == cudaSuccess) e = launch_pdl(join_kernel<D>, dim3(p.ctas, 4), dim3(256), 0, s, p);
+    return e;
+}
+
+}  // namespace
+
+extern "C" size_t nvfp4_paged_extend_attention_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
+                                                              int32_t num_q_heads) {
+    if (!layout_ok(layout) || batch < 0 || num_q_heads <= 0 || !shape_ok(layout, num_q_heads)) return 0;
+    return carve(batch, layout->head_dim, num_sms()).total;
+}
+
+extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
+    const nvfp4kv_layout* layout, int32_t batch, int32_t num_rows, int32_t num_q_heads, const void* q,
+    int64_t q_row_stride, const int32_t* row_starts, const uint8_t* k_pages, const float* k_block_scales,
+    const float* k_scale, const uint8_t* v_pages, const float* v_block_scales, const float* v_scale,
+    int32_t pool_pages, const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+    int32_t window, int32_t sink_tokens, float sm_scale, void* workspace, size_t workspace_bytes, void* out,
+    int64_t out_row_stride, float* lse, int32_t* status, nvfp4kv_stream_t stream) {
+    if (!layout_ok(layout) || batch < 0 || num_rows < 0 || num_q_heads <= 0 || max_pages_per_seq <= 0 ||
+        pool_pages <= 0 || window < 0 || sink_tokens < 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (!shape_ok(layout, num_q_heads)) return NVFP4KV_ERR_UNSUPPORTED;
+    if (batch == 0 || num_rows == 0) return NVFP4KV_OK;
+    const int D = layout->head_dim, H = layout->num_kv_heads, T = layout->page_size;
+    const int64_t width = static_cast<int64_t>(num_q_heads) * D;
+    if (!q || !row_starts || !k_pages || !v_pages || !page_table || !seq_lens || !out || q == out)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || q_row_stride % 8 != 0 ||
+        out_row_stride % 8 != 0 || q_row_stride < width || out_row_stride < width)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (batch > 65535 || num_q_heads > 65535 || static_cast<int64_t>(max_pages_per_seq) * T > INT32_MAX - 1024)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    const int ctas = num_sms();
+    const Carve c = carve(batch, D, ctas);
+    if (!workspace || workspace_bytes < c.total || !aligned16(workspace)) return NVFP4KV_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    ExtendParams p{};
+    p.q = static_cast<const uint16_t*>(q);
+    p.k = k_pages;
+    p.v = v_pages;
+    p.kbs = k_block_scales;
+    p.vbs = v_block_scales;
+    p.gk = k_scale;
+    p.gv = v_scale;
+    p.table = page_table;
+    p.lens = seq_lens;
+    p.starts = row_starts;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.status = status;
+    p.plan = reinterpret_cast<PlanEntry*>(ws + c.plan);
+    p.cost = reinterpret_cast<int64_t*>(ws + c.cost);
+    p.rec_ml = reinterpret_cast<float2*>(ws + c.ml);
+    p.rec_o = reinterpret_cast<float*>(ws + c.o);
+    p.q_stride = q_row_stride;
+    p.out_stride = out_row_stride;
+    p.t_magic = UINT64_MAX / static_cast<uint64_t>(T) + 1;
+    p.B = batch;
+    p.rows = num_rows;
+    p.Hq = num_q_heads;
+    p.H = H;
+    p.G = num_q_heads / H;
+    p.T = T;
+    p.pool_pages = pool_pages;
+    p.max_pages = max_pages_per_seq;
+    p.window = window > 0 ? window : INT32_MAX;
+    p.sinks = sink_tokens;
+    p.ctas = ctas;
+    p.sm_scale = sm_scale;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    switch (D) {
+    case 64: return launched(launch_extend<64>(p, s));
+    case 128: return launched(launch_extend<128>(p, s));
+    default: return launched(launch_extend<256>(p, s));
+    }
+}
