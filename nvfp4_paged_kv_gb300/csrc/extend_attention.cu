@@ -34,6 +34,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
+constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126: the least factor of a score (0 would turn a hidden one, -inf, into NaN)
 constexpr int kMaxGroup = 8;
 constexpr int kRowsM = 128;       // rows of a tile
 constexpr int kLoaderWarps = 4;
@@ -53,7 +54,7 @@ struct Shape {
     static constexpr int V_OFF = K_OFF + STAGES * KB;
     static constexpr int SMEM = V_OFF + STAGES * KB + 1024;  // the base is rounded up to 1024
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 1;
+    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 4;  // (the issuer's warpgroup has three idle warps)
     static constexpr int THREADS = WARPS * 32;
     // TMEM columns: two score slots, then the outputs
     static constexpr int S_COL = TK;                 // columns of a slot
@@ -312,52 +313,67 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
         : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
-// Waits for the phase of this parity; false when the wait, or another role's, has given up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    if (mbar_try(bar, parity)) return true;
+// Waits for the phase of this parity. Once a wait of the CTA has given up, `dead`, none waits any more: every role runs through
+// its list over whatever is there (all of it in bounds) and the kernel ends.
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    if (mbar_try(bar, parity)) return;
     const long long t0 = clock64();
     while (!mbar_try(bar, parity)) {
-        if (*dead) return false;
+        if (*dead) return;
         if (clock64() - t0 > kWaitClocks) {
             *dead = 1;
-            return false;
+            return;
         }
     }
-    return true;
 }
-// The same for a whole warp: all lanes go on together, or none.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, dead));
+// The same for a whole warp.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    mbar_wait(bar, parity, dead);
+    __syncwarp();
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(elected)
+        : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand of tcgen05.mma: 128-byte swizzle, start address and byte offsets in units of 16. For K-major
 // operands `stride` is the distance of 8-row groups; for MN-major ones `lead` that of 64-element columns and `stride`
 // that of groups of 8 along K.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
-           static_cast<uint64_t>(stride >> 4) << 32 | uint64_t{1} << 46 | uint64_t{2} << 61;
+struct Operand {
+    uint32_t lo, hi;
+    // `bytes` further on (a multiple of 16; the address field does not overflow)
+    __device__ __forceinline__ uint64_t at(uint32_t bytes) const { return static_cast<uint64_t>(hi) << 32 | (lo + (bytes >> 4)); }
+};
+__device__ __forceinline__ Operand operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+    Operand o{((addr & 0x3FFFFu) >> 4) | (lead >> 4) << 16, (stride >> 4) | 1u << 14 | 2u << 29};
+    asm volatile("" : "+r"(o.lo));  // the steps' descriptors are made when they are used, not kept in registers for the whole kernel
+    return o;
 }
 // Instruction descriptor: FP16 operands, FP32 accumulators, M = 128, N; B K-major or MN-major.
 __host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n) >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// (Whole warps call these and one lane, `elected`, issues: the operands then stay in uniform registers, which is where the
+// instruction takes them from. With one lane in a branch of its own each was moved there first, and issuing took as long as
+// the products.)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(elected)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(elected)
         : "memory");
 }
 // 32 columns of this warp's lanes (with the wait: nothing may use the registers before it).
@@ -371,15 +387,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -387,6 +401,35 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+// All columns of a slot of this warp's lanes.
+__device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[64], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
+        "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[128], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%128+32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%128+64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128+96];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]), "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]), "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47]), "=&r"(r[48]), "=&r"(r[49]), "=&r"(r[50]), "=&r"(r[51]), "=&r"(r[52]), "=&r"(r[53]), "=&r"(r[54]), "=&r"(r[55]), "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63]), "=&r"(r[64]), "=&r"(r[65]), "=&r"(r[66]), "=&r"(r[67]), "=&r"(r[68]), "=&r"(r[69]), "=&r"(r[70]), "=&r"(r[71]), "=&r"(r[72]), "=&r"(r[73]), "=&r"(r[74]), "=&r"(r[75]), "=&r"(r[76]), "=&r"(r[77]), "=&r"(r[78]), "=&r"(r[79]), "=&r"(r[80]), "=&r"(r[81]), "=&r"(r[82]), "=&r"(r[83]), "=&r"(r[84]), "=&r"(r[85]), "=&r"(r[86]), "=&r"(r[87]), "=&r"(r[88]), "=&r"(r[89]), "=&r"(r[90]), "=&r"(r[91]), "=&r"(r[92]), "=&r"(r[93]), "=&r"(r[94]), "=&r"(r[95]), "=&r"(r[96]), "=&r"(r[97]), "=&r"(r[98]), "=&r"(r[99]), "=&r"(r[100]), "=&r"(r[101]), "=&r"(r[102]), "=&r"(r[103]), "=&r"(r[104]), "=&r"(r[105]), "=&r"(r[106]), "=&r"(r[107]), "=&r"(r[108]), "=&r"(r[109]), "=&r"(r[110]), "=&r"(r[111]), "=&r"(r[112]), "=&r"(r[113]), "=&r"(r[114]), "=&r"(r[115]), "=&r"(r[116]), "=&r"(r[117]), "=&r"(r[118]), "=&r"(r[119]), "=&r"(r[120]), "=&r"(r[121]), "=&r"(r[122]), "=&r"(r[123]), "=&r"(r[124]), "=&r"(r[125]), "=&r"(r[126]), "=&r"(r[127])
+        : "r"(addr));
+}
+// (a, b) * c + d and (a, b) + (c, d), each rounded as by the scalar instructions.
+__device__ __forceinline__ void fma2(uint32_t& a, uint32_t& b, float c, float d) {
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+r"(a), "+r"(b) : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, uint32_t c, uint32_t d) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b) : "r"(c), "r"(d));
 }
 __device__ __forceinline__ uint4 ldg16(const void* p) {
     uint4 r;
@@ -406,29 +449,38 @@ struct Shared {
     uint64_t drained;
     float4 scales[4][8];  // (s_K, log2 s_V, 1 / s_V) of a KV tile's groups, in a ring of tiles
     uint32_t tmem;
-    int dead;
+    int dead;   // a wait gave up
+    int never;  // (stays 0)
 };
 
-// The loader's threads: warp w takes row groups of 8 tokens w, w + 4, ..; a lane one 16-byte chunk of one row of it, so
-// that the eight lanes of a store phase lie in rows 0, 1, 4, 5 (or 2, 3, 6, 7) and two neighbouring chunks and hit distinct banks.
+// The loader's threads: a warp's load covers R rows of 64 or 128 bytes (whole lines of a row), a lane one 16-byte chunk, which
+// becomes two in the swizzled layout. The eight lanes of a store phase lie in an even row and the odd one after it, four chunks
+// each: the even row's land in even 16-byte columns or in odd ones, the odd row's in the others, so they hit distinct banks.
 template <int D>
 __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, uint32_t kbuf, uint32_t vbuf, int warp, int lane) {
     using S_ = Shape<D>;
-    constexpr int RG = S_::TK / 8 / kLoaderWarps;  // row groups of a warp
-    constexpr int N = RG * S_::BLOCKS;             // chunks of a lane
-    const int r8 = ((lane >> 1) & 1) | ((lane >> 3) & 1) << 1 | ((lane >> 2) & 1) << 2;
-    const int ch = (lane & 1) | (lane >> 4) << 1;
-    const uint32_t at0 = static_cast<uint32_t>(r8 * 128 + (((2 * ch) ^ r8) << 4));
+    constexpr int WIDE = D >= 128 ? 2 : 1;               // 64-byte columns of a load
+    constexpr int R = 8 / WIDE;                          // its rows
+    constexpr int STEPS = S_::TK / R / kLoaderWarps;     // loads of a column: rows R (warp + 4 g) on
+    constexpr int COLS = S_::BLOCKS / WIDE;
+    constexpr int N = STEPS * COLS;                      // chunks of a lane
+    const int ch = lane & 3, blk = WIDE == 2 ? (lane >> 3) & 1 : 0;
+    const int r0 = R * warp + (((lane >> 2) & 1) | (WIDE == 2 ? (lane >> 4) << 1 : (lane >> 3) << 1));  // the lane's first row
+    const int g0 = r0 >> 4;                              // its 16-token group; further rows lie in every (R / 4)th group on
+    const uint32_t at0 = static_cast<uint32_t>(blk * (S_::TK * 128) + r0 * 128 + (((2 * ch) ^ (r0 & 7)) << 4));
+    const uint32_t src0 = static_cast<uint32_t>((r0 & 15) * D + 64 * blk + 16 * ch);
     volatile int* dead = &sh.dead;
-    const int64_t head_stride = static_cast<int64_t>(p.T) * D;
 
     Walk<D> w;
     w.start(p);
     if (!w.more()) return;
-    // the next tile's page ids are loaded before the current tile's values: lane l < GRP has the page of group l
+    // A tile: lane l < GRP has the pool row of the first token of group l, or kNone.
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
     struct Tile {
-        int t0, page;  // first token; page of group `lane`, -1: none, or none visible
-        int lo, hi, h;
+        int t0, lo, hi;
+        uint32_t row;
+        int page, h;
+        bool full;  // every token is there and visible to a row
     };
     int j = 0;  // tile within the piece
     auto look = [&]() {
@@ -437,17 +489,29 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
         t.lo = w.u.lo;
         t.hi = w.u.hi;
         t.h = w.h;
+        t.row = kNone;
         t.page = -1;
         const int a = t.t0 + 16 * lane;
         if (lane < S_::GRP && a < t.hi && (a + 15 >= t.lo || a < p.sinks)) {
             const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(a), p.t_magic));
             t.page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + idx);
+            t.row = static_cast<uint32_t>(a - idx * p.T);
+        }
+        t.full = t.t0 + S_::TK <= t.hi && (t.t0 >= t.lo || t.t0 + S_::TK <= p.sinks);
+        return t;
+    };
+    // the page ids have arrived: pool rows (fewer than 2^32)
+    auto place = [&](Tile& t) {
+        if (t.row != kNone) {
             if (t.page < 0 || t.page >= p.pool_pages) {
                 flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
                 t.page = -1;
+                t.row = kNone;
+            } else {
+                t.row += (static_cast<uint32_t>(t.page) * p.H + t.h) * static_cast<uint32_t>(p.T);
             }
         }
-        return t;
+        t.full = __all_sync(0xFFFFFFFFu, t.full && (lane >= S_::GRP || t.row != kNone));
     };
     auto advance = [&]() {  // to the next tile; false at the end
         if (++j < w.piece_tiles) return true;
@@ -456,134 +520,157 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
         return w.more();
     };
     auto load = [&](const Tile& t, const uint8_t* pool, uint4 (&r)[N]) {
+        const uint8_t* base = pool + src0;
+        if (t.full) {
 #pragma unroll
-        for (int g = 0; g < RG; ++g) {
-            const int rg = warp + kLoaderWarps * g, row = rg * 8 + r8, tok = t.t0 + row;
-            const int pg = __shfl_sync(0xFFFFFFFFu, t.page, rg >> 1);
-            const bool ok = pg >= 0 && tok < t.hi && (tok >= t.lo || tok < p.sinks);
-            const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(tok), p.t_magic));
-            const uint8_t* src = pool + (static_cast<int64_t>(pg) * p.H + t.h) * head_stride + static_cast<int64_t>(tok - idx * p.T) * D + 16 * ch;
+            for (int g = 0; g < STEPS; ++g) {
+                const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
+                const uint8_t* src = base + static_cast<uint64_t>(row) * D;
 #pragma unroll
-            for (int c = 0; c < S_::BLOCKS; ++c) r[g * S_::BLOCKS + c] = ok ? ldg16(src + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < STEPS; ++g) {
+                const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
+                const int tok = t.t0 + r0 + g * R * kLoaderWarps;
+                const bool ok = row != kNone && tok < t.hi && (tok >= t.lo || tok < p.sinks);
+                const uint8_t* src = base + static_cast<uint64_t>(row) * D;
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ok ? ldg16(src + 64 * WIDE * c) : make_uint4(0u, 0u, 0u, 0u);
+            }
         }
     };
     auto store = [&](uint32_t buf, const uint4 (&r)[N]) {
+        const uint32_t at = buf + at0, at1 = at ^ 16u;
 #pragma unroll
-        for (int g = 0; g < RG; ++g)
+        for (int g = 0; g < STEPS; ++g)
 #pragma unroll
-            for (int c = 0; c < S_::BLOCKS; ++c) {
-                const uint4 x = r[g * S_::BLOCKS + c];
-                const uint32_t at = buf + c * (S_::TK * 128) + (warp + kLoaderWarps * g) * 1024 + at0;
+            for (int c = 0; c < COLS; ++c) {
+                const uint4 x = r[g * COLS + c];
+                const uint32_t off = WIDE * c * (S_::TK * 128) + g * (R * kLoaderWarps * 128);
                 uint32_t a[2], b[2];
                 e4m3x4_to_f16x2x2(x.x, a);
                 e4m3x4_to_f16x2x2(x.y, b);
-                sts16(at, a[0], a[1], b[0], b[1]);
+                sts16(at + off, a[0], a[1], b[0], b[1]);
                 e4m3x4_to_f16x2x2(x.z, a);
                 e4m3x4_to_f16x2x2(x.w, b);
-                sts16(at ^ 16u, a[0], a[1], b[0], b[1]);
+                sts16(at1 + off, a[0], a[1], b[0], b[1]);
             }
     };
 
-    Tile now = look();
+    // page ids are two tiles ahead, values one: a register set is loaded again as soon as it is stored
+    Tile now = look(), then{};
     uint4 rk[N], rv[N];
+    place(now);
     load(now, p.k, rk);
+    load(now, p.v, rv);
+    bool more = advance();
+    if (more) then = look();
     for (uint32_t n = 0;; ++n) {
         const uint32_t stage = n & 1u, phase = (n >> 1) & 1u;
-        load(now, p.v, rv);
         float sk = 1.0f, sv = 1.0f;
         if (warp == 0 && now.page >= 0) {
             const int64_t at = static_cast<int64_t>(now.page) * p.H + now.h;
             if (p.kbs) sk = __ldg(p.kbs + at);
             if (p.vbs) sv = __ldg(p.vbs + at);
         }
-        if (!warp_wait(smem_u32(&sh.kempty[stage]), phase ^ 1u, dead)) return;
+        const bool after = more && advance();
+        Tile third{};
+        if (after) third = look();
+        warp_wait(smem_u32(&sh.kempty[stage]), phase ^ 1u, dead);
         // the groups' scales: the products of tile n - 2 are done, so the weights of tile n - 4 have been made
         if (warp == 0 && lane < S_::GRP)
             sh.scales[n & 3u][lane] = now.page >= 0 ? make_float4(sk, log2f(sv), 1.0f / sv, 0.0f)
                                                     : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
         store(kbuf + stage * S_::KB, rk);
+        if (more) {
+            place(then);
+            load(then, p.k, rk);
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.kfull[stage]));
-        const bool more = advance();
-        Tile then = now;
-        if (more) {
-            then = look();
-            load(then, p.k, rk);
-        }
-        if (!warp_wait(smem_u32(&sh.vempty[stage]), phase ^ 1u, dead)) return;
+        warp_wait(smem_u32(&sh.vempty[stage]), phase ^ 1u, dead);
         store(vbuf + stage * S_::KB, rv);
+        if (more) load(then, p.v, rv);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sh.vfull[stage]));
         if (!more) return;
         now = then;
+        then = third;
+        more = after;
     }
 }
 
-// The thread that issues the products.
+// The warp that issues the products.
 template <int D>
-__device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem) {
+__device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem, uint32_t elected) {
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
     constexpr uint32_t qk = instruction(S_::TK, false), pv = instruction(D, true);
     uint32_t kn = 0, vn = 0;        // K and V tiles taken
     uint32_t units = 0, units1 = 0;  // units of row tile 0, 1
-    uint32_t pn[2] = {0, 0};        // weights taken of slot 0, 1
+    uint32_t pn0 = 0, pn1 = 0;      // weights taken of slot 0, 1
     Walk<D> w;
     w.start(p);
     auto scores = [&](int tile, int slot, uint32_t kstage) {
-        const uint32_t a = qbuf + tile * S_::QB, b = kbuf + kstage * S_::KB;
+        const Operand a = operand(qbuf + tile * S_::QB, 16, 1024), b = operand(kbuf + kstage * S_::KB, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss(tmem + slot * S_::S_COL, operand(a + (ks / 4) * (kRowsM * 128) + (ks % 4) * 32, 16, 1024),
-                   operand(b + (ks / 4) * (S_::TK * 128) + (ks % 4) * 32, 16, 1024), qk, ks > 0);
-        tc_commit(smem_u32(&sh.sfull[slot]));
+            mma_ss(tmem + slot * S_::S_COL, a.at((ks / 4) * (kRowsM * 128) + (ks % 4) * 32),
+                   b.at((ks / 4) * (S_::TK * 128) + (ks % 4) * 32), qk, ks > 0, elected);
+        tc_commit(smem_u32(&sh.sfull[slot]), elected);
     };
     auto weighted = [&](int tile, int slot, uint32_t vstage, bool first) {
-        const uint32_t b = vbuf + vstage * S_::KB;
+        const Operand b = operand(vbuf + vstage * S_::KB, S_::TK * 128, 1024);
 #pragma unroll
         for (int ks = 0; ks < S_::TK / 16; ++ks)
-            mma_ts(tmem + S_::O_COL + tile * D, tmem + slot * S_::S_COL + 8 * ks, operand(b + ks * 2048, S_::TK * 128, 1024), pv,
-                   !first || ks > 0);
-        tc_commit(smem_u32(&sh.ofull[tile]));
+            mma_ts(tmem + S_::O_COL + tile * D, tmem + slot * S_::S_COL + 8 * ks, b.at(ks * 2048), pv, !first || ks > 0, elected);
+        tc_commit(smem_u32(&sh.ofull[tile]), elected);
     };
     for (; w.more(); w.next(p)) {
         const int n = w.piece_tiles;
         const int tiles = (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G) ? 2 : 1;
-        if (!mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
-        for (int x = 0; x < tiles; ++x) {
-            uint32_t& un = x ? units1 : units;
-            if (!mbar_wait(smem_u32(&sh.qfull[x]), un & 1u, dead)) return;
-            ++un;
+        warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
+#pragma unroll
+        for (int x = 0; x < S_::MT; ++x) {
+            if (x >= tiles) break;
+            warp_wait(smem_u32(&sh.qfull[x]), (x ? units1 : units) & 1u, dead);
+            if (x) ++units1;
+            else ++units;
             tc_after();
             scores(x, S_::MT == 2 ? x : static_cast<int>(kn & 1u), kn & 1u);
         }
-        tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+        tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
         ++kn;
         for (int j = 0; j < n; ++j) {
             const bool again = j + 1 < n;
             if (S_::MT == 1 && again) {
                 // the other slot's weights of tile j - 1 have been taken
-                if (!mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
+                warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
                 tc_after();
                 scores(0, static_cast<int>(kn & 1u), kn & 1u);
-                tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+                tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
                 ++kn;
             }
-            for (int x = 0; x < tiles; ++x) {
+#pragma unroll
+            for (int x = 0; x < S_::MT; ++x) {
+                if (x >= tiles) break;
                 const int slot = S_::MT == 2 ? x : static_cast<int>(vn & 1u);
-                if (!mbar_wait(smem_u32(&sh.pfull[slot]), pn[slot] & 1u, dead)) return;
-                ++pn[slot];
-                if (x == 0 && !mbar_wait(smem_u32(&sh.vfull[vn & 1u]), (vn >> 1) & 1u, dead)) return;
+                warp_wait(smem_u32(&sh.pfull[slot]), (slot ? pn1 : pn0) & 1u, dead);
+                if (slot) ++pn1;
+                else ++pn0;
+                if (x == 0) warp_wait(smem_u32(&sh.vfull[vn & 1u]), (vn >> 1) & 1u, dead);
                 tc_after();
                 weighted(x, slot, vn & 1u, j == 0);
-                if (x == tiles - 1) tc_commit(smem_u32(&sh.vempty[vn & 1u]));
+                if (x == tiles - 1) tc_commit(smem_u32(&sh.vempty[vn & 1u]), elected);
                 if (S_::MT == 2 && again) {
-                    if (x == 0 && !mbar_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead)) return;
+                    if (x == 0) warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
                     tc_after();
                     scores(x, x, kn & 1u);
-                    if (x == tiles - 1) tc_commit(smem_u32(&sh.kempty[kn & 1u]));
+                    if (x == tiles - 1) tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
                 }
             }
             ++vn;
@@ -654,7 +741,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             const int slot = S_::MT == 2 ? x : static_cast<int>(tn & 1u);
             const uint32_t s_col = lanes + slot * S_::S_COL;
             const int t0 = tile_start<D>(w.u, w.tile0 + j);
-            if (!warp_wait(smem_u32(&sh.sfull[slot]), (S_::MT == 2 ? tn : tn >> 1) & 1u, dead)) return;
+            warp_wait(smem_u32(&sh.sfull[slot]), (S_::MT == 2 ? tn : tn >> 1) & 1u, dead);
             ++tn;
             tc_after();
             const float4* sc = sh.scales[(scale_n + j) & 3u];
@@ -665,26 +752,25 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
                 return below(hi - c0) & (~below(lo - c0) | below(sk - c0));
             };
-            float mt = -INFINITY;
+            uint32_t x_[S_::TK];  // the row's scores, then its weights
+            tmem_ld_row(x_, s_col);
+            if (edge) {
 #pragma unroll
-            for (int c = 0; c < S_::TK / 32; ++c) {
-                uint32_t s[32];
-                tmem_ld32(s, s_col + 32 * c);
-                if (edge) {
+                for (int c = 0; c < S_::TK / 32; ++c) {
                     const uint32_t ok = seen(32 * c);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (!((ok >> i) & 1u)) s[i] = 0xFF800000u;
+                        if (!((ok >> i) & 1u)) x_[32 * c + i] = 0xFF800000u;
                 }
+            }
+            float mt = -INFINITY;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float a = __uint_as_float(s[16 * g]);
+            for (int g = 0; g < S_::GRP; ++g) {
+                const float4 f = sc[g];
+                float a = fmaxf(__uint_as_float(x_[16 * g]), __uint_as_float(x_[16 * g + 1]));
 #pragma unroll
-                    for (int i = 1; i < 16; ++i) a = fmaxf(a, __uint_as_float(s[16 * g + i]));
-                    const float4 f = sc[2 * c + g];
-                    // (a row without scale, c = 0, sees -inf only where a column is hidden)
-                    mt = fmaxf(mt, a == -INFINITY ? a : fmaf(a, cs * f.x, f.y));
-                }
+                for (int i = 2; i < 16; i += 2) a = fmaxf(a, fmaxf(__uint_as_float(x_[16 * g + i]), __uint_as_float(x_[16 * g + i + 1])));
+                mt = fmaxf(mt, fmaf(a, fmaxf(cs * f.x, kTiny), f.y));
             }
             if (__any_sync(0xFFFFFFFFu, mt > m + kRescale)) {
                 const float mn = fmaxf(m, mt);
@@ -692,49 +778,40 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 m = mn;
                 l *= a;
                 if (j > 0) {
-                    if (!warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead)) return;
+                    warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead);
                     tc_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {  // (16 at a time: the scores are held in registers meanwhile)
+                        uint32_t o[16];
+                        tmem_ld16(o, o_col + c);
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o, o_col + 32 * c);
-        #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-                        tmem_st32(o_col + 32 * c, o);
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                        tmem_st16(o_col + c, o);
                     }
                 }
             }
             const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int c = 0; c < S_::TK / 32; ++c) {
-                uint32_t s[32], pk[16];
-                tmem_ld32(s, s_col + 32 * c);
+            for (int g = 0; g < S_::GRP; ++g) {
+                const float4 f = sc[g];
+                const float cg = fmaxf(cs * f.x, kTiny), off = f.y - mu;
+                float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float4 f = sc[2 * c + g];
-                    const float cg = cs * f.x, off = f.y - mu;
-                    float sum = 0.0f;
-                    if (edge) {
-                        const uint32_t ok = seen(32 * c) >> (16 * g);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float e = ((ok >> i) & 1u) ? ex2_approx(fmaf(__uint_as_float(s[16 * g + i]), cg, off)) : 0.0f;
-                            s[16 * g + i] = __float_as_uint(e);
-                            sum += e;
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float e = ex2_approx(fmaf(__uint_as_float(s[16 * g + i]), cg, off));
-                            s[16 * g + i] = __float_as_uint(e);
-                            sum += e;
-                        }
-                    }
-                    l = fmaf(sum, f.z, l);
+                for (int i = 0; i < 16; i += 2) {
+                    uint32_t &u0 = x_[16 * g + i], &u1 = x_[16 * g + i + 1];
+                    fma2(u0, u1, cg, off);
+                    u0 = __float_as_uint(ex2_approx(__uint_as_float(u0)));
+                    u1 = __float_as_uint(ex2_approx(__uint_as_float(u1)));
+                    add2(sum0, sum1, u0, u1);
                 }
+                l = fmaf(sum0 + sum1, f.z, l);
+                if (g % 2 == 1) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) pk[i] = pack_f16x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-                tmem_st16(s_col + 16 * c, pk);
+                    for (int i = 0; i < 16; ++i)
+                        pk[i] = pack_f16x2(__uint_as_float(x_[16 * (g - 1) + 2 * i]), __uint_as_float(x_[16 * (g - 1) + 2 * i + 1]));
+                    tmem_st16(s_col + 8 * (g - 1), pk);
+                }
             }
             tc_wait_st();
             tc_before();
@@ -745,15 +822,15 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         // ---- the piece's end: outputs, or a partial result
         // (a parity tells only the last phase from the one before: the last tile's scores stand for all products with V
         // before them, but at head_dim 256 they were issued before those of the last tile but one)
-        if (S_::MT == 1 && n > 1 && !warp_wait(smem_u32(&sh.ofull[x]), (on + n - 2) & 1u, dead)) return;
-        if (!warp_wait(smem_u32(&sh.ofull[x]), (on + n - 1) & 1u, dead)) return;
+        if (S_::MT == 1 && n > 1) warp_wait(smem_u32(&sh.ofull[x]), (on + n - 2) & 1u, dead);
+        warp_wait(smem_u32(&sh.ofull[x]), (on + n - 1) & 1u, dead);
         on += n;
         tc_after();
         const bool whole = w.whole();
         const int64_t rec = (2 * static_cast<int64_t>(blockIdx.x) + (w.tile0 > 0 ? 0 : 1)) * (S_::MT * kRowsM) + x * kRowsM + row;
         const float f = l > 0.0f ? gv / l : 0.0f;
         uint16_t* dst = p.out + out_row * p.out_stride + (w.h * p.G + head) * D;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o, o_col + 32 * c);
@@ -801,10 +878,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
             mbar_init(smem_u32(&sh.ofull[i]), 1);
         }
         mbar_init(smem_u32(&sh.drained), 1);
-        sh.dead = 0;
+        sh.dead = sh.never = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    constexpr int kIssuer = S_::WARPS - 1;
+    constexpr int kIssuer = S_::WARPS - 4;
     if (warp == kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -814,17 +891,21 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
     tc_after();
     const uint32_t tmem = sh.tmem;
     pdl_enter();
+    // registers: 512 threads start with 128 each; a softmax thread holds its row's 128 scores. 184 + 184 + 88 + 56 = 4 x 128
     if (warp < S_::SOFT_WARPS) {
+        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
     } else if (warp < kIssuer) {
+        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         load_tiles<D>(p, sh, base + S_::K_OFF, base + S_::V_OFF, warp - S_::SOFT_WARPS, lane);
     } else {
-        if (lane == 0) {
-            issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem);
+        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == kIssuer) {
+            const uint32_t elected = lane == 0;
+            issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
             // all products are done before TMEM is given back
-            tc_commit(smem_u32(&sh.drained));
-            volatile int alive = 0;
-            mbar_wait(smem_u32(&sh.drained), 0, &alive);
+            tc_commit(smem_u32(&sh.drained), elected);
+            warp_wait(smem_u32(&sh.drained), 0, &sh.never);
         }
         __syncwarp();
     }
@@ -960,7 +1041,9 @@ extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
     if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || q_row_stride % 8 != 0 ||
         out_row_stride % 8 != 0 || q_row_stride < width || out_row_stride < width)
         return NVFP4KV_ERR_INVALID_ARG;
-    if (batch > 65535 || num_q_heads > 65535 || static_cast<int64_t>(max_pages_per_seq) * T > INT32_MAX - 1024)
+    // token positions and the rows of a pool in 32 bits
+    if (batch > 65535 || num_q_heads > 65535 || static_cast<int64_t>(max_pages_per_seq) * T > INT32_MAX - 1024 ||
+        static_cast<int64_t>(pool_pages) * H > UINT32_MAX / T)
         return NVFP4KV_ERR_UNSUPPORTED;
     const int ctas = num_sms();
     const Carve c = carve(batch, D, ctas);
