@@ -13,8 +13,8 @@
 //  * 4 loader warps bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so they are
 //    loaded there directly, one tile ahead of the conversion, and stored in the 128-byte-swizzled layout that tcgen05.mma
 //    reads: K with the head dims contiguous (K-major), V with the same store and read as MN-major.
-//  * 1 warp issues S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), P read from TMEM where it
-//    lies over the scores it came from.
+//  * A warp per row tile issues its S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), P read from
+//    TMEM where it lies over the scores it came from. (One warp for both left the tensor core waiting between its products.)
 //  * 4 softmax warps per tile, one row a thread, so that row maxima and sums need no exchange. While one tile's weights are
 //    made the tensor core works on the other's products; at head_dim 256 the next KV tile's scores are under way instead.
 // The running maximum moves only when it grows by more than 2^8, so rescaling O in TMEM is rare.
@@ -37,6 +37,7 @@ constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126: the least factor of a score (0 would turn a hidden one, -inf, into NaN)
 constexpr int kMaxGroup = 8;
 constexpr int kRowsM = 128;       // rows of a tile
+constexpr int kSub = 64;          // tokens of a step: scores, weights, product with V
 constexpr int kLoaderWarps = 4;
 constexpr int kUnitCost = 1;      // of a unit beside its tiles: queries in, outputs out (in tiles)
 constexpr long long kWaitClocks = 8000000000ll;  // a wait gives up after about 4 s (a defect: no wait depends on another CTA)
@@ -54,11 +55,11 @@ struct Shape {
     static constexpr int V_OFF = K_OFF + STAGES * KB;
     static constexpr int SMEM = V_OFF + STAGES * KB + 1024;  // the base is rounded up to 1024
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 4;  // (the issuer's warpgroup has three idle warps)
+    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 4;  // (the issuers' warpgroup has idle warps)
     static constexpr int THREADS = WARPS * 32;
-    // TMEM columns: two score slots, then the outputs
-    static constexpr int S_COL = TK;                 // columns of a slot
-    static constexpr int O_COL = 2 * S_COL;
+    static constexpr int SUBS = TK / kSub;           // steps of the softmax in a KV tile
+    // TMEM columns: two slots of scores for each row tile, then the outputs
+    static constexpr int O_COL = MT * 2 * kSub;
     static_assert(O_COL + MT * D <= 512, "TMEM");
     static_assert(SMEM <= 232448 - 1024, "shared memory");
 };
@@ -402,23 +403,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// All columns of a slot of this warp's lanes.
+// The scores of a step, 64 columns of this warp's lanes.
 __device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[64], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
         "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,"
         "%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-        : "r"(addr));
-}
-__device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[128], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%128+32];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%128+64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128+96];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]), "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]), "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]), "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31]), "=&r"(r[32]), "=&r"(r[33]), "=&r"(r[34]), "=&r"(r[35]), "=&r"(r[36]), "=&r"(r[37]), "=&r"(r[38]), "=&r"(r[39]), "=&r"(r[40]), "=&r"(r[41]), "=&r"(r[42]), "=&r"(r[43]), "=&r"(r[44]), "=&r"(r[45]), "=&r"(r[46]), "=&r"(r[47]), "=&r"(r[48]), "=&r"(r[49]), "=&r"(r[50]), "=&r"(r[51]), "=&r"(r[52]), "=&r"(r[53]), "=&r"(r[54]), "=&r"(r[55]), "=&r"(r[56]), "=&r"(r[57]), "=&r"(r[58]), "=&r"(r[59]), "=&r"(r[60]), "=&r"(r[61]), "=&r"(r[62]), "=&r"(r[63]), "=&r"(r[64]), "=&r"(r[65]), "=&r"(r[66]), "=&r"(r[67]), "=&r"(r[68]), "=&r"(r[69]), "=&r"(r[70]), "=&r"(r[71]), "=&r"(r[72]), "=&r"(r[73]), "=&r"(r[74]), "=&r"(r[75]), "=&r"(r[76]), "=&r"(r[77]), "=&r"(r[78]), "=&r"(r[79]), "=&r"(r[80]), "=&r"(r[81]), "=&r"(r[82]), "=&r"(r[83]), "=&r"(r[84]), "=&r"(r[85]), "=&r"(r[86]), "=&r"(r[87]), "=&r"(r[88]), "=&r"(r[89]), "=&r"(r[90]), "=&r"(r[91]), "=&r"(r[92]), "=&r"(r[93]), "=&r"(r[94]), "=&r"(r[95]), "=&r"(r[96]), "=&r"(r[97]), "=&r"(r[98]), "=&r"(r[99]), "=&r"(r[100]), "=&r"(r[101]), "=&r"(r[102]), "=&r"(r[103]), "=&r"(r[104]), "=&r"(r[105]), "=&r"(r[106]), "=&r"(r[107]), "=&r"(r[108]), "=&r"(r[109]), "=&r"(r[110]), "=&r"(r[111]), "=&r"(r[112]), "=&r"(r[113]), "=&r"(r[114]), "=&r"(r[115]), "=&r"(r[116]), "=&r"(r[117]), "=&r"(r[118]), "=&r"(r[119]), "=&r"(r[120]), "=&r"(r[121]), "=&r"(r[122]), "=&r"(r[123]), "=&r"(r[124]), "=&r"(r[125]), "=&r"(r[126]), "=&r"(r[127])
         : "r"(addr));
 }
 // (a, b) * c + d and (a, b) + (c, d), each rounded as by the scalar instructions.
@@ -436,6 +427,16 @@ __device__ __forceinline__ uint4 ldg16(const void* p) {
     asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
+// The same where `ok`, else zeros. (A predicate, not a branch: the values of two branches meet in copies of registers, and
+// those wait for the load.)
+__device__ __forceinline__ uint4 ldg16_if(const void* p, bool ok) {
+    uint4 r;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@q ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
+        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"(ok ? 1u : 0u));
+    return r;
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -445,7 +446,7 @@ __device__ __forceinline__ float scalar_or_1(const float* p) { return p ? __ldg(
 
 struct Shared {
     uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-    uint64_t qfull[2], sfull[2], pfull[2], ofull[2];
+    uint64_t qfull[2], sfull[2][2], pfull[2][2], ofull[2];  // [row tile], [row tile][slot]
     uint64_t drained;
     float4 scales[4][8];  // (s_K, log2 s_V, 1 / s_V) of a KV tile's groups, in a ring of tiles
     uint32_t tmem;
@@ -521,24 +522,14 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
     };
     auto load = [&](const Tile& t, const uint8_t* pool, uint4 (&r)[N]) {
         const uint8_t* base = pool + src0;
-        if (t.full) {
 #pragma unroll
-            for (int g = 0; g < STEPS; ++g) {
-                const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
-                const uint8_t* src = base + static_cast<uint64_t>(row) * D;
+        for (int g = 0; g < STEPS; ++g) {
+            const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
+            const int tok = t.t0 + r0 + g * R * kLoaderWarps;
+            const bool ok = t.full || (row != kNone && tok < t.hi && (tok >= t.lo || tok < p.sinks));
+            const uint8_t* src = base + static_cast<uint64_t>(row) * D;
 #pragma unroll
-                for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
-            }
-        } else {
-#pragma unroll
-            for (int g = 0; g < STEPS; ++g) {
-                const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
-                const int tok = t.t0 + r0 + g * R * kLoaderWarps;
-                const bool ok = row != kNone && tok < t.hi && (tok >= t.lo || tok < p.sinks);
-                const uint8_t* src = base + static_cast<uint64_t>(row) * D;
-#pragma unroll
-                for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ok ? ldg16(src + 64 * WIDE * c) : make_uint4(0u, 0u, 0u, 0u);
-            }
+            for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16_if(src + 64 * WIDE * c, ok);
         }
     };
     auto store = [&](uint32_t buf, const uint4 (&r)[N]) {
@@ -604,77 +595,69 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
     }
 }
 
-// The warp that issues the products.
-template <int D>
+// The warp that issues the products of row tile x (a constant, so that all addresses are uniform).
+template <int D, int x>
 __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem, uint32_t elected) {
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
-    constexpr uint32_t qk = instruction(S_::TK, false), pv = instruction(D, true);
-    uint32_t kn = 0, vn = 0;        // K and V tiles taken
-    uint32_t units = 0, units1 = 0;  // units of row tile 0, 1
-    uint32_t pn0 = 0, pn1 = 0;      // weights taken of slot 0, 1
+    constexpr uint32_t qk = instruction(kSub, false), pv = instruction(D, true);
+    uint32_t kt = 0, vt = 0;  // KV tiles of the CTA's part whose scores, whose product with V are issued
+    uint32_t kn = 0, vn = 0;  // the same of this row tile's steps: step i has slot i % 2
+    uint32_t units = 0;       // units with this row tile
     Walk<D> w;
     w.start(p);
-    auto scores = [&](int tile, int slot, uint32_t kstage) {
-        const Operand a = operand(qbuf + tile * S_::QB, 16, 1024), b = operand(kbuf + kstage * S_::KB, 16, 1024);
+    auto scores = [&]() {
+        const uint32_t part = kn % S_::SUBS, stage = kt & 1u, slot = kn & 1u;
+        if (part == 0) warp_wait(smem_u32(&sh.kfull[stage]), (kt >> 1) & 1u, dead);
+        tc_after();
+        const Operand a = operand(qbuf + x * S_::QB, 16, 1024), b = operand(kbuf + stage * S_::KB + part * (kSub * 128), 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss(tmem + slot * S_::S_COL, a.at((ks / 4) * (kRowsM * 128) + (ks % 4) * 32),
+            mma_ss(tmem + (2 * x + slot) * kSub, a.at((ks / 4) * (kRowsM * 128) + (ks % 4) * 32),
                    b.at((ks / 4) * (S_::TK * 128) + (ks % 4) * 32), qk, ks > 0, elected);
-        tc_commit(smem_u32(&sh.sfull[slot]), elected);
+        tc_commit(smem_u32(&sh.sfull[x][slot]), elected);
+        if (part == S_::SUBS - 1) {
+            tc_commit(smem_u32(&sh.kempty[stage]), elected);
+            ++kt;
+        }
+        ++kn;
     };
-    auto weighted = [&](int tile, int slot, uint32_t vstage, bool first) {
-        const Operand b = operand(vbuf + vstage * S_::KB, S_::TK * 128, 1024);
+    auto weighted = [&](bool first) {
+        const uint32_t part = vn % S_::SUBS, stage = vt & 1u, slot = vn & 1u;
+        if (part == 0) warp_wait(smem_u32(&sh.vfull[stage]), (vt >> 1) & 1u, dead);
+        warp_wait(smem_u32(&sh.pfull[x][slot]), (vn >> 1) & 1u, dead);
+        tc_after();
+        const Operand b = operand(vbuf + stage * S_::KB + part * (kSub * 128), S_::TK * 128, 1024);
 #pragma unroll
-        for (int ks = 0; ks < S_::TK / 16; ++ks)
-            mma_ts(tmem + S_::O_COL + tile * D, tmem + slot * S_::S_COL + 8 * ks, b.at(ks * 2048), pv, !first || ks > 0, elected);
-        tc_commit(smem_u32(&sh.ofull[tile]), elected);
+        for (int ks = 0; ks < kSub / 16; ++ks)
+            mma_ts(tmem + S_::O_COL + x * D, tmem + (2 * x + slot) * kSub + 8 * ks, b.at(ks * 2048), pv, !first || ks > 0, elected);
+        tc_commit(smem_u32(&sh.ofull[x]), elected);
+        if (part == S_::SUBS - 1) {
+            tc_commit(smem_u32(&sh.vempty[stage]), elected);
+            ++vt;
+        }
+        ++vn;
     };
     for (; w.more(); w.next(p)) {
-        const int n = w.piece_tiles;
-        const int tiles = (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G) ? 2 : 1;
-        warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
-#pragma unroll
-        for (int x = 0; x < S_::MT; ++x) {
-            if (x >= tiles) break;
-            warp_wait(smem_u32(&sh.qfull[x]), (x ? units1 : units) & 1u, dead);
-            if (x) ++units1;
-            else ++units;
-            tc_after();
-            scores(x, S_::MT == 2 ? x : static_cast<int>(kn & 1u), kn & 1u);
+        const int n = w.piece_tiles * S_::SUBS;
+        if (S_::MT == 2 && x > 0 && w.u.t1 - w.u.t0 <= kRowsM / p.G) {
+            // a unit without this row tile: its stages are free as soon as they are full
+            for (int j = 0; j < w.piece_tiles; ++j, ++kt, ++vt) {
+                warp_wait(smem_u32(&sh.kfull[kt & 1u]), (kt >> 1) & 1u, dead);
+                if (elected) mbar_arrive(smem_u32(&sh.kempty[kt & 1u]));
+                warp_wait(smem_u32(&sh.vfull[vt & 1u]), (vt >> 1) & 1u, dead);
+                if (elected) mbar_arrive(smem_u32(&sh.vempty[vt & 1u]));
+            }
+            continue;
         }
-        tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
-        ++kn;
+        warp_wait(smem_u32(&sh.qfull[x]), units & 1u, dead);
+        ++units;
+        scores();
+        if (n > 1) scores();
         for (int j = 0; j < n; ++j) {
-            const bool again = j + 1 < n;
-            if (S_::MT == 1 && again) {
-                // the other slot's weights of tile j - 1 have been taken
-                warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
-                tc_after();
-                scores(0, static_cast<int>(kn & 1u), kn & 1u);
-                tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
-                ++kn;
-            }
-#pragma unroll
-            for (int x = 0; x < S_::MT; ++x) {
-                if (x >= tiles) break;
-                const int slot = S_::MT == 2 ? x : static_cast<int>(vn & 1u);
-                warp_wait(smem_u32(&sh.pfull[slot]), (slot ? pn1 : pn0) & 1u, dead);
-                if (slot) ++pn1;
-                else ++pn0;
-                if (x == 0) warp_wait(smem_u32(&sh.vfull[vn & 1u]), (vn >> 1) & 1u, dead);
-                tc_after();
-                weighted(x, slot, vn & 1u, j == 0);
-                if (x == tiles - 1) tc_commit(smem_u32(&sh.vempty[vn & 1u]), elected);
-                if (S_::MT == 2 && again) {
-                    if (x == 0) warp_wait(smem_u32(&sh.kfull[kn & 1u]), (kn >> 1) & 1u, dead);
-                    tc_after();
-                    scores(x, x, kn & 1u);
-                    if (x == tiles - 1) tc_commit(smem_u32(&sh.kempty[kn & 1u]), elected);
-                }
-            }
-            ++vn;
-            if (S_::MT == 2 && again) ++kn;
+            // the scores after the next overwrite these weights, in the order of issue; the next are there already
+            weighted(j == 0);
+            if (j + 2 < n) scores();
         }
     }
 }
@@ -692,14 +675,13 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     const uint32_t qrow = qbuf + x * S_::QB + row * 128;
     const float scale = p.sm_scale * scalar_or_1(p.gk);
     const float gv = scalar_or_1(p.gv);
-    uint32_t tn = 0, on = 0;  // KV tiles seen (slots: MT 2: one; MT 1: two in turn), products with V done before
+    uint32_t tn = 0, on = 0;  // steps seen, products with V done before this piece
     uint32_t scale_n = 0;     // tiles of the CTA so far: place in the ring of scales
     Walk<D> w;
     for (w.start(p); w.more(); w.next(p)) {
-        const int n = w.piece_tiles;
-        const int tiles = (S_::MT == 2 && w.u.t1 - w.u.t0 > per) ? 2 : 1;
-        if (x >= tiles) {
-            scale_n += n;
+        const int n = w.piece_tiles * S_::SUBS;  // steps
+        if (S_::MT == 2 && x > 0 && w.u.t1 - w.u.t0 <= per) {  // a unit without this row tile
+            scale_n += w.piece_tiles;
             continue;
         }
         // ---- queries: this thread's row, to FP16 by a power of two
@@ -738,25 +720,25 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         float m = -INFINITY, l = 0.0f;
         const int first_pos = w.s.len - w.s.n + w.u.t0 + x * per, last_pos = w.s.len - w.s.n + min(w.u.t1, w.u.t0 + (x + 1) * per) - 1;
         for (int j = 0; j < n; ++j) {
-            const int slot = S_::MT == 2 ? x : static_cast<int>(tn & 1u);
-            const uint32_t s_col = lanes + slot * S_::S_COL;
-            const int t0 = tile_start<D>(w.u, w.tile0 + j);
-            warp_wait(smem_u32(&sh.sfull[slot]), (S_::MT == 2 ? tn : tn >> 1) & 1u, dead);
+            const uint32_t slot = tn & 1u, part = j % S_::SUBS;
+            const uint32_t s_col = lanes + (2 * x + slot) * kSub;
+            const int t0 = tile_start<D>(w.u, w.tile0 + j / S_::SUBS) + part * kSub;
+            warp_wait(smem_u32(&sh.sfull[x][slot]), (tn >> 1) & 1u, dead);
             ++tn;
             tc_after();
-            const float4* sc = sh.scales[(scale_n + j) & 3u];
-            // columns [0, hi) of the tile are at or before the row, those below lo hidden by the window but for the first `sk`
-            const bool edge = t0 + S_::TK - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + S_::TK > p.sinks);
+            const float4* sc = sh.scales[(scale_n + j / S_::SUBS) & 3u] + 4 * part;
+            // columns [0, hi) of the step are at or before the row, those below lo hidden by the window but for the first `sk`
+            const bool edge = t0 + kSub - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + kSub > p.sinks);
             const int hi = pos - t0 + 1, lo = pos >= p.window ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
             auto seen = [&](int c0) {  // bit i: column c0 + i is visible
                 auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
                 return below(hi - c0) & (~below(lo - c0) | below(sk - c0));
             };
-            uint32_t x_[S_::TK];  // the row's scores, then its weights
+            uint32_t x_[kSub];  // the row's scores, then its weights
             tmem_ld_row(x_, s_col);
             if (edge) {
 #pragma unroll
-                for (int c = 0; c < S_::TK / 32; ++c) {
+                for (int c = 0; c < kSub / 32; ++c) {
                     const uint32_t ok = seen(32 * c);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -765,7 +747,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             }
             float mt = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < S_::GRP; ++g) {
+            for (int g = 0; g < kSub / 16; ++g) {
                 const float4 f = sc[g];
                 float a = fmaxf(__uint_as_float(x_[16 * g]), __uint_as_float(x_[16 * g + 1]));
 #pragma unroll
@@ -792,7 +774,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             }
             const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int g = 0; g < S_::GRP; ++g) {
+            for (int g = 0; g < kSub / 16; ++g) {
                 const float4 f = sc[g];
                 const float cg = fmaxf(cs * f.x, kTiny), off = f.y - mu;
                 float sum0 = 0.0f, sum1 = 0.0f;
@@ -814,15 +796,16 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 }
             }
             tc_wait_st();
+            // A parity tells a phase from the one before and the one after alone. The wait for the last product with V, below,
+            // must not find the barrier two phases back, and this one, for the last but one, not two ahead: so it stands here,
+            // before these weights are handed over.
+            if (j == n - 1 && j > 0) warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead);
             tc_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[slot]));
+            if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
         }
-        scale_n += n;
+        scale_n += w.piece_tiles;
         // ---- the piece's end: outputs, or a partial result
-        // (a parity tells only the last phase from the one before: the last tile's scores stand for all products with V
-        // before them, but at head_dim 256 they were issued before those of the last tile but one)
-        if (S_::MT == 1 && n > 1) warp_wait(smem_u32(&sh.ofull[x]), (on + n - 2) & 1u, dead);
         warp_wait(smem_u32(&sh.ofull[x]), (on + n - 1) & 1u, dead);
         on += n;
         tc_after();
@@ -870,14 +853,16 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.kfull[i]), kLoaderWarps);
             mbar_init(smem_u32(&sh.vfull[i]), kLoaderWarps);
-            mbar_init(smem_u32(&sh.kempty[i]), 1);
-            mbar_init(smem_u32(&sh.vempty[i]), 1);
+            mbar_init(smem_u32(&sh.kempty[i]), S_::MT);
+            mbar_init(smem_u32(&sh.vempty[i]), S_::MT);
             mbar_init(smem_u32(&sh.qfull[i]), 4);
-            mbar_init(smem_u32(&sh.sfull[i]), 1);
-            mbar_init(smem_u32(&sh.pfull[i]), 4);
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(smem_u32(&sh.sfull[i][k]), 1);
+                mbar_init(smem_u32(&sh.pfull[i][k]), 4);
+            }
             mbar_init(smem_u32(&sh.ofull[i]), 1);
         }
-        mbar_init(smem_u32(&sh.drained), 1);
+        mbar_init(smem_u32(&sh.drained), S_::MT);
         sh.dead = sh.never = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -891,18 +876,15 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
     tc_after();
     const uint32_t tmem = sh.tmem;
     pdl_enter();
-    // registers: 512 threads start with 128 each; a softmax thread holds its row's 128 scores. 184 + 184 + 88 + 56 = 4 x 128
     if (warp < S_::SOFT_WARPS) {
-        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
     } else if (warp < kIssuer) {
-        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         load_tiles<D>(p, sh, base + S_::K_OFF, base + S_::V_OFF, warp - S_::SOFT_WARPS, lane);
     } else {
-        if constexpr (S_::MT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == kIssuer) {
+        if (warp < kIssuer + S_::MT) {
             const uint32_t elected = lane == 0;
-            issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
+            if (warp == kIssuer) issue_products<D, 0>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
+            else if constexpr (S_::MT == 2) issue_products<D, 1>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
             // all products are done before TMEM is given back
             tc_commit(smem_u32(&sh.drained), elected);
             warp_wait(smem_u32(&sh.drained), 0, &sh.never);
