@@ -37,10 +37,11 @@ constexpr float kRescale = 8.0f;  // log2 units
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126: the least factor of a score (0 would turn a hidden one, -inf, into NaN)
 constexpr int kMaxGroup = 8;
 constexpr int kRowsM = 128;       // rows of a tile
-constexpr int kSub = 64;          // tokens of a step: scores, weights, product with V
-constexpr int kLoaderWarps = 4;
+constexpr int kStep = 64;         // tokens of a step: scores, weights, product with V
+constexpr int kLoaderWarps = 4;   // for K, and as many for V
 constexpr int kUnitCost = 1;      // of a unit beside its tiles: queries in, outputs out (in tiles)
-constexpr long long kWaitClocks = 8000000000ll;  // a wait gives up after about 4 s (a defect: no wait depends on another CTA)
+// A wait gives up after kTries tries of at most about kTryNs, seconds (a defect: no wait depends on another CTA).
+constexpr uint32_t kTryNs = 2000, kTries = 2000000;
 
 template <int D>
 struct Shape {
@@ -55,11 +56,11 @@ struct Shape {
     static constexpr int V_OFF = K_OFF + STAGES * KB;
     static constexpr int SMEM = V_OFF + STAGES * KB + 1024;  // the base is rounded up to 1024
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int WARPS = SOFT_WARPS + kLoaderWarps + 4;  // (the issuers' warpgroup has idle warps)
+    static constexpr int WARPS = SOFT_WARPS + 2 * kLoaderWarps + 4;  // (an idle one in the issuers' warpgroup)
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int SUBS = TK / kSub;           // steps of the softmax in a KV tile
+    static constexpr int STEPS = TK / kStep;         // of a KV tile
     // TMEM columns: two slots of scores for each row tile, then the outputs
-    static constexpr int O_COL = MT * 2 * kSub;
+    static constexpr int O_COL = MT * 2 * kStep;
     static_assert(O_COL + MT * D <= 512, "TMEM");
     static_assert(SMEM <= 232448 - 1024, "shared memory");
 };
@@ -307,39 +308,35 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("{\n\t.reg .b64 s;\n\tmbarrier.arrive.shared::cta.b64 s, [%0];\n\t}" ::"r"(bar) : "memory");
 }
+// (returns after kTryNs at the latest)
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "n"(kTryNs) : "memory");
     return ok != 0;
 }
-// Waits for the phase of this parity. Once a wait of the CTA has given up, `dead`, none waits any more: every role runs through
-// its list over whatever is there (all of it in bounds) and the kernel ends.
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    if (mbar_try(bar, parity)) return;
-    const long long t0 = clock64();
-    while (!mbar_try(bar, parity)) {
-        if (*dead) return;
-        if (clock64() - t0 > kWaitClocks) {
-            *dead = 1;
-            return;
-        }
+// A warp waits for the phase of this parity. Once a wait of the CTA has given up, `dead`, none waits any more: every role runs
+// through its list over whatever is there (all of it in bounds) and the kernel ends.
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
+    for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try(bar, parity)); ++i) {
+        if (i == kTries) *dead = 1;
+        if (__any_sync(0xFFFFFFFFu, *dead)) return;
     }
 }
-// The same for a whole warp.
-__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
-    mbar_wait(bar, parity, dead);
-    __syncwarp();
-}
+// A value that is the same in all lanes, so that the compiler knows it.
+__device__ __forceinline__ int uniform(int x) { return static_cast<int>(__reduce_or_sync(0xFFFFFFFFu, static_cast<unsigned>(x))); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t elected) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(elected)
-        : "memory");
+// One lane of the (converged) warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -360,21 +357,26 @@ __device__ __forceinline__ Operand operand(uint32_t addr, uint32_t lead, uint32_
 __host__ __device__ constexpr uint32_t instruction(int n, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n) >> 3) << 17 | (128u >> 4) << 24;
 }
-// (Whole warps call these and one lane, `elected`, issues: the operands then stay in uniform registers, which is where the
-// instruction takes them from. With one lane in a branch of its own each was moved there first, and issuing took as long as
-// the products.)
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
+// D (+)= A B over 64 values of K: A and B K-major, four steps of 32 bytes. (These are called by the lane that elect_one chose: the
+// instruction takes its operands from uniform registers, and with a lane that the compiler cannot know to be one alone it
+// moves them there in a loop over lanes.)
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(elected)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t elected) {
+// D (+)= A B over 32 values of K: A in TMEM, B MN-major, two steps of 16 rows of 128 bytes.
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(elected)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 b, %2, 128;\n\tadd.s32 a, %1, 8;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 // 32 columns of this warp's lanes (with the wait: nothing may use the registers before it).
@@ -403,7 +405,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// The scores of a step, 64 columns of this warp's lanes.
+// The scores of a step, of this warp's lanes.
 __device__ __forceinline__ void tmem_ld_row(uint32_t (&r)[64], uint32_t addr) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -427,16 +429,6 @@ __device__ __forceinline__ uint4 ldg16(const void* p) {
     asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
     return r;
 }
-// The same where `ok`, else zeros. (A predicate, not a branch: the values of two branches meet in copies of registers, and
-// those wait for the load.)
-__device__ __forceinline__ uint4 ldg16_if(const void* p, bool ok) {
-    uint4 r;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@q ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];\n\t}"
-        : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w) : "l"(p), "r"(ok ? 1u : 0u));
-    return r;
-}
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -444,27 +436,120 @@ __device__ __forceinline__ float scalar_or_1(const float* p) { return p ? __ldg(
 
 // ------------------------------------------------------------------------------------------ the attention
 
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
+constexpr uint32_t kRing = 8;
+
+enum PlaceFlags {
+    kFirst = 1,   // tile of a piece (the part of a unit that this CTA does)
+    kLast = 2,
+    kEnd = 4,     // last tile of the CTA's part
+    kTwo = 8,     // the unit has its second row tile
+    kFull = 16,   // every token of the tile is there and visible to a row
+    kWhole = 32,  // the piece is its unit
+    kGoesOn = 64  // the piece goes on with a unit that another CTA began
+};
+
+// What the other roles need of a KV tile: of its 16-token groups the first token's row in the pools (kNoRow: no page, or no
+// token a row sees) and the scales (s_K, log2 s_V, 1 / s_V); its first token, and its unit: visible are tokens lo .. hi and
+// the first ones; rows of tokens c0 .. c1 of the chunk, whose row 0 is `row0` and has position pos0; KV head h.
+struct Place {
+    float4 scales[8];
+    uint32_t row[8];
+    int t0, lo, hi, flags, c0, c1, row0, pos0, h;
+};
+
 struct Shared {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-    uint64_t qfull[2], sfull[2][2], pfull[2][2], ofull[2];  // [row tile], [row tile][slot]
+    uint64_t full[2][2], empty[2][2];       // [K, V][stage]
+    uint64_t qfull[2], ofull[2];             // [row tile]
+    uint64_t sfull[2][2], pfull[2][2];       // [row tile][slot]
     uint64_t drained;
-    float4 scales[4][8];  // (s_K, log2 s_V, 1 / s_V) of a KV tile's groups, in a ring of tiles
+    uint64_t placed[kRing];
+    Place ring[kRing];
+    uint32_t loaded;  // tiles of V that its first loader warp has stored
     uint32_t tmem;
     int dead;   // a wait gave up
     int never;  // (stays 0)
 };
 
+// The scout: one warp that walks over the CTA's part and looks up where the KV tiles lie, ahead of the others, into a ring of
+// places. (With every role walking by itself the kernel had 90 KB of code, and 15 % of the warps' time went into waiting for
+// instructions.)
+template <int D>
+__device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, int lane) {
+    using S_ = Shape<D>;
+    volatile int* dead = &sh.dead;
+    uint32_t n = 0;
+    Walk<D> w;
+    for (w.start(p); w.more(); w.next(p)) {
+        const int unit = (w.whole() ? kWhole : 0) | (w.tile0 > 0 ? kGoesOn : 0) |
+                         (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G ? kTwo : 0);
+        const bool final = w.unit_begin + kUnitCost + w.u.tiles >= w.end;
+#pragma unroll 1
+        for (int j = 0; j < w.piece_tiles; ++j, ++n) {
+            const int t0 = tile_start<D>(w.u, w.tile0 + j), a = t0 + 16 * lane;
+            uint32_t row = kNoRow;  // (pools have fewer than 2^32 rows)
+            float sk = 1.0f, sv = 1.0f;
+            if (lane < S_::GRP && a < w.u.hi && (a + 15 >= w.u.lo || a < p.sinks)) {
+                const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(a), p.t_magic));
+                const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + idx);
+                if (page < 0 || page >= p.pool_pages) {
+                    flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
+                } else {
+                    const uint32_t at = static_cast<uint32_t>(page) * p.H + w.h;
+                    row = at * static_cast<uint32_t>(p.T) + static_cast<uint32_t>(a - idx * p.T);
+                    if (p.kbs) sk = __ldg(p.kbs + at);
+                    if (p.vbs) sv = __ldg(p.vbs + at);
+                }
+            }
+            const bool seen = t0 + S_::TK <= w.u.hi && (t0 >= w.u.lo || t0 + S_::TK <= p.sinks);
+            const bool full = __all_sync(0xFFFFFFFFu, seen && (lane >= S_::GRP || row != kNoRow));
+            // V of tile m is stored after the products with V of tile m - 2 are done, hence the weights of that tile made and the
+            // places up to it read by all: once V of tile n - 6 is stored, the place of tile n - 8 is free.
+            if (n >= kRing) {
+                for (uint32_t i = 0; *static_cast<volatile uint32_t*>(&sh.loaded) < n - (kRing - 3) && !*dead; ++i) {
+                    __nanosleep(100);
+                    if (i == 20 * kTries) *dead = 1;
+                }
+                __syncwarp();
+            }
+            Place& d = sh.ring[n % kRing];
+            if (lane < S_::GRP) {
+                d.row[lane] = row;
+                d.scales[lane] = row != kNoRow ? make_float4(sk, log2f(sv), 1.0f / sv, 0.0f) : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
+            }
+            if (lane == 0) {
+                const bool last = j + 1 == w.piece_tiles;
+                d.t0 = t0;
+                d.lo = w.u.lo;
+                d.hi = w.u.hi;
+                d.flags = unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0);
+                d.c0 = w.u.t0;
+                d.c1 = w.u.t1;
+                d.row0 = w.s.first;
+                d.pos0 = w.s.len - w.s.n;
+                d.h = w.h;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.placed[n % kRing]));
+        }
+    }
+}
+
+// What a lane reads for a token that no row sees, or that has no page. (Two branches, one of them without a load, would meet in
+// copies of registers, and those wait for the load.)
+__device__ uint4 g_zeros[16];
+
 // The loader's threads: a warp's load covers R rows of 64 or 128 bytes (whole lines of a row), a lane one 16-byte chunk, which
 // becomes two in the swizzled layout. The eight lanes of a store phase lie in an even row and the odd one after it, four chunks
 // each: the even row's land in even 16-byte columns or in odd ones, the odd row's in the others, so they hit distinct banks.
 template <int D>
-__device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, uint32_t kbuf, uint32_t vbuf, int warp, int lane) {
+__device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, uint32_t smem, int kv, int warp, int lane) {
     using S_ = Shape<D>;
     constexpr int WIDE = D >= 128 ? 2 : 1;               // 64-byte columns of a load
     constexpr int R = 8 / WIDE;                          // its rows
-    constexpr int STEPS = S_::TK / R / kLoaderWarps;     // loads of a column: rows R (warp + 4 g) on
+    constexpr int LOADS = S_::TK / R / kLoaderWarps;     // of a column: rows R (warp + 4 g) on
     constexpr int COLS = S_::BLOCKS / WIDE;
-    constexpr int N = STEPS * COLS;                      // chunks of a lane
+    constexpr int N = LOADS * COLS;                      // chunks of a lane
     const int ch = lane & 3, blk = WIDE == 2 ? (lane >> 3) & 1 : 0;
     const int r0 = R * warp + (((lane >> 2) & 1) | (WIDE == 2 ? (lane >> 4) << 1 : (lane >> 3) << 1));  // the lane's first row
     const int g0 = r0 >> 4;                              // its 16-token group; further rows lie in every (R / 4)th group on
@@ -472,70 +557,33 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
     const uint32_t src0 = static_cast<uint32_t>((r0 & 15) * D + 64 * blk + 16 * ch);
     volatile int* dead = &sh.dead;
 
-    Walk<D> w;
-    w.start(p);
-    if (!w.more()) return;
-    // A tile: lane l < GRP has the pool row of the first token of group l, or kNone.
-    constexpr uint32_t kNone = 0xFFFFFFFFu;
-    struct Tile {
-        int t0, lo, hi;
-        uint32_t row;
-        int page, h;
-        bool full;  // every token is there and visible to a row
-    };
-    int j = 0;  // tile within the piece
-    auto look = [&]() {
-        Tile t;
-        t.t0 = tile_start<D>(w.u, w.tile0 + j);
-        t.lo = w.u.lo;
-        t.hi = w.u.hi;
-        t.h = w.h;
-        t.row = kNone;
-        t.page = -1;
-        const int a = t.t0 + 16 * lane;
-        if (lane < S_::GRP && a < t.hi && (a + 15 >= t.lo || a < p.sinks)) {
-            const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(a), p.t_magic));
-            t.page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + idx);
-            t.row = static_cast<uint32_t>(a - idx * p.T);
-        }
-        t.full = t.t0 + S_::TK <= t.hi && (t.t0 >= t.lo || t.t0 + S_::TK <= p.sinks);
-        return t;
-    };
-    // the page ids have arrived: pool rows (fewer than 2^32)
-    auto place = [&](Tile& t) {
-        if (t.row != kNone) {
-            if (t.page < 0 || t.page >= p.pool_pages) {
-                flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
-                t.page = -1;
-                t.row = kNone;
-            } else {
-                t.row += (static_cast<uint32_t>(t.page) * p.H + t.h) * static_cast<uint32_t>(p.T);
-            }
-        }
-        t.full = __all_sync(0xFFFFFFFFu, t.full && (lane >= S_::GRP || t.row != kNone));
-    };
-    auto advance = [&]() {  // to the next tile; false at the end
-        if (++j < w.piece_tiles) return true;
-        j = 0;
-        w.next(p);
-        return w.more();
-    };
-    auto load = [&](const Tile& t, const uint8_t* pool, uint4 (&r)[N]) {
-        const uint8_t* base = pool + src0;
+    const uint8_t* base = (kv ? p.v : p.k) + src0;
+    const uint32_t buf = smem + (kv ? S_::V_OFF : S_::K_OFF) + at0;
+    const uint32_t full = smem_u32(&sh.full[kv][0]), empty = smem_u32(&sh.empty[kv][0]);
+    uint4 r[N];
+    // (tile n's values are loaded as soon as the ones before are stored; K and V have warps of their own, so each waits for its
+    // own loads alone)
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        const Place& t = sh.ring[n % kRing];
+        warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
+        const int flags = uniform(t.flags);
 #pragma unroll
-        for (int g = 0; g < STEPS; ++g) {
-            const uint32_t row = __shfl_sync(0xFFFFFFFFu, t.row, g0 + g * (R * kLoaderWarps / 16));
-            const int tok = t.t0 + r0 + g * R * kLoaderWarps;
-            const bool ok = t.full || (row != kNone && tok < t.hi && (tok >= t.lo || tok < p.sinks));
+        for (int g = 0; g < LOADS; ++g) {
+            const uint32_t row = t.row[g0 + g * (R * kLoaderWarps / 16)];
             const uint8_t* src = base + static_cast<uint64_t>(row) * D;
+            if (!(flags & kFull)) {
+                const int tok = t.t0 + r0 + g * R * kLoaderWarps;
+                if (row == kNoRow || tok >= t.hi || (tok < t.lo && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
+            }
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16_if(src + 64 * WIDE * c, ok);
+            for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
         }
-    };
-    auto store = [&](uint32_t buf, const uint4 (&r)[N]) {
-        const uint32_t at = buf + at0, at1 = at ^ 16u;
+        const uint32_t stage = n & 1u;
+        warp_wait(empty + 8 * stage, ((n >> 1) & 1u) ^ 1u, dead);
+        const uint32_t at = buf + stage * S_::KB, at1 = at ^ 16u;
 #pragma unroll
-        for (int g = 0; g < STEPS; ++g)
+        for (int g = 0; g < LOADS; ++g)
 #pragma unroll
             for (int c = 0; c < COLS; ++c) {
                 const uint4 x = r[g * COLS + c];
@@ -548,117 +596,90 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
                 e4m3x4_to_f16x2x2(x.w, b);
                 sts16(at1 + off, a[0], a[1], b[0], b[1]);
             }
-    };
-
-    // page ids are two tiles ahead, values one: a register set is loaded again as soon as it is stored
-    Tile now = look(), then{};
-    uint4 rk[N], rv[N];
-    place(now);
-    load(now, p.k, rk);
-    load(now, p.v, rv);
-    bool more = advance();
-    if (more) then = look();
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t stage = n & 1u, phase = (n >> 1) & 1u;
-        float sk = 1.0f, sv = 1.0f;
-        if (warp == 0 && now.page >= 0) {
-            const int64_t at = static_cast<int64_t>(now.page) * p.H + now.h;
-            if (p.kbs) sk = __ldg(p.kbs + at);
-            if (p.vbs) sv = __ldg(p.vbs + at);
-        }
-        const bool after = more && advance();
-        Tile third{};
-        if (after) third = look();
-        warp_wait(smem_u32(&sh.kempty[stage]), phase ^ 1u, dead);
-        // the groups' scales: the products of tile n - 2 are done, so the weights of tile n - 4 have been made
-        if (warp == 0 && lane < S_::GRP)
-            sh.scales[n & 3u][lane] = now.page >= 0 ? make_float4(sk, log2f(sv), 1.0f / sv, 0.0f)
-                                                    : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
-        store(kbuf + stage * S_::KB, rk);
-        if (more) {
-            place(then);
-            load(then, p.k, rk);
-        }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.kfull[stage]));
-        warp_wait(smem_u32(&sh.vempty[stage]), phase ^ 1u, dead);
-        store(vbuf + stage * S_::KB, rv);
-        if (more) load(then, p.v, rv);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.vfull[stage]));
-        if (!more) return;
-        now = then;
-        then = third;
-        more = after;
+        if (lane == 0) {
+            mbar_arrive(full + 8 * stage);
+            if (kv == 1 && warp == 0) *static_cast<volatile uint32_t*>(&sh.loaded) = n + 1;
+        }
+        if (flags & kEnd) return;
     }
 }
 
-// The warp that issues the products of row tile x (a constant, so that all addresses are uniform).
-template <int D, int x>
-__device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem, uint32_t elected) {
+// The warp that issues the products of row tile x.
+template <int D>
+__device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh, uint32_t qbuf, uint32_t kbuf, uint32_t vbuf, uint32_t tmem, int x, int lane) {
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
-    constexpr uint32_t qk = instruction(kSub, false), pv = instruction(D, true);
-    uint32_t kt = 0, vt = 0;  // KV tiles of the CTA's part whose scores, whose product with V are issued
-    uint32_t kn = 0, vn = 0;  // the same of this row tile's steps: step i has slot i % 2
-    uint32_t units = 0;       // units with this row tile
-    Walk<D> w;
-    w.start(p);
-    auto scores = [&]() {
-        const uint32_t part = kn % S_::SUBS, stage = kt & 1u, slot = kn & 1u;
-        if (part == 0) warp_wait(smem_u32(&sh.kfull[stage]), (kt >> 1) & 1u, dead);
+    constexpr uint32_t qk = instruction(kStep, false), pv = instruction(D, true);
+    uint32_t units = 0;  // pieces with this row tile
+    // step `part` of KV tile n has slot `part`, or n % 2 where a tile is one step
+    auto slot_of = [](uint32_t n, uint32_t part) { return S_::STEPS == 2 ? part : n & 1u; };
+    auto phase_of = [](uint32_t n) { return (S_::STEPS == 2 ? n : n >> 1) & 1u; };
+    auto scores = [&](uint32_t n, uint32_t part) {
+        const uint32_t stage = n & 1u, slot = slot_of(n, part);
+        if (part == 0) warp_wait(smem_u32(&sh.full[0][stage]), (n >> 1) & 1u, dead);
         tc_after();
-        const Operand a = operand(qbuf + x * S_::QB, 16, 1024), b = operand(kbuf + stage * S_::KB + part * (kSub * 128), 16, 1024);
+        if (elect_one()) {
+            const Operand a = operand(qbuf + x * S_::QB, 16, 1024), b = operand(kbuf + stage * S_::KB + part * (kStep * 128), 16, 1024);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-            mma_ss(tmem + (2 * x + slot) * kSub, a.at((ks / 4) * (kRowsM * 128) + (ks % 4) * 32),
-                   b.at((ks / 4) * (S_::TK * 128) + (ks % 4) * 32), qk, ks > 0, elected);
-        tc_commit(smem_u32(&sh.sfull[x][slot]), elected);
-        if (part == S_::SUBS - 1) {
-            tc_commit(smem_u32(&sh.kempty[stage]), elected);
-            ++kt;
+            for (int k = 0; k < D / 64; ++k)
+                mma4_ss(tmem + (2 * x + slot) * kStep, a.at(k * (kRowsM * 128)), b.at(k * (S_::TK * 128)), qk, k > 0);
+            tc_commit(smem_u32(&sh.sfull[x][slot]));
+            if (part == S_::STEPS - 1) tc_commit(smem_u32(&sh.empty[0][stage]));
         }
-        ++kn;
+        __syncwarp();
     };
-    auto weighted = [&](bool first) {
-        const uint32_t part = vn % S_::SUBS, stage = vt & 1u, slot = vn & 1u;
-        if (part == 0) warp_wait(smem_u32(&sh.vfull[stage]), (vt >> 1) & 1u, dead);
-        warp_wait(smem_u32(&sh.pfull[x][slot]), (vn >> 1) & 1u, dead);
+    auto weighted = [&](uint32_t n, uint32_t part, bool first) {
+        const uint32_t stage = n & 1u, slot = slot_of(n, part);
+        if (part == 0) warp_wait(smem_u32(&sh.full[1][stage]), (n >> 1) & 1u, dead);
+        warp_wait(smem_u32(&sh.pfull[x][slot]), phase_of(n), dead);
         tc_after();
-        const Operand b = operand(vbuf + stage * S_::KB + part * (kSub * 128), S_::TK * 128, 1024);
+        if (elect_one()) {
+            const Operand b = operand(vbuf + stage * S_::KB + part * (kStep * 128), S_::TK * 128, 1024);
 #pragma unroll
-        for (int ks = 0; ks < kSub / 16; ++ks)
-            mma_ts(tmem + S_::O_COL + x * D, tmem + (2 * x + slot) * kSub + 8 * ks, b.at(ks * 2048), pv, !first || ks > 0, elected);
-        tc_commit(smem_u32(&sh.ofull[x]), elected);
-        if (part == S_::SUBS - 1) {
-            tc_commit(smem_u32(&sh.vempty[stage]), elected);
-            ++vt;
+            for (int k = 0; k < kStep; k += 32)
+                mma2_ts(tmem + S_::O_COL + x * D, tmem + (2 * x + slot) * kStep + k / 2, b.at(k * 128), pv, k > 0 || !first);
+            tc_commit(smem_u32(&sh.ofull[x]));
+            if (part == S_::STEPS - 1) tc_commit(smem_u32(&sh.empty[1][stage]));
         }
-        ++vn;
+        __syncwarp();
     };
-    for (; w.more(); w.next(p)) {
-        const int n = w.piece_tiles * S_::SUBS;
-        if (S_::MT == 2 && x > 0 && w.u.t1 - w.u.t0 <= kRowsM / p.G) {
-            // a unit without this row tile: its stages are free as soon as they are full
-            for (int j = 0; j < w.piece_tiles; ++j, ++kt, ++vt) {
-                warp_wait(smem_u32(&sh.kfull[kt & 1u]), (kt >> 1) & 1u, dead);
-                if (elected) mbar_arrive(smem_u32(&sh.kempty[kt & 1u]));
-                warp_wait(smem_u32(&sh.vfull[vt & 1u]), (vt >> 1) & 1u, dead);
-                if (elected) mbar_arrive(smem_u32(&sh.vempty[vt & 1u]));
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
+        const int flags = uniform(sh.ring[n % kRing].flags);
+        if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {
+            // A unit without this row tile: a stage is free as soon as it is full. Its softmax warps are taken along step by
+            // step, as ever (a barrier's parity does not tell them two tiles ahead).
+            const uint32_t stage = n & 1u;
+            warp_wait(smem_u32(&sh.full[0][stage]), (n >> 1) & 1u, dead);
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sh.empty[0][stage]));
+                mbar_arrive(smem_u32(&sh.sfull[x][0]));
+                mbar_arrive(smem_u32(&sh.sfull[x][1]));
             }
-            continue;
+            warp_wait(smem_u32(&sh.full[1][stage]), (n >> 1) & 1u, dead);
+            warp_wait(smem_u32(&sh.pfull[x][0]), phase_of(n), dead);
+            warp_wait(smem_u32(&sh.pfull[x][1]), phase_of(n), dead);
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[1][stage]));
+        } else {
+            // A step's scores are issued two steps ahead (one, where a KV tile is one step), behind the product with V of the
+            // step whose weights they overwrite.
+            if (flags & kFirst) {
+                warp_wait(smem_u32(&sh.qfull[x]), units & 1u, dead);
+                ++units;
+#pragma unroll 1
+                for (uint32_t part = 0; part < S_::STEPS; ++part) scores(n, part);
+            }
+#pragma unroll 1
+            for (uint32_t part = 0; part < S_::STEPS; ++part) {
+                if (S_::STEPS == 1 && !(flags & kLast)) scores(n + 1, part);
+                weighted(n, part, (flags & kFirst) && part == 0);
+                if (S_::STEPS == 2 && !(flags & kLast)) scores(n + 1, part);
+            }
         }
-        warp_wait(smem_u32(&sh.qfull[x]), units & 1u, dead);
-        ++units;
-        scores();
-        if (n > 1) scores();
-        for (int j = 0; j < n; ++j) {
-            // the scores after the next overwrite these weights, in the order of issue; the next are there already
-            weighted(j == 0);
-            if (j + 2 < n) scores();
-        }
+        if (flags & kEnd) return;
     }
 }
 
@@ -675,23 +696,35 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     const uint32_t qrow = qbuf + x * S_::QB + row * 128;
     const float scale = p.sm_scale * scalar_or_1(p.gk);
     const float gv = scalar_or_1(p.gv);
-    uint32_t tn = 0, on = 0;  // steps seen, products with V done before this piece
-    uint32_t scale_n = 0;     // tiles of the CTA so far: place in the ring of scales
-    Walk<D> w;
-    for (w.start(p); w.more(); w.next(p)) {
-        const int n = w.piece_tiles * S_::SUBS;  // steps
-        if (S_::MT == 2 && x > 0 && w.u.t1 - w.u.t0 <= per) {  // a unit without this row tile
-            scale_n += w.piece_tiles;
+    uint32_t on = 0;  // products with V asked for
+    int flags = 0, pos = 0, first_pos = 0, last_pos = 0, hq = 0;
+    int64_t out_row = 0;
+    bool real = false;
+    float cs = 0.0f, m = 0.0f, l = 0.0f;
+#pragma unroll 1
+    for (uint32_t n = 0; !(flags & kEnd); ++n) {
+        const Place& at = sh.ring[n % kRing];
+        warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
+        flags = uniform(at.flags);
+        if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {  // a unit without this row tile
+            for (int slot = 0; slot < 2; ++slot) {
+                warp_wait(smem_u32(&sh.sfull[x][slot]), n & 1u, dead);
+                if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
+            }
             continue;
         }
-        // ---- queries: this thread's row, to FP16 by a power of two
-        const int t = w.u.t0 + x * per + tok;  // token of the chunk
-        const bool real = tok < per && t < w.u.t1;
-        const int pos = w.s.len - w.s.n + (real ? t : w.u.t1 - 1);
-        const int64_t out_row = w.s.first + t;
-        float cs;
-        {
-            const uint16_t* src = p.q + out_row * p.q_stride + (w.h * p.G + head) * D;
+        if (flags & kFirst) {
+            // ---- queries: this thread's row, to FP16 by a power of two
+            const int t = at.c0 + x * per + tok;  // token of the chunk
+            real = tok < per && t < at.c1;
+            pos = at.pos0 + (real ? t : at.c1 - 1);
+            first_pos = at.pos0 + at.c0 + x * per;
+            last_pos = at.pos0 + min(at.c1, at.c0 + (x + 1) * per) - 1;
+            out_row = at.row0 + t;
+            hq = at.h * p.G + head;
+            m = -INFINITY;
+            l = 0.0f;
+            const uint16_t* src = p.q + out_row * p.q_stride + hq * D;
             float top = 0.0f;
             if (real) {
 #pragma unroll 4
@@ -717,37 +750,33 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[x]));
         }
-        float m = -INFINITY, l = 0.0f;
-        const int first_pos = w.s.len - w.s.n + w.u.t0 + x * per, last_pos = w.s.len - w.s.n + min(w.u.t1, w.u.t0 + (x + 1) * per) - 1;
-        for (int j = 0; j < n; ++j) {
-            const uint32_t slot = tn & 1u, part = j % S_::SUBS;
-            const uint32_t s_col = lanes + (2 * x + slot) * kSub;
-            const int t0 = tile_start<D>(w.u, w.tile0 + j / S_::SUBS) + part * kSub;
-            warp_wait(smem_u32(&sh.sfull[x][slot]), (tn >> 1) & 1u, dead);
-            ++tn;
-            tc_after();
-            const float4* sc = sh.scales[(scale_n + j / S_::SUBS) & 3u] + 4 * part;
+#pragma unroll 1
+        for (uint32_t part = 0; part < S_::STEPS; ++part) {
+            const uint32_t slot = S_::STEPS == 2 ? part : n & 1u;
+            const uint32_t s_col = lanes + (2 * x + slot) * kStep;
+            const int t0 = at.t0 + static_cast<int>(part) * kStep;
+            const bool begins = (flags & kFirst) && part == 0, ends = (flags & kLast) && part == S_::STEPS - 1;
             // columns [0, hi) of the step are at or before the row, those below lo hidden by the window but for the first `sk`
-            const bool edge = t0 + kSub - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + kSub > p.sinks);
-            const int hi = pos - t0 + 1, lo = pos >= p.window ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
-            auto seen = [&](int c0) {  // bit i: column c0 + i is visible
-                auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
-                return below(hi - c0) & (~below(lo - c0) | below(sk - c0));
-            };
-            uint32_t x_[kSub];  // the row's scores, then its weights
+            const bool edge = t0 + kStep - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + kStep > p.sinks);
+            const float4* sc = at.scales + 4 * part;
+            warp_wait(smem_u32(&sh.sfull[x][slot]), (S_::STEPS == 2 ? n : n >> 1) & 1u, dead);
+            tc_after();
+            uint32_t x_[kStep];  // the row's scores, then its weights
             tmem_ld_row(x_, s_col);
             if (edge) {
+                const int hi = pos - t0 + 1, lo = pos >= p.window ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
+                auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
 #pragma unroll
-                for (int c = 0; c < kSub / 32; ++c) {
-                    const uint32_t ok = seen(32 * c);
+                for (int c = 0; c < kStep; c += 32) {
+                    const uint32_t seen = below(hi - c) & (~below(lo - c) | below(sk - c));  // bit i: column c + i is visible
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (!((ok >> i) & 1u)) x_[32 * c + i] = 0xFF800000u;
+                        if (!((seen >> i) & 1u)) x_[c + i] = 0xFF800000u;
                 }
             }
             float mt = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < kSub / 16; ++g) {
+            for (int g = 0; g < kStep / 16; ++g) {
                 const float4 f = sc[g];
                 float a = fmaxf(__uint_as_float(x_[16 * g]), __uint_as_float(x_[16 * g + 1]));
 #pragma unroll
@@ -759,8 +788,8 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 const float a = mn == -INFINITY ? 1.0f : ex2_approx(m - mn);
                 m = mn;
                 l *= a;
-                if (j > 0) {
-                    warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead);
+                if (!begins) {
+                    warp_wait(smem_u32(&sh.ofull[x]), (on - 1) & 1u, dead);
                     tc_after();
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {  // (16 at a time: the scores are held in registers meanwhile)
@@ -774,7 +803,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             }
             const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int g = 0; g < kSub / 16; ++g) {
+            for (int g = 0; g < kStep / 16; ++g) {
                 const float4 f = sc[g];
                 const float cg = fmaxf(cs * f.x, kTiny), off = f.y - mu;
                 float sum0 = 0.0f, sum1 = 0.0f;
@@ -798,21 +827,21 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             tc_wait_st();
             // A parity tells a phase from the one before and the one after alone. The wait for the last product with V, below,
             // must not find the barrier two phases back, and this one, for the last but one, not two ahead: so it stands here,
-            // before these weights are handed over.
-            if (j == n - 1 && j > 0) warp_wait(smem_u32(&sh.ofull[x]), (on + j - 1) & 1u, dead);
+            // before the last weights are handed over.
+            if (ends && !begins) warp_wait(smem_u32(&sh.ofull[x]), (on - 1) & 1u, dead);
+            ++on;
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
         }
-        scale_n += w.piece_tiles;
+        if (!(flags & kLast)) continue;
         // ---- the piece's end: outputs, or a partial result
-        warp_wait(smem_u32(&sh.ofull[x]), (on + n - 1) & 1u, dead);
-        on += n;
+        warp_wait(smem_u32(&sh.ofull[x]), (on - 1) & 1u, dead);
         tc_after();
-        const bool whole = w.whole();
-        const int64_t rec = (2 * static_cast<int64_t>(blockIdx.x) + (w.tile0 > 0 ? 0 : 1)) * (S_::MT * kRowsM) + x * kRowsM + row;
+        const bool whole = flags & kWhole;
+        const int64_t rec = (2 * static_cast<int64_t>(blockIdx.x) + (flags & kGoesOn ? 0 : 1)) * (S_::MT * kRowsM) + x * kRowsM + row;
         const float f = l > 0.0f ? gv / l : 0.0f;
-        uint16_t* dst = p.out + out_row * p.out_stride + (w.h * p.G + head) * D;
+        uint16_t* dst = p.out + out_row * p.out_stride + hq * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
@@ -836,7 +865,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         }
         if (real) {
             if (!whole) p.rec_ml[rec] = make_float2(m, l);
-            else if (p.lse) p.lse[out_row * p.Hq + w.h * p.G + head] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            else if (p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
         tc_before();  // the next unit's products overwrite what was read here
     }
@@ -851,10 +880,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
     const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.kfull[i]), kLoaderWarps);
-            mbar_init(smem_u32(&sh.vfull[i]), kLoaderWarps);
-            mbar_init(smem_u32(&sh.kempty[i]), S_::MT);
-            mbar_init(smem_u32(&sh.vempty[i]), S_::MT);
+            for (int kv = 0; kv < 2; ++kv) {
+                mbar_init(smem_u32(&sh.full[kv][i]), kLoaderWarps);
+                mbar_init(smem_u32(&sh.empty[kv][i]), S_::MT);
+            }
             mbar_init(smem_u32(&sh.qfull[i]), 4);
             for (int k = 0; k < 2; ++k) {
                 mbar_init(smem_u32(&sh.sfull[i][k]), 1);
@@ -862,8 +891,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
             }
             mbar_init(smem_u32(&sh.ofull[i]), 1);
         }
+        for (uint32_t i = 0; i < kRing; ++i) mbar_init(smem_u32(&sh.placed[i]), 1);
         mbar_init(smem_u32(&sh.drained), S_::MT);
         sh.dead = sh.never = 0;
+        sh.loaded = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     constexpr int kIssuer = S_::WARPS - 4;
@@ -876,20 +907,26 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
     tc_after();
     const uint32_t tmem = sh.tmem;
     pdl_enter();
+    const bool work = p.plan[blockIdx.x].cut < p.plan[blockIdx.x + 1].cut;
+    // registers: 640 threads start with 96 each; a softmax thread holds a row's scores of a step: 2 x 128 + 2 x 72 + 80 = 5 x 96
+    if constexpr (S_::MT == 2) {
+        if (warp < S_::SOFT_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        else if (warp < kIssuer) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
     if (warp < S_::SOFT_WARPS) {
-        softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
+        if (work) softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
     } else if (warp < kIssuer) {
-        load_tiles<D>(p, sh, base + S_::K_OFF, base + S_::V_OFF, warp - S_::SOFT_WARPS, lane);
-    } else {
-        if (warp < kIssuer + S_::MT) {
-            const uint32_t elected = lane == 0;
-            if (warp == kIssuer) issue_products<D, 0>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
-            else if constexpr (S_::MT == 2) issue_products<D, 1>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, elected);
-            // all products are done before TMEM is given back
-            tc_commit(smem_u32(&sh.drained), elected);
-            warp_wait(smem_u32(&sh.drained), 0, &sh.never);
-        }
+        const int i = warp - S_::SOFT_WARPS;
+        if (work) load_tiles<D>(p, sh, base, i / kLoaderWarps, i % kLoaderWarps, lane);
+    } else if (warp < kIssuer + S_::MT) {
+        if (work) issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, uniform(warp - kIssuer), lane);
+        // all products are done before TMEM is given back
+        if (elect_one()) tc_commit(smem_u32(&sh.drained));
         __syncwarp();
+        warp_wait(smem_u32(&sh.drained), 0, &sh.never);
+    } else if (work && warp == kIssuer + S_::MT) {
+        scout_tiles<D>(p, sh, lane);
     }
     __syncwarp();
     tc_before();
