@@ -455,7 +455,9 @@ enum PlaceFlags {
 struct Place {
     float4 scales[8];
     uint32_t row[8];
-    int t0, lo, hi, flags, c0, c1, row0, pos0, h;
+    int4 head;  // flags, t0, lo, hi
+    int4 unit;  // c0, c1, row0, pos0
+    int h;
 };
 
 struct Shared {
@@ -519,14 +521,8 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, i
             }
             if (lane == 0) {
                 const bool last = j + 1 == w.piece_tiles;
-                d.t0 = t0;
-                d.lo = w.u.lo;
-                d.hi = w.u.hi;
-                d.flags = unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0);
-                d.c0 = w.u.t0;
-                d.c1 = w.u.t1;
-                d.row0 = w.s.first;
-                d.pos0 = w.s.len - w.s.n;
+                d.head = make_int4(unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0), t0, w.u.lo, w.u.hi);
+                d.unit = make_int4(w.u.t0, w.u.t1, w.s.first, w.s.len - w.s.n);
                 d.h = w.h;
             }
             __syncwarp();
@@ -567,14 +563,15 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
     for (uint32_t n = 0;; ++n) {
         const Place& t = sh.ring[n % kRing];
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
-        const int flags = uniform(t.flags);
+        const int4 head = t.head;
+        const int flags = uniform(head.x);
 #pragma unroll
         for (int g = 0; g < LOADS; ++g) {
             const uint32_t row = t.row[g0 + g * (R * kLoaderWarps / 16)];
             const uint8_t* src = base + static_cast<uint64_t>(row) * D;
             if (!(flags & kFull)) {
-                const int tok = t.t0 + r0 + g * R * kLoaderWarps;
-                if (row == kNoRow || tok >= t.hi || (tok < t.lo && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
+                const int tok = head.y + r0 + g * R * kLoaderWarps;
+                if (row == kNoRow || tok >= head.w || (tok < head.z && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
             }
 #pragma unroll
             for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
@@ -648,7 +645,7 @@ __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
-        const int flags = uniform(sh.ring[n % kRing].flags);
+        const int flags = uniform(sh.ring[n % kRing].head.x);
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {
             // A unit without this row tile: a stage is free as soon as it is full. Its softmax warps are taken along step by
             // step, as ever (a barrier's parity does not tell them two tiles ahead).
@@ -697,33 +694,35 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     const float scale = p.sm_scale * scalar_or_1(p.gk);
     const float gv = scalar_or_1(p.gv);
     uint32_t on = 0;  // products with V asked for
-    int flags = 0, pos = 0, first_pos = 0, last_pos = 0, hq = 0;
-    int64_t out_row = 0;
-    bool real = false;
-    float cs = 0.0f, m = 0.0f, l = 0.0f;
 #pragma unroll 1
-    for (uint32_t n = 0; !(flags & kEnd); ++n) {
-        const Place& at = sh.ring[n % kRing];
+    for (uint32_t n = 0;;) {  // a piece; n: its first KV tile
+        const Place& begin = sh.ring[n % kRing];
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
-        flags = uniform(at.flags);
+        int flags = begin.head.x;
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {  // a unit without this row tile
-            for (int slot = 0; slot < 2; ++slot) {
-                warp_wait(smem_u32(&sh.sfull[x][slot]), n & 1u, dead);
-                if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
+            while (true) {
+                for (int slot = 0; slot < 2; ++slot) {
+                    warp_wait(smem_u32(&sh.sfull[x][slot]), n & 1u, dead);
+                    flags = sh.ring[n % kRing].head.x;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
+                }
+                ++n;
+                if (flags & kLast) break;
             }
+            if (flags & kEnd) return;
             continue;
         }
-        if (flags & kFirst) {
-            // ---- queries: this thread's row, to FP16 by a power of two
-            const int t = at.c0 + x * per + tok;  // token of the chunk
-            real = tok < per && t < at.c1;
-            pos = at.pos0 + (real ? t : at.c1 - 1);
-            first_pos = at.pos0 + at.c0 + x * per;
-            last_pos = at.pos0 + min(at.c1, at.c0 + (x + 1) * per) - 1;
-            out_row = at.row0 + t;
-            hq = at.h * p.G + head;
-            m = -INFINITY;
-            l = 0.0f;
+        // ---- queries: this thread's row, to FP16 by a power of two
+        const int4 unit = begin.unit;
+        const int t = unit.x + x * per + tok;  // token of the chunk
+        const bool real = tok < per && t < unit.y;
+        const int pos = unit.w + (real ? t : unit.y - 1);
+        const int first_pos = unit.w + unit.x + x * per, last_pos = unit.w + min(unit.y, unit.x + (x + 1) * per) - 1;
+        const int64_t out_row = unit.z + t;
+        const int hq = begin.h * p.G + head;
+        float cs, m = -INFINITY, l = 0.0f;
+        {
             const uint16_t* src = p.q + out_row * p.q_stride + hq * D;
             float top = 0.0f;
             if (real) {
@@ -750,19 +749,28 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[x]));
         }
+        bool begins = true;
+        int t0 = 0;
 #pragma unroll 1
-        for (uint32_t part = 0; part < S_::STEPS; ++part) {
+        for (uint32_t part = 0;; begins = false) {
             const uint32_t slot = S_::STEPS == 2 ? part : n & 1u;
             const uint32_t s_col = lanes + (2 * x + slot) * kStep;
-            const int t0 = at.t0 + static_cast<int>(part) * kStep;
-            const bool begins = (flags & kFirst) && part == 0, ends = (flags & kLast) && part == S_::STEPS - 1;
-            // columns [0, hi) of the step are at or before the row, those below lo hidden by the window but for the first `sk`
-            const bool edge = t0 + kStep - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + kStep > p.sinks);
-            const float4* sc = at.scales + 4 * part;
             warp_wait(smem_u32(&sh.sfull[x][slot]), (S_::STEPS == 2 ? n : n >> 1) & 1u, dead);
             tc_after();
+            // (where the tile's scores are, its place is there: read while the scores come, as shared memory is slow beside the
+            // tensor core's reads)
+            const Place& at = sh.ring[n % kRing];
+            const int4 info = at.head;
+            float4 f[kStep / 16];
+#pragma unroll
+            for (int g = 0; g < kStep / 16; ++g) f[g] = at.scales[4 * part + g];
             uint32_t x_[kStep];  // the row's scores, then its weights
             tmem_ld_row(x_, s_col);
+            flags = info.x;
+            t0 = info.y + static_cast<int>(part) * kStep;
+            const bool ends = (flags & kLast) && part == S_::STEPS - 1;
+            // columns [0, hi) of the step are at or before the row, those below lo hidden by the window but for the first `sk`
+            const bool edge = t0 + kStep - 1 > first_pos || (t0 < last_pos - p.window + 1 && t0 + kStep > p.sinks);
             if (edge) {
                 const int hi = pos - t0 + 1, lo = pos >= p.window ? pos - p.window + 1 - t0 : 0, sk = p.sinks - t0;
                 auto below = [](int k) { return k >= 32 ? 0xFFFFFFFFu : (k <= 0 ? 0u : (1u << k) - 1u); };
@@ -777,11 +785,11 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             float mt = -INFINITY;
 #pragma unroll
             for (int g = 0; g < kStep / 16; ++g) {
-                const float4 f = sc[g];
+                f[g].x = fmaxf(cs * f[g].x, kTiny);
                 float a = fmaxf(__uint_as_float(x_[16 * g]), __uint_as_float(x_[16 * g + 1]));
 #pragma unroll
                 for (int i = 2; i < 16; i += 2) a = fmaxf(a, fmaxf(__uint_as_float(x_[16 * g + i]), __uint_as_float(x_[16 * g + i + 1])));
-                mt = fmaxf(mt, fmaf(a, fmaxf(cs * f.x, kTiny), f.y));
+                mt = fmaxf(mt, fmaf(a, f[g].x, f[g].y));
             }
             if (__any_sync(0xFFFFFFFFu, mt > m + kRescale)) {
                 const float mn = fmaxf(m, mt);
@@ -804,18 +812,17 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             const float mu = m == -INFINITY ? 0.0f : m;
 #pragma unroll
             for (int g = 0; g < kStep / 16; ++g) {
-                const float4 f = sc[g];
-                const float cg = fmaxf(cs * f.x, kTiny), off = f.y - mu;
+                const float off = f[g].y - mu;
                 float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     uint32_t &u0 = x_[16 * g + i], &u1 = x_[16 * g + i + 1];
-                    fma2(u0, u1, cg, off);
+                    fma2(u0, u1, f[g].x, off);
                     u0 = __float_as_uint(ex2_approx(__uint_as_float(u0)));
                     u1 = __float_as_uint(ex2_approx(__uint_as_float(u1)));
                     add2(sum0, sum1, u0, u1);
                 }
-                l = fmaf(sum0 + sum1, f.z, l);
+                l = fmaf(sum0 + sum1, f[g].z, l);
                 if (g % 2 == 1) {
                     uint32_t pk[16];
 #pragma unroll
@@ -833,8 +840,12 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[x][slot]));
+            if (++part == S_::STEPS) {
+                part = 0;
+                ++n;
+                if (flags & kLast) break;
+            }
         }
-        if (!(flags & kLast)) continue;
         // ---- the piece's end: outputs, or a partial result
         warp_wait(smem_u32(&sh.ofull[x]), (on - 1) & 1u, dead);
         tc_after();
@@ -868,6 +879,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
             else if (p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
         }
         tc_before();  // the next unit's products overwrite what was read here
+        if (flags & kEnd) return;
     }
 }
 
