@@ -7,10 +7,11 @@
 // head; its work is the list of KV tiles (128 tokens, 64 at head_dim 256) that hold a token visible to a row of it. The
 // tiles of all units form one list, cut into equal parts, one per SM: a part that begins or ends inside a unit leaves a
 // partial result (row maxima, sums, unnormalised output) that a second kernel joins. Cuts close to a unit's border are
-// moved onto it. The cuts are made on the GPU, from the lengths, by a kernel before it (plan_kernel).
+// moved onto it. The cuts are made from the lengths, by every CTA for itself.
 //
 // A CTA per SM, with a role for each warp:
-//  * 4 loader warps bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so they are
+//  * The scout walks over the CTA's part and looks up where the tiles lie.
+//  * 4 loader warps each for K and V bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so they are
 //    loaded there directly, one tile ahead of the conversion, and stored in the 128-byte-swizzled layout that tcgen05.mma
 //    reads: K with the head dims contiguous (K-major), V with the same store and read as MN-major.
 //  * A warp per row tile issues its S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), P read from
@@ -87,7 +88,6 @@ struct ExtendParams {
     float* lse;
     int32_t* status;
     PlanEntry* plan;    // [ctas + 1]
-    int64_t* cost;      // [B + 1] first position of each sequence
     float* rec_o;       // [2 ctas][MT * 128][D]
     float2* rec_ml;     // [2 ctas][MT * 128]
     int64_t q_stride, out_stride;
@@ -148,127 +148,137 @@ __device__ __forceinline__ int tile_start(const Unit& u, int j) {
 
 // ------------------------------------------------------------------------------------------ the cuts
 
+// Positions in the list that one KV head of a sequence takes, summed by a whole warp or by one thread.
+template <int D>
+__device__ __forceinline__ int64_t cost_of(const ExtendParams& p, const Seq& s, int lane, int lanes) {
+    int64_t sum = 0;
+    for (int qb = lane, n = blocks_of<D>(p, s.n); qb < n; qb += lanes) sum += unit_of<D>(p, s, qb).tiles + kUnitCost;
+    return sum;
+}
 __device__ __forceinline__ int64_t warp_sum64(int64_t v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
     return v;
 }
-
-// One CTA: positions of the sequences in the list, then the cut of each CTA of the attention, a warp each.
-template <int D>
-__global__ void __launch_bounds__(1024, 1) plan_kernel(const ExtendParams p) {
-    pdl_enter();
-    __shared__ int64_t part[32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // positions of one sequence and one KV head, a warp per sequence
-    for (int b = warp; b < p.B; b += 32) {
-        const Seq s = sequence(p, b);
-        if (s.bad && lane == 0) flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
-        int64_t sum = 0;
-        const int nqb = blocks_of<D>(p, s.n);
-        for (int qb = lane; qb < nqb; qb += 32) sum += unit_of<D>(p, s, qb).tiles + kUnitCost;
-        sum = warp_sum64(sum);
-        if (lane == 0) p.cost[b] = sum;
-    }
-    __syncthreads();
-    const int each = (p.B + 1023) / 1024, b_lo = min(p.B, tid * each), b_hi = min(p.B, b_lo + each);
-    int64_t local = 0;
-    for (int b = b_lo; b < b_hi; ++b) local += p.cost[b] * p.H;
-    int64_t incl = local;
+__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += v;
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += u;
     }
+    return v;
+}
+
+// Every CTA makes the list for itself: thread t owns sequences [t C, t C + C), and chunk[t] is where they begin. (A kernel of its
+// own that made all cuts took 17 us; this takes about 2, while the CTA sets itself up.) Returns the list's length. All threads.
+template <int D>
+__device__ __forceinline__ int64_t list_sequences(const ExtendParams& p, int64_t* chunk, int64_t* part) {
+    constexpr int NT = Shape<D>::THREADS, kSerial = 4;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int each = (p.B + NT - 1) / NT;
+    int64_t local = 0;
+    for (int i = 0; i < each; ++i) {  // (the same for all threads, so that a warp can share its long sequences)
+        const int b = tid * each + i;
+        Seq s{0, 0, 0, false};
+        if (b < p.B) s = sequence(p, b);
+        if (s.bad && blockIdx.x == 0) flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
+        const bool is_long = blocks_of<D>(p, s.n) > kSerial;
+        if (!is_long) local += cost_of<D>(p, s, 0, 1);
+        for (uint32_t left = __ballot_sync(0xFFFFFFFFu, is_long); left; left &= left - 1) {
+            const int l = __ffs(static_cast<int>(left)) - 1;
+            Seq t{0, __shfl_sync(0xFFFFFFFFu, s.n, l), __shfl_sync(0xFFFFFFFFu, s.len, l), false};
+            const int64_t c = warp_sum64(cost_of<D>(p, t, lane, 32));
+            if (lane == l) local += c;
+        }
+    }
+    local *= p.H;
+    const int64_t incl = warp_scan64(local, lane);
     if (lane == 31) part[warp] = incl;
     __syncthreads();
     int64_t at = incl - local, total = 0;
-    for (int w = 0; w < 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) at += part[w];
         total += part[w];
     }
+    chunk[tid] = at;
     __syncthreads();
-    for (int b = b_lo; b < b_hi; ++b) {
-        const int64_t c = p.cost[b] * p.H;
-        p.cost[b] = at;
-        at += c;
-    }
-    if (tid == 0) p.cost[p.B] = total;
-    __threadfence_block();
-    __syncthreads();
-
-    // the unit at position x (< total), a warp together
-    auto find = [&](int64_t x) {
-        PlanEntry e{};
-        int lo = 0, hi = p.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.cost[mid] <= x) lo = mid; else hi = mid;
-        }
-        const Seq s = sequence(p, lo);
-        const int64_t per_head = (p.cost[lo + 1] - p.cost[lo]) / p.H;
-        e.b = lo;
-        e.h = static_cast<int>((x - p.cost[lo]) / per_head);
-        const int64_t head = p.cost[lo] + e.h * per_head;
-        const int nqb = blocks_of<D>(p, s.n);
-        int64_t base = head;
-        for (int q0 = 0; q0 < nqb; q0 += 32) {
-            const int64_t c = q0 + lane < nqb ? unit_of<D>(p, s, q0 + lane).tiles + kUnitCost : 0;
-            int64_t inc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-                if (lane >= o) inc += v;
-            }
-            const uint32_t in = __ballot_sync(0xFFFFFFFFu, c > 0 && x < base + inc);
-            if (in) {
-                const int l = __ffs(static_cast<int>(in)) - 1;
-                e.qb = q0 + l;
-                e.end = base + __shfl_sync(0xFFFFFFFFu, inc, l);
-                e.begin = e.end - __shfl_sync(0xFFFFFFFFu, c, l);
-                break;
-            }
-            base += __shfl_sync(0xFFFFFFFFu, inc, 31);
-        }
-        return e;
-    };
-    const int64_t share = (total + p.ctas - 1) / p.ctas, slack = share / 8;
-    for (int c = warp; c <= p.ctas; c += 32) {
-        int64_t x = min(total, share * c);
-        PlanEntry e{};
-        e.cut = e.begin = e.end = x;
-        if (x < total) {
-            e = find(x);
-            if (x - e.begin <= max(slack, static_cast<int64_t>(kUnitCost))) {
-                x = e.begin;
-            } else if (e.end - x <= slack) {
-                x = e.end;
-                if (x < total) e = find(x);
-                else e.begin = e.end = x;
-            }
-            e.cut = x;
-            e.tile = static_cast<int32_t>(max(static_cast<int64_t>(0), x - e.begin - kUnitCost));
-        }
-        if (lane == 0) p.plan[c] = e;
-    }
+    return total;
 }
 
-// The pieces of a CTA's part, in order: every role walks over the same ones.
+// The unit at position x (below the list's length), found by a warp together.
+template <int D>
+__device__ __forceinline__ PlanEntry find_unit(const ExtendParams& p, const int64_t* chunk, int64_t x, int lane) {
+    constexpr int NT = Shape<D>::THREADS;
+    PlanEntry e{};
+    int lo = 0, hi = NT;
+    while (hi - lo > 1) {  // the last chunk that begins at or before x
+        const int mid = (lo + hi) >> 1;
+        if (chunk[mid] <= x) lo = mid; else hi = mid;
+    }
+    int64_t at = chunk[lo], per_head;
+    Seq s;
+    for (e.b = lo * ((p.B + NT - 1) / NT);; ++e.b) {
+        s = sequence(p, e.b);
+        per_head = warp_sum64(cost_of<D>(p, s, lane, 32));
+        if (x < at + per_head * p.H) break;
+        at += per_head * p.H;
+    }
+    e.h = static_cast<int>((x - at) / per_head);
+    at += e.h * per_head;
+    const int nqb = blocks_of<D>(p, s.n);
+    for (int q0 = 0; q0 < nqb; q0 += 32) {
+        const int64_t c = q0 + lane < nqb ? unit_of<D>(p, s, q0 + lane).tiles + kUnitCost : 0;
+        const int64_t incl = warp_scan64(c, lane);
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, c > 0 && x < at + incl);
+        if (in) {
+            const int l = __ffs(static_cast<int>(in)) - 1;
+            e.qb = q0 + l;
+            e.end = at + __shfl_sync(0xFFFFFFFFu, incl, l);
+            e.begin = e.end - __shfl_sync(0xFFFFFFFFu, c, l);
+            break;
+        }
+        at += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    }
+    return e;
+}
+
+// Where CTA c's part begins: c-th of equal parts, on the border of a unit where that is near.
+template <int D>
+__device__ __forceinline__ PlanEntry cut_at(const ExtendParams& p, const int64_t* chunk, int64_t total, int c, int lane) {
+    const int64_t share = (total + p.ctas - 1) / p.ctas, slack = share / 8;
+    int64_t x = min(total, share * c);
+    PlanEntry e{};
+    e.begin = e.end = x;
+#pragma unroll 1
+    while (x < total) {
+        e = find_unit<D>(p, chunk, x, lane);
+        if (x - e.begin <= max(slack, static_cast<int64_t>(kUnitCost))) {
+            x = e.begin;
+            break;
+        }
+        if (e.end - x > slack) break;
+        x = e.begin = e.end;  // the next unit's begin, if there is one
+    }
+    e.cut = x;
+    e.tile = static_cast<int32_t>(max(static_cast<int64_t>(0), x - e.begin - kUnitCost));
+    return e;
+}
+
+// The pieces of a CTA's part, in order.
 template <int D>
 struct Walk {
     int64_t pos, end, unit_begin;
     int b, h, qb, tile0, piece_tiles;
     Seq s;
     Unit u;
-    __device__ __forceinline__ void start(const ExtendParams& p) {
-        const PlanEntry* e = p.plan + blockIdx.x;
-        pos = e->cut;
-        end = e[1].cut;
-        unit_begin = e->begin;
-        b = e->b;
-        h = e->h;
-        qb = e->qb;
-        tile0 = e->tile;
+    __device__ __forceinline__ void start(const ExtendParams& p, const PlanEntry& e, int64_t part_end) {
+        pos = e.cut;
+        end = part_end;
+        unit_begin = e.begin;
+        b = e.b;
+        h = e.h;
+        qb = e.qb;
+        tile0 = e.tile;
         if (pos < end) {
             s = sequence(p, b);
             measure(p);
@@ -446,7 +456,8 @@ enum PlaceFlags {
     kTwo = 8,     // the unit has its second row tile
     kFull = 16,   // every token of the tile is there and visible to a row
     kWhole = 32,  // the piece is its unit
-    kGoesOn = 64  // the piece goes on with a unit that another CTA began
+    kGoesOn = 64, // the piece goes on with a unit that another CTA began
+    kNothing = 128  // the CTA's part is empty
 };
 
 // What the other roles need of a KV tile: of its 16-token groups the first token's row in the pools (kNoRow: no page, or no
@@ -465,6 +476,7 @@ struct Shared {
     uint64_t qfull[2], ofull[2];             // [row tile]
     uint64_t sfull[2][2], pfull[2][2];       // [row tile][slot]
     uint64_t drained;
+    int64_t part[Shape<64>::WARPS];  // (as many as any)
     uint64_t placed[kRing];
     Place ring[kRing];
     uint32_t loaded;  // tiles of V that its first loader warp has stored
@@ -477,12 +489,27 @@ struct Shared {
 // places. (With every role walking by itself the kernel had 90 KB of code, and 15 % of the warps' time went into waiting for
 // instructions.)
 template <int D>
-__device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, int lane) {
+__device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, const int64_t* chunk, int64_t total, int lane) {
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
+    PlanEntry mine{};
+    int64_t part_end = 0;
+#pragma unroll 1
+    for (int i = 1; i >= 0; --i) {
+        mine = cut_at<D>(p, chunk, total, blockIdx.x + i, lane);
+        if (i) part_end = mine.cut;
+        if (lane == 0 && (!i || blockIdx.x == gridDim.x - 1)) p.plan[blockIdx.x + i] = mine;  // (for the join)
+    }
+    if (mine.cut >= part_end) {  // nothing to do: the others are told by a place without a tile
+        if (lane == 0) {
+            sh.ring[0].head = make_int4(kNothing, 0, 0, 0);
+            mbar_arrive(smem_u32(&sh.placed[0]));
+        }
+        return;
+    }
     uint32_t n = 0;
     Walk<D> w;
-    for (w.start(p); w.more(); w.next(p)) {
+    for (w.start(p, mine, part_end); w.more(); w.next(p)) {
         const int unit = (w.whole() ? kWhole : 0) | (w.tile0 > 0 ? kGoesOn : 0) |
                          (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G ? kTwo : 0);
         const bool final = w.unit_begin + kUnitCost + w.u.tiles >= w.end;
@@ -565,6 +592,7 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
         const int4 head = t.head;
         const int flags = uniform(head.x);
+        if (flags & kNothing) return;
 #pragma unroll
         for (int g = 0; g < LOADS; ++g) {
             const uint32_t row = t.row[g0 + g * (R * kLoaderWarps / 16)];
@@ -646,6 +674,7 @@ __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh
     for (uint32_t n = 0;; ++n) {
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
         const int flags = uniform(sh.ring[n % kRing].head.x);
+        if (flags & kNothing) return;
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {
             // A unit without this row tile: a stage is free as soon as it is full. Its softmax warps are taken along step by
             // step, as ever (a barrier's parity does not tell them two tiles ahead).
@@ -699,6 +728,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         const Place& begin = sh.ring[n % kRing];
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
         int flags = begin.head.x;
+        if (flags & kNothing) return;
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {  // a unit without this row tile
             while (true) {
                 for (int slot = 0; slot < 2; ++slot) {
@@ -919,7 +949,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
     tc_after();
     const uint32_t tmem = sh.tmem;
     pdl_enter();
-    const bool work = p.plan[blockIdx.x].cut < p.plan[blockIdx.x + 1].cut;
+    // (the list's chunks lie where the first tiles of K and V will)
+    int64_t* chunk = reinterpret_cast<int64_t*>(raw + (base - smem_u32(raw)) + S_::K_OFF);
+    const int64_t total = list_sequences<D>(p, chunk, sh.part);
     // registers: 640 threads start with 96 each; a softmax thread holds a row's scores of a step: 2 x 128 + 2 x 72 + 80 = 5 x 96
     if constexpr (S_::MT == 2) {
         if (warp < S_::SOFT_WARPS) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
@@ -927,18 +959,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
     if (warp < S_::SOFT_WARPS) {
-        if (work) softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
+        softmax_rows<D>(p, sh, base, tmem, warp / 4, warp, lane);
     } else if (warp < kIssuer) {
         const int i = warp - S_::SOFT_WARPS;
-        if (work) load_tiles<D>(p, sh, base, i / kLoaderWarps, i % kLoaderWarps, lane);
+        load_tiles<D>(p, sh, base, i / kLoaderWarps, i % kLoaderWarps, lane);
     } else if (warp < kIssuer + S_::MT) {
-        if (work) issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, uniform(warp - kIssuer), lane);
+        issue_products<D>(p, sh, base, base + S_::K_OFF, base + S_::V_OFF, tmem, uniform(warp - kIssuer), lane);
         // all products are done before TMEM is given back
         if (elect_one()) tc_commit(smem_u32(&sh.drained));
         __syncwarp();
         warp_wait(smem_u32(&sh.drained), 0, &sh.never);
-    } else if (work && warp == kIssuer + S_::MT) {
-        scout_tiles<D>(p, sh, lane);
+    } else if (warp == kIssuer + S_::MT) {
+        scout_tiles<D>(p, sh, chunk, total, lane);
     }
     __syncwarp();
     tc_before();
@@ -1015,15 +1047,14 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
 // ------------------------------------------------------------------------------------------ host
 
 struct Carve {
-    size_t plan, cost, ml, o, total;
+    size_t plan, ml, o, total;
 };
-Carve carve(int B, int D, int ctas) {
+Carve carve(int D, int ctas) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
     const size_t records = static_cast<size_t>(2 * ctas) * (D == 256 ? 1 : 2) * kRowsM;
     Carve c;
     c.plan = 0;
-    c.cost = up(static_cast<size_t>(ctas + 1) * sizeof(PlanEntry));
-    c.ml = c.cost + up((static_cast<size_t>(B) + 1) * sizeof(int64_t));
+    c.ml = up(static_cast<size_t>(ctas + 1) * sizeof(PlanEntry));
     c.o = c.ml + up(records * sizeof(float2));
     c.total = c.o + records * D * sizeof(float);
     return c;
@@ -1039,9 +1070,8 @@ template <int D>
 cudaError_t launch_extend(const ExtendParams& p, cudaStream_t s) {
     using S_ = Shape<D>;
     cudaError_t e = cudaFuncSetAttribute(extend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_::SMEM);
-    if (e == cudaSuccess) e = launch_pdl(plan_kernel<D>, dim3(1), dim3(1024), 0, s, p);
     if (e == cudaSuccess) e = launch_pdl(extend_kernel<D>, dim3(p.ctas), dim3(S_::THREADS), S_::SMEM, s, p);
-    if (e == cudaSuccess) e = launch_pdl(join_kernel<D>, dim3(p.ctas, 4), dim3(256), 0, s, p);
+    if (e == cudaSuccess) e = launch_pdl(join_kernel<D>, dim3(p.ctas, 16), dim3(256), 0, s, p);
     return e;
 }
 
@@ -1050,7 +1080,7 @@ cudaError_t launch_extend(const ExtendParams& p, cudaStream_t s) {
 extern "C" size_t nvfp4_paged_extend_attention_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
                                                               int32_t num_q_heads) {
     if (!layout_ok(layout) || batch < 0 || num_q_heads <= 0 || !shape_ok(layout, num_q_heads)) return 0;
-    return carve(batch, layout->head_dim, num_sms()).total;
+    return carve(layout->head_dim, num_sms()).total;
 }
 
 extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
@@ -1077,7 +1107,7 @@ extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
         static_cast<int64_t>(pool_pages) * H > UINT32_MAX / T)
         return NVFP4KV_ERR_UNSUPPORTED;
     const int ctas = num_sms();
-    const Carve c = carve(batch, D, ctas);
+    const Carve c = carve(D, ctas);
     if (!workspace || workspace_bytes < c.total || !aligned16(workspace)) return NVFP4KV_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     ExtendParams p{};
@@ -1095,7 +1125,6 @@ extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
     p.lse = lse;
     p.status = status;
     p.plan = reinterpret_cast<PlanEntry*>(ws + c.plan);
-    p.cost = reinterpret_cast<int64_t*>(ws + c.cost);
     p.rec_ml = reinterpret_cast<float2*>(ws + c.ml);
     p.rec_o = reinterpret_cast<float*>(ws + c.o);
     p.q_stride = q_row_stride;
