@@ -4,12 +4,15 @@
 // all that a step's other calls take follows from prefix sums over the sequences: of a (the rows), of n (which pages of
 // the free stack are whose), of the pages given back, and of the pages that become full.
 //
-// One cluster of 1 to 8 CTAs. Every CTA makes all the prefix sums for itself, in shared memory (1024 threads, a few
-// sequences each: reading 8 bytes a sequence again costs less than passing sums on), so the CTAs meet only once, at a
-// cluster barrier between the last read of what may be written in place (lengths, the count of free pages) and the first
-// write. After it nothing is read that is written: pages are popped below the old count of the stack and pushed from it
-// on, and table entries are read below ceil(p_b / T) and written from it on. The outputs are spread over all threads;
-// each finds its sequence by bisection in shared memory.
+// Every CTA makes all the prefix sums for itself, in shared memory (1024 threads, a few sequences each: reading 8 bytes a
+// sequence again costs less than passing sums on). Outputs are spread over the threads of all CTAs; each finds its sequence by
+// bisection in shared memory, four outputs at a time so that their loads overlap. Nothing is read that the call writes, but for
+// lengths and the count of free pages where they are written in place: pages are popped below the old count of the stack and
+// pushed from it on, and table entries are read below ceil(p_b / T) and written from it on. In place the CTAs are one cluster (up
+// to 8), with its barrier between the last read of those and the first write; otherwise there are as many as the outputs ask for.
+//
+// Bound: latency. A step of 256 requests, 13 of which ended with 1024 pages each, is two dependent round trips to memory, two
+// block-wide sums and the launch.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -24,9 +27,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBatch = 8192;      // 21 bytes of shared memory each
-constexpr int kMaxCtas = 8;          // portable cluster size
-constexpr int kItemsPerCta = 2048;   // outputs that one CTA writes before a second one is worth its cluster
+constexpr int kMaxBatch = 8192;      // 24 bytes of shared memory each
+constexpr int kMaxCluster = 8;       // CTAs where lengths or the count are written in place (portable cluster size)
+constexpr int kMaxCtas = 64;
+constexpr int kItemsPerCta = 2048;   // outputs of a CTA before another one is worth it
 
 struct TablesParams {
     const int32_t* past;   // in and out arrays may be the same memory: no __restrict__, no __ldg
@@ -41,166 +45,186 @@ struct TablesParams {
     int32_t* full;
     int32_t* left;
     int32_t* status;
+    uint64_t t_magic;  // ceil(2^64 / T)
     int32_t B, T, max_pages, capacity, rows, full_cap;
+    bool in_place;     // lengths or the count are written where they are read
 };
 
-__device__ __forceinline__ int clamp_i32(int64_t x) {
-    return static_cast<int>(min(x, static_cast<int64_t>(INT32_MAX)));
+// Sums of counts, held at 2^31 - 1 once there (which is associative).
+__device__ __forceinline__ int add_sat(int a, int b) {
+    return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7FFFFFFFu));
 }
 
-// Exclusive prefix sums over the CTA's threads of N values each, and their totals. All threads call.
+// Exclusive prefix sums over the CTA's threads of N counts each, and their totals. All threads call.
 template <int N>
-__device__ __forceinline__ void block_scan(int64_t (&v)[N], int64_t (&total)[N], int64_t (*part)[kWarps]) {
+__device__ __forceinline__ void block_scan(int (&v)[N], int (&total)[N], int (*part)[kWarps]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl[N];
+    int incl[N], before[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) incl[k] = v[k];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int u = __shfl_up_sync(0xFFFFFFFFu, incl[k], o);
+            if (lane >= o) incl[k] = add_sat(incl[k], u);
+        }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        incl[k] = v[k];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, incl[k], o);
-            if (lane >= o) incl[k] += u;
-        }
+        before[k] = __shfl_up_sync(0xFFFFFFFFu, incl[k], 1);
+        if (lane == 0) before[k] = 0;
         if (lane == 31) part[k][warp] = incl[k];
     }
     __syncthreads();
     if (warp < N) {
-        int64_t s = part[warp][lane];
+        int s = part[warp][lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, s, o);
-            if (lane >= o) s += u;
+            const int u = __shfl_up_sync(0xFFFFFFFFu, s, o);
+            if (lane >= o) s = add_sat(s, u);
         }
         part[warp][lane] = s;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        v[k] = incl[k] - v[k] + (warp > 0 ? part[k][warp - 1] : 0);
+        v[k] = warp > 0 ? add_sat(before[k], part[k][warp - 1]) : before[k];
         total[k] = part[k][kWarps - 1];
     }
     __syncthreads();
 }
 
-// The last b with first[b] <= i, for first[0] = 0 <= i: the sequence that element i of a list belongs to.
-__device__ __forceinline__ int owner(const int* first, int B, int i) {
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= i) lo = mid; else hi = mid;
-    }
-    return lo;
+// For each of N elements the last b with first[b] <= i, for first[0] = 0 <= i: the sequence that element i of a list belongs
+// to. `half` is the largest power of two below B.
+template <int N>
+__device__ __forceinline__ void owners(const int* first, int B, int half, const int (&i)[N], int (&b)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) b[k] = 0;
+    for (int s = half; s > 0; s >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (b[k] + s < B && first[b[k] + s] <= i[k]) b[k] += s;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesParams p) {
     pdl_enter();
     extern __shared__ __align__(16) int smem[];
-    __shared__ int64_t part[3][kWarps];
+    __shared__ int part[3][kWarps];
     const int B = p.B, T = p.T;
     // of each sequence: its first row, its first page popped, given back and becoming full, its tokens cached and to
     // add (kUnserved: it keeps what it has)
     int *row0 = smem, *need0 = row0 + B, *back0 = need0 + B, *full0 = back0 + B, *past_s = full0 + B, *add_s = past_s + B;
     constexpr int kUnserved = -2;
 
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
     const int tid = threadIdx.x;
     const int max_tokens = p.max_pages * T;  // (the host bounds it)
     const int each = (B + kThreads - 1) / kThreads;
     const int b_lo = min(B, tid * each), b_hi = min(B, b_lo + each);
-    auto pages_of = [&](int tokens) { return tokens / T + (tokens % T != 0); };
+    // 0 <= x < 2^31
+    auto whole_pages = [&](int x) { return T == 1 ? x : static_cast<int>(__umul64hi(static_cast<uint64_t>(x), p.t_magic)); };
+    auto pages_of = [&](int x) {
+        const int n = whole_pages(x);
+        return n + (n * T != x);
+    };
     struct Seq {
-        int past, add, rows, need, back;
+        int past, add, rows, have, need, back;
         bool ok;
     };
     auto look = [&](int b) {
-        Seq s{p.past[b], p.add[b], 0, 0, 0, true};
+        Seq s{p.past[b], p.add[b], 0, 0, 0, 0, true};
         s.rows = max(s.add, 0);
         if (s.past < 0 || s.past > max_tokens) {
             s.past = 0;
             s.ok = false;
         } else if (s.add < -1 || s.rows > max_tokens - s.past) {
             s.ok = false;
-        } else if (s.add < 0) {
-            s.back = pages_of(s.past);
         } else {
-            s.need = pages_of(s.past + s.add) - pages_of(s.past);
+            s.have = pages_of(s.past);
+            if (s.add < 0) s.back = s.have;
+            else s.need = pages_of(s.past + s.add) - s.have;
         }
         return s;
     };
 
     // ------------------------------------------------ rows, pages to pop, pages given back
-    int64_t at[3] = {0, 0, 0}, total[3];
+    const int given_count = *p.count;
+    int at[3] = {0, 0, 0}, total[3];
+    Seq kept{};
     for (int b = b_lo; b < b_hi; ++b) {
-        const Seq s = look(b);
-        at[0] += s.rows;
-        at[1] += s.need;
-        at[2] += s.back;
+        kept = look(b);
+        at[0] = add_sat(at[0], kept.rows);
+        at[1] = add_sat(at[1], kept.need);
+        at[2] = add_sat(at[2], kept.back);
     }
     block_scan<3>(at, total, part);
-    int count = *p.count;
     int32_t flags = 0;
-    if (count < 0 || count > p.capacity) {
-        flags |= NVFP4KV_STATUS_PAGE_OOB;
-        count = max(0, min(count, p.capacity));
-    }
-    const int returned = static_cast<int>(min(total[2], static_cast<int64_t>(p.capacity - count)));
+    const int count = max(0, min(given_count, p.capacity));
+    if (count != given_count) flags |= NVFP4KV_STATUS_PAGE_OOB;
+    const int returned = min(total[2], p.capacity - count);
     if (total[2] > returned) flags |= NVFP4KV_STATUS_PAGE_OOB;
     const int top = count + returned;
 
     // ------------------------------------------------ who is served
     // A sequence that needs pages is served when its needs and those of all before it fit, and one with rows when
-    // they fit, so the pages of those that are served are the first of the stack, without gaps.
-    int64_t done[2] = {0, 0}, done_total[2];  // pages that become full, pages popped
+    // they fit, so the pages of those that are served are the first of the stack, without gaps. (A sum that was held at
+    // 2^31 - 1 is above both bounds.)
+    int done[2] = {0, 0}, done_total[2];  // pages that become full, pages popped
     for (int b = b_lo; b < b_hi; ++b) {
-        const Seq s = look(b);
+        if (each > 1) kept = look(b);
+        const Seq& s = kept;
         bool ok = s.ok;
-        if (!ok || (s.rows > 0 && at[0] + s.rows > p.rows)) {
+        if (!ok || (s.rows > 0 && add_sat(at[0], s.rows) > p.rows)) {
             flags |= NVFP4KV_STATUS_BAD_SEQ_LEN;
             ok = false;
-        } else if (s.need > 0 && at[1] + s.need > top) {
+        } else if (s.need > 0 && add_sat(at[1], s.need) > top) {
             flags |= NVFP4KV_STATUS_NO_PAGES;
             ok = false;
         }
-        row0[b] = clamp_i32(at[0]);
-        need0[b] = clamp_i32(at[1]);
-        back0[b] = clamp_i32(at[2]);
+        row0[b] = at[0];
+        need0[b] = at[1];
+        back0[b] = at[2];
         past_s[b] = s.past;
         add_s[b] = ok ? s.add : kUnserved;
         if (ok && s.add > 0) {
-            done[0] += (s.past + s.add) / T - s.past / T;
+            done[0] += whole_pages(s.past + s.add) - whole_pages(s.past);  // (rows fit into 2^30)
             done[1] += s.need;
         }
-        at[0] += s.rows;
-        at[1] += s.need;
-        at[2] += s.back;
+        at[0] = add_sat(at[0], s.rows);
+        at[1] = add_sat(at[1], s.need);
+        at[2] = add_sat(at[2], s.back);
     }
     block_scan<2>(done, done_total, part);
     for (int b = b_lo; b < b_hi; ++b) {
-        full0[b] = clamp_i32(done[0]);
-        if (add_s[b] > 0) done[0] += (past_s[b] + add_s[b]) / T - past_s[b] / T;
+        full0[b] = done[0];
+        if (add_s[b] > 0) done[0] += whole_pages(past_s[b] + add_s[b]) - whole_pages(past_s[b]);
     }
-    if (flags && rank == 0) flag_status(p.status, flags);
-    // the last read of what may be written in place is behind every CTA
-    if (ctas > 1) cluster.sync();
+    if (flags && blockIdx.x == 0) flag_status(p.status, flags);
+    // in place, every CTA's last read comes before any write
+    if (p.in_place && gridDim.x > 1) cg::this_cluster().sync();
     else __syncthreads();
 
     // ------------------------------------------------ outputs
-    const int g = rank * kThreads + tid, step = ctas * kThreads;
-    const int n_rows = static_cast<int>(min(total[0], static_cast<int64_t>(p.rows)));
+    const int g = blockIdx.x * kThreads + tid, step = gridDim.x * kThreads;
+    const int n_rows = min(total[0], p.rows);
+    int half = 1;
+    while (half * 2 < B) half *= 2;
+    constexpr int U = 4;  // outputs of a thread at a time
+    const int nothing = -1;
+    // where page k of the stack's top lies, counted down: in the stack, or, where this very call gives it back, in its table
     auto given_back = [&](int i) {
-        const int b = owner(back0, B, i);
-        return p.table[static_cast<int64_t>(b) * p.max_pages + (i - back0[b])];
+        const int ii[1] = {i};
+        int b[1];
+        owners<1>(back0, B, half, ii, b);
+        return p.table + static_cast<int64_t>(b[0]) * p.max_pages + (i - back0[b[0]]);
     };
-    // page k of the stack's top, counted down: from the stack, or, where this very call gives it back, from its table
-    auto pop = [&](int k) {
+    auto popped = [&](int k) -> const int32_t* {
         const int i = top - 1 - k;
-        return i < count ? p.stack[i] : given_back(i - count);
+        return i < count ? p.stack + i : given_back(i - count);
     };
-    // page j of sequence b, cached or new
-    auto page_at = [&](int b, int j) {
+    // and page j of sequence b, cached or new
+    auto page_at = [&](int b, int j) -> const int32_t* {
         const int have = pages_of(past_s[b]);
-        return j < have ? p.table[static_cast<int64_t>(b) * p.max_pages + j] : pop(need0[b] + j - have);
+        return j < have ? p.table + static_cast<int64_t>(b) * p.max_pages + j : popped(need0[b] + j - have);
     };
     for (int b = g; b < B; b += step) {
         const int add = add_s[b];
@@ -209,37 +233,58 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     }
     if (g == 0) {
         p.starts[B] = n_rows;
-        *p.left = top - static_cast<int>(done_total[1]);
+        *p.left = top - done_total[1];
     }
-    for (int i = g; i < returned; i += step) p.stack[count + i] = given_back(i);
-    for (int i = g; i < done_total[1]; i += step) {
-        const int b = owner(need0, B, i);
-        p.table[static_cast<int64_t>(b) * p.max_pages + pages_of(past_s[b]) + (i - need0[b])] = pop(i);
-    }
-    for (int r = g; r < p.rows; r += step) {
-        int64_t slot = -1;
-        int pos = 0;
-        if (r < n_rows) {
-            const int b = owner(row0, B, r);
-            if (add_s[b] > 0) {
-                pos = past_s[b] + (r - row0[b]);
-                const int j = pos / T;
-                slot = static_cast<int64_t>(page_at(b, j)) * T + (pos - j * T);
+    for (int64_t r0 = g; r0 < p.rows; r0 += int64_t{U} * step) {
+        int r[U], b[U], pos[U], j[U], page[U];
+        const int32_t* src[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) r[k] = static_cast<int>(min(r0 + static_cast<int64_t>(k) * step, static_cast<int64_t>(INT32_MAX)));
+        owners<U>(row0, B, half, r, b);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            pos[k] = j[k] = 0;
+            src[k] = nullptr;
+            if (r[k] < n_rows && add_s[b[k]] > 0) {
+                pos[k] = past_s[b[k]] + (r[k] - row0[b[k]]);
+                j[k] = whole_pages(pos[k]);
+                src[k] = page_at(b[k], j[k]);
             }
         }
-        p.slots[r] = slot;
-        p.positions[r] = pos;
-    }
-    if (p.full) {
-        for (int i = g; i < p.full_cap; i += step) {
-            int page = -1;
-            if (i < done_total[0]) {
-                const int b = owner(full0, B, i);
-                page = page_at(b, past_s[b] / T + (i - full0[b]));
+#pragma unroll
+        for (int k = 0; k < U; ++k) page[k] = src[k] ? *src[k] : nothing;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (r[k] < p.rows) {
+                p.slots[r[k]] = src[k] ? static_cast<int64_t>(page[k]) * T + (pos[k] - j[k] * T) : -1;
+                p.positions[r[k]] = pos[k];
             }
-            p.full[i] = page;
-        }
     }
+    // new pages into the tables, full pages into their list, pages given back on the stack: (sequence, page) pairs alike
+    auto copy_pages = [&](const int* first, int n, auto from, auto to) {
+        for (int64_t i0 = g; i0 < n; i0 += int64_t{U} * step) {
+            int i[U], b[U], page[U];
+            const int32_t* src[U];
+#pragma unroll
+            for (int k = 0; k < U; ++k) i[k] = static_cast<int>(min(i0 + static_cast<int64_t>(k) * step, static_cast<int64_t>(INT32_MAX)));
+            owners<U>(first, B, half, i, b);
+#pragma unroll
+            for (int k = 0; k < U; ++k) src[k] = i[k] < n ? from(b[k], i[k]) : nullptr;
+#pragma unroll
+            for (int k = 0; k < U; ++k) page[k] = src[k] ? *src[k] : nothing;
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (i[k] < n) *to(b[k], i[k]) = page[k];
+        }
+    };
+    copy_pages(back0, returned, [&](int b, int i) -> const int32_t* { return p.table + static_cast<int64_t>(b) * p.max_pages + (i - back0[b]); },
+               [&](int, int i) { return p.stack + count + i; });
+    copy_pages(need0, done_total[1], [&](int, int i) { return popped(i); },
+               [&](int b, int i) { return p.table + static_cast<int64_t>(b) * p.max_pages + pages_of(past_s[b]) + (i - need0[b]); });
+    if (p.full)
+        copy_pages(full0, p.full_cap,
+                   [&](int b, int i) -> const int32_t* { return i < done_total[0] ? page_at(b, whole_pages(past_s[b]) + (i - full0[b])) : nullptr; },
+                   [&](int, int i) { return p.full + i; });
 }
 
 }  // namespace
@@ -287,9 +332,20 @@ extern "C" nvfp4kv_status nvfp4_kv_step_tables(
     const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kMaxBatch * 6 * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return launched(e);
-    const int64_t items = static_cast<int64_t>(num_rows) + (full_pages ? full_capacity : 0) + batch;
+    p.t_magic = UINT64_MAX / static_cast<uint64_t>(T) + 1;
+    auto apart = [](const int32_t* a, size_t na, const int32_t* b, size_t nb) { return a + na <= b || b + nb <= a; };
+    const size_t n = static_cast<size_t>(batch);
+    p.in_place = !(apart(seq_lens, n, past_lens, n) && apart(seq_lens, n, new_lens, n) && apart(row_starts, n + 1, past_lens, n) &&
+                   apart(row_starts, n + 1, new_lens, n) && free_left != free_count && apart(free_left, 1, past_lens, n) &&
+                   apart(free_left, 1, new_lens, n) && apart(seq_lens, n, free_count, 1) && apart(row_starts, n + 1, free_count, 1));
+    // outputs, and a share of the pages that may come back (of 256 requests with up to 2048 pages each 13 ended: one CTA
+    // took 16.8 us)
+    const int64_t back = static_cast<int64_t>(batch) * max_pages_per_seq;
+    const int64_t items = static_cast<int64_t>(num_rows) + (full_pages ? full_capacity : 0) + batch +
+                          (back < free_capacity ? back : free_capacity) / 16;
+    const int most = p.in_place ? kMaxCluster : kMaxCtas;
     int ctas = 1;
-    while (ctas < kMaxCtas && items > static_cast<int64_t>(ctas) * kItemsPerCta) ctas *= 2;
+    while (ctas < most && items > static_cast<int64_t>(ctas) * kItemsPerCta) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas));
     cfg.blockDim = dim3(kThreads);
@@ -303,6 +359,6 @@ extern "C" nvfp4kv_status nvfp4_kv_step_tables(
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    cfg.numAttrs = p.in_place && ctas > 1 ? 2 : 1;
     return launched(cudaLaunchKernelEx(&cfg, step_tables_kernel, static_cast<const TablesParams&>(p)));
 }
