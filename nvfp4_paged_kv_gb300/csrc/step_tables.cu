@@ -27,10 +27,10 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxBatch = 8192;      // 24 bytes of shared memory each
+constexpr int kMaxBatch = 8192;      // 28 bytes of shared memory each
 constexpr int kMaxCluster = 8;       // CTAs where lengths or the count are written in place (portable cluster size)
 constexpr int kMaxCtas = 64;
-constexpr int kItemsPerCta = 2048;   // outputs of a CTA before another one is worth it
+constexpr int kItemsPerCta = 4096;   // outputs of a CTA before another one is worth it
 
 struct TablesParams {
     const int32_t* past;   // in and out arrays may be the same memory: no __restrict__, no __ldg
@@ -45,7 +45,7 @@ struct TablesParams {
     int32_t* full;
     int32_t* left;
     int32_t* status;
-    uint64_t t_magic;  // ceil(2^64 / T)
+    uint32_t t_magic, t_shift;  // x / T = (x t_magic >> 32) >> t_shift for 0 <= x < 2^31, T > 1
     int32_t B, T, max_pages, capacity, rows, full_cap;
     bool in_place;     // lengths or the count are written where they are read
 };
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     __shared__ int part[3][kWarps];
     const int B = p.B, T = p.T;
     // of each sequence: its first row, its first page popped, given back and becoming full, its tokens cached and to
-    // add (kUnserved: it keeps what it has)
-    int *row0 = smem, *need0 = row0 + B, *back0 = need0 + B, *full0 = back0 + B, *past_s = full0 + B, *add_s = past_s + B;
+    // add (kUnserved: it keeps what it has), and its full pages
+    int *row0 = smem, *need0 = row0 + B, *back0 = need0 + B, *full0 = back0 + B, *past_s = full0 + B, *add_s = past_s + B, *whole_s = add_s + B;
     constexpr int kUnserved = -2;
 
     const int tid = threadIdx.x;
@@ -121,13 +121,13 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     const int each = (B + kThreads - 1) / kThreads;
     const int b_lo = min(B, tid * each), b_hi = min(B, b_lo + each);
     // 0 <= x < 2^31
-    auto whole_pages = [&](int x) { return T == 1 ? x : static_cast<int>(__umul64hi(static_cast<uint64_t>(x), p.t_magic)); };
+    auto whole_pages = [&](int x) { return T == 1 ? x : static_cast<int>(__umulhi(static_cast<unsigned>(x), p.t_magic) >> p.t_shift); };
     auto pages_of = [&](int x) {
         const int n = whole_pages(x);
         return n + (n * T != x);
     };
     struct Seq {
-        int past, add, rows, have, need, back;
+        int past, add, rows, whole, need, back;
         bool ok;
     };
     auto look = [&](int b) {
@@ -139,9 +139,10 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         } else if (s.add < -1 || s.rows > max_tokens - s.past) {
             s.ok = false;
         } else {
-            s.have = pages_of(s.past);
-            if (s.add < 0) s.back = s.have;
-            else s.need = pages_of(s.past + s.add) - s.have;
+            s.whole = whole_pages(s.past);
+            const int have = s.whole + (s.whole * T != s.past);
+            if (s.add < 0) s.back = have;
+            else s.need = pages_of(s.past + s.add) - have;
         }
         return s;
     };
@@ -185,8 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         back0[b] = at[2];
         past_s[b] = s.past;
         add_s[b] = ok ? s.add : kUnserved;
+        whole_s[b] = s.whole;
         if (ok && s.add > 0) {
-            done[0] += whole_pages(s.past + s.add) - whole_pages(s.past);  // (rows fit into 2^30)
+            done[0] += whole_pages(s.past + s.add) - s.whole;  // (rows fit into 2^30)
             done[1] += s.need;
         }
         at[0] = add_sat(at[0], s.rows);
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     block_scan<2>(done, done_total, part);
     for (int b = b_lo; b < b_hi; ++b) {
         full0[b] = done[0];
-        if (add_s[b] > 0) done[0] += whole_pages(past_s[b] + add_s[b]) - whole_pages(past_s[b]);
+        if (add_s[b] > 0) done[0] += whole_pages(past_s[b] + add_s[b]) - whole_s[b];
     }
     if (flags && blockIdx.x == 0) flag_status(p.status, flags);
     // in place, every CTA's last read comes before any write
@@ -221,9 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         const int i = top - 1 - k;
         return i < count ? p.stack + i : given_back(i - count);
     };
+    auto have_of = [&](int b) { return whole_s[b] + (whole_s[b] * T != past_s[b]); };
     // and page j of sequence b, cached or new
     auto page_at = [&](int b, int j) -> const int32_t* {
-        const int have = pages_of(past_s[b]);
+        const int have = have_of(b);
         return j < have ? p.table + static_cast<int64_t>(b) * p.max_pages + j : popped(need0[b] + j - have);
     };
     for (int b = g; b < B; b += step) {
@@ -280,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     copy_pages(back0, returned, [&](int b, int i) -> const int32_t* { return p.table + static_cast<int64_t>(b) * p.max_pages + (i - back0[b]); },
                [&](int, int i) { return p.stack + count + i; });
     copy_pages(need0, done_total[1], [&](int, int i) { return popped(i); },
-               [&](int b, int i) { return p.table + static_cast<int64_t>(b) * p.max_pages + pages_of(past_s[b]) + (i - need0[b]); });
+               [&](int b, int i) { return p.table + static_cast<int64_t>(b) * p.max_pages + have_of(b) + (i - need0[b]); });
     if (p.full)
         copy_pages(full0, p.full_cap,
-                   [&](int b, int i) -> const int32_t* { return i < done_total[0] ? page_at(b, whole_pages(past_s[b]) + (i - full0[b])) : nullptr; },
+                   [&](int b, int i) -> const int32_t* { return i < done_total[0] ? page_at(b, whole_s[b] + (i - full0[b])) : nullptr; },
                    [&](int, int i) { return p.full + i; });
 }
 
@@ -328,11 +331,16 @@ extern "C" nvfp4kv_status nvfp4_kv_step_tables(
     p.capacity = free_capacity;
     p.rows = num_rows;
     p.full_cap = full_capacity;
-    const size_t smem = static_cast<size_t>(batch) * 6 * sizeof(int);
+    const size_t smem = static_cast<size_t>(batch) * 7 * sizeof(int);
     const cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxBatch * 6 * static_cast<int>(sizeof(int)));
+                                               kMaxBatch * 7 * static_cast<int>(sizeof(int)));
     if (e != cudaSuccess) return launched(e);
-    p.t_magic = UINT64_MAX / static_cast<uint64_t>(T) + 1;
+    // 2^l >= T > 2^(l - 1), m = ceil(2^(31 + l) / T) < 2^32: m T = 2^(31 + l) + e with e < T <= 2^l, so x m / 2^(31 + l) exceeds
+    // x / T by less than 1 / T for x < 2^31
+    int l = 0;
+    while ((int64_t{1} << l) < T) ++l;
+    p.t_magic = l ? static_cast<uint32_t>(((uint64_t{1} << (31 + l)) + T - 1) / T) : 0u;
+    p.t_shift = l ? l - 1 : 0;
     auto apart = [](const int32_t* a, size_t na, const int32_t* b, size_t nb) { return a + na <= b || b + nb <= a; };
     const size_t n = static_cast<size_t>(batch);
     p.in_place = !(apart(seq_lens, n, past_lens, n) && apart(seq_lens, n, new_lens, n) && apart(row_starts, n + 1, past_lens, n) &&
