@@ -9,6 +9,7 @@
 // Bound: HBM, 3 bytes a value from 16 bits and 1.5625 from NVFP4. The maximum stands between the loads and the stores of a run,
 // so a CTA alternates between the two; the 16 CTAs of an SM (128 threads at 64 x 128) are what keeps both under way.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "codec_core.cuh"
@@ -18,9 +19,11 @@ using namespace nvfp4kv;
 
 namespace {
 
-constexpr int kKept = 2;           // steps of 32 values that a thread keeps in registers
-constexpr int kMaxThreads = 512;   // of a CTA: runs of up to 512 x 2 x 32 values are read once
+constexpr int kMaxThreads = 512;   // of a CTA: runs of up to 512 x 32 values and the steps that a thread keeps are read once
 constexpr int kPairs = NVFP4KV_NVFP4 + 1;  // NVFP4 in NVFP4KV_PACK_TOKEN_PAIRS, as a source of its own
+
+// Steps of 32 values that a thread keeps in registers: 16 words each of a 16-bit source, 5 of a packed one.
+__host__ __device__ constexpr int kept_steps(int src) { return src == NVFP4KV_BF16 || src == NVFP4KV_FP16 ? 2 : 4; }
 
 struct Fp8Params {
     const uint8_t* src;
@@ -34,13 +37,7 @@ struct Fp8Params {
     int32_t* status;
     uint64_t row_magic;  // div_magic(D / 16)
     int32_t src_pages, dst_pages, H, T, nb;  // nb = D / 16
-    int64_t units;
-};
-
-// Two blocks of 16 source values as loaded.
-struct Raw {
-    uint32_t w[16];
-    uint32_t scales;
+    uint32_t units;
 };
 
 // Step i of a run covers blocks first and second (blocks of 16 values, numbered through the run).
@@ -56,94 +53,172 @@ __device__ __forceinline__ void blocks_of(const Fp8Params& p, uint32_t i, uint32
     }
 }
 
-// Loads what of step i lies below block `end` (whole blocks); the rest reads as 0.
-template <int SRC>
-__device__ __forceinline__ Raw load_step(const uint8_t* src, const uint8_t* scales, uint32_t i, bool one, bool two) {
-    Raw r;
+// The two blocks of a step of a 16-bit source, as pairs of values.
+struct Step {
+    uint32_t w[16];
+};
+
+// A step of 16-bit values: what lies below the valid blocks' end (whole blocks, `one` and `two`); the rest is 0.
+__device__ __forceinline__ void load_16bit(Step& s, const uint8_t* src, uint32_t i, bool one, bool two) {
+    const uint8_t* a = src + static_cast<size_t>(i) * 64;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 v[4] = {zero, zero, zero, zero};
+    if (one) {
+        v[0] = ld_stream_16B(a);
+        v[1] = ld_stream_16B(a + 16);
+    }
+    if (two) {
+        v[2] = ld_stream_16B(a + 32);
+        v[3] = ld_stream_16B(a + 48);
+    }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r.w[k] = 0u;
-    r.scales = 0u;
-    if constexpr (SRC == NVFP4KV_BF16 || SRC == NVFP4KV_FP16) {
-        const uint8_t* a = src + static_cast<size_t>(i) * 64;
+    for (int k = 0; k < 4; ++k) {
+        s.w[4 * k] = v[k].x;
+        s.w[4 * k + 1] = v[k].y;
+        s.w[4 * k + 2] = v[k].z;
+        s.w[4 * k + 3] = v[k].w;
+    }
+}
+
+// The same of packed ones, as loaded.
+struct Packed {
+    uint4 codes;
+    uint32_t scales;
+};
+template <int SRC>
+__device__ __forceinline__ Packed load_packed(const uint8_t* src, const uint8_t* scales, uint32_t i, bool one, bool two, bool even) {
+    Packed r{make_uint4(0u, 0u, 0u, 0u), 0u};
+    const uint8_t* a = src + static_cast<size_t>(i) * 16;
+    const uint8_t* sc = scales + static_cast<size_t>(i) * 2;
+    if (SRC == kPairs || even) {  // 16 bytes of codes and 2 of scales, aligned (runs of an odd number of blocks are not)
         if (one) {
-            const uint4 x = ld_stream_16B(a), y = ld_stream_16B(a + 16);
-            r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
-            r.w[4] = y.x; r.w[5] = y.y; r.w[6] = y.z; r.w[7] = y.w;
+            r.codes = ld_stream_16B(a);
+            uint16_t h;
+            asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(h) : "l"(sc));
+            r.scales = h;
+        }
+        if (SRC == NVFP4KV_NVFP4 && !two) {  // (the second block may be past the valid ones, its scale anything)
+            r.codes.z = r.codes.w = 0u;
+            r.scales &= 0xFFu;
+        }
+    } else {
+        if (one) {
+            const uint2 x = ld_stream_8B(a);
+            r.codes.x = x.x;
+            r.codes.y = x.y;
+            r.scales = ld_stream_1B(sc);
         }
         if (two) {
-            const uint4 x = ld_stream_16B(a + 32), y = ld_stream_16B(a + 48);
-            r.w[8] = x.x; r.w[9] = x.y; r.w[10] = x.z; r.w[11] = x.w;
-            r.w[12] = y.x; r.w[13] = y.y; r.w[14] = y.z; r.w[15] = y.w;
+            const uint2 x = ld_stream_8B(a + 8);
+            r.codes.z = x.x;
+            r.codes.w = x.y;
+            r.scales |= ld_stream_1B(sc + 1) << 8;
         }
-    } else if constexpr (SRC == NVFP4KV_NVFP4) {
-        if (one) {
-            const uint2 x = ld_stream_8B(src + static_cast<size_t>(i) * 16);
-            r.w[0] = x.x; r.w[1] = x.y;
-            r.scales = ld_stream_1B(scales + static_cast<size_t>(i) * 2);
-        }
-        if (two) {
-            const uint2 x = ld_stream_8B(src + static_cast<size_t>(i) * 16 + 8);
-            r.w[2] = x.x; r.w[3] = x.y;
-            r.scales |= ld_stream_1B(scales + static_cast<size_t>(i) * 2 + 1) << 8;
-        }
-    } else if (one) {
-        const uint4 x = ld_stream_16B(src + static_cast<size_t>(i) * 16);
-        r.w[0] = x.x; r.w[1] = x.y; r.w[2] = x.z; r.w[3] = x.w;
-        r.scales = ld_stream_1B(scales + static_cast<size_t>(i) * 2);
-        if (two) r.scales |= ld_stream_1B(scales + static_cast<size_t>(i) * 2 + 1) << 8;
     }
     return r;
 }
 
-// The 16 values of block `half` of a step, in FP32 (16-bit sources exactly, NVFP4 as fp32(v g)).
+// Two blocks of NVFP4 as codes, eight to a word in the order of the dims, and scales. (Token pairs: a byte holds two tokens of one
+// dim, and a step is a block of each.)
+struct Codes {
+    uint32_t c[4];
+    uint32_t scales;
+};
 template <int SRC>
-__device__ __forceinline__ void values_of(const Raw& r, int half, float g, float (&x)[16]) {
-    if constexpr (SRC == NVFP4KV_BF16 || SRC == NVFP4KV_FP16) {
+__device__ __forceinline__ Codes unpack(const Packed& r, bool two) {
+    Codes o{{r.codes.x, r.codes.y, r.codes.z, r.codes.w}, r.scales};
+    if constexpr (SRC == kPairs) {
+        const uint32_t w[4] = {r.codes.x, r.codes.y, r.codes.z, r.codes.w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w = r.w[8 * half + j];
-            x[2 * j] = SRC == NVFP4KV_BF16 ? bf16_lo(w) : f16_lo(w);
-            x[2 * j + 1] = SRC == NVFP4KV_BF16 ? bf16_hi(w) : f16_hi(w);
-        }
-    } else {
-        uint2 code;
-        if constexpr (SRC == NVFP4KV_NVFP4) {
-            code = make_uint2(r.w[2 * half], r.w[2 * half + 1]);
-        } else {  // a byte holds two tokens of one dim: this token's nibbles, two dims to a byte
-            uint32_t n[2];
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const uint32_t a = (r.w[2 * k] >> (4 * half)) & 0x0F0F0F0Fu, b = (r.w[2 * k + 1] >> (4 * half)) & 0x0F0F0F0Fu;
+                const uint32_t a = (w[2 * k] >> (4 * half)) & 0x0F0F0F0Fu, b = (w[2 * k + 1] >> (4 * half)) & 0x0F0F0F0Fu;
                 const uint32_t lo = (a | (a >> 4)) & 0x00FF00FFu, hi = (b | (b >> 4)) & 0x00FF00FFu;
-                n[k] = __byte_perm(lo, hi, 0x6420);
+                o.c[2 * half + k] = half == 0 || two ? __byte_perm(lo, hi, 0x6420) : 0u;
             }
-            code = make_uint2(n[0], n[1]);
-        }
-        block_values(code, (r.scales >> (8 * half)) & 0xFFu, x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn(x[j], g);
+        if (!two) o.scales &= 0xFFu;
     }
+    return o;
 }
 
-__device__ __forceinline__ void store_block(uint8_t* dst, uint32_t block, const float (&x)[16], float r) {
-    uint32_t w[4];
+// Largest e2m1 * e4m3 magnitude of a block (exact).
+__device__ __forceinline__ float largest(uint32_t c0, uint32_t c1, uint32_t scale) {
+    uint32_t h[8];
+    e2m1x8_to_f16x2x4(c0, *reinterpret_cast<uint32_t(*)[4]>(h));
+    e2m1x8_to_f16x2x4(c1, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
+    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&h[0]));
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        w[j] = f32x2_to_e4m3x2(__fmul_rn(x[4 * j], r), __fmul_rn(x[4 * j + 1], r)) |
-               f32x2_to_e4m3x2(__fmul_rn(x[4 * j + 2], r), __fmul_rn(x[4 * j + 3], r)) << 16;
-    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(block) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int k = 1; k < 8; ++k) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&h[k])));
+    return fmaxf(__low2float(m), __high2float(m)) * e4m3_to_f32(scale & 0xFFu);
+}
+
+// Largest magnitudes of a step's low and high halves: positive FP16 and BF16 values order as their bits do.
+__device__ __forceinline__ uint32_t largest(const Step& s, uint32_t m) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) m = __vmaxu2(m, s.w[k] & 0x7FFF7FFFu);
+    return m;
+}
+
+__device__ __forceinline__ void mul2(float& a, float& b, float c) {
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b) : "f"(c));
+}
+
+// FP8 codes of a block of 16-bit values.
+template <int SRC>
+__device__ __forceinline__ void store_16bit(uint8_t* dst, uint32_t block, const uint32_t* w, float r) {
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t v = w[2 * j + k];
+            x[2 * k] = SRC == NVFP4KV_BF16 ? bf16_lo(v) : f16_lo(v);
+            x[2 * k + 1] = SRC == NVFP4KV_BF16 ? bf16_hi(v) : f16_hi(v);
+            mul2(x[2 * k], x[2 * k + 1], r);
+        }
+        o[j] = f32x2_to_e4m3x2(x[0], x[1]) | f32x2_to_e4m3x2(x[2], x[3]) << 16;
+    }
+    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(block) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// FP8 codes of a block of NVFP4. A block has eight magnitudes, so their codes fp32(fp32(v g) r) are made once, and byte
+// permutes look them up: an E2M1 code's low bits are the selector, its sign becomes the E4M3 sign. (Converting all 16 values
+// took 10.2 instructions a value in all.)
+__device__ __forceinline__ void store_packed(uint8_t* dst, uint32_t block, uint32_t c0, uint32_t c1, uint32_t scale, float g, float r) {
+    const float sf = e4m3_to_f32(scale & 0xFFu);
+    float x[8] = {0.0f, 0.5f * sf, sf, 1.5f * sf, 2.0f * sf, 3.0f * sf, 4.0f * sf, 6.0f * sf};  // exact
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+        mul2(x[k], x[k + 1], g);
+        mul2(x[k], x[k + 1], r);
+    }
+    const uint32_t lo = f32x2_to_e4m3x2(x[0], x[1]) | f32x2_to_e4m3x2(x[2], x[3]) << 16;
+    const uint32_t hi = f32x2_to_e4m3x2(x[4], x[5]) | f32x2_to_e4m3x2(x[6], x[7]) << 16;
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t c = (k < 2 ? c0 : c1) >> (16 * (k & 1));  // four codes
+        o[k] = __byte_perm(lo, hi, c & 0x7777u) | __byte_perm(0x8000u, 0u, (c >> 3) & 0x1111u);
+    }
+    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(block) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 template <int SRC, bool KEPT>
 __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params p) {
     pdl_enter();
+    constexpr bool kPacked = SRC != NVFP4KV_BF16 && SRC != NVFP4KV_FP16;
+    constexpr int N = KEPT ? kept_steps(SRC) : 1;
     __shared__ float most[2][kMaxThreads / 32];  // two sets: the next run's maxima do not wait for this one's readers
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const uint32_t blocks = static_cast<uint32_t>(p.T) * p.nb, steps = (blocks + 1) / 2;
+    const bool even = blocks % 2 == 0;
     const float g = p.g ? __ldg(p.g) : 1.0f;
     int set = 0;
-    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const int64_t i = u / p.H;
+    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const uint32_t i = u / static_cast<uint32_t>(p.H);
         const int h = static_cast<int>(u - i * p.H);
         const int from = p.src_ids ? __ldg(p.src_ids + i) : static_cast<int>(i);
         const int to = p.dst_ids ? __ldg(p.dst_ids + i) : static_cast<int>(i);
@@ -152,84 +227,92 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
         if (from < 0 || from >= p.src_pages || to < 0 || to >= p.dst_pages) bad |= NVFP4KV_STATUS_PAGE_OOB;
         if (tokens < 0 || tokens > p.T) bad |= NVFP4KV_STATUS_BAD_SEQ_LEN;
         if (bad) {  // the same for every thread of the CTA
-            if (tid == 0 && h == 0 && !(from == -1 || to == -1)) flag_status(p.status, bad);
+            if (tid == 0 && h == 0 && from != -1 && to != -1) flag_status(p.status, bad);
             continue;
         }
         const uint32_t end = static_cast<uint32_t>(tokens) * p.nb;  // blocks of valid tokens
-        const int64_t run = static_cast<int64_t>(from) * p.H + h;
-        constexpr int kBytes = SRC == NVFP4KV_BF16 || SRC == NVFP4KV_FP16 ? 32 : 8;  // of a block
-        const uint8_t* src = p.src + run * blocks * kBytes;
-        const uint8_t* scales = p.src_scales + run * blocks;
-        uint8_t* dst = p.dst + (static_cast<int64_t>(to) * p.H + h) * blocks * 16;
+        const int64_t run = static_cast<int64_t>(from) * p.H + h, out = static_cast<int64_t>(to) * p.H + h;
+        uint8_t* dst = p.dst + out * blocks * 16;
 
+        // a step's values (16 bits) or codes
+        using Held = std::conditional_t<kPacked, Packed, Step>;
+        auto take = [&](Held& v, uint32_t j) {
+            uint32_t b0, b1;
+            blocks_of<SRC>(p, j, b0, b1);
+            if constexpr (kPacked)
+                v = load_packed<SRC>(p.src + run * blocks * 8, p.src_scales + run * blocks, j, b0 < end, b1 < end, even);
+            else
+                load_16bit(v, p.src + run * blocks * 32, j, b0 < end, b1 < end);
+        };
+        uint32_t bits = 0u;
         float a = 0.0f;
-        auto take = [&](uint32_t j) {
-            uint32_t b0, b1;
-            blocks_of<SRC>(p, j, b0, b1);
-            return load_step<SRC>(src, scales, j, b0 < end, b1 < end);
-        };
-        auto look = [&](const Raw& r, uint32_t j) {  // the maximum over the step's valid blocks
-            uint32_t b0, b1;
-            blocks_of<SRC>(p, j, b0, b1);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[16];
-                values_of<SRC>(r, half, g, x);
-                float m = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 16; ++k) m = fmaxf(m, fabsf(x[k]));
-                if ((half ? b1 : b0) < end) a = fmaxf(a, m);
+        auto look = [&](const Held& v, uint32_t j) {
+            if constexpr (kPacked) {
+                uint32_t b0, b1;
+                blocks_of<SRC>(p, j, b0, b1);
+                const Codes c = unpack<SRC>(v, b1 < end);
+                a = fmaxf(a, fmaxf(largest(c.c[0], c.c[1], c.scales), largest(c.c[2], c.c[3], c.scales >> 8)));
+            } else {
+                bits = largest(v, bits);
             }
         };
-        auto put = [&](const Raw& r, uint32_t j, float rs) {
+        auto put = [&](const Held& v, uint32_t j, float r) {
             uint32_t b0, b1;
             blocks_of<SRC>(p, j, b0, b1);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t b = half ? b1 : b0;
-                float x[16];
-                values_of<SRC>(r, half, g, x);
-                if (b >= end)
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] = 0.0f;
-                if (b < blocks) store_block(dst, b, x, rs);
+            if constexpr (kPacked) {
+                const Codes c = unpack<SRC>(v, b1 < end);
+                store_packed(dst, b0, c.c[0], c.c[1], c.scales, g, r);
+                if (b1 < blocks) store_packed(dst, b1, c.c[2], c.c[3], c.scales >> 8, g, r);
+            } else {
+                store_16bit<SRC>(dst, b0, v.w, r);
+                if (b1 < blocks) store_16bit<SRC>(dst, b1, v.w + 8, r);
             }
         };
-        Raw kept[KEPT ? kKept : 1];
+        Held held[N];
         if constexpr (KEPT) {
 #pragma unroll
-            for (int k = 0; k < kKept; ++k) {
+            for (int k = 0; k < N; ++k) {
                 const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) kept[k] = take(j);
+                if (j < steps) take(held[k], j);
             }
 #pragma unroll
-            for (int k = 0; k < kKept; ++k) {
+            for (int k = 0; k < N; ++k) {
                 const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) look(kept[k], j);
+                if (j < steps) look(held[k], j);
             }
         } else {
-            for (uint32_t j = tid; j < steps; j += blockDim.x) look(take(j), j);
+            for (uint32_t j = tid; j < steps; j += blockDim.x) {
+                take(held[0], j);
+                look(held[0], j);
+            }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        if constexpr (!kPacked) {
+            bits = max(bits & 0xFFFFu, bits >> 16);
+            a = SRC == NVFP4KV_BF16 ? __uint_as_float(bits << 16) : f16_lo(bits);
+        }
+        a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));  // (a >= 0: floats order as their bits)
         if (warps > 1) {
             if (lane == 0) most[set][warp] = a;
             __syncthreads();
             for (int w = 0; w < warps; ++w) a = fmaxf(a, most[set][w]);
             set ^= 1;
         }
+        if constexpr (kPacked) a = __fmul_rn(a, fabsf(g));  // (the largest of fp32(|v| |g|))
         float s = __fdiv_rn(a, 448.0f);
         if (s < 7.8886090522101181e-31f) s = 1.0f;  // 2^-100: all values become 0
         const float r = __frcp_rn(s);
-        if (tid == 0) p.dst_scales[static_cast<int64_t>(to) * p.H + h] = s;
+        if (tid == 0) p.dst_scales[out] = s;
         if constexpr (KEPT) {
 #pragma unroll
-            for (int k = 0; k < kKept; ++k) {
+            for (int k = 0; k < N; ++k) {
                 const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) put(kept[k], j, r);
+                if (j < steps) put(held[k], j, r);
             }
         } else {
-            for (uint32_t j = tid; j < steps; j += blockDim.x) put(take(j), j, r);
+            for (uint32_t j = tid; j < steps; j += blockDim.x) {
+                take(held[0], j);
+                put(held[0], j, r);
+            }
         }
     }
 }
@@ -237,14 +320,12 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
 template <int SRC>
 cudaError_t launch_fp8(const Fp8Params& p, cudaStream_t s) {
     const int64_t steps = (static_cast<int64_t>(p.T) * p.nb + 1) / 2;
+    constexpr int N = kept_steps(SRC);
     int threads = 32;
-    while (threads < kMaxThreads && static_cast<int64_t>(threads) * kKept < steps) threads *= 2;
-    const bool kept = static_cast<int64_t>(threads) * kKept >= steps;
-    // CTAs come and go: a run is short, and a CTA per run keeps an SM full without a tail of its own
-    const int64_t most = (int64_t{1} << 31) - 1;
-    const unsigned grid = static_cast<unsigned>(p.units < most ? p.units : most);
-    return kept ? launch_pdl(fp8_pages_kernel<SRC, true>, dim3(grid), dim3(threads), 0, s, p)
-                : launch_pdl(fp8_pages_kernel<SRC, false>, dim3(grid), dim3(threads), 0, s, p);
+    while (threads < kMaxThreads && static_cast<int64_t>(threads) * N < steps) threads *= 2;
+    // a CTA for each run: runs are short, and CTAs that come and go keep an SM full without a tail of its own
+    return static_cast<int64_t>(threads) * N >= steps ? launch_pdl(fp8_pages_kernel<SRC, true>, dim3(p.units), dim3(threads), 0, s, p)
+                                                      : launch_pdl(fp8_pages_kernel<SRC, false>, dim3(p.units), dim3(threads), 0, s, p);
 }
 
 }  // namespace
@@ -268,8 +349,10 @@ extern "C" nvfp4kv_status nvfp4_kv_fp8_pages(
     if ((!src_page_ids && num_pages > src_pool_pages) || (!dst_page_ids && num_pages > dst_pool_pages))
         return NVFP4KV_ERR_INVALID_ARG;
     const int nb = layout->head_dim / 16;
-    // a run's blocks are numbered in 32 bits, and divided by nb with a multiply (fast_div)
-    if (static_cast<int64_t>(layout->page_size) * nb > (1 << 24) || nb > (1 << 12)) return NVFP4KV_ERR_UNSUPPORTED;
+    // a run's blocks are numbered in 32 bits, and divided by nb with a multiply (fast_div); so are the runs
+    if (static_cast<int64_t>(layout->page_size) * nb > (1 << 24) || nb > (1 << 12) ||
+        static_cast<int64_t>(num_pages) * layout->num_kv_heads > (1 << 30))
+        return NVFP4KV_ERR_UNSUPPORTED;
     Fp8Params p{};
     p.src = static_cast<const uint8_t*>(src);
     p.src_scales = packed ? src_scales : nullptr;
@@ -286,7 +369,7 @@ extern "C" nvfp4kv_status nvfp4_kv_fp8_pages(
     p.H = layout->num_kv_heads;
     p.T = layout->page_size;
     p.nb = nb;
-    p.units = static_cast<int64_t>(num_pages) * p.H;
+    p.units = static_cast<uint32_t>(num_pages) * p.H;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (pairs) return launched(launch_fp8<kPairs>(p, s));
     switch (src_dtype) {
