@@ -23,7 +23,7 @@ constexpr int kMaxThreads = 512;   // of a CTA: runs of up to 512 x 32 values an
 constexpr int kPairs = NVFP4KV_NVFP4 + 1;  // NVFP4 in NVFP4KV_PACK_TOKEN_PAIRS, as a source of its own
 
 // Steps of 32 values that a thread keeps in registers: 16 words each of a 16-bit source, 5 of a packed one.
-__host__ __device__ constexpr int kept_steps(int src) { return src == NVFP4KV_BF16 || src == NVFP4KV_FP16 ? 2 : 4; }
+__host__ __device__ constexpr int kept_steps(int src) { return src == NVFP4KV_BF16 || src == NVFP4KV_FP16 ? 2 : 2; }
 
 struct Fp8Params {
     const uint8_t* src;
