@@ -623,8 +623,8 @@ nvfp4kv_status nvfp4_paged_fp8_decode_attention(
  * the sequence's rows, where they lie in range, get out = 0 and lse = -inf. A page id outside the pool sets PAGE_OOB and its
  * tokens are left out; a row that sees no token gets the same. TIMEOUT: a wait inside the kernel gave up (a defect;
  * the outputs are incomplete).
- * Three launches. Supported: head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; page_size % 16 == 0;
- * batch <= 65535.
+ * Two launches. Supported: head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; page_size % 16 == 0;
+ * batch <= 65535; pool_pages * num_kv_heads * page_size < 2^32.
  * ------------------------------------------------------------------------------------------ */
 size_t nvfp4_paged_extend_attention_workspace_size(const nvfp4kv_layout* layout, int32_t batch,
                                                    int32_t num_q_heads);

@@ -2,27 +2,43 @@
 // window and first tokens that stay visible (LMSYS, "Accelerating Long-Context and Agentic Inference with NVFP4 KV
 // Cache": "Path 2: Chunked prefill / Extend", whose attention reads the FP8 workspace).
 //
-// Work. The query heads of a KV head share its keys, so a tile of M = 128 rows holds floor(128 / G) tokens times the G
-// heads of a group. A unit is a block of such rows (two tiles at head_dim 64 and 128, one at 256) of one sequence and KV
+// Work. The query heads of a KV head share its keys, so a row tile of M = 128 rows holds floor(128 / G) tokens times the G
+// heads of a group. A unit is a block of such rows (two row tiles at head_dim 64 and 128, one at 256) of one sequence and KV
 // head; its work is the list of KV tiles (128 tokens, 64 at head_dim 256) that hold a token visible to a row of it. The
 // tiles of all units form one list, cut into equal parts, one per SM: a part that begins or ends inside a unit leaves a
 // partial result (row maxima, sums, unnormalised output) that a second kernel joins. Cuts close to a unit's border are
 // moved onto it. The cuts are made from the lengths, by every CTA for itself.
 //
 // A CTA per SM, with a role for each warp:
-//  * The scout walks over the CTA's part and looks up where the tiles lie.
-//  * 4 loader warps each for K and V bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so they are
-//    loaded there directly, one tile ahead of the conversion, and stored in the 128-byte-swizzled layout that tcgen05.mma
-//    reads: K with the head dims contiguous (K-major), V with the same store and read as MN-major.
-//  * A warp per row tile issues its S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), P read from
-//    TMEM where it lies over the scores it came from. (One warp for both left the tensor core waiting between its products.)
-//  * 4 softmax warps per tile, one row a thread, so that row maxima and sums need no exchange. While one tile's weights are
-//    made the tensor core works on the other's products; at head_dim 256 the next KV tile's scores are under way instead.
+//  * The scout walks over the CTA's part and writes into a ring where each tile lies and what the others need to know of it.
+//  * 4 loader warps each for K and V bring the tiles in. FP8 values have to pass through registers to become FP16 (exact), so
+//    they are loaded there directly and stored in the 128-byte-swizzled layout that tcgen05.mma reads: K with the head dims
+//    contiguous (K-major), V with the same store and read as MN-major.
+//  * A warp per row tile issues its S = Q K^T and O += P V (tcgen05.mma, FP16 in, FP32 accumulators in TMEM), in steps of 64
+//    tokens. P lies in TMEM over the scores it came from. Each row tile has two slots of scores, so a step's scores are there
+//    when its softmax begins.
+//  * 4 softmax warps per row tile, one row a thread, so that row maxima and sums need no exchange.
 // The running maximum moves only when it grows by more than 2^8, so rescaling O in TMEM is rare.
 //
 // Scales. With a page's scales s_K, s_V, a score becomes x = S c s_K + log2(s_V) in log2 units, so that p = 2^(x - m) is the
 // weight times s_V, as the sum over V needs it, with one FMA and one 2^x an element; the sum of the weights takes p / s_V. Q is
-// brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest).
+// brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest); P is rounded
+// to FP16 (11 bits, where the output has 8).
+//
+// Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 551 us, 1060 TFLOP/s,
+// 0.55 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 2.0 ms, 1086 TFLOP/s; 24 ragged sequences with a window
+// at head_dim 64 (15.6 GFLOP): 69 us.
+// Bound, at head_dim 128: the tensor core is busy for 3/4 of the time, with products at less than its rate. A 128 x 64 x 16 product
+// with both operands in shared memory takes 72 clocks, hardly more than a 128 x 128 x 16 one (64): its 128 rows of Q have to
+// be read either way. Scores of 128 tokens at once leave no room in TMEM (512 columns) for two slots beside two outputs, and then
+// the softmax waits for its scores: 640 to 730 us for the 16 chunks, in three arrangements. The rest is the softmax, whose
+// 2^x alone take 1024 clocks for 256 x 128 scores, of 4500 measured.
+// What it took, for the 16 chunks: 975 us with one issuing lane and scores read from TMEM twice; 683 a row's scores in registers, packed
+// FMAs, pool addresses once a tile; 641 in steps of 64 tokens with two slots; 627 the scout, so that the roles' code fits the
+// instruction cache (90 KB of code had warps waiting for instructions 15 % of the time), and products issued by an elected lane
+// (the instruction takes its operands from uniform registers; with a lane that the compiler does not know to be one alone, it
+// fills them in a loop over lanes); 551 a tile's place read from shared memory while its scores come from TMEM, as shared memory
+// is slow beside the tensor core's reads.
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -218,6 +234,10 @@ __device__ __forceinline__ PlanEntry find_unit(const ExtendParams& p, const int6
     int64_t at = chunk[lo], per_head;
     Seq s;
     for (e.b = lo * ((p.B + NT - 1) / NT);; ++e.b) {
+        if (e.b >= p.B) {  // (only where lengths change under the call)
+            e.begin = e.end = x;
+            return e;
+        }
         s = sequence(p, e.b);
         per_head = warp_sum64(cost_of<D>(p, s, lane, 32));
         if (x < at + per_head * p.H) break;
@@ -279,6 +299,7 @@ struct Walk {
         h = e.h;
         qb = e.qb;
         tile0 = e.tile;
+        if (b >= p.B) pos = end;
         if (pos < end) {
             s = sequence(p, b);
             measure(p);
@@ -300,8 +321,13 @@ struct Walk {
             qb = 0;
             if (++h == p.H) {
                 h = 0;
-                do s = sequence(p, ++b);
-                while (s.n == 0);
+                do {
+                    if (++b >= p.B) {  // (as above)
+                        pos = end;
+                        return;
+                    }
+                    s = sequence(p, b);
+                } while (s.n == 0);
             }
         }
         measure(p);
