@@ -109,6 +109,8 @@ struct ExtendParams {
     int64_t q_stride, out_stride;
     uint64_t t_magic;
     int32_t B, rows, Hq, H, G, T, pool_pages, max_pages, window, sinks, ctas;
+    int32_t per;  // tokens of a row tile, floor(128 / G)
+    uint32_t unit_magic;  // ceil(2^32 / tokens of a unit)
     float sm_scale;
 };
 
@@ -140,22 +142,27 @@ struct Unit {
 template <int D>
 __device__ __forceinline__ Unit unit_of(const ExtendParams& p, const Seq& s, int qb) {
     using G_ = Shape<D>;
-    const int each = G_::MT * (kRowsM / p.G);
+    const int each = G_::MT * p.per;
     Unit u;
     u.t0 = qb * each;
     u.t1 = min(s.n, u.t0 + each);
     const int p0 = s.len - s.n + u.t0;
     u.hi = s.len - s.n + u.t1;
     u.lo = p0 >= p.window ? p0 - p.window + 1 : 0;
-    u.sink = (min(p.sinks, u.lo) + G_::TK - 1) / G_::TK;
-    u.first = max(u.lo / G_::TK, u.sink);
-    u.tiles = u.sink + (u.hi + G_::TK - 1) / G_::TK - u.first;
+    constexpr unsigned kTk = G_::TK;  // (unsigned: shifts)
+    u.sink = static_cast<int>((static_cast<unsigned>(min(p.sinks, u.lo)) + kTk - 1) / kTk);
+    u.first = max(static_cast<int>(static_cast<unsigned>(u.lo) / kTk), u.sink);
+    u.tiles = u.sink + static_cast<int>((static_cast<unsigned>(u.hi) + kTk - 1) / kTk) - u.first;
     return u;
 }
+// ceil(n / tokens of a unit): the magic number's quotient may be one too large, where n is large.
 template <int D>
 __device__ __forceinline__ int blocks_of(const ExtendParams& p, int n) {
-    const int each = Shape<D>::MT * (kRowsM / p.G);
-    return (n + each - 1) / each;
+    const int each = Shape<D>::MT * p.per;
+    if (each == 1) return n;
+    int q = static_cast<int>(__umulhi(static_cast<unsigned>(n), p.unit_magic));
+    q -= static_cast<int64_t>(q) * each > n;
+    return q + (q * each != n);
 }
 template <int D>
 __device__ __forceinline__ int tile_start(const Unit& u, int j) {
@@ -189,7 +196,7 @@ __device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {  // inclus
 // own that made all cuts took 17 us; this takes about 2, while the CTA sets itself up.) Returns the list's length. All threads.
 template <int D>
 __device__ __forceinline__ int64_t list_sequences(const ExtendParams& p, int64_t* chunk, int64_t* part) {
-    constexpr int NT = Shape<D>::THREADS, kSerial = 4;
+    constexpr int NT = Shape<D>::THREADS, kSerial = 8;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int each = (p.B + NT - 1) / NT;
     int64_t local = 0;
@@ -537,7 +544,7 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
     Walk<D> w;
     for (w.start(p, mine, part_end); w.more(); w.next(p)) {
         const int unit = (w.whole() ? kWhole : 0) | (w.tile0 > 0 ? kGoesOn : 0) |
-                         (S_::MT == 2 && w.u.t1 - w.u.t0 > kRowsM / p.G ? kTwo : 0);
+                         (S_::MT == 2 && w.u.t1 - w.u.t0 > p.per ? kTwo : 0);
         const bool final = w.unit_begin + kUnitCost + w.u.tiles >= w.end;
 #pragma unroll 1
         for (int j = 0; j < w.piece_tiles; ++j, ++n) {
@@ -741,7 +748,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
     const int row = 32 * (warp & 3) + lane;       // of the tile
-    const int per = kRowsM / p.G;                 // tokens of a tile
+    const int per = p.per;                        // tokens of a tile
     const int tok = row / p.G, head = row - tok * p.G;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const uint32_t o_col = lanes + S_::O_COL + x * D;
@@ -779,27 +786,38 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         const int hq = begin.h * p.G + head;
         float cs, m = -INFINITY, l = 0.0f;
         {
+            // (all of the row in flight at once; at head_dim 256 half of it, read a second time to be stored)
             const uint16_t* src = p.q + out_row * p.q_stride + hq * D;
-            float top = 0.0f;
-            if (real) {
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = ldg16(src + 8 * c);
-                    top = fmaxf(top, fmaxf(fmaxf(fmaxf(fabsf(bf16_lo(v.x)), fabsf(bf16_hi(v.x))), fmaxf(fabsf(bf16_lo(v.y)), fabsf(bf16_hi(v.y)))),
-                                           fmaxf(fmaxf(fabsf(bf16_lo(v.z)), fabsf(bf16_hi(v.z))), fmaxf(fabsf(bf16_lo(v.w)), fabsf(bf16_hi(v.w))))));
+            constexpr int N = D >= 256 ? 16 : D / 8;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            uint4 v[N];
+            __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 8; c0 += N) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) v[c] = real ? ldg16(src + 8 * (c0 + c)) : zero;
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
                 }
             }
+            const float top = fmaxf(__low2float(most), __high2float(most));
             int kq = top > 0.0f ? 14 - ilogbf(top) : 0;
             kq = max(-120, min(kq, 120));
             const float up = copysignf(ldexpf(1.0f, kq), scale);  // a negative scale turns the queries: c is never negative
             cs = fabsf(scale) * kLog2e * ldexpf(1.0f, -kq);
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (real) v = ldg16(src + 8 * c);
-                sts16(qrow + (c / 8) * (kRowsM * 128) + (((c & 7) ^ (row & 7)) << 4), pack_f16x2(bf16_lo(v.x) * up, bf16_hi(v.x) * up),
-                      pack_f16x2(bf16_lo(v.y) * up, bf16_hi(v.y) * up), pack_f16x2(bf16_lo(v.z) * up, bf16_hi(v.z) * up),
-                      pack_f16x2(bf16_lo(v.w) * up, bf16_hi(v.w) * up));
+#pragma unroll 1
+            for (int c0 = D / 8 - N; c0 >= 0; c0 -= N) {
+                if (c0 < D / 8 - N)
+#pragma unroll
+                    for (int c = 0; c < N; ++c) v[c] = real ? ldg16(src + 8 * (c0 + c)) : zero;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    sts16(qrow + ((c0 + c) / 8) * (kRowsM * 128) + (((c & 7) ^ (row & 7)) << 4), pack_f16x2(bf16_lo(v[c].x) * up, bf16_hi(v[c].x) * up),
+                          pack_f16x2(bf16_lo(v[c].y) * up, bf16_hi(v[c].y) * up), pack_f16x2(bf16_lo(v[c].z) * up, bf16_hi(v[c].z) * up),
+                          pack_f16x2(bf16_lo(v[c].w) * up, bf16_hi(v[c].w) * up));
             }
             fence_async_smem();
             __syncwarp();
@@ -1037,7 +1055,7 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
     while (last + 1 < p.ctas && p.plan[last + 1].cut < next.end) ++last;
     const Seq s = sequence(p, next.b);
     const Unit u = unit_of<D>(p, s, next.qb);
-    const int per = kRowsM / p.G;
+    const int per = p.per;
     const float gv = scalar_or_1(p.gv);
     for (int row = blockIdx.y * 8 + warp; row < S_::MT * kRowsM; row += gridDim.y * 8) {
         const int x = row / kRowsM, r = row - x * kRowsM, tok = r / p.G, head = r - tok * p.G;
@@ -1161,6 +1179,9 @@ extern "C" nvfp4kv_status nvfp4_paged_extend_attention(
     p.Hq = num_q_heads;
     p.H = H;
     p.G = num_q_heads / H;
+    p.per = kRowsM / p.G;
+    const unsigned unit = static_cast<unsigned>((D == 256 ? 1 : 2) * p.per);
+    p.unit_magic = static_cast<uint32_t>(((uint64_t{1} << 32) + unit - 1) / unit);
     p.T = T;
     p.pool_pages = pool_pages;
     p.max_pages = max_pages_per_seq;
