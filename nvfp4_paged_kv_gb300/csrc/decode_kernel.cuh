@@ -66,24 +66,20 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t kFirst = 1u, kLast = 2u;  // slot header flags: first / last stage of a piece
 constexpr int kSmemPerSm = 233472;           // shared memory of an SM (228 KiB)
 
-// What the cache holds: NVFP4 (packed as above), or FP8 E4M3 rows of D bytes for K and for V.
-enum Format { kNvfp4 = 0, kFp8 = 1 };
-
-template <int D, int F = kNvfp4>
+template <int D>
 struct Geo {
-    static constexpr int TOK = ((D == 256) ? 32 : 64) >> F;  // tokens of a stage (8 or 9 KB of K and V)
-    static constexpr int ROW = (F == kFp8) ? D : D / 2;      // bytes of a token's K
+    static constexpr int TOK = (D == 256) ? 32 : 64;  // tokens of a stage
     static constexpr int SUB = TOK / 16;              // 16-token MMA tiles of a stage
     static constexpr int NB = D / 16;                 // blocks (= scales) per token row
-    static constexpr int SK = TOK * ROW;              // packed K rows of a stage
-    static constexpr int SV = TOK * ROW;              // V rows of D bytes (NVFP4: TOK / 2, of token pairs)
-    static constexpr int SS = (F == kFp8) ? 0 : TOK * NB;  // one scale pool of a stage
+    static constexpr int SK = TOK * D / 2;            // packed K rows of a stage
+    static constexpr int SV = TOK * D / 2;            // token-pair V rows (TOK / 2 rows of D)
+    static constexpr int SS = TOK * NB;               // one scale pool of a stage
     static constexpr int K_OFF = 0;
     static constexpr int V_OFF = SK;
     static constexpr int KS_OFF = SK + SV;
     static constexpr int VS_OFF = KS_OFF + SS;
-    static constexpr int HDR_OFF = VS_OFF + SS;  // slot header (8 words; FP8: then the sub-tiles' scales of K, of V)
-    static constexpr int SLOT = HDR_OFF + 32 + (F == kFp8 ? 16 : 0);
+    static constexpr int HDR_OFF = VS_OFF + SS;  // slot header (8 words)
+    static constexpr int SLOT = HDR_OFF + 32;
     static constexpr int SLOTS = 2;              // ring slots per warp: one in flight, one computed
     // warps of the one CTA per SM (register budget: 16 x 32 x 128, 12 x 32 x 170, 8 x 32 x 255)
     static constexpr int WARPS = (D == 64) ? 16 : (D == 128 ? 12 : 8);
@@ -93,17 +89,16 @@ struct Geo {
     static constexpr int Q_OFF = WARPS * RING;
     static constexpr int SMEM = Q_OFF + QCACHE;
     static constexpr int KSTEPS = D / 16;       // k-steps of S^T = K Q^T
-    static constexpr int CHUNK = ROW / 4;       // bytes of a row one quad lane owns
+    static constexpr int CHUNK = D / 8;         // bytes of a row one quad lane owns
     static constexpr int CW = CHUNK / 4;        // ... as 32-bit words
     static constexpr int VCH = D / 16;          // 16-byte chunks per V pair row
     static constexpr int SWZ = (VCH < 8 ? VCH : 8) - 1;  // chunk XOR mask
     static constexpr int DCH = SK / (16 * 32);  // 16-byte chunks per lane of one data pool
-    static constexpr int SUB_DIV = DCH / SUB;   // data chunk i of a lane lies in sub-tile i / SUB_DIV
+    static constexpr int SUB_DIV = D / 64;      // data chunk i of a lane lies in sub-tile i / SUB_DIV
     static constexpr int SCH = SS / 16;         // 16-byte chunks of one scale pool
     static constexpr int SC_PER_LANE = 2 * SCH / 32;
     static_assert(DCH * 32 * 16 == SK && DCH == SUB * SUB_DIV, "copy split");
     static_assert(SC_PER_LANE * 32 == 2 * SCH, "scale copy split");
-    static_assert(F == kNvfp4 || 2 * SUB * 4 <= 16, "scales in the slot header");
     static_assert(SLOT % 16 == 0 && RING % 16 == 0, "16-byte aligned slots");
     static_assert(SMEM + 1024 + 512 <= kSmemPerSm, "shared memory budget");
 };
@@ -128,22 +123,6 @@ struct DecodeParams {
     uint32_t nonce;     // tag of this call
     int32_t B, Hq, H, G, T, pool_pages, max_pages, num_runs;
     float sm_scale;
-};
-
-// With a sliding window: a sequence of L tokens shows those from L - window on and the first `sinks`. FP8 pages have a
-// scale for each page and head (null: 1).
-struct WindowParams : DecodeParams {
-    const float* kbs;  // [pool_pages][H]
-    const float* vbs;
-    int32_t window, sinks;
-};
-template <bool WIN>
-struct ParamsOf {
-    using type = DecodeParams;
-};
-template <>
-struct ParamsOf<true> {
-    using type = WindowParams;
 };
 
 __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
@@ -193,32 +172,6 @@ __device__ __forceinline__ uint32_t v_swz(int pr, int x) {
     return static_cast<uint32_t>(pr * D + ((((x >> 4) ^ (pr & Geo<D>::SWZ))) << 4) + (x & 15));
 }
 
-// FP8 rows in shared memory, 16-byte chunks XOR-swizzled so that the eight lanes of a quarter warp hit distinct banks.
-// K: lanes (r, c) of rows r, r + 1 take chunk c D/64 + k; V: lanes of rows 2c take the chunk of dims rho D/8.
-template <int D>
-__device__ __forceinline__ uint32_t k8_swz(int row, int ch) {
-    if constexpr (D == 64) return static_cast<uint32_t>(row * D + 16 * ch);
-    else if constexpr (D == 128) return static_cast<uint32_t>(row * D + 16 * (ch ^ (row & 1)));
-    else return static_cast<uint32_t>(row * D + 16 * (ch ^ (((ch >> 3) & 1) | ((row & 1) << 1))));
-}
-template <int D>
-__device__ __forceinline__ uint32_t v8_swz(int row, int ch) {
-    const int g = (row >> 1) & 3;
-    if constexpr (D == 64)  // two rows to a 128-byte line
-        return static_cast<uint32_t>((row >> 1) * 128 + 16 * (((row & 1) * 4 + ch) ^ ((g & 1) | ((g & 2) << 1))));
-    else if constexpr (D == 128) return static_cast<uint32_t>(row * D + 16 * (ch ^ g));
-    else return static_cast<uint32_t>(row * D + 16 * (ch ^ ((g << 1) | ((ch >> 3) & 1))));
-}
-
-// A device scalar that may be left out.
-__device__ __forceinline__ float scalar_or_1(const float* p) { return p ? __ldg(p) : 1.0f; }
-
-__device__ __forceinline__ float lg2_approx(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 16-byte asynchronous copy global -> shared, with compile-time offsets on both addresses, under
 // the L2 policy `pol` (evict-first for the K/V stream: each byte is read once per call, so its
 // lines are the first to go and other lines, such as outputs still waiting to be written back,
@@ -235,9 +188,6 @@ __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, 
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
                  "l"(src), "r"(bytes), "l"(pol)
                  : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // 16-byte asynchronous copy with the default L2 policy (the queries: read once per piece).
 __device__ __forceinline__ void cp_async16_plain(uint32_t dst, const void* src) {
@@ -262,22 +212,6 @@ __device__ __forceinline__ void static_for(F&& f) {
 // Stages (of tok tokens) of a sequence of length L; 0 for an invalid length.
 __device__ __forceinline__ int seq_stages(int L, int max_tokens, int tok) {
     return (L > 0 && L <= max_tokens) ? (L + tok - 1) / tok : 0;
-}
-
-// The stages of a sequence with a window: those of the first tokens, then those from the window's first token on.
-struct WindowStages {
-    int lo;     // first token of the window; those between `sinks` and it are hidden
-    int sink;   // stages of the first tokens that do not belong to the window's stages
-    int first;  // first stage of the window
-    int count;  // of both
-};
-__device__ __forceinline__ WindowStages window_stages(int L, int max_tokens, int tok, int window, int sinks) {
-    WindowStages w;
-    w.lo = L > window ? L - window : 0;
-    w.sink = (min(sinks, w.lo) + tok - 1) / tok;
-    w.first = max(w.lo / tok, w.sink);
-    w.count = (L > 0 && L <= max_tokens) ? w.sink + (L + tok - 1) / tok - w.first : 0;
-    return w;
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -324,11 +258,11 @@ __device__ __forceinline__ void column_maxima(float lm0, float lm1, float& mx0, 
 // block is staged in shared memory by asynchronous copies (one round trip), the (max, sum) of
 // each query head reduced by one warp per head, and the weighted sum of the records' outputs
 // split over the threads: thread t takes one float4 column of the G x D outputs and every R-th
-// record of the chunk, R = threads / columns.
-template <int D, int F = kNvfp4>
+// record of the chunk, R = threads / columns. G_: the calling kernel's geometry; GV_MAY_LACK: a
+// null V scale means 1 (FP8 pages).
+template <int D, class G_ = Geo<D>, bool GV_MAY_LACK = false>
 __device__ __forceinline__ void merge_pair(const DecodeParams& p, int b, int h, int64_t rec0,
                                            int n, uint8_t* smem) {
-    using G_ = Geo<D, F>;
     constexpr int NT = G_::THREADS;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = p.G;
@@ -436,7 +370,7 @@ __device__ __forceinline__ void merge_pair(const DecodeParams& p, int b, int h, 
             }
         }
     }
-    const float gvs = F == kFp8 ? scalar_or_1(p.gv) : __ldg(p.gv);
+    const float gvs = GV_MAY_LACK && !p.gv ? 1.0f : __ldg(p.gv);
 #pragma unroll
     for (int j = 0; j < CPT; ++j) {
         const int col = col0 + NT * j;
@@ -470,10 +404,9 @@ __device__ __forceinline__ int align16i(int x) { return (x + 15) & ~15; }
 // from the staged maxima itself, so no reduction across threads and no second barrier is needed.
 // Returns how many pairs were merged (0 when the first pair alone does not fit: the caller merges
 // it by chunks).
-template <int D, int F = kNvfp4>
+template <int D, class G_ = Geo<D>, bool GV_MAY_LACK = false>
 __device__ __forceinline__ int merge_batch(const DecodeParams& p, const int (*pend)[4], int first,
                                            int n_pend, uint8_t* smem) {
-    using G_ = Geo<D, F>;
     constexpr int NT = G_::THREADS;
     const int tid = threadIdx.x;
     const int G = p.G;
@@ -510,7 +443,7 @@ __device__ __forceinline__ int merge_batch(const DecodeParams& p, const int (*pe
         cp_async_wait<0>();
     }
     __syncthreads();
-    const float gvs = F == kFp8 ? scalar_or_1(p.gv) : __ldg(p.gv);
+    const float gvs = GV_MAY_LACK && !p.gv ? 1.0f : __ldg(p.gv);
     const int C4 = G * D / 4;
     int i = first, off = 0, base = 0;  // columns [base, base + C4) belong to pair i, staged at off
     for (int cc = tid; cc < cnt * C4; cc += NT) {
@@ -549,13 +482,10 @@ __device__ __forceinline__ int merge_batch(const DecodeParams& p, const int (*pe
     return cnt;
 }
 
-// F: what the cache holds; WIN: with a sliding window (FP8 always, with one that no length passes where there is none).
-template <int D, int F = kNvfp4, bool WIN = false>
-__global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
-    decode_split_kernel(const typename ParamsOf<WIN>::type p) {
+template <int D>
+__global__ void __launch_bounds__(Geo<D>::THREADS, 1) decode_split_kernel(const DecodeParams p) {
     pdl_enter();
-    using G_ = Geo<D, F>;
-    static_assert(F == kNvfp4 || WIN, "the FP8 cache's scales are in WindowParams");
+    using G_ = Geo<D>;
     constexpr int TOK = G_::TOK;
     constexpr int NW = G_::WARPS;
     constexpr int NT = G_::THREADS;
@@ -573,10 +503,6 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     const int c = lane & 3;   // column pair of the MMA fragments
     const int H = p.H, G = p.G, T = p.T;
     const int max_tokens = p.max_pages * T;
-    auto stages_of = [&](int L) {
-        if constexpr (WIN) return window_stages(L, max_tokens, TOK, p.window, p.sinks).count;
-        else return seq_stages(L, max_tokens, TOK);
-    };
 
     // ------------------------------------------------ stage prefix over the sequences
     // Thread t owns sequences [t C, t C + C); PS_b = H * sum_{b' < b} stages(b').
@@ -594,7 +520,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
         const int L = len_of(b);
         if (blockIdx.x == 0 && (L < 0 || L > max_tokens))
             flag_status(p.status, NVFP4KV_STATUS_BAD_SEQ_LEN);
-        local += H * stages_of(L);
+        local += H * seq_stages(L, max_tokens, TOK);
     }
     int incl = local;
 #pragma unroll
@@ -618,7 +544,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     if (blockIdx.x == 0) {
         // sequences without stages (length 0 or invalid): output 0, LSE -inf
         for (int b = b_lo; b < b_hi; ++b) {
-            if (stages_of(__ldg(p.seq_lens + b)) != 0) continue;
+            if (seq_stages(__ldg(p.seq_lens + b), max_tokens, TOK) != 0) continue;
             uint16_t* ob = p.out + static_cast<int64_t>(b) * p.Hq * D;
             for (int i = 0; i < p.Hq * D; ++i) ob[i] = 0;
             if (p.lse)
@@ -627,26 +553,15 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     }
     // One walk over this thread's sequences finds the sequence holding each of the CTA's run
     // starts and its two span ends (32-bit arithmetic: the host bounds stages + runs below 2^31).
-    int gw0 = blockIdx.x * NW;
-    int n_runs_cta = max(0, min(num_runs - gw0, NW));
-    if constexpr (WIN) {
-        // Few runs are spread over the CTAs (a window leaves few stages: 136 of them, 8 pairs of 1005 tokens, on 9 of the 152 SMs
-        // took 14.2 us, spread over all 10.6): run k is at place k num_runs / R of all warps, and a CTA has the runs at its places.
-        const int R = (total + W - 1) / W;
-        if (R < num_runs) {
-            auto first_at = [&](int place) { return static_cast<int>((static_cast<int64_t>(place) * R + num_runs - 1) / num_runs); };
-            const int end = min(R, first_at(gw0 + n_runs_cta));
-            gw0 = min(R, first_at(gw0));
-            n_runs_cta = max(0, end - gw0);
-        }
-    }
+    const int gw0 = blockIdx.x * NW;
+    const int n_runs_cta = max(0, min(num_runs - gw0, NW));
     const int span_lo = (n_runs_cta > 0 && gw0 < (total + W - 1) / W) ? gw0 * W : total;
     const int span_hi = min(total, (gw0 + n_runs_cta) * W);
     if (local > 0 && span_lo < span_hi && span_lo < excl + local && span_hi > excl) {
         int acc = excl;
         for (int b = b_lo; b < b_hi && acc < span_hi; ++b) {
             const int L = len_of(b);
-            const int S = stages_of(L);
+            const int S = seq_stages(L, max_tokens, TOK);
             const int n = H * S;
             if (n > 0 && acc + n > span_lo) {
                 // runs of this CTA starting in [acc, acc + n): w in [w_a, w_b)
@@ -682,7 +597,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
 
     const int gw = gw0 + warp;
     const int64_t s_begin64 = static_cast<int64_t>(gw) * W;
-    const bool has_run = (WIN ? warp < n_runs_cta : gw < num_runs) && s_begin64 < total;
+    const bool has_run = gw < num_runs && s_begin64 < total;
     const int s_begin = has_run ? static_cast<int>(s_begin64) : 0;
     const int n_st = has_run ? min(total - s_begin, W) : 0;
 
@@ -694,17 +609,14 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     for (int i = 0; i < G_::DCH; ++i) {
         const int j = lane + 32 * i;
         const int pr = j / G_::VCH, cj = j - pr * G_::VCH;
-        if constexpr (F == kFp8) v_dst[i] = G_::V_OFF + v8_swz<D>(pr, cj);
-        else v_dst[i] = G_::V_OFF + pr * D + 16 * (cj ^ (pr & G_::SWZ));
+        v_dst[i] = G_::V_OFF + pr * D + 16 * (cj ^ (pr & G_::SWZ));
     }
-    // K chunk lane + 32 i: at 512 i bytes from the lane's first (rows of FP8 swizzled by their parity, the same for all i)
-    const uint32_t k_dst = F == kFp8 ? G_::K_OFF + k8_swz<D>(lane / G_::VCH, lane % G_::VCH) : G_::K_OFF + 16 * lane;
     const int rho = (r >> 1) | ((r & 1) << 2);  // V rows of this lane: chunk rho of a pair row
 
     // ------------------------------------------------ issue side: the walk over the run
     int ib = has_run ? start_bp[warp][0] : 0;
     int ilen = has_run ? start_bp[warp][2] : 0;
-    int iS = has_run ? stages_of(ilen) : 1;
+    int iS = has_run ? seq_stages(ilen, max_tokens, TOK) : 1;
     int ih = has_run ? (s_begin - start_bp[warp][1]) / iS : 0;
     int ij = has_run ? (s_begin - start_bp[warp][1]) - ih * iS : 0;
     int ips = has_run ? start_bp[warp][1] + ih * iS : 0;  // flat index of stage 0 of (ib, ih)
@@ -751,68 +663,40 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     // issue the next stage of the walk into `slot`, then advance the walk
     auto issue_next = [&](uint32_t slot) {
         const uint64_t kv_pol = l2_policy_evict_first();
-        int t0 = ij * TOK;
-        [[maybe_unused]] int lo = 0;  // tokens of the sequence from `sinks` to lo are hidden by the window
-        if constexpr (WIN) {
-            const WindowStages w = window_stages(ilen, max_tokens, TOK, p.window, p.sinks);
-            lo = w.lo;
-            if (ij >= w.sink) t0 = (ij - w.sink + w.first) * TOK;
-        }
-        // sub-tile u has tokens of the sequence, and not all of them hidden
-        auto seen = [&](int u) {
-            if constexpr (WIN) return t0 + 16 * u < ilen && (t0 + 16 * u + 15 >= lo || t0 + 16 * u < p.sinks);
-            else return 16 * u < min(TOK, ilen - t0);
-        };
+        const int t0 = ij * TOK;
         const int nval = min(TOK, ilen - t0);
         const int64_t head_rows = static_cast<int64_t>(ih) * T;
         int64_t row0[G_::SUB];  // token row of each sub-tile in its pool, -1: not real
-        [[maybe_unused]] int pgs[G_::SUB];
         if (page_aligned) {
             const int pidx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t0), p.t_magic));
             const int pg = page_of(pidx);
             const int64_t r0 = pg * page_rows + head_rows + (t0 - pidx * T);
 #pragma unroll
             for (int u = 0; u < G_::SUB; ++u)
-                row0[u] = (pg >= 0 && seen(u)) ? r0 + 16 * u : -1;
-            if constexpr (F == kFp8) {
-#pragma unroll
-                for (int u = 0; u < G_::SUB; ++u) pgs[u] = pg;
-            }
+                row0[u] = (pg >= 0 && 16 * u < nval) ? r0 + 16 * u : -1;
         } else {
 #pragma unroll
             for (int u = 0; u < G_::SUB; ++u) {
                 const int t = t0 + 16 * u;
                 const int pidx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t), p.t_magic));
-                if constexpr (WIN) {
-                    // (warp-uniform; the page of a hidden sub-tile may have been given back)
-                    const int pg = seen(u) ? page_of(pidx) : -1;
-                    row0[u] = pg >= 0 ? pg * page_rows + head_rows + (t - pidx * T) : -1;
-                    pgs[u] = pg;
-                } else {
-                    const int pg = page_of(min(pidx, max(0, (ilen - 1) / T)));
-                    row0[u] = (pg >= 0 && 16 * u < nval) ? pg * page_rows + head_rows + (t - pidx * T)
-                                                          : -1;
-                }
+                const int pg = page_of(min(pidx, max(0, (ilen - 1) / T)));
+                row0[u] = (pg >= 0 && 16 * u < nval) ? pg * page_rows + head_rows + (t - pidx * T)
+                                                      : -1;
             }
         }
         uint32_t okbits = 0;
 #pragma unroll
         for (int u = 0; u < G_::SUB; ++u) okbits |= (row0[u] >= 0 ? 1u : 0u) << u;
-        uint32_t want = (1u << ((nval + 15) / 16)) - 1u;
-        if constexpr (WIN) {
-            want = 0;
-#pragma unroll
-            for (int u = 0; u < G_::SUB; ++u) want |= (seen(u) ? 1u : 0u) << u;
-        }
+        const uint32_t want = (1u << ((nval + 15) / 16)) - 1u;
         if (okbits != want && lane == 0) flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
         if (page_aligned && okbits == (1u << G_::SUB) - 1) {
             // the whole stage is one run of each pool: offsets are compile-time constants
-            const int64_t doff = row0[0] * G_::ROW + 16 * lane;
+            const int64_t doff = row0[0] * (D / 2) + 16 * lane;
             const uint8_t* ksrc = p.kd + doff;
             const uint8_t* vsrc = p.vd + doff;
             static_for<G_::DCH>([&](auto I) {
                 constexpr int i = decltype(I)::value;
-                cp_async16<512 * i, 512 * i>(slot + k_dst, ksrc, kv_pol);
+                cp_async16<G_::K_OFF + 512 * i, 512 * i>(slot + 16 * lane, ksrc, kv_pol);
                 cp_async16<0, 512 * i>(slot + v_dst[i], vsrc, kv_pol);
             });
             const int64_t soff = row0[0] * G_::NB;
@@ -828,10 +712,10 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < G_::DCH; ++i) {
                 const int u = i / G_::SUB_DIV;
-                const int jj = lane + 32 * i - u * G_::ROW;  // chunk within the sub-tile
+                const int jj = lane + 32 * i - u * (D / 2);  // chunk within the sub-tile
                 const bool ok = row0[u] >= 0;
-                const int64_t off = ok ? row0[u] * G_::ROW + 16 * jj : 0;
-                cp_async16_zfill(slot + k_dst + 512 * i, p.kd + off,
+                const int64_t off = ok ? row0[u] * (D / 2) + 16 * jj : 0;
+                cp_async16_zfill(slot + G_::K_OFF + 16 * (lane + 32 * i), p.kd + off,
                                  ok ? 16u : 0u, kv_pol);
                 cp_async16_zfill(slot + v_dst[i], p.vd + off, ok ? 16u : 0u, kv_pol);
             }
@@ -851,27 +735,13 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
                                  (kpool ? p.ks : p.vs) + off, ok ? 16u : 0u, kv_pol);
             }
         }
-        if constexpr (F == kFp8) {
-            // scales of the sub-tiles' pages: K's from lanes 0 .. SUB-1, V's from the next
-            const int u = lane % G_::SUB;
-            const float* pool = lane < G_::SUB ? p.kbs : p.vbs;
-            int pg = pgs[0];
-#pragma unroll
-            for (int uu = 1; uu < G_::SUB; ++uu)
-                if (u == uu) pg = pgs[uu];
-            if (lane < 2 * G_::SUB && pool && ((okbits >> u) & 1u))
-                cp_async4(slot + G_::HDR_OFF + 32 + 4 * lane, pool + static_cast<int64_t>(pg) * H + ih);
-        }
         const bool last = (ij == iS - 1) || (issued == n_st - 1);
         const uint32_t flags = (ifirst ? kFirst : 0u) | (last ? kLast : 0u);
         if (lane == 0) {
             sts_v4(slot + G_::HDR_OFF, okbits | (static_cast<uint32_t>(nval) << 8), flags,
                    static_cast<uint32_t>(ib), static_cast<uint32_t>(ih));
-            uint32_t hide = 0u;  // the stage's tokens from the low half on to the high half are hidden
-            if constexpr (WIN)
-                hide = static_cast<uint32_t>(min(max(p.sinks - t0, 0), TOK)) | (static_cast<uint32_t>(min(max(lo - t0, 0), TOK)) << 16);
             sts_v4(slot + G_::HDR_OFF + 16, static_cast<uint32_t>(ips), static_cast<uint32_t>(iS),
-                   hide, 0u);
+                   0u, 0u);
         }
         // advance the walk
         ++issued;
@@ -884,11 +754,11 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
                 ih = 0;
                 ++ib;
                 ilen = nlen;
-                iS = stages_of(ilen);
+                iS = seq_stages(ilen, max_tokens, TOK);
                 while (iS == 0) {  // sequences without stages are not in the list
                     ++ib;
                     ilen = __ldg(p.seq_lens + ib);
-                    iS = stages_of(ilen);
+                    iS = seq_stages(ilen, max_tokens, TOK);
                 }
                 nlen = (ib + 1 < p.B) ? __ldg(p.seq_lens + ib + 1) : 0;
             }
@@ -910,7 +780,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     float cs0 = 0.0f, cs1 = 0.0f;
     float o[G_::KSTEPS][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-    const float gvs = F == kFp8 ? scalar_or_1(p.gv) : __ldg(p.gv);
+    const float gvs = __ldg(p.gv);
 
 #pragma unroll 1
     for (int i = 0; i < n_st; ++i) {
@@ -972,8 +842,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
                 qf[kk][0] = pack_f16x2(qv[4 * kk] * up, qv[4 * kk + 1] * up);
                 qf[kk][1] = pack_f16x2(qv[4 * kk + 2] * up, qv[4 * kk + 3] * up);
             }
-            const float gk = F == kFp8 ? scalar_or_1(p.gk) : __ldg(p.gk);
-            const float cs_row = (r < G) ? p.sm_scale * gk * kLog2e * ldexpf(1.0f, -kq)
+            const float cs_row = (r < G) ? p.sm_scale * __ldg(p.gk) * kLog2e * ldexpf(1.0f, -kq)
                                          : 0.0f;
             // score scale of this lane's two S^T columns (query heads 2c, 2c+1)
             cs0 = __shfl_sync(0xFFFFFFFFu, cs_row, 8 * c);
@@ -987,40 +856,13 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
         }
 
         if (okbits != 0u) {
-            bool full = (okbits == (1u << G_::SUB) - 1) && nval >= TOK;
-            uint32_t hide0 = 0u, hide1 = 0u;
-            if constexpr (WIN) {
-                uint32_t h[1];
-                lds_words(h, st + G_::HDR_OFF + 24);
-                hide0 = h[0] & 0xFFFFu;
-                hide1 = h[0] >> 16;
-                full = full && hide0 >= hide1;
-            }
+            const bool full = (okbits == (1u << G_::SUB) - 1) && nval >= TOK;
             // valid-token bits of each sub-tile (only read when !full)
             uint32_t tmask[G_::SUB];
 #pragma unroll
             for (int u = 0; u < G_::SUB; ++u) {
                 const int nv = min(16, max(0, nval - 16 * u));
                 tmask[u] = ((okbits >> u) & 1u) ? ((nv >= 16) ? 0xFFFFu : ((1u << nv) - 1u)) : 0u;
-                if constexpr (WIN) {
-                    const int a = min(16, max(0, static_cast<int>(hide0) - 16 * u)), b = min(16, max(0, static_cast<int>(hide1) - 16 * u));
-                    if (a < b) tmask[u] &= ~(((1u << b) - 1u) & ~((1u << a) - 1u));
-                }
-            }
-            // FP8 pages: with the page's scales s_K, s_V, a score x s_K + log2(s_V) (log2 units) makes the weight
-            // p s_V, which is what the sum over V needs; the sum of the weights takes it times 1 / s_V
-            [[maybe_unused]] float ksc[G_::SUB], vlog[G_::SUB], vinv[G_::SUB];
-            if constexpr (F == kFp8) {
-                uint32_t w[4];
-                lds_words(w, st + G_::HDR_OFF + 32);
-#pragma unroll
-                for (int u = 0; u < G_::SUB; ++u) {
-                    const bool ok = (okbits >> u) & 1u;
-                    ksc[u] = ok && p.kbs ? __uint_as_float(w[u]) : 1.0f;
-                    const float s = ok && p.vbs ? __uint_as_float(w[G_::SUB + u]) : 1.0f;
-                    vlog[u] = lg2_approx(s);
-                    vinv[u] = __fdividef(1.0f, s);
-                }
             }
 
             // ---- S^T = K^ Q^T for the SUB sub-tiles
@@ -1029,62 +871,41 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
             for (int u = 0; u < G_::SUB; ++u) {
                 const int row0 = 16 * u + r;
                 const int row1 = row0 + 8;
+                uint32_t kw0[G_::CW], kw1[G_::CW];
+                lds_words(kw0, st + G_::K_OFF + row0 * (D / 2) + c * G_::CHUNK);
+                lds_words(kw1, st + G_::K_OFF + row1 * (D / 2) + c * G_::CHUNK);
+                // FP16 (s, s) of the lane's D/64 blocks in rows row0 / row1: the scale byte
+                // is duplicated by an integer multiply, then converted as an E4M3 pair
+                uint32_t ks0[D / 64], ks1[D / 64];
+#pragma unroll
+                for (int q = 0; q < D / 64; ++q) {
+                    ks0[q] = e4m3x2_to_f16x2(
+                        lds_u8(st + G_::KS_OFF + row0 * G_::NB + c * (D / 64) + q) * 0x0101u);
+                    ks1[q] = e4m3x2_to_f16x2(
+                        lds_u8(st + G_::KS_OFF + row1 * G_::NB + c * (D / 64) + q) * 0x0101u);
+                }
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if constexpr (F == kFp8) {
 #pragma unroll
-                    for (int k = 0; k < D / 64; ++k) {
-                        uint32_t w0[4], w1[4];
-                        lds_words(w0, st + G_::K_OFF + k8_swz<D>(row0, c * (D / 64) + k));
-                        lds_words(w1, st + G_::K_OFF + k8_swz<D>(row1, c * (D / 64) + k));
+                for (int q = 0; q < G_::CW; ++q) {
+                    uint32_t c0[4], c1[4];
+                    e2m1x8_to_f16x2x4(kw0[q], c0);
+                    e2m1x8_to_f16x2x4(kw1[q], c1);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t c0[2], c1[2];
-                            e4m3x4_to_f16x2x2(w0[q], c0);
-                            e4m3x4_to_f16x2x2(w1[q], c1);
-                            const uint32_t a[4] = {c0[0], c1[0], c0[1], c1[1]};
-                            mma_f16_16816(acc, a, qf[4 * k + q][0], qf[4 * k + q][1]);
-                        }
-                    }
-                } else {
-                    uint32_t kw0[G_::CW], kw1[G_::CW];
-                    lds_words(kw0, st + G_::K_OFF + row0 * (D / 2) + c * G_::CHUNK);
-                    lds_words(kw1, st + G_::K_OFF + row1 * (D / 2) + c * G_::CHUNK);
-                    // FP16 (s, s) of the lane's D/64 blocks in rows row0 / row1: the scale byte
-                    // is duplicated by an integer multiply, then converted as an E4M3 pair
-                    uint32_t ks0[D / 64], ks1[D / 64];
-#pragma unroll
-                    for (int q = 0; q < D / 64; ++q) {
-                        ks0[q] = e4m3x2_to_f16x2(
-                            lds_u8(st + G_::KS_OFF + row0 * G_::NB + c * (D / 64) + q) * 0x0101u);
-                        ks1[q] = e4m3x2_to_f16x2(
-                            lds_u8(st + G_::KS_OFF + row1 * G_::NB + c * (D / 64) + q) * 0x0101u);
-                    }
-#pragma unroll
-                    for (int q = 0; q < G_::CW; ++q) {
-                        uint32_t c0[4], c1[4];
-                        e2m1x8_to_f16x2x4(kw0[q], c0);
-                        e2m1x8_to_f16x2x4(kw1[q], c1);
-#pragma unroll
-                        for (int hk = 0; hk < 2; ++hk) {
-                            const int kk = 2 * q + hk;  // k-step: bytes 2kk, 2kk+1 of the chunk
-                            const int blk = kk / 4;     // block of the lane's chunk
-                            uint32_t a[4];
-                            a[0] = h2_mul(c0[2 * hk], ks0[blk]);
-                            a[1] = h2_mul(c1[2 * hk], ks1[blk]);
-                            a[2] = h2_mul(c0[2 * hk + 1], ks0[blk]);
-                            a[3] = h2_mul(c1[2 * hk + 1], ks1[blk]);
-                            mma_f16_16816(acc, a, qf[kk][0], qf[kk][1]);
-                        }
+                    for (int hk = 0; hk < 2; ++hk) {
+                        const int kk = 2 * q + hk;  // k-step: bytes 2kk, 2kk+1 of the chunk
+                        const int blk = kk / 4;     // block of the lane's chunk
+                        uint32_t a[4];
+                        a[0] = h2_mul(c0[2 * hk], ks0[blk]);
+                        a[1] = h2_mul(c1[2 * hk], ks1[blk]);
+                        a[2] = h2_mul(c0[2 * hk + 1], ks0[blk]);
+                        a[3] = h2_mul(c1[2 * hk + 1], ks1[blk]);
+                        mma_f16_16816(acc, a, qf[kk][0], qf[kk][1]);
                     }
                 }
                 x[u][0] = acc[0] * cs0;
                 x[u][1] = acc[1] * cs1;
                 x[u][2] = acc[2] * cs0;
                 x[u][3] = acc[3] * cs1;
-                if constexpr (F == kFp8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[u][k] = fmaf(x[u][k], ksc[u], vlog[u]);
-                }
             }
 
             // ---- online softmax over the stage, columns = query heads 2c, 2c+1
@@ -1124,13 +945,8 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
             for (int u = 0; u < G_::SUB; ++u) {
                 const float p0 = ex2_approx(x[u][0] - m0), p1 = ex2_approx(x[u][1] - m1);
                 const float p2 = ex2_approx(x[u][2] - m0), p3 = ex2_approx(x[u][3] - m1);
-                if constexpr (F == kFp8) {
-                    l0 = fmaf(p0 + p2, vinv[u], l0);
-                    l1 = fmaf(p1 + p3, vinv[u], l1);
-                } else {
-                    l0 += p0 + p2;
-                    l1 += p1 + p3;
-                }
+                l0 += p0 + p2;
+                l1 += p1 + p3;
                 // P^T (tokens x heads) -> B operand (k = tokens, n = heads), rounded to FP16: 11 bits
                 // where the output has 8, and FP16 is what V is exact in; the sum takes p as it is
                 pb[u][0] = movmatrix_trans(pack_f16x2(p0, p1));
@@ -1140,38 +956,6 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
             // ---- O^T += V^^T P^T. Lane pairs: pr0 (tokens 2c, 2c+1), pr1 (tokens 2c+8, 2c+9)
 #pragma unroll
             for (int u = 0; u < G_::SUB; ++u) {
-                if constexpr (F == kFp8) {
-                    // the lane's chunk of tokens 2c, 2c + 1, 2c + 8, 2c + 9; pairs of tokens are made byte by byte
-                    constexpr int VW = D / 32;
-                    uint32_t vw[4][VW];
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        const int row = 16 * u + 2 * c + (t & 1) + 8 * (t >> 1);
-                        if constexpr (D == 64) {
-                            lds_words(vw[t], st + G_::V_OFF + v8_swz<D>(row, rho >> 1) + 8 * (rho & 1));
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < D / 128; ++k)
-                                lds_words(*reinterpret_cast<uint32_t(*)[4]>(vw[t] + 4 * k), st + G_::V_OFF + v8_swz<D>(row, rho * (D / 128) + k));
-                        }
-                        // a hidden token's V may be anything, and 0 times it need not be 0
-                        if (!full && !((tmask[u] >> (row - 16 * u)) & 1u))
-#pragma unroll
-                            for (int k = 0; k < VW; ++k) vw[t][k] = 0u;
-                    }
-#pragma unroll
-                    for (int q = 0; q < VW; ++q) {
-#pragma unroll
-                        for (int hm2 = 0; hm2 < 2; ++hm2) {
-                            uint32_t lo2[2], hi2[2];
-                            e4m3x4_to_f16x2x2(__byte_perm(vw[0][q], vw[1][q], hm2 ? 0x7362 : 0x5140), lo2);
-                            e4m3x4_to_f16x2x2(__byte_perm(vw[2][q], vw[3][q], hm2 ? 0x7362 : 0x5140), hi2);
-                            const uint32_t a[4] = {lo2[0], lo2[1], hi2[0], hi2[1]};
-                            mma_f16_16816(o[2 * q + hm2], a, pb[u][0], pb[u][1]);
-                        }
-                    }
-                    continue;
-                }
                 const int pr0 = 8 * u + c, pr1 = pr0 + 4;
                 // the lane's chunk covers head dims rho*D/8 .. +D/8-1: blocks (rho*D/8)/16 ...
                 constexpr int kBlkPerChunk = (D / 8 + 15) / 16;
@@ -1302,9 +1086,9 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
     __syncthreads();  // every warp's run is done: the rings are free for the merge
     const int n_pend = pend_n;
     for (int k = 0; k < n_pend;) {
-        const int m = merge_batch<D, F>(p, pend, k, n_pend, smem);
+        const int m = merge_batch<D>(p, pend, k, n_pend, smem);
         if (m == 0) {  // a pair whose records do not fit at once: by chunks
-            merge_pair<D, F>(p, pend[k][0], pend[k][1], pend[k][2], pend[k][3], smem);
+            merge_pair<D>(p, pend[k][0], pend[k][1], pend[k][2], pend[k][3], smem);
             ++k;
         }
         k += m;
@@ -1316,7 +1100,7 @@ __global__ void __launch_bounds__(Geo<D, F>::THREADS, 1)
 // ------------------------------------------------------------------------------------------
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-int stage_tokens(int D, int format = kNvfp4) { return (D == 256 ? 32 : 64) >> format; }
+int stage_tokens(int D) { return D == 256 ? 32 : 64; }
 int warps_per_cta(int D) { return D == 64 ? 16 : (D == 128 ? 12 : 8); }
 
 // Warp runs of the split kernel: one per warp of one CTA per SM (automatic), or n runs per
@@ -1354,23 +1138,25 @@ bool decode_shape_ok(const nvfp4kv_layout* l, int Hq) {
 }
 
 // The flat stage list, the token positions and the records index with 32-bit integers.
-bool decode_size_ok(int batch, int H, int D, int max_pages, int T, int64_t runs, int format = kNvfp4) {
+bool stage_list_ok(int batch, int H, int64_t tok, int max_pages, int T, int64_t runs) {
     const int64_t max_tokens = static_cast<int64_t>(max_pages) * T;
-    const int64_t tok = stage_tokens(D, format);
     const int64_t stages = (max_tokens + tok - 1) / tok * batch * H;
     const int64_t lim = (int64_t{1} << 31) - 1;
     return max_tokens < lim - tok && stages + runs < lim &&
            runs + static_cast<int64_t>(batch) * H < lim;
 }
+bool decode_size_ok(int batch, int H, int D, int max_pages, int T, int64_t runs) {
+    return stage_list_ok(batch, H, stage_tokens(D), max_pages, T, runs);
+}
 
-template <int D, int F = kNvfp4, bool WIN = false>
-cudaError_t launch_decode(const typename ParamsOf<WIN>::type& p, int64_t runs, cudaStream_t s) {
-    using G_ = Geo<D, F>;
-    const cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D, F, WIN>,
+template <int D>
+cudaError_t launch_decode(const DecodeParams& p, int64_t runs, cudaStream_t s) {
+    using G_ = Geo<D>;
+    const cudaError_t e = cudaFuncSetAttribute(decode_split_kernel<D>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
-    return launch_pdl(decode_split_kernel<D, F, WIN>, static_cast<unsigned>(ctas), G_::THREADS,
+    return launch_pdl(decode_split_kernel<D>, static_cast<unsigned>(ctas), G_::THREADS,
                       static_cast<size_t>(G_::SMEM), s, p);
 }
 

@@ -1,9 +1,9 @@
 // C entry point of the paged decode attention over FP8 pages (a scale for each page and head), with or without a sliding
-// window: the NVFP4 decode's kernel (decode_kernel.cuh) with another cache format.
+// window; the kernel is in window_kernel.cuh.
 #include <cstdint>
 #include <cuda_runtime.h>
 
-#include "decode_kernel.cuh"
+#include "window_kernel.cuh"
 
 using namespace nvfp4kv;
 
@@ -31,7 +31,7 @@ extern "C" nvfp4kv_status nvfp4_paged_fp8_decode_attention(
     if (batch > 65535 || num_q_heads > 65535) return NVFP4KV_ERR_UNSUPPORTED;
     const int D = layout->head_dim, H = layout->num_kv_heads, T = layout->page_size;
     const int64_t runs = decode_runs(batch, H, D, 0);
-    if (!decode_size_ok(batch, H, D, max_pages_per_seq, T, runs, kFp8)) return NVFP4KV_ERR_UNSUPPORTED;
+    if (!window_size_ok(batch, H, D, max_pages_per_seq, T, runs, kFp8)) return NVFP4KV_ERR_UNSUPPORTED;
     const WsLayout wl = ws_layout(batch, H, num_q_heads, D, runs);
     if (!workspace || workspace_bytes < wl.total || !aligned16(workspace)) return NVFP4KV_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -68,8 +68,8 @@ extern "C" nvfp4kv_status nvfp4_paged_fp8_decode_attention(
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (D) {
-    case 64: return launched(launch_decode<64, kFp8, true>(p, runs, s));
-    case 128: return launched(launch_decode<128, kFp8, true>(p, runs, s));
-    default: return launched(launch_decode<256, kFp8, true>(p, runs, s));
+    case 64: return launched(launch_window<64, kFp8>(p, runs, s));
+    case 128: return launched(launch_window<128, kFp8>(p, runs, s));
+    default: return launched(launch_window<256, kFp8>(p, runs, s));
     }
 }
