@@ -58,8 +58,9 @@
  *     holding a larger tag (garbage) by a compare-and-swap loop bounded at 256 rounds; if that
  *     loop runs out (other CTAs kept changing the word), the count it served never completes,
  *     so the affected (sequence, KV head) pair of a decode call keeps its previous output and
- *     LSE, and a global-scale call may leave g unwritten or too small. No kernel spins on a flag
- *     or a barrier; the decode's asynchronous copies complete without polling.
+ *     LSE, and a global-scale call may leave g unwritten or too small. No kernel waits for another
+ *     block's flag; the decode's asynchronous copies complete without polling, and the extend
+ *     attention's warps wait for one another, inside a block, on barriers whose waits are bounded.
  *   - `stream` must belong to the current device (or be 0), and every pointer must be memory
  *     that device can address: grids are sized for the current device.
  *   - Buffers must be 16-byte aligned; sources and destinations must not overlap.
