@@ -525,7 +525,7 @@ nvfp4kv_status nvfp4_paged_sparse_decode_attention(
  *                  free_count outside 0 .. free_capacity, which is taken as the nearer of the two
  * A length or addition out of range (p < 0, a < -1, p + a > max_pages_per_seq * T) or rows past num_rows
  * set BAD_SEQ_LEN: the sequence is not served (a bad p counts as 0). Only page_size of the layout is read.
- * Supported: batch <= 8192.
+ * Supported: batch <= 8192. With batch = 0 nothing is written, the padding of slots neither.
  * ------------------------------------------------------------------------------------------ */
 nvfp4kv_status nvfp4_kv_step_tables(
     const nvfp4kv_layout* layout, int32_t batch, const int32_t* past_lens, const int32_t* new_lens,
@@ -620,10 +620,10 @@ nvfp4kv_status nvfp4_paged_fp8_decode_attention(
  *   workspace      device scratch of nvfp4_paged_extend_attention_workspace_size(...) bytes; needs no clearing,
  *                  and calls that can overlap on the GPU must not share it
  * Numerics as in nvfp4_paged_decode_attention: queries and weights in FP16, K and V exact, the rest in FP32.
- * Rows outside 0 .. num_rows, a length outside [0, max_pages_per_seq * T] and more rows than tokens set BAD_SEQ_LEN:
- * the sequence's rows, where they lie in range, get out = 0 and lse = -inf. A page id outside the pool sets PAGE_OOB and its
- * tokens are left out; a row that sees no token gets the same. TIMEOUT: a wait inside the kernel gave up (a defect;
- * the outputs are incomplete).
+ * BAD_SEQ_LEN: rows that do not lie in 0 .. num_rows (nothing is written for the sequence), a length outside
+ * [0, max_pages_per_seq * T] or more rows than tokens (its rows get out = 0 and lse = -inf). A page id outside the pool sets
+ * PAGE_OOB and its tokens are left out; a row that sees no token gets out = 0 and lse = -inf. TIMEOUT: a wait inside the kernel
+ * gave up (a defect; the outputs are incomplete).
  * Two launches. Supported: head_dim 64, 128 or 256; 1 <= num_q_heads / num_kv_heads <= 8; page_size % 16 == 0;
  * batch <= 65535; pool_pages * num_kv_heads * page_size < 2^32.
  * ------------------------------------------------------------------------------------------ */

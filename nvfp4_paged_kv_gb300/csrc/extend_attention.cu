@@ -159,7 +159,6 @@ __device__ __forceinline__ Unit unit_of(const ExtendParams& p, const Seq& s, int
 template <int D>
 __device__ __forceinline__ int blocks_of(const ExtendParams& p, int n) {
     const int each = Shape<D>::MT * p.per;
-    if (each == 1) return n;
     int q = static_cast<int>(__umulhi(static_cast<unsigned>(n), p.unit_magic));
     q -= static_cast<int64_t>(q) * each > n;
     return q + (q * each != n);

@@ -8,9 +8,9 @@
 //
 // Bound: HBM, 3 bytes a value from 16 bits and 1.5625 from NVFP4. The maximum stands between the loads and the stores of a run,
 // so a CTA alternates between the two; the CTAs of an SM (8 of 128 threads at 64 x 128) keep both under way. 4096 BF16 pages of
-// 64 tokens, 8 heads, 128 dims (805 MB): 131 us, 6.1 TB/s, 0.90 of the copy rate. 1024 NVFP4 pages (105 MB): 26.7 us, 3.9 TB/s,
-// 0.58: 3 of it launch and the first loads, the rest 6.8 instructions a value and their waits (10.2 and 29.8 us with every value
-// converted by itself; loading the next run ahead of the stores, 10 registers a thread, gained nothing).
+// 64 tokens, 8 heads, 128 dims (805 MB): 131 us, 6.1 TB/s, 0.90 of the copy rate. 1024 NVFP4 pages (105 MB): 24.9 us, 4.2 TB/s,
+// 0.62: 3 of it launch and the first loads, the rest 6.8 instructions a value and their waits (10.2 and 28 us with every value
+// converted by itself; CTAs that go on to further runs, 26.7, and load the next one ahead of the stores, the same).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -25,7 +25,7 @@ namespace {
 constexpr int kMaxThreads = 512;   // of a CTA: runs of up to 512 x 2 x 32 values are read once
 constexpr int kPairs = NVFP4KV_NVFP4 + 1;  // NVFP4 in NVFP4KV_PACK_TOKEN_PAIRS, as a source of its own
 
-constexpr int kKept = 2;           // steps of 32 values that a thread keeps in registers (packed ones: 1 to 4 took 28.0, 26.7, 26.8, 27.7 us)
+constexpr int kKept = 2;           // steps of 32 values that a thread keeps in registers (of 1 to 4, 2 was the soonest for packed ones, by 0.1 to 1.3 us)
 
 struct Fp8Params {
     const uint8_t* src;
@@ -39,7 +39,6 @@ struct Fp8Params {
     int32_t* status;
     uint64_t row_magic;  // div_magic(D / 16)
     int32_t src_pages, dst_pages, H, T, nb;  // nb = D / 16
-    uint32_t units;
 };
 
 // Step i of a run covers blocks first and second (blocks of 16 values, numbered through the run).
@@ -213,121 +212,118 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
     pdl_enter();
     constexpr bool kPacked = SRC != NVFP4KV_BF16 && SRC != NVFP4KV_FP16;
     constexpr int N = KEPT ? kKept : 1;
-    __shared__ float most[2][kMaxThreads / 32];  // two sets: the next run's maxima do not wait for this one's readers
+    __shared__ float most[kMaxThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const uint32_t blocks = static_cast<uint32_t>(p.T) * p.nb, steps = (blocks + 1) / 2;
     const bool even = blocks % 2 == 0;
     const float g = p.g ? __ldg(p.g) : 1.0f;
-    int set = 0;
-    for (uint32_t u = blockIdx.x; u < p.units; u += gridDim.x) {
-        const uint32_t i = u / static_cast<uint32_t>(p.H);
-        const int h = static_cast<int>(u - i * p.H);
-        const int from = p.src_ids ? __ldg(p.src_ids + i) : static_cast<int>(i);
-        const int to = p.dst_ids ? __ldg(p.dst_ids + i) : static_cast<int>(i);
-        const int tokens = p.tokens ? __ldg(p.tokens + i) : p.T;
-        int32_t bad = 0;
-        if (from < 0 || from >= p.src_pages || to < 0 || to >= p.dst_pages) bad |= NVFP4KV_STATUS_PAGE_OOB;
-        if (tokens < 0 || tokens > p.T) bad |= NVFP4KV_STATUS_BAD_SEQ_LEN;
-        if (bad) {  // the same for every thread of the CTA
-            if (tid == 0 && h == 0 && from != -1 && to != -1) flag_status(p.status, bad);
-            continue;
-        }
-        const uint32_t end = static_cast<uint32_t>(tokens) * p.nb;  // blocks of valid tokens
-        const int64_t run = static_cast<int64_t>(from) * p.H + h, out = static_cast<int64_t>(to) * p.H + h;
-        uint8_t* dst = p.dst + out * blocks * 16;
+    const uint32_t u = blockIdx.x;
+    const uint32_t i = u / static_cast<uint32_t>(p.H);
+    const int h = static_cast<int>(u - i * p.H);
+    const int from = p.src_ids ? __ldg(p.src_ids + i) : static_cast<int>(i);
+    const int to = p.dst_ids ? __ldg(p.dst_ids + i) : static_cast<int>(i);
+    const int tokens = p.tokens ? __ldg(p.tokens + i) : p.T;
+    int32_t bad = 0;
+    if (from < 0 || from >= p.src_pages || to < 0 || to >= p.dst_pages) bad |= NVFP4KV_STATUS_PAGE_OOB;
+    if (tokens < 0 || tokens > p.T) bad |= NVFP4KV_STATUS_BAD_SEQ_LEN;
+    if (bad) {  // the same for every thread of the CTA
+        if (tid == 0 && h == 0 && from != -1 && to != -1) flag_status(p.status, bad);
+        return;
+    }
+    const uint32_t end = static_cast<uint32_t>(tokens) * p.nb;  // blocks of valid tokens
+    const int64_t run = static_cast<int64_t>(from) * p.H + h, out = static_cast<int64_t>(to) * p.H + h;
+    uint8_t* dst = p.dst + out * blocks * 16;
 
-        // a step's values (16 bits) or codes
-        using Held = std::conditional_t<kPacked, Packed, Step>;
-        auto take = [&](Held& v, uint32_t j) {
+    // a step's values (16 bits) or codes
+    using Held = std::conditional_t<kPacked, Packed, Step>;
+    auto take = [&](Held& v, uint32_t j) {
+        uint32_t b0, b1;
+        blocks_of<SRC>(p, j, b0, b1);
+        if constexpr (kPacked)
+            v = load_packed<SRC>(p.src + run * blocks * 8, p.src_scales + run * blocks, j, b0 < end, b1 < end, even);
+        else
+            load_16bit(v, p.src + run * blocks * 32, j, b0 < end, b1 < end);
+    };
+    uint32_t bits = 0u;
+    float a = 0.0f;
+    auto look = [&](const Held& v, uint32_t j) {
+        if constexpr (kPacked) {
             uint32_t b0, b1;
             blocks_of<SRC>(p, j, b0, b1);
-            if constexpr (kPacked)
-                v = load_packed<SRC>(p.src + run * blocks * 8, p.src_scales + run * blocks, j, b0 < end, b1 < end, even);
-            else
-                load_16bit(v, p.src + run * blocks * 32, j, b0 < end, b1 < end);
-        };
-        uint32_t bits = 0u;
-        float a = 0.0f;
-        auto look = [&](const Held& v, uint32_t j) {
-            if constexpr (kPacked) {
-                uint32_t b0, b1;
-                blocks_of<SRC>(p, j, b0, b1);
-                const Codes c = unpack<SRC>(v, b1 < end);
-                a = fmaxf(a, fmaxf(largest(c.c[0], c.c[1], c.scales), largest(c.c[2], c.c[3], c.scales >> 8)));
-            } else {
-                bits = largest(v, bits);
-            }
-        };
-        auto put = [&](const Held& v, uint32_t j, float r) {
-            uint32_t b0, b1;
-            blocks_of<SRC>(p, j, b0, b1);
-            if constexpr (kPacked) {
-                const Codes c = unpack<SRC>(v, b1 < end);
-                store_packed(dst, b0, c.c[0], c.c[1], c.scales, g, r);
-                if (b1 < blocks) store_packed(dst, b1, c.c[2], c.c[3], c.scales >> 8, g, r);
-            } else {
-                store_16bit<SRC>(dst, b0, v.w, r);
-                if (b1 < blocks) store_16bit<SRC>(dst, b1, v.w + 8, r);
-            }
-        };
-        Held held[N];
-        if constexpr (KEPT) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) take(held[k], j);
-            }
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) look(held[k], j);
-            }
+            const Codes c = unpack<SRC>(v, b1 < end);
+            a = fmaxf(a, fmaxf(largest(c.c[0], c.c[1], c.scales), largest(c.c[2], c.c[3], c.scales >> 8)));
         } else {
-            for (uint32_t j = tid; j < steps; j += blockDim.x) {
-                take(held[0], j);
-                look(held[0], j);
-            }
+            bits = largest(v, bits);
         }
-        if constexpr (!kPacked) {
-            bits = max(bits & 0xFFFFu, bits >> 16);
-            a = SRC == NVFP4KV_BF16 ? __uint_as_float(bits << 16) : f16_lo(bits);
-        }
-        a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));  // (a >= 0: floats order as their bits)
-        if (warps > 1) {
-            if (lane == 0) most[set][warp] = a;
-            __syncthreads();
-            for (int w = 0; w < warps; ++w) a = fmaxf(a, most[set][w]);
-            set ^= 1;
-        }
-        if constexpr (kPacked) a = __fmul_rn(a, fabsf(g));  // (the largest of fp32(|v| |g|))
-        float s = __fdiv_rn(a, 448.0f);
-        if (s < 7.8886090522101181e-31f) s = 1.0f;  // 2^-100: all values become 0
-        const float r = __frcp_rn(s);
-        if (tid == 0) p.dst_scales[out] = s;
-        if constexpr (KEPT) {
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const uint32_t j = tid + k * blockDim.x;
-                if (j < steps) put(held[k], j, r);
-            }
+    };
+    auto put = [&](const Held& v, uint32_t j, float r) {
+        uint32_t b0, b1;
+        blocks_of<SRC>(p, j, b0, b1);
+        if constexpr (kPacked) {
+            const Codes c = unpack<SRC>(v, b1 < end);
+            store_packed(dst, b0, c.c[0], c.c[1], c.scales, g, r);
+            if (b1 < blocks) store_packed(dst, b1, c.c[2], c.c[3], c.scales >> 8, g, r);
         } else {
-            for (uint32_t j = tid; j < steps; j += blockDim.x) {
-                take(held[0], j);
-                put(held[0], j, r);
-            }
+            store_16bit<SRC>(dst, b0, v.w, r);
+            if (b1 < blocks) store_16bit<SRC>(dst, b1, v.w + 8, r);
+        }
+    };
+    Held held[N];
+    if constexpr (KEPT) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t j = tid + k * blockDim.x;
+            if (j < steps) take(held[k], j);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t j = tid + k * blockDim.x;
+            if (j < steps) look(held[k], j);
+        }
+    } else {
+        for (uint32_t j = tid; j < steps; j += blockDim.x) {
+            take(held[0], j);
+            look(held[0], j);
+        }
+    }
+    if constexpr (!kPacked) {
+        bits = max(bits & 0xFFFFu, bits >> 16);
+        a = SRC == NVFP4KV_BF16 ? __uint_as_float(bits << 16) : f16_lo(bits);
+    }
+    a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));  // (a >= 0: floats order as their bits)
+    if (warps > 1) {
+        if (lane == 0) most[warp] = a;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) a = fmaxf(a, most[w]);
+    }
+    if constexpr (kPacked) a = __fmul_rn(a, fabsf(g));  // (the largest of fp32(|v| |g|))
+    float s = __fdiv_rn(a, 448.0f);
+    if (s < 7.8886090522101181e-31f) s = 1.0f;  // 2^-100: all values become 0
+    const float r = __frcp_rn(s);
+    if (tid == 0) p.dst_scales[out] = s;
+    if constexpr (KEPT) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t j = tid + k * blockDim.x;
+            if (j < steps) put(held[k], j, r);
+        }
+    } else {
+        for (uint32_t j = tid; j < steps; j += blockDim.x) {
+            take(held[0], j);
+            put(held[0], j, r);
         }
     }
 }
 
 template <int SRC>
-cudaError_t launch_fp8(const Fp8Params& p, cudaStream_t s) {
+cudaError_t launch_fp8(const Fp8Params& p, uint32_t runs, cudaStream_t s) {
     const int64_t steps = (static_cast<int64_t>(p.T) * p.nb + 1) / 2;
     constexpr int N = kKept;
     int threads = 32;
     while (threads < kMaxThreads && static_cast<int64_t>(threads) * N < steps) threads *= 2;
     // a CTA for each run: runs are short, and CTAs that come and go keep an SM full without a tail of its own
-    return static_cast<int64_t>(threads) * N >= steps ? launch_pdl(fp8_pages_kernel<SRC, true>, dim3(p.units), dim3(threads), 0, s, p)
-                                                      : launch_pdl(fp8_pages_kernel<SRC, false>, dim3(p.units), dim3(threads), 0, s, p);
+    return static_cast<int64_t>(threads) * N >= steps ? launch_pdl(fp8_pages_kernel<SRC, true>, dim3(runs), dim3(threads), 0, s, p)
+                                                      : launch_pdl(fp8_pages_kernel<SRC, false>, dim3(runs), dim3(threads), 0, s, p);
 }
 
 }  // namespace
@@ -371,12 +367,12 @@ extern "C" nvfp4kv_status nvfp4_kv_fp8_pages(
     p.H = layout->num_kv_heads;
     p.T = layout->page_size;
     p.nb = nb;
-    p.units = static_cast<uint32_t>(num_pages) * p.H;
+    const uint32_t runs = static_cast<uint32_t>(num_pages) * p.H;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (pairs) return launched(launch_fp8<kPairs>(p, s));
+    if (pairs) return launched(launch_fp8<kPairs>(p, runs, s));
     switch (src_dtype) {
-    case NVFP4KV_BF16: return launched(launch_fp8<NVFP4KV_BF16>(p, s));
-    case NVFP4KV_FP16: return launched(launch_fp8<NVFP4KV_FP16>(p, s));
-    default: return launched(launch_fp8<NVFP4KV_NVFP4>(p, s));
+    case NVFP4KV_BF16: return launched(launch_fp8<NVFP4KV_BF16>(p, runs, s));
+    case NVFP4KV_FP16: return launched(launch_fp8<NVFP4KV_FP16>(p, runs, s));
+    default: return launched(launch_fp8<NVFP4KV_NVFP4>(p, runs, s));
     }
 }
