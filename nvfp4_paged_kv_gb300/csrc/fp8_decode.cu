@@ -67,9 +67,10 @@ extern "C" nvfp4kv_status nvfp4_paged_fp8_decode_attention(
     p.sinks = sink_tokens;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool win = window > 0;
     switch (D) {
-    case 64: return launched(launch_window<64, kFp8>(p, runs, s));
-    case 128: return launched(launch_window<128, kFp8>(p, runs, s));
-    default: return launched(launch_window<256, kFp8>(p, runs, s));
+    case 64: return launched(win ? launch_window<64, kFp8, true>(p, runs, s) : launch_window<64, kFp8, false>(p, runs, s));
+    case 128: return launched(win ? launch_window<128, kFp8, true>(p, runs, s) : launch_window<128, kFp8, false>(p, runs, s));
+    default: return launched(win ? launch_window<256, kFp8, true>(p, runs, s) : launch_window<256, kFp8, false>(p, runs, s));
     }
 }

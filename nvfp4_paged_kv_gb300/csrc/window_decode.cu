@@ -72,8 +72,8 @@ extern "C" nvfp4kv_status nvfp4_paged_window_decode_attention(
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     switch (D) {
-    case 64: return launched(launch_window<64, kNvfp4>(p, runs, s));
-    case 128: return launched(launch_window<128, kNvfp4>(p, runs, s));
-    default: return launched(launch_window<256, kNvfp4>(p, runs, s));
+    case 64: return launched(launch_window<64, kNvfp4, true>(p, runs, s));
+    case 128: return launched(launch_window<128, kNvfp4, true>(p, runs, s));
+    default: return launched(launch_window<256, kNvfp4, true>(p, runs, s));
     }
 }

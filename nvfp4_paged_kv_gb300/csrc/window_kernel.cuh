@@ -7,8 +7,9 @@
 // The window. A sequence of L tokens shows token t if t >= L - window or t < sinks. Its stages are those of the first
 // tokens, then those from the window's first token on; none between is listed, so the work is the visible tokens' and a
 // table entry of a page without a visible token is never read as a page. A token of a stage that is hidden has its score
-// set to -inf and, since 0 times anything need not be 0, its V to 0. FP8 pages without a window take one that no length
-// passes.
+// set to -inf and, since 0 times anything need not be 0, its V to 0. Without a window
+// (FP8 pages alone; WIN = false) what tells hidden tokens is left out: 32 sequences of 8192 tokens 99.5 us, so 101 with a
+// window that no length passes.
 //
 // FP8. An E4M3 value is exact in FP16, so K and V are converted (cvt.rn.f16x2.e4m3x2) and multiplied without scales:
 // the page's K scale multiplies the score in FP32, and the page's V scale s becomes log2(s) added to the score, so that
@@ -121,7 +122,7 @@ __device__ __forceinline__ WindowStages window_stages(int L, int max_tokens, int
     return w;
 }
 
-template <int D, int F>
+template <int D, int F, bool WIN>
 __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(const WindowParams p) {
     pdl_enter();
     using G_ = WGeo<D, F>;
@@ -142,7 +143,8 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
     const int c = lane & 3;   // column pair of the MMA fragments
     const int H = p.H, G = p.G, T = p.T;
     const int max_tokens = p.max_pages * T;
-    auto stages_of = [&](int L) { return window_stages(L, max_tokens, TOK, p.window, p.sinks).count; };
+    const int window = WIN ? p.window : INT32_MAX, sinks = WIN ? p.sinks : 0;
+    auto stages_of = [&](int L) { return window_stages(L, max_tokens, TOK, window, sinks).count; };
 
     // ------------------------------------------------ stage prefix over the sequences
     // Thread t owns sequences [t C, t C + C); PS_b = H * sum_{b' < b} stages(b').
@@ -318,12 +320,12 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
     // issue the next stage of the walk into `slot`, then advance the walk
     auto issue_next = [&](uint32_t slot) {
         const uint64_t kv_pol = l2_policy_evict_first();
-        const WindowStages w = window_stages(ilen, max_tokens, TOK, p.window, p.sinks);
+        const WindowStages w = window_stages(ilen, max_tokens, TOK, window, sinks);
         const int t0 = (ij >= w.sink ? ij - w.sink + w.first : ij) * TOK;
         const int lo = w.lo;  // tokens of the sequence from `sinks` to lo are hidden by the window
         // sub-tile u has tokens of the sequence, and not all of them hidden
         auto seen = [&](int u) {
-            return t0 + 16 * u < ilen && (t0 + 16 * u + 15 >= lo || t0 + 16 * u < p.sinks);
+            return t0 + 16 * u < ilen && (!WIN || t0 + 16 * u + 15 >= lo || t0 + 16 * u < sinks);
         };
         const int nval = min(TOK, ilen - t0);
         const int64_t head_rows = static_cast<int64_t>(ih) * T;
@@ -421,8 +423,9 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
             sts_v4(slot + G_::HDR_OFF, okbits | (static_cast<uint32_t>(nval) << 8), flags,
                    static_cast<uint32_t>(ib), static_cast<uint32_t>(ih));
             // the stage's tokens from the low half on to the high half are hidden
-            const uint32_t hide = static_cast<uint32_t>(min(max(p.sinks - t0, 0), TOK)) |
-                                  (static_cast<uint32_t>(min(max(lo - t0, 0), TOK)) << 16);
+            const uint32_t hide = !WIN ? 0u
+                                       : static_cast<uint32_t>(min(max(sinks - t0, 0), TOK)) |
+                                             (static_cast<uint32_t>(min(max(lo - t0, 0), TOK)) << 16);
             sts_v4(slot + G_::HDR_OFF + 16, static_cast<uint32_t>(ips), static_cast<uint32_t>(iS),
                    hide, 0u);
         }
@@ -540,8 +543,8 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
         }
 
         if (okbits != 0u) {
-            uint32_t hide[1];
-            lds_words(hide, st + G_::HDR_OFF + 24);
+            uint32_t hide[1] = {0u};
+            if constexpr (WIN) lds_words(hide, st + G_::HDR_OFF + 24);
             const int hide0 = hide[0] & 0xFFFFu, hide1 = hide[0] >> 16;
             const bool full = (okbits == (1u << G_::SUB) - 1) && nval >= TOK && hide0 >= hide1;
             // valid-token bits of each sub-tile (only read when !full)
@@ -623,13 +626,17 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
                         }
                     }
                 }
-                x[u][0] = acc[0] * cs0;
-                x[u][1] = acc[1] * cs1;
-                x[u][2] = acc[2] * cs0;
-                x[u][3] = acc[3] * cs1;
                 if constexpr (F == kFp8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[u][k] = fmaf(x[u][k], ksc[u], vlog[u]);
+                    const float c0 = cs0 * ksc[u], c1 = cs1 * ksc[u];
+                    x[u][0] = fmaf(acc[0], c0, vlog[u]);
+                    x[u][1] = fmaf(acc[1], c1, vlog[u]);
+                    x[u][2] = fmaf(acc[2], c0, vlog[u]);
+                    x[u][3] = fmaf(acc[3], c1, vlog[u]);
+                } else {
+                    x[u][0] = acc[0] * cs0;
+                    x[u][1] = acc[1] * cs1;
+                    x[u][2] = acc[2] * cs0;
+                    x[u][3] = acc[3] * cs1;
                 }
             }
 
@@ -862,14 +869,14 @@ bool window_size_ok(int batch, int H, int D, int max_pages, int T, int64_t runs,
     return stage_list_ok(batch, H, stage_tokens(D) >> format, max_pages, T, runs);
 }
 
-template <int D, int F>
+template <int D, int F, bool WIN>
 cudaError_t launch_window(const WindowParams& p, int64_t runs, cudaStream_t s) {
     using G_ = WGeo<D, F>;
-    const cudaError_t e = cudaFuncSetAttribute(window_split_kernel<D, F>,
+    const cudaError_t e = cudaFuncSetAttribute(window_split_kernel<D, F, WIN>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, G_::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t ctas = (runs + G_::WARPS - 1) / G_::WARPS;
-    return launch_pdl(window_split_kernel<D, F>, static_cast<unsigned>(ctas), G_::THREADS,
+    return launch_pdl(window_split_kernel<D, F, WIN>, static_cast<unsigned>(ctas), G_::THREADS,
                       static_cast<size_t>(G_::SMEM), s, p);
 }
 
