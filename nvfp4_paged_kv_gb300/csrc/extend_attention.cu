@@ -25,20 +25,26 @@
 // brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest); P is rounded
 // to FP16 (11 bits, where the output has 8).
 //
-// Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 551 us, 1060 TFLOP/s,
-// 0.55 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 2.0 ms, 1086 TFLOP/s; 24 ragged sequences with a window
-// at head_dim 64 (15.6 GFLOP): 69 us.
-// Bound, at head_dim 128: the tensor core is busy for 3/4 of the time, with products at less than its rate. A 128 x 64 x 16 product
-// with both operands in shared memory takes 72 clocks, hardly more than a 128 x 128 x 16 one (64): its 128 rows of Q have to
-// be read either way. Scores of 128 tokens at once leave no room in TMEM (512 columns) for two slots beside two outputs, and then
-// the softmax waits for its scores: 640 to 730 us for the 16 chunks, in three arrangements. The rest is the softmax, whose
-// 2^x alone take 1024 clocks for 256 x 128 scores, of 4500 measured.
+// Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
+// 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
+// window at head_dim 64 (15.6 GFLOP): 58.7 us.
+// Bound, at head_dim 128: the tensor core, busy for nine tenths of the time (in the long case, 3600 clocks for 256 x 128 scores),
+// with products at less than its rate. A 128 x 64 x 16 product with both operands in shared memory takes 72 clocks, hardly more than
+// a 128 x 128 x 16 one (64): its 128 rows of Q have to be read either way. Scores of 128 tokens at once leave no room in TMEM (512
+// columns) for two slots beside two outputs, and then the softmax waits for its scores: 640 to 730 us for the 16 chunks, in
+// three arrangements.
+// Pairs of CTAs (cta_group::2, a row tile in each, half of each KV tile loaded by each, three slots of 128 scores) keep the
+// tensor core busy for 42 % alone: the two softmax warps of a scheduler then share their rows and work in step, maxima while the
+// other's are taken and powers of two while the other's are; 604 us (1.86 ms the long case). The two row tiles of a CTA
+// alternate by themselves.
 // What it took, for the 16 chunks: 975 us with one issuing lane and scores read from TMEM twice; 683 a row's scores in registers, packed
 // FMAs, pool addresses once a tile; 641 in steps of 64 tokens with two slots; 627 the scout, so that the roles' code fits the
 // instruction cache (90 KB of code had warps waiting for instructions 15 % of the time), and products issued by an elected lane
 // (the instruction takes its operands from uniform registers; with a lane that the compiler does not know to be one alone, it
 // fills them in a loop over lanes); 551 a tile's place read from shared memory while its scores come from TMEM, as shared memory
-// is slow beside the tensor core's reads.
+// is slow beside the tensor core's reads; 529 queries in one pass and no divisions in the walk; 521 the next piece's queries
+// before this one's outputs; 509 a tile's barriers waited for at once (the long case 1.69 ms before, 1.98 with cuts moved by up to
+// an eighth of a part).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -56,6 +62,9 @@ constexpr int kMaxGroup = 8;
 constexpr int kRowsM = 128;       // rows of a tile
 constexpr int kStep = 64;         // tokens of a step: scores, weights, product with V
 constexpr int kLoaderWarps = 4;   // for K, and as many for V
+// Tiles that a cut may move to meet a unit's border, and at most an eighth of a part: parts of unequal length against partial results
+// (2, 6, 24 tiles: 16 chunks 516, 515, 509 us, 2048 rows at 65536 tokens 1.60, 1.60, 1.62 ms; an eighth alone, 110 tiles there, 1.98).
+constexpr int kSlack = 24;
 constexpr int kUnitCost = 1;      // of a unit beside its tiles: queries in, outputs out (in tiles)
 // A wait gives up after kTries tries of at most about kTryNs, seconds (a defect: no wait depends on another CTA).
 constexpr uint32_t kTryNs = 2000, kTries = 2000000;
@@ -271,7 +280,7 @@ __device__ __forceinline__ PlanEntry find_unit(const ExtendParams& p, const int6
 // Where CTA c's part begins: c-th of equal parts, on the border of a unit where that is near.
 template <int D>
 __device__ __forceinline__ PlanEntry cut_at(const ExtendParams& p, const int64_t* chunk, int64_t total, int c, int lane) {
-    const int64_t share = (total + p.ctas - 1) / p.ctas, slack = share / 8;
+    const int64_t share = (total + p.ctas - 1) / p.ctas, slack = min(share / 8, static_cast<int64_t>(kSlack));
     int64_t x = min(total, share * c);
     PlanEntry e{};
     e.begin = e.end = x;
@@ -687,11 +696,19 @@ __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh
         }
         __syncwarp();
     };
+    int flags = 0, next = 0;  // of tiles n and n + 1
+    // (Shared memory answers late beside the tensor core's reads, so a tile's barriers are waited for at once, each by lanes of its
+    // own, and the next tile's flags are read meanwhile.)
     auto weighted = [&](uint32_t n, uint32_t part, bool first) {
         const uint32_t stage = n & 1u, slot = slot_of(n, part);
-        if (part == 0) warp_wait(smem_u32(&sh.full[1][stage]), (n >> 1) & 1u, dead);
-        warp_wait(smem_u32(&sh.pfull[x][slot]), phase_of(n), dead);
+        uint32_t bar = smem_u32(&sh.pfull[x][slot]), parity = phase_of(n);
+        if (part == 0) {
+            if (lane == 1) bar = smem_u32(&sh.full[1][stage]), parity = (n >> 1) & 1u;
+            if (lane == 2 && !(flags & kEnd)) bar = smem_u32(&sh.placed[(n + 1) % kRing]), parity = ((n + 1) / kRing) & 1u;
+        }
+        warp_wait(bar, parity, dead);
         tc_after();
+        if (part == 0) next = sh.ring[(n + 1) % kRing].head.x;
         if (elect_one()) {
             const Operand b = operand(vbuf + stage * S_::KB + part * (kStep * 128), S_::TK * 128, 1024);
 #pragma unroll
@@ -702,10 +719,11 @@ __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh
         }
         __syncwarp();
     };
+    warp_wait(smem_u32(&sh.placed[0]), 0, dead);
+    next = sh.ring[0].head.x;
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
-        warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
-        const int flags = uniform(sh.ring[n % kRing].head.x);
+        flags = uniform(next);
         if (flags & kNothing) return;
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {
             // A unit without this row tile: a stage is free as soon as it is full. Its softmax warps are taken along step by
@@ -721,6 +739,10 @@ __device__ __forceinline__ void issue_products(const ExtendParams& p, Shared& sh
             warp_wait(smem_u32(&sh.pfull[x][0]), phase_of(n), dead);
             warp_wait(smem_u32(&sh.pfull[x][1]), phase_of(n), dead);
             if (lane == 0) mbar_arrive(smem_u32(&sh.empty[1][stage]));
+            if (!(flags & kEnd)) {
+                warp_wait(smem_u32(&sh.placed[(n + 1) % kRing]), ((n + 1) / kRing) & 1u, dead);
+                next = sh.ring[(n + 1) % kRing].head.x;
+            }
         } else {
             // A step's scores are issued two steps ahead (one, where a KV tile is one step), behind the product with V of the
             // step whose weights they overwrite.
@@ -755,12 +777,73 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     const float scale = p.sm_scale * scalar_or_1(p.gk);
     const float gv = scalar_or_1(p.gv);
     uint32_t on = 0;  // products with V asked for
-#pragma unroll 1
-    for (uint32_t n = 0;;) {  // a piece; n: its first KV tile
+    // A row's piece: its unit's flags, the row's position, those of the tile's first and last row, its place in q and out, and the
+    // factor of its scores.
+    struct Piece {
+        int flags, pos, first_pos, last_pos, hq;
+        int64_t out_row;
+        float cs;
+        bool real;
+    };
+    // The piece that begins with KV tile n: this thread's row of the queries, to FP16 by a power of two.
+    auto begin_piece = [&](uint32_t n, Piece& u) {
         const Place& begin = sh.ring[n % kRing];
         warp_wait(smem_u32(&sh.placed[n % kRing]), (n / kRing) & 1u, dead);
-        int flags = begin.head.x;
-        if (flags & kNothing) return;
+        u.flags = begin.head.x;
+        if ((u.flags & kNothing) || (S_::MT == 2 && x > 0 && !(u.flags & kTwo))) return;
+        const int4 unit = begin.unit;
+        const int t = unit.x + x * per + tok;  // token of the chunk
+        u.real = tok < per && t < unit.y;
+        u.pos = unit.w + (u.real ? t : unit.y - 1);
+        u.first_pos = unit.w + unit.x + x * per;
+        u.last_pos = unit.w + min(unit.y, unit.x + (x + 1) * per) - 1;
+        u.out_row = unit.z + t;
+        u.hq = begin.h * p.G + head;
+        {
+            // (all of the row in flight at once; at head_dim 256 half of it, read a second time to be stored)
+            const uint16_t* src = p.q + u.out_row * p.q_stride + u.hq * D;
+            constexpr int N = D >= 256 ? 16 : D / 8;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            uint4 v[N];
+            __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 8; c0 += N) {
+#pragma unroll
+                for (int c = 0; c < N; ++c) v[c] = u.real ? ldg16(src + 8 * (c0 + c)) : zero;
+#pragma unroll
+                for (int c = 0; c < N; ++c) {
+                    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
+                }
+            }
+            const float top = fmaxf(__low2float(most), __high2float(most));
+            int kq = top > 0.0f ? 14 - ilogbf(top) : 0;
+            kq = max(-120, min(kq, 120));
+            const float up = copysignf(ldexpf(1.0f, kq), scale);  // a negative scale turns the queries: c is never negative
+            u.cs = fabsf(scale) * kLog2e * ldexpf(1.0f, -kq);
+#pragma unroll 1
+            for (int c0 = D / 8 - N; c0 >= 0; c0 -= N) {
+                if (c0 < D / 8 - N)
+#pragma unroll
+                    for (int c = 0; c < N; ++c) v[c] = u.real ? ldg16(src + 8 * (c0 + c)) : zero;
+#pragma unroll
+                for (int c = 0; c < N; ++c)
+                    sts16(qrow + ((c0 + c) / 8) * (kRowsM * 128) + (((c & 7) ^ (row & 7)) << 4), pack_f16x2(bf16_lo(v[c].x) * up, bf16_hi(v[c].x) * up),
+                          pack_f16x2(bf16_lo(v[c].y) * up, bf16_hi(v[c].y) * up), pack_f16x2(bf16_lo(v[c].z) * up, bf16_hi(v[c].z) * up),
+                          pack_f16x2(bf16_lo(v[c].w) * up, bf16_hi(v[c].w) * up));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[x]));
+        }
+    };
+    Piece u;
+    begin_piece(0, u);
+    if (u.flags & kNothing) return;
+#pragma unroll 1
+    for (uint32_t n = 0;;) {  // a piece; n: its first KV tile
+        int flags = u.flags;
         if (S_::MT == 2 && x > 0 && !(flags & kTwo)) {  // a unit without this row tile
             while (true) {
                 for (int slot = 0; slot < 2; ++slot) {
@@ -773,55 +856,14 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 if (flags & kLast) break;
             }
             if (flags & kEnd) return;
+            begin_piece(n, u);
             continue;
         }
-        // ---- queries: this thread's row, to FP16 by a power of two
-        const int4 unit = begin.unit;
-        const int t = unit.x + x * per + tok;  // token of the chunk
-        const bool real = tok < per && t < unit.y;
-        const int pos = unit.w + (real ? t : unit.y - 1);
-        const int first_pos = unit.w + unit.x + x * per, last_pos = unit.w + min(unit.y, unit.x + (x + 1) * per) - 1;
-        const int64_t out_row = unit.z + t;
-        const int hq = begin.h * p.G + head;
-        float cs, m = -INFINITY, l = 0.0f;
-        {
-            // (all of the row in flight at once; at head_dim 256 half of it, read a second time to be stored)
-            const uint16_t* src = p.q + out_row * p.q_stride + hq * D;
-            constexpr int N = D >= 256 ? 16 : D / 8;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            uint4 v[N];
-            __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
-#pragma unroll 1
-            for (int c0 = 0; c0 < D / 8; c0 += N) {
-#pragma unroll
-                for (int c = 0; c < N; ++c) v[c] = real ? ldg16(src + 8 * (c0 + c)) : zero;
-#pragma unroll
-                for (int c = 0; c < N; ++c) {
-                    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) most = __hmax2(most, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-                }
-            }
-            const float top = fmaxf(__low2float(most), __high2float(most));
-            int kq = top > 0.0f ? 14 - ilogbf(top) : 0;
-            kq = max(-120, min(kq, 120));
-            const float up = copysignf(ldexpf(1.0f, kq), scale);  // a negative scale turns the queries: c is never negative
-            cs = fabsf(scale) * kLog2e * ldexpf(1.0f, -kq);
-#pragma unroll 1
-            for (int c0 = D / 8 - N; c0 >= 0; c0 -= N) {
-                if (c0 < D / 8 - N)
-#pragma unroll
-                    for (int c = 0; c < N; ++c) v[c] = real ? ldg16(src + 8 * (c0 + c)) : zero;
-#pragma unroll
-                for (int c = 0; c < N; ++c)
-                    sts16(qrow + ((c0 + c) / 8) * (kRowsM * 128) + (((c & 7) ^ (row & 7)) << 4), pack_f16x2(bf16_lo(v[c].x) * up, bf16_hi(v[c].x) * up),
-                          pack_f16x2(bf16_lo(v[c].y) * up, bf16_hi(v[c].y) * up), pack_f16x2(bf16_lo(v[c].z) * up, bf16_hi(v[c].z) * up),
-                          pack_f16x2(bf16_lo(v[c].w) * up, bf16_hi(v[c].w) * up));
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[x]));
-        }
+        const bool real = u.real;
+        const int pos = u.pos, first_pos = u.first_pos, last_pos = u.last_pos, hq = u.hq;
+        const int64_t out_row = u.out_row;
+        const float cs = u.cs;
+        float m = -INFINITY, l = 0.0f;
         bool begins = true;
         int t0 = 0;
 #pragma unroll 1
@@ -919,6 +961,8 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
                 if (flags & kLast) break;
             }
         }
+        // the next piece's queries: its first scores come while this one's outputs are written (ragged windows 57.3 us, so 61.2)
+        if (!(flags & kEnd)) begin_piece(n, u);
         // ---- the piece's end: outputs, or a partial result
         warp_wait(smem_u32(&sh.ofull[x]), (on - 1) & 1u, dead);
         tc_after();
