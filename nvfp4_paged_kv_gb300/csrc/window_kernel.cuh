@@ -18,10 +18,12 @@
 // 8 KB of K and V in flight for each warp. V rows of two tokens are paired byte by byte in registers (__byte_perm).
 // Weights go to P V in FP16 (2^-11), as in the dense decode, the sum takes them in FP32.
 //
-// Measured (head_dim 128, 32 heads on 8): FP8, 32 sequences of 8192 tokens (537 MB) 99.9 us, 5.4 TB/s, 0.79 of the copy rate; bound by
-// the bytes in flight (12 warps with two slots of 8 KB fill shared memory; 10 % fewer instructions gave 1.5 %). NVFP4 with a
-// window of 4096 and 4 first tokens, 32 sequences (151 MB) 43.0 us, of which start and join are 15; one sequence of 1005 tokens
-// 10.9 us, all latency. FP8, head_dim 256, 19 ragged sequences with a window of 2048, pages of 16 (100 MB) 34.2 us.
+// Measured (head_dim 128, 32 heads on 8): FP8, 32 sequences of 8192 tokens (537 MB) 99.9 us, 5.4 TB/s, 0.79 of the copy rate.
+// Bound by the latency of a warp's own chain (3 warps a scheduler, an instruction each 7 clocks): 10 % fewer instructions
+// gave 1.5 %, three slots instead of two at head_dim 64 and 256, where they fit, nothing; 12 warps instead of 8 at
+// head_dim 256 took 93 us for 87. NVFP4 with a window of 4096 and 4 first tokens, 32 sequences (151 MB) 43.0 us, of which start
+// and join are 15; one sequence of 1005 tokens 10.9 us, all latency. FP8, head_dim 256, 19 ragged sequences with a window of
+// 2048, pages of 16 (100 MB) 33.8 us.
 //
 #pragma once
 #include <algorithm>
@@ -585,6 +587,10 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
                 const int row1 = row0 + 8;
                 float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if constexpr (F == kFp8) {
+                    // (head_dim 256 has one tile a stage: four sums, as a product waits for the one before into the same, take 86.1 us,
+                    // so 87.4, for 32 sequences of 4096 tokens; with more tiles a stage two sums gained nothing)
+                    constexpr int NS = D == 256 ? 4 : 1;
+                    float part[NS][4] = {};
 #pragma unroll
                     for (int k = 0; k < D / 64; ++k) {
                         uint32_t w0[4], w1[4];
@@ -596,9 +602,13 @@ __global__ void __launch_bounds__(WGeo<D, F>::THREADS, 1) window_split_kernel(co
                             e4m3x4_to_f16x2x2(w0[q], c0);
                             e4m3x4_to_f16x2x2(w1[q], c1);
                             const uint32_t a[4] = {c0[0], c1[0], c0[1], c1[1]};
-                            mma_f16_16816(acc, a, qf[4 * k + q][0], qf[4 * k + q][1]);
+                            mma_f16_16816(part[(4 * k + q) % NS], a, qf[4 * k + q][0], qf[4 * k + q][1]);
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < NS; ++j) acc[i] += part[j][i];
                 } else {
                     uint32_t kw0[G_::CW], kw1[G_::CW];
                     lds_words(kw0, st + G_::K_OFF + row0 * (D / 2) + c * G_::CHUNK);
