@@ -606,7 +606,8 @@ nvfp4kv_status nvfp4_paged_fp8_decode_attention(
  * Attention of an extend step (LMSYS page, "Path 2: Chunked prefill / Extend": the attention that reads the
  * FP8 workspace of cached prefix and chunk): rows row_starts[b] .. row_starts[b + 1] - 1 of q are the last tokens
  * of sequence b, so row i of its n has position seq_lens[b] - n + i, and sees the tokens up to its own, all of
- * them or with a sliding window as above. Sequences of one row (decode) may stand beside others. The pages hold
+ * them or with a sliding window as above. Sequences of one row (decode) may stand beside others; many
+ * of them are served sooner by nvfp4_paged_fp8_decode_attention. The pages hold
  * the chunk's own keys and values too, as nvfp4_kv_extend_step and nvfp4_kv_fp8_pages write them.
  *   num_rows       rows of q, out and lse. Rows from row_starts[batch] on (padding) are left as they were
  *   q              BF16, row n at q + n * q_row_stride elements, [heads][D] contiguous in a row; 16-byte

@@ -27,7 +27,7 @@
 //
 // Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
 // 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
-// window at head_dim 64 (15.6 GFLOP): 58.7 us.
+// window at head_dim 64 (15.6 GFLOP): 57.4 us.
 // Bound, at head_dim 128: the tensor core, busy for nine tenths of the time (in the long case, 3600 clocks for 256 x 128 scores),
 // with products at less than its rate. A 128 x 64 x 16 product with both operands in shared memory takes 72 clocks, hardly more than
 // a 128 x 128 x 16 one (64): its 128 rows of Q have to be read either way. Scores of 128 tokens at once leave no room in TMEM (512
@@ -82,7 +82,7 @@ struct Shape {
     static constexpr int V_OFF = K_OFF + STAGES * KB;
     static constexpr int SMEM = V_OFF + STAGES * KB + 1024;  // the base is rounded up to 1024
     static constexpr int SOFT_WARPS = 4 * MT;
-    static constexpr int WARPS = SOFT_WARPS + 2 * kLoaderWarps + 4;  // (an idle one in the issuers' warpgroup)
+    static constexpr int WARPS = SOFT_WARPS + 2 * kLoaderWarps + 4;  // (the issuers' warpgroup: they, the scout, one that finds the part's end, and an idle one where MT = 1)
     static constexpr int THREADS = WARPS * 32;
     static constexpr int STEPS = TK / kStep;         // of a KV tile
     // TMEM columns: two slots of scores for each row tile, then the outputs
@@ -516,7 +516,8 @@ struct Shared {
     uint64_t full[2][2], empty[2][2];       // [K, V][stage]
     uint64_t qfull[2], ofull[2];             // [row tile]
     uint64_t sfull[2][2], pfull[2][2];       // [row tile][slot]
-    uint64_t drained;
+    uint64_t drained, ended;
+    int64_t part_end;
     int64_t part[Shape<64>::WARPS];  // (as many as any)
     uint64_t placed[kRing];
     Place ring[kRing];
@@ -533,14 +534,10 @@ template <int D>
 __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, const int64_t* chunk, int64_t total, int lane) {
     using S_ = Shape<D>;
     volatile int* dead = &sh.dead;
-    PlanEntry mine{};
-    int64_t part_end = 0;
-#pragma unroll 1
-    for (int i = 1; i >= 0; --i) {
-        mine = cut_at<D>(p, chunk, total, blockIdx.x + i, lane);
-        if (i) part_end = mine.cut;
-        if (lane == 0 && (!i || blockIdx.x == gridDim.x - 1)) p.plan[blockIdx.x + i] = mine;  // (for the join)
-    }
+    const PlanEntry mine = cut_at<D>(p, chunk, total, blockIdx.x, lane);
+    if (lane == 0) p.plan[blockIdx.x] = mine;  // (for the join)
+    warp_wait(smem_u32(&sh.ended), 0, dead);
+    const int64_t part_end = sh.part_end;
     if (mine.cut >= part_end) {  // nothing to do: the others are told by a place without a tile
         if (lane == 0) {
             sh.ring[0].head = make_int4(kNothing, 0, 0, 0);
@@ -596,6 +593,17 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.placed[n % kRing]));
         }
+    }
+}
+
+// Where the CTA's part ends, found by a warp of its own beside the scout (ragged windows 57.4 us, so 58.8).
+template <int D>
+__device__ __forceinline__ void find_end(const ExtendParams& p, Shared& sh, const int64_t* chunk, int64_t total, int lane) {
+    const PlanEntry end = cut_at<D>(p, chunk, total, blockIdx.x + 1, lane);
+    if (lane == 0) {
+        if (blockIdx.x == gridDim.x - 1) p.plan[gridDim.x] = end;
+        sh.part_end = end.cut;
+        mbar_arrive(smem_u32(&sh.ended));
     }
 }
 
@@ -1022,6 +1030,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
         }
         for (uint32_t i = 0; i < kRing; ++i) mbar_init(smem_u32(&sh.placed[i]), 1);
         mbar_init(smem_u32(&sh.drained), S_::MT);
+        mbar_init(smem_u32(&sh.ended), 1);
         sh.dead = sh.never = 0;
         sh.loaded = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1058,6 +1067,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
         warp_wait(smem_u32(&sh.drained), 0, &sh.never);
     } else if (warp == kIssuer + S_::MT) {
         scout_tiles<D>(p, sh, chunk, total, lane);
+    } else if (warp == kIssuer + S_::MT + 1) {
+        find_end<D>(p, sh, chunk, total, lane);
     }
     __syncwarp();
     tc_before();

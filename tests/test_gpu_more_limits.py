@@ -153,3 +153,37 @@ def test_step_tables_of_one_page_of_one_token(kv, cuda):
         want = plain_windows.step_tables(past, new, [4, 5, 6], 3, table, T, 3, 6)
         for name in ("lens", "starts", "slots", "positions", "full", "table", "stack"):
             assert t[name].tolist() == want[name], (T, name)
+
+
+def test_extend_of_many_shapes_on_two_streams(kv, cuda):
+    """Drawn shapes, each four times on two streams with scratch of their own: the same result, nothing flagged, nothing NaN."""
+    import random
+    r = random.Random(7)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(300):
+        D, H, G, T = r.choice((64, 128, 256)), r.randint(1, 8), r.randint(1, 8), r.choice((16, 32, 48, 64, 128))
+        lens = [r.randint(0, int(2 ** r.uniform(0, 11))) for _ in range(r.choice((1, 2, 5, 17, 40)))]
+        new = [r.choice((0, 1, min(n, r.randint(0, 600)))) if n else 0 for n in lens]
+        pages = [-(-n // T) for n in lens]
+        P = sum(pages) + 1
+        if P * H * T * D > 10 ** 8:
+            continue
+        k, v = (torch.randn((P, H, T, D), device=cuda).to(torch.float8_e4m3fn) for _ in range(2))
+        table = torch.full((len(lens), max(1, max(pages))), -1, dtype=torch.int32)
+        ids, at = torch.randperm(P).int(), 0
+        for b, m in enumerate(pages):
+            table[b, :m] = ids[at:at + m]
+            at += m
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+        starts = i32([sum(new[:b]) for b in range(len(new) + 1)])
+        q = torch.randn((max(1, sum(new)), H * G, D), device=cuda).to(torch.bfloat16)
+        args = kv.Layout(H, D, T), q, k, v, table.to(cuda), i32(lens), starts, D ** -0.5
+        more = dict(window=r.choice((0, 0, 1, 100, 1000)), sink_tokens=r.choice((0, 4, 200)), status=status)
+        outs = [torch.zeros_like(q) for _ in range(4)]
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            kv.nvfp4_paged_extend_attention(*args, o, stream=streams[i % 2], **more)
+        torch.cuda.synchronize()
+        assert status.item() == 0 and bool(torch.isfinite(outs[0]).all())
+        assert all(torch.equal(o, outs[0]) for o in outs[1:])
