@@ -785,7 +785,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
     const float scale = p.sm_scale * scalar_or_1(p.gk);
     const float gv = scalar_or_1(p.gv);
     uint32_t on = 0;  // products with V asked for
-    // A row's piece: its unit's flags, the row's position, those of the tile's first and last row, its place in q and out, and the
+    // A row's piece: its unit's flags, the row's position, those of the warp's first and last row, its place in q and out, and the
     // factor of its scores.
     struct Piece {
         int flags, pos, first_pos, last_pos, hq;
@@ -803,8 +803,9 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         const int t = unit.x + x * per + tok;  // token of the chunk
         u.real = tok < per && t < unit.y;
         u.pos = unit.w + (u.real ? t : unit.y - 1);
-        u.first_pos = unit.w + unit.x + x * per;
-        u.last_pos = unit.w + min(unit.y, unit.x + (x + 1) * per) - 1;
+        // (of the warp's rows, not of the tile's: fewer steps are masked, 16 chunks 508 us, so 513)
+        u.first_pos = __reduce_min_sync(0xFFFFFFFFu, u.real ? u.pos : INT32_MAX);
+        u.last_pos = __reduce_max_sync(0xFFFFFFFFu, u.real ? u.pos : -1);
         u.out_row = unit.z + t;
         u.hq = begin.h * p.G + head;
         {
