@@ -27,7 +27,7 @@
 //
 // Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
 // 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
-// window at head_dim 64 (15.6 GFLOP): 57.4 us.
+// window at head_dim 64 (15.6 GFLOP): 56.0 us.
 // Bound, at head_dim 128: the tensor core, busy for nine tenths of the time (in the long case, 3600 clocks for 256 x 128 scores),
 // with products at less than its rate. A 128 x 64 x 16 product with both operands in shared memory takes 72 clocks, hardly more than
 // a 128 x 128 x 16 one (64): its 128 rows of Q have to be read either way. Scores of 128 tokens at once leave no room in TMEM (512
@@ -1083,8 +1083,24 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
 
 // ------------------------------------------------------------------------------------------ the join
 
-// Block (c, y): the unit that CTA c begins and others go on with, rows y, y + gridDim.y, .. of it; and the rows of
-// sequences with lengths out of range.
+// Over N lanes side by side.
+template <int N>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
+}
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// Block (c, y): the unit that CTA c begins and others go on with, rows of it for every 8 gridDim.y warps; and the rows of
+// sequences with lengths out of range. A row's pieces lie side by side in a warp (maxima, sums) and its values are all loaded at
+// once, two rows to a warp at head_dim 64. Bound by latency: 8 blocks for each CTA (with 16 a call of one row took 12.5 us, so 11.3; with 6 a
+// chunk of 100 rows at 3000 tokens, ten pieces a unit, 35.5, so 33.4).
 template <int D>
 __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
     pdl_enter();
@@ -1106,40 +1122,70 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
     const int c = blockIdx.x;
     const PlanEntry next = p.plan[c + 1];
     if (!(next.cut > next.begin && next.cut < next.end) || next.begin < p.plan[c].cut) return;
-    int last = c + 1;  // the last CTA with a piece of the unit
-    while (last + 1 < p.ctas && p.plan[last + 1].cut < next.end) ++last;
+    int pieces = 2;  // of the unit: CTA c's, c + 1's and those of the ones after that begin before its end
+    for (int k = c + 2;; k += 32) {
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, k + lane < p.ctas && p.plan[k + lane].cut < next.end));
+        pieces += n;
+        if (n < 32) break;
+    }
     const Seq s = sequence(p, next.b);
     const Unit u = unit_of<D>(p, s, next.qb);
     const int per = p.per;
     const float gv = scalar_or_1(p.gv);
-    for (int row = blockIdx.y * 8 + warp; row < S_::MT * kRowsM; row += gridDim.y * 8) {
-        const int x = row / kRowsM, r = row - x * kRowsM, tok = r / p.G, head = r - tok * p.G;
+    constexpr int N = D == 64 ? 16 : 32, V = D / N;  // lanes of a row, values of a lane
+    struct alignas(16) Values {
+        float x[V];
+    };
+    const int at = lane % N;
+    for (int row0 = (blockIdx.y * 8 + warp) * (32 / N); row0 < S_::MT * kRowsM; row0 += gridDim.y * 8 * (32 / N)) {
+        const int row = row0 + lane / N, x = row / kRowsM, r = row - x * kRowsM, tok = r / p.G, head = r - tok * p.G;
         const int t = u.t0 + x * per + tok;
-        if (tok >= per || t >= u.t1) continue;
-        auto rec = [&](int k) { return (2 * static_cast<int64_t>(k) + (k == c ? 1 : 0)) * (S_::MT * kRowsM) + row; };
-        float m = -INFINITY;
-        for (int k = c; k <= last; ++k) m = fmaxf(m, p.rec_ml[rec(k)].x);
-        float l = 0.0f, o[D / 32];
+        const bool real = tok < per && t < u.t1;
+        if (!__any_sync(0xFFFFFFFFu, real)) continue;
+        auto rec = [&](int k) { return (2 * static_cast<int64_t>(c + k) + (k == 0 ? 1 : 0)) * (S_::MT * kRowsM) + row; };
+        // running maximum, sum and outputs, over N pieces at a time: a lane has a piece's maximum and sum
+        float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] = 0.0f;
-        for (int k = c; k <= last; ++k) {
-            const float2 ml = p.rec_ml[rec(k)];
-            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - m);
-            l = fmaf(w, ml.y, l);
+        for (int i = 0; i < V; ++i) o[i] = 0.0f;
+        for (int k0 = 0; k0 < pieces; k0 += N) {
+            const int n = min(N, pieces - k0);
+            const float2 ml = real && at < n ? p.rec_ml[rec(k0 + at)] : make_float2(-INFINITY, 0.0f);
+            constexpr int U = 4;
+            Values v[U];
+            auto load = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const float2 v = *reinterpret_cast<const float2*>(p.rec_o + rec(k) * D + 64 * i + 2 * lane);
-                o[2 * i] = fmaf(w, v.x, o[2 * i]);
-                o[2 * i + 1] = fmaf(w, v.y, o[2 * i + 1]);
+                for (int i = 0; i < U; ++i)
+                    if (real && k + i < n) v[i] = *reinterpret_cast<const Values*>(p.rec_o + rec(k0 + k + i) * D + V * at);
+            };
+            load(0);
+            const float mn = fmaxf(m, lanes_max<N>(ml.x)), back = m == -INFINITY ? 0.0f : exp2f(m - mn);
+            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mn);
+            m = mn;
+            l = l * back + lanes_sum<N>(w * ml.y);
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] *= back;
+            for (int k = 0; k < n; k += U) {
+                if (k > 0) load(k);
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const float wk = __shfl_sync(0xFFFFFFFFu, w, k + i, N);
+                    if (real && k + i < n)
+#pragma unroll
+                        for (int e = 0; e < V; ++e) o[e] = fmaf(wk, v[i].x[e], o[e]);
+                }
             }
         }
+        if (!real) continue;
         const float f = l > 0.0f ? gv / l : 0.0f;
         const int64_t out_row = s.first + t;
         const int hq = next.h * p.G + head;
+        uint16_t* dst = p.out + out_row * p.out_stride + hq * D + V * at;
+        uint32_t b[V / 2];
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-            *reinterpret_cast<uint32_t*>(p.out + out_row * p.out_stride + hq * D + 64 * i + 2 * lane) = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
-        if (lane == 0 && p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        for (int i = 0; i < V / 2; ++i) b[i] = pack_bf16x2(o[2 * i] * f, o[2 * i + 1] * f);
+        if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(b[0], b[1]);
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(b[0], b[1], b[2], b[3]);
+        if (at == 0 && p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -1170,7 +1216,7 @@ cudaError_t launch_extend(const ExtendParams& p, cudaStream_t s) {
     using S_ = Shape<D>;
     cudaError_t e = cudaFuncSetAttribute(extend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_::SMEM);
     if (e == cudaSuccess) e = launch_pdl(extend_kernel<D>, dim3(p.ctas), dim3(S_::THREADS), S_::SMEM, s, p);
-    if (e == cudaSuccess) e = launch_pdl(join_kernel<D>, dim3(p.ctas, 16), dim3(256), 0, s, p);
+    if (e == cudaSuccess) e = launch_pdl(join_kernel<D>, dim3(p.ctas, 8), dim3(256), 0, s, p);
     return e;
 }
 
