@@ -507,7 +507,8 @@ nvfp4kv_status nvfp4_paged_sparse_decode_attention(
  * of the table it needs n = ceil((p + a) / T) - ceil(p / T) more. free_pages is a stack of page ids,
  * the first free_count of them free.
  *   1. The pages of the sequences that ended are pushed on it, in the order of the sequences and of
- *      their tables (the table rows are left as they are).
+ *      their tables (the table rows are left as they are). An entry below 0 is no page: a sequence whose layer has a
+ *      sliding window may have given pages back before, and whoever puts them on the stack sets their entries to -1.
  *   2. Pages are popped from its top, in the order of the sequences, into their tables from entry
  *      ceil(p / T) on. A sequence that needs pages is served when its needs and those of all sequences
  *      before it fit into the pages that are left; if not (NO_PAGES) it gets none and keeps its length.
@@ -515,12 +516,13 @@ nvfp4kv_status nvfp4_paged_sparse_decode_attention(
  *   row_starts     int32 [batch + 1]: the first of the step's rows of each sequence (max(a, 0) each, served
  *                  or not), and their number
  *   slots          int64 [num_rows]: page * T + token of each row, as nvfp4_kv_append takes them; -1 for the
- *                  rows of a sequence that is not served and for those behind the last (padding)
+ *                  rows of a sequence that is not served, for those behind the last (padding), and for those whose
+ *                  page id is below 0 (PAGE_OOB)
  *   positions      int32 [num_rows]: p, p + 1, ..; 0 where the slot is -1
  *   full_pages     optional int32 [full_capacity >= batch + num_rows / T]: ids of the pages that became
  *                  full, in order, then -1: the page_ids of nvfp4_kv_page_bounds
  *   free_left      int32: free pages after the call (may be free_count)
- *   free_capacity  entries of free_pages; page ids on it and in the tables are passed on unchecked, and
+ *   free_capacity  entries of free_pages; page ids on it and in the tables are otherwise passed on unchecked, and
  *                  a page must be in one place only. Pages given back past it are lost (PAGE_OOB), as is a
  *                  free_count outside 0 .. free_capacity, which is taken as the nearer of the two
  * A length or addition out of range (p < 0, a < -1, p + a > max_pages_per_seq * T) or rows past num_rows

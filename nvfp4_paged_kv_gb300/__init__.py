@@ -789,7 +789,8 @@ def nvfp4_kv_step_tables(layout: Layout, past_lens: torch.Tensor, new_lens: torc
                          full_pages=None, status=None, stream=None):
     """Page tables and token slots of a step from the lengths of its requests: `past_lens` (tokens cached) and `new_lens`
     (to add; -1: ended) int32 [B]. `free_pages` int32 is a stack of page ids with `free_count` (int32, one value) of them
-    free; pages of sequences that ended are pushed on it, new ones popped into `page_table` [B, max pages] int32. Writes
+    free; pages of sequences that ended are pushed on it (entries below 0 are none: given back before), new ones popped into
+    `page_table` [B, max pages] int32. Writes
     `seq_lens` [B] (may be past_lens), `row_starts` [B + 1] int32, `slots` int64 and `positions` int32 of the step's rows
     (-1 and 0: no row), `free_left` (None: free_count) and optionally `full_pages` int32, the pages that became full,
     then -1, of B + rows // page_size entries or more."""

@@ -11,9 +11,13 @@
 // pushed from it on, and table entries are read below ceil(p_b / T) and written from it on. In place the CTAs are one cluster (up
 // to 8), with its barrier between the last read of those and the first write; otherwise there are as many as the outputs ask for.
 //
-// Bound: latency. A step of 256 requests, 13 of which ended with 1024 pages each, is two dependent round trips to memory, two
-// block-wide sums and the launch: 9.6 us in a graph (16.8 with one CTA, 64-bit sums and an output at a time); 16 chunks of 512
-// rows 7.5 us, 700 ragged requests in place, on a cluster of 8, 15.0 us.
+// A sequence that ended may have given pages back before (a sliding window leaves its first pages and its last): entries
+// below 0. How many of its entries are pages is counted first; where none is missing the k-th page is the k-th entry, otherwise it
+// is looked for from the nearer end of the row, which finds a window's pages at once.
+//
+// Bound: latency. A step of 256 requests, 13 of which ended with 1024 pages each, is three dependent round trips to memory, two
+// block-wide sums and the launch: 11.1 us, call after call; 16 chunks of 512 rows 11.9 us (the launch's cost), 700 ragged requests, 70 of
+// them ended, 18 us. (With one CTA, 64-bit sums and an output at a time the first took 7 us more.)
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -110,7 +114,7 @@ __device__ __forceinline__ void owners(const int* first, int B, int half, const 
 __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesParams p) {
     pdl_enter();
     extern __shared__ __align__(16) int smem[];
-    __shared__ int part[3][kWarps];
+    __shared__ int part[3][kWarps], n_ended;
     const int B = p.B, T = p.T;
     // of each sequence: its first row, its first page popped, given back and becoming full, its tokens cached and to
     // add (kUnserved: it keeps what it has), and its full pages
@@ -150,13 +154,58 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
 
     // ------------------------------------------------ rows, pages to pop, pages given back
     const int given_count = *p.count;
+    if (tid == 0) n_ended = 0;
     int at[3] = {0, 0, 0}, total[3];
     Seq kept{};
+    bool ends = false;
     for (int b = b_lo; b < b_hi; ++b) {
         kept = look(b);
         at[0] = add_sat(at[0], kept.rows);
         at[1] = add_sat(at[1], kept.need);
-        at[2] = add_sat(at[2], kept.back);
+        ends |= kept.back > 0;
+    }
+    // Sequences that ended: which of their entries are pages. (In a list, so that rows are spread over the warps, several of
+    // which share a row where there are few: 70 rows of 280 entries on average take 4 us, 13 of 1024 less than 1. A thread for each of
+    // all entries, with its sequence bisected, took 10 and 4.)
+    if (__syncthreads_or(ends)) {
+        int *list = need0, *missing = back0;
+        for (int k = 0; k < each; ++k) {
+            const int b = b_lo + k;
+            if (each > 1 && b < b_hi) kept = look(b);
+            const bool mine = b < b_hi && kept.back > 0;
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, mine), lane = tid & 31;
+            int first = 0;
+            if (lane == 0 && who) first = atomicAdd(&n_ended, __popc(who));
+            first = __shfl_sync(0xFFFFFFFFu, first, 0);
+            if (mine) {
+                list[first + __popc(who & ((1u << lane) - 1u))] = b;
+                past_s[b] = kept.past;
+                missing[b] = 0;
+            }
+        }
+        __syncthreads();
+        constexpr int U = 16;  // entries of a lane at a time
+        const int n = n_ended, share = n < kWarps ? kWarps / n : 1, warp = tid / 32, lane = tid & 31;
+        for (int e = warp / share; e < n; e += kWarps / share) {
+            const int b = list[e], have = pages_of(past_s[b]);
+            const int32_t* row = p.table + static_cast<int64_t>(b) * p.max_pages;
+            int holes = 0;
+            for (int64_t j0 = static_cast<int64_t>(warp % share) * 32 * U + lane; j0 < have; j0 += share * 32 * U) {
+                int page[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k) page[k] = j0 + 32 * k < have ? row[j0 + 32 * k] : 0;
+#pragma unroll
+                for (int k = 0; k < U; ++k) holes += page[k] < 0;
+            }
+            holes = __reduce_add_sync(0xFFFFFFFFu, holes);
+            if (lane == 0 && holes) atomicAdd(&missing[b], holes);
+        }
+        __syncthreads();
+        for (int b = b_lo; b < b_hi; ++b) {
+            if (each > 1) kept = look(b);
+            if (kept.back > 0) kept.back -= missing[b];
+            at[2] = add_sat(at[2], kept.back);
+        }
     }
     block_scan<3>(at, total, part);
     int32_t flags = 0;
@@ -184,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         }
         row0[b] = at[0];
         need0[b] = at[1];
+        const int left = s.back > 0 && each > 1 ? s.back - back0[b] : s.back;  // (back0 still counts what is missing)
         back0[b] = at[2];
         past_s[b] = s.past;
         add_s[b] = ok ? s.add : kUnserved;
@@ -194,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         }
         at[0] = add_sat(at[0], s.rows);
         at[1] = add_sat(at[1], s.need);
-        at[2] = add_sat(at[2], s.back);
+        at[2] = add_sat(at[2], left);
     }
     block_scan<2>(done, done_total, part);
     for (int b = b_lo; b < b_hi; ++b) {
@@ -213,18 +263,34 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
     while (half * 2 < B) half *= 2;
     constexpr int U = 4;  // outputs of a thread at a time
     const int nothing = -1;
+    auto have_of = [&](int b) { return whole_s[b] + (whole_s[b] * T != past_s[b]); };
+    // the entry of page i of those given back, of sequence b
+    auto entry_of = [&](int b, int i) -> const int32_t* {
+        const int32_t* row = p.table + static_cast<int64_t>(b) * p.max_pages;
+        const int have = have_of(b), pages = (b + 1 < B ? back0[b + 1] : total[2]) - back0[b];
+        int k = i - back0[b];
+        if (pages == have) return row + k;
+        if (2 * static_cast<int64_t>(k) < pages) {
+            for (int j = 0; j < have; ++j)
+                if (row[j] >= 0 && k-- == 0) return row + j;
+        } else {
+            k = pages - 1 - k;
+            for (int j = have - 1; j >= 0; --j)
+                if (row[j] >= 0 && k-- == 0) return row + j;
+        }
+        return row;  // (only where the table changes under the call)
+    };
     // where page k of the stack's top lies, counted down: in the stack, or, where this very call gives it back, in its table
     auto given_back = [&](int i) {
         const int ii[1] = {i};
         int b[1];
         owners<1>(back0, B, half, ii, b);
-        return p.table + static_cast<int64_t>(b[0]) * p.max_pages + (i - back0[b[0]]);
+        return entry_of(b[0], i);
     };
     auto popped = [&](int k) -> const int32_t* {
         const int i = top - 1 - k;
         return i < count ? p.stack + i : given_back(i - count);
     };
-    auto have_of = [&](int b) { return whole_s[b] + (whole_s[b] * T != past_s[b]); };
     // and page j of sequence b, cached or new
     auto page_at = [&](int b, int j) -> const int32_t* {
         const int have = have_of(b);
@@ -239,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
         p.starts[B] = n_rows;
         *p.left = top - done_total[1];
     }
+    bool no_page = false;
     for (int64_t r0 = g; r0 < p.rows; r0 += int64_t{U} * step) {
         int r[U], b[U], pos[U], j[U], page[U];
         const int32_t* src[U];
@@ -260,10 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
 #pragma unroll
         for (int k = 0; k < U; ++k)
             if (r[k] < p.rows) {
-                p.slots[r[k]] = src[k] ? static_cast<int64_t>(page[k]) * T + (pos[k] - j[k] * T) : -1;
-                p.positions[r[k]] = pos[k];
+                const bool there = page[k] >= 0;
+                no_page |= src[k] && !there;
+                p.slots[r[k]] = there ? static_cast<int64_t>(page[k]) * T + (pos[k] - j[k] * T) : -1;
+                p.positions[r[k]] = there ? pos[k] : 0;
             }
     }
+    if (no_page) flag_status(p.status, NVFP4KV_STATUS_PAGE_OOB);
     // new pages into the tables, full pages into their list, pages given back on the stack: (sequence, page) pairs alike
     auto copy_pages = [&](const int* first, int n, auto from, auto to) {
         for (int64_t i0 = g; i0 < n; i0 += int64_t{U} * step) {
@@ -281,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) step_tables_kernel(const TablesPa
                 if (i[k] < n) *to(b[k], i[k]) = page[k];
         }
     };
-    copy_pages(back0, returned, [&](int b, int i) -> const int32_t* { return p.table + static_cast<int64_t>(b) * p.max_pages + (i - back0[b]); },
+    copy_pages(back0, returned, [&](int b, int i) { return entry_of(b, i); },
                [&](int, int i) { return p.stack + count + i; });
     copy_pages(need0, done_total[1], [&](int, int i) { return popped(i); },
                [&](int b, int i) { return p.table + static_cast<int64_t>(b) * p.max_pages + have_of(b) + (i - need0[b]); });
