@@ -582,11 +582,14 @@ nvfp4kv_status nvfp4_paged_window_decode_attention(
 /* ------------------------------------------------------------------------------------------
  * nvfp4_paged_decode_attention over FP8 pages: k_t = e4m3 * k_block_scales[page][head] * k_scale, and v_t
  * likewise. The same numerics: K and V are exact in FP16, scales are applied to the scores and the weights
- * in FP32, and the weights are rounded to FP16 before P V.
+ * in FP32, and the weights, times the page's V scale, are rounded to FP16 before P V: relative to 2^-11, and to 2^-25 of
+ * the largest of them that the row sees.
  *   k_pages, v_pages               E4M3 [pool_pages][H][T][D], as nvfp4_kv_fp8_pages, nvfp4_kv_extend_step and
  *                                  nvfp4_kv_dequantize_pages write them
- *   k_block_scales, v_block_scales float [pool_pages][H], each positive and finite, those of V that one
- *                                  sequence reads within a factor of 2^90 (NULL = 1)
+ *   k_block_scales, v_block_scales float [pool_pages][H], each within 2^-100 .. 2^100, those of V that one
+ *                                  sequence reads within a factor of 2^90 (NULL = 1). A page of V that holds no
+ *                                  value at all has scale 1, as nvfp4_kv_fp8_pages writes it (or none above the
+ *                                  others'): it counts in the softmax alone, for others of 2^-58 or more
  *   k_scale, v_scale               device scalars of the whole tensor, positive (NULL = 1)
  *   window, sink_tokens            as above; window = 0: none, every token is visible
  *   workspace      device scratch of nvfp4_paged_fp8_decode_workspace_size(...) bytes; needs no clearing, and

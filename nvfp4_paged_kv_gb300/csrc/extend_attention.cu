@@ -23,7 +23,9 @@
 // Scales. With a page's scales s_K, s_V, a score becomes x = S c s_K + log2(s_V) in log2 units, so that p = 2^(x - m) is the
 // weight times s_V, as the sum over V needs it, with one FMA and one 2^x an element; the sum of the weights takes p / s_V. Q is
 // brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest); P is rounded
-// to FP16 (11 bits, where the output has 8).
+// to FP16 (11 bits, where the output has 8). P is relative to the largest p s_V, so a page must not raise that for nothing: V of a page
+// without a value has scale 1, whatever the others' scales, and beside pages of 2^-20 it would leave them in FP16's subnormals. The
+// scout looks at groups of scale 1, and those that are all 0 take part with a scale of 2^-50 (any is right for them).
 //
 // Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
 // 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
@@ -57,6 +59,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2 units
+constexpr float kZeroScale = 8.8817841970012523e-16f;  // 2^-50: of V that is all 0, below the others', far from where p s_V leaves FP32's range
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126: the least factor of a score (0 would turn a hidden one, -inf, into NaN)
 constexpr int kMaxGroup = 8;
 constexpr int kRowsM = 128;       // rows of a tile
@@ -527,6 +530,37 @@ struct Shared {
     int never;  // (stays 0)
 };
 
+// The groups of a tile (a lane for each; `ones`: those to look at) whose V is 0 in every token that a row of the unit sees. `row` and
+// `a`: a group's first row in the pool and its first token. First a token of each group at once, which settles nearly all of them,
+// then the rest one by one. A whole warp.
+template <int D>
+__device__ __forceinline__ uint32_t zero_groups(const ExtendParams& p, const Unit& u, uint32_t ones, uint32_t row, int a, int lane) {
+    constexpr int GRP = Shape<D>::GRP, EACH = 32 / GRP;
+    auto some = [](const uint4& x) { return ((x.x | x.y | x.z | x.w) & 0x7F7F7F7Fu) != 0u; };
+    {
+        const int g = lane / EACH, ag = __shfl_sync(0xFFFFFFFFu, a, g);
+        const uint32_t rg = __shfl_sync(0xFFFFFFFFu, row, g);
+        const bool mine = (ones >> g) & 1u;
+        const int t = ag < p.sinks ? 0 : max(0, u.lo - ag);  // a token that a row sees
+        const bool any = mine && some(ldg16(p.v + (static_cast<uint64_t>(rg) + t) * D + 16 * (lane % EACH)));
+        const uint32_t found = __ballot_sync(0xFFFFFFFFu, any);
+#pragma unroll
+        for (int k = 0; k < GRP; ++k)
+            if ((found >> (k * EACH)) & ((1u << EACH) - 1u)) ones &= ~(1u << k);
+    }
+    for (uint32_t left = ones; left; left &= left - 1) {
+        const int g = __ffs(static_cast<int>(left)) - 1, ag = __shfl_sync(0xFFFFFFFFu, a, g);
+        const uint8_t* v = p.v + static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, g)) * D;
+        bool any = false;
+        for (int i = lane; i < D; i += 32) {  // 16-byte chunks of 16 tokens
+            const int t = ag + i / (D / 16);
+            if (t < u.hi && (t >= u.lo || t < p.sinks)) any |= some(ldg16(v + 16 * i));
+        }
+        if (__any_sync(0xFFFFFFFFu, any)) ones &= ~(1u << g);
+    }
+    return ones;
+}
+
 // The scout: one warp that walks over the CTA's part and looks up where the KV tiles lie, ahead of the others, into a ring of
 // places. (With every role walking by itself the kernel had 90 KB of code, and 15 % of the warps' time went into waiting for
 // instructions.)
@@ -568,6 +602,8 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
                     if (p.vbs) sv = __ldg(p.vbs + at);
                 }
             }
+            if (const uint32_t ones = __ballot_sync(0xFFFFFFFFu, p.vbs && row != kNoRow && sv == 1.0f))
+                if ((zero_groups<D>(p, w.u, ones, row, a, lane) >> lane) & 1u) sv = kZeroScale;
             const bool seen = t0 + S_::TK <= w.u.hi && (t0 >= w.u.lo || t0 + S_::TK <= p.sinks);
             const bool full = __all_sync(0xFFFFFFFFu, seen && (lane >= S_::GRP || row != kNoRow));
             // V of tile m is stored after the products with V of tile m - 2 are done, hence the weights of that tile made and the
