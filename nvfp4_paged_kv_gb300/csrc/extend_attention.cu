@@ -371,7 +371,9 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 // A warp waits for the phase of this parity. Once a wait of the CTA has given up, `dead`, none waits any more: every role runs
-// through its list over whatever is there (all of it in bounds) and the kernel ends.
+// on over the places that are there until it meets the end of the list, which is what places that were never written say, and what the
+// scout makes of all of them as soon as it sees `dead`. A place may then be read while it is written, so each of its words is in
+// bounds by itself, with whatever flags it is read: rows of the pool (0 where a group has none), rows of q, heads.
 __device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity, volatile int* dead) {
     for (uint32_t i = 0; !__all_sync(0xFFFFFFFFu, mbar_try(bar, parity)); ++i) {
         if (i == kTries) *dead = 1;
@@ -501,11 +503,13 @@ enum PlaceFlags {
     kFull = 16,   // every token of the tile is there and visible to a row
     kWhole = 32,  // the piece is its unit
     kGoesOn = 64, // the piece goes on with a unit that another CTA began
-    kNothing = 128  // the CTA's part is empty
+    kNothing = 128, // the CTA's part is empty
+    kMissing = 256  // times 2^g: group g is not to be read: no page, or no token a row sees
 };
+constexpr int kOver = kNothing | kLast | kEnd;  // no tile, and none after it
 
-// What the other roles need of a KV tile: of its 16-token groups the first token's row in the pools (kNoRow: no page, or no
-// token a row sees) and the scales (s_K, log2 s_V, 1 / s_V); its first token, and its unit: visible are tokens lo .. hi and
+// What the other roles need of a KV tile: of its 16-token groups the first token's row in the pools (0 where it is not to be
+// read) and the scales (s_K, log2 s_V, 1 / s_V); its first token, and its unit: visible are tokens lo .. hi and
 // the first ones; rows of tokens c0 .. c1 of the chunk, whose row 0 is `row0` and has position pos0; KV head h.
 struct Place {
     float4 scales[8];
@@ -572,11 +576,12 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
     if (lane == 0) p.plan[blockIdx.x] = mine;  // (for the join)
     warp_wait(smem_u32(&sh.ended), 0, dead);
     const int64_t part_end = sh.part_end;
-    if (mine.cut >= part_end) {  // nothing to do: the others are told by a place without a tile
-        if (lane == 0) {
-            sh.ring[0].head = make_int4(kNothing, 0, 0, 0);
-            mbar_arrive(smem_u32(&sh.placed[0]));
-        }
+    auto give_up = [&]() {  // (the flags alone: what else a place holds may be in use)
+        if (lane < static_cast<int>(kRing)) *static_cast<volatile int*>(&sh.ring[lane].head.x) = kOver;
+    };
+    if (__any_sync(0xFFFFFFFFu, *dead)) return give_up();
+    if (mine.cut >= part_end) {  // nothing to do: the others are told by a place without a tile (all are at first)
+        if (lane == 0) mbar_arrive(smem_u32(&sh.placed[0]));
         return;
     }
     uint32_t n = 0;
@@ -614,15 +619,17 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
                     if (i == 20 * kTries) *dead = 1;
                 }
                 __syncwarp();
+                if (__any_sync(0xFFFFFFFFu, *dead)) return give_up();
             }
+            const uint32_t missing = __ballot_sync(0xFFFFFFFFu, lane < S_::GRP && row == kNoRow);
             Place& d = sh.ring[n % kRing];
             if (lane < S_::GRP) {
-                d.row[lane] = row;
+                d.row[lane] = row != kNoRow ? row : 0u;
                 d.scales[lane] = row != kNoRow ? make_float4(sk, log2f(sv), 1.0f / sv, 0.0f) : make_float4(1.0f, -INFINITY, 0.0f, 0.0f);
             }
             if (lane == 0) {
                 const bool last = j + 1 == w.piece_tiles;
-                d.head = make_int4(unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0), t0, w.u.lo, w.u.hi);
+                d.head = make_int4(unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0) | static_cast<int>(missing) * kMissing, t0, w.u.lo, w.u.hi);
                 d.unit = make_int4(w.u.t0, w.u.t1, w.s.first, w.s.len - w.s.n);
                 d.h = w.h;
             }
@@ -684,7 +691,7 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
             const uint8_t* src = base + static_cast<uint64_t>(row) * D;
             if (!(flags & kFull)) {
                 const int tok = head.y + r0 + g * R * kLoaderWarps;
-                if (row == kNoRow || tok >= head.w || (tok < head.z && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
+                if ((flags >> (8 + g0 + g * (R * kLoaderWarps / 16))) & 1 || tok >= head.w || (tok < head.z && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
             }
 #pragma unroll
             for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
@@ -837,7 +844,7 @@ __device__ __forceinline__ void softmax_rows(const ExtendParams& p, Shared& sh, 
         if ((u.flags & kNothing) || (S_::MT == 2 && x > 0 && !(u.flags & kTwo))) return;
         const int4 unit = begin.unit;
         const int t = unit.x + x * per + tok;  // token of the chunk
-        u.real = tok < per && t < unit.y;
+        u.real = tok < per && t < unit.y && unit.z + t < p.rows;  // (the last for places read while they are written)
         u.pos = unit.w + (u.real ? t : unit.y - 1);
         // (of the warp's rows, not of the tile's: fewer steps are masked, 16 chunks 508 us, so 513)
         u.first_pos = __reduce_min_sync(0xFFFFFFFFu, u.real ? u.pos : INT32_MAX);
@@ -1065,7 +1072,15 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) extend_kernel(const Exte
             }
             mbar_init(smem_u32(&sh.ofull[i]), 1);
         }
-        for (uint32_t i = 0; i < kRing; ++i) mbar_init(smem_u32(&sh.placed[i]), 1);
+        for (uint32_t i = 0; i < kRing; ++i) {
+            mbar_init(smem_u32(&sh.placed[i]), 1);
+            Place& d = sh.ring[i];
+            for (int g = 0; g < 8; ++g) d.row[g] = 0u;
+            d.head = make_int4(kOver, 0, 0, 0);
+            d.unit = make_int4(0, 0, 0, 0);
+            d.h = 0;
+        }
+        sh.part_end = 0;
         mbar_init(smem_u32(&sh.drained), S_::MT);
         mbar_init(smem_u32(&sh.ended), 1);
         sh.dead = sh.never = 0;
