@@ -20,6 +20,11 @@
 //  * 4 softmax warps per row tile, one row a thread, so that row maxima and sums need no exchange.
 // The running maximum moves only when it grows by more than 2^8, so rescaling O in TMEM is rare.
 //
+// NaN. A hidden token's score is set to -inf, but its weight 0 times a NaN in V is NaN. A tile that hides a token from one row of its
+// unit and not from another (`uneven`: the last tokens of a chunk, a window's begin) is stored with NaN codes of V as 0, and where
+// there were any, the join looks for those that each row sees and puts NaN into their dims. A page whose scale is not
+// finite (nvfp4_kv_fp8_pages, of a page with NaN) has NaN keys instead, so that the rows that see it are NaN and no others.
+//
 // Scales. With a page's scales s_K, s_V, a score becomes x = S c s_K + log2(s_V) in log2 units, so that p = 2^(x - m) is the
 // weight times s_V, as the sum over V needs it, with one FMA and one 2^x an element; the sum of the weights takes p / s_V. Q is
 // brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest); P is rounded
@@ -99,6 +104,7 @@ struct PlanEntry {
     int64_t begin;   // of the unit that holds it: its first position ...
     int64_t end;     // ... and its end
     int32_t b, h, qb, tile;  // the unit, and the first tile
+    int32_t nan, unused;     // the CTA met NaN in V of a tile that is not seen evenly
 };
 
 struct ExtendParams {
@@ -166,6 +172,11 @@ __device__ __forceinline__ Unit unit_of(const ExtendParams& p, const Seq& s, int
     u.first = max(static_cast<int>(static_cast<unsigned>(u.lo) / kTk), u.sink);
     u.tiles = u.sink + static_cast<int>((static_cast<unsigned>(u.hi) + kTk - 1) / kTk) - u.first;
     return u;
+}
+// Tile t0 hides a token from one row of the unit, whose first row has position p0, and not from another.
+template <int D>
+__device__ __forceinline__ bool uneven(const ExtendParams& p, const Unit& u, int p0, int t0) {
+    return p0 + 1 < u.hi && (t0 + Shape<D>::TK - 1 > p0 || (t0 < u.hi - p.window && t0 + Shape<D>::TK > p.sinks));
 }
 // ceil(n / tokens of a unit): the magic number's quotient may be one too large, where n is large.
 template <int D>
@@ -504,7 +515,9 @@ enum PlaceFlags {
     kWhole = 32,  // the piece is its unit
     kGoesOn = 64, // the piece goes on with a unit that another CTA began
     kNothing = 128, // the CTA's part is empty
-    kMissing = 256  // times 2^g: group g is not to be read: no page, or no token a row sees
+    kMissing = 1 << 8,  // times 2^g: group g is not to be read: no page, or no token a row sees
+    kNoNumber = 1 << 16, // times 2^g: group g has a scale that is not finite
+    kUneven = 1 << 24   // a token of the tile is hidden from one row of the unit and not from another
 };
 constexpr int kOver = kNothing | kLast | kEnd;  // no tile, and none after it
 
@@ -595,6 +608,7 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
             const int t0 = tile_start<D>(w.u, w.tile0 + j), a = t0 + 16 * lane;
             uint32_t row = kNoRow;  // (pools have fewer than 2^32 rows)
             float sk = 1.0f, sv = 1.0f;
+            bool no_number = false;
             if (lane < S_::GRP && a < w.u.hi && (a + 15 >= w.u.lo || a < p.sinks)) {
                 const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(a), p.t_magic));
                 const int page = __ldg(p.table + static_cast<int64_t>(w.b) * p.max_pages + idx);
@@ -605,12 +619,17 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
                     row = at * static_cast<uint32_t>(p.T) + static_cast<uint32_t>(a - idx * p.T);
                     if (p.kbs) sk = __ldg(p.kbs + at);
                     if (p.vbs) sv = __ldg(p.vbs + at);
+                    if (!(fabsf(sk) < INFINITY && fabsf(sv) < INFINITY)) {
+                        no_number = true;
+                        sk = sv = 1.0f;
+                    }
                 }
             }
-            if (const uint32_t ones = __ballot_sync(0xFFFFFFFFu, p.vbs && row != kNoRow && sv == 1.0f))
+            const uint32_t no_numbers = __ballot_sync(0xFFFFFFFFu, no_number);
+            if (const uint32_t ones = __ballot_sync(0xFFFFFFFFu, p.vbs && row != kNoRow && sv == 1.0f && !no_number))
                 if ((zero_groups<D>(p, w.u, ones, row, a, lane) >> lane) & 1u) sv = kZeroScale;
             const bool seen = t0 + S_::TK <= w.u.hi && (t0 >= w.u.lo || t0 + S_::TK <= p.sinks);
-            const bool full = __all_sync(0xFFFFFFFFu, seen && (lane >= S_::GRP || row != kNoRow));
+            const bool full = __all_sync(0xFFFFFFFFu, seen && (lane >= S_::GRP || row != kNoRow) && !no_number);
             // V of tile m is stored after the products with V of tile m - 2 are done, hence the weights of that tile made and the
             // places up to it read by all: once V of tile n - 6 is stored, the place of tile n - 8 is free.
             if (n >= kRing) {
@@ -629,7 +648,9 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
             }
             if (lane == 0) {
                 const bool last = j + 1 == w.piece_tiles;
-                d.head = make_int4(unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0) | static_cast<int>(missing) * kMissing, t0, w.u.lo, w.u.hi);
+                d.head = make_int4(unit | (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (last && final ? kEnd : 0) | (full ? kFull : 0) | static_cast<int>(missing) * kMissing |
+                                          static_cast<int>(no_numbers) * kNoNumber | (uneven<D>(p, w.u, w.s.len - w.s.n + w.u.t0, t0) ? kUneven : 0),
+                                      t0, w.u.lo, w.u.hi);
                 d.unit = make_int4(w.u.t0, w.u.t1, w.s.first, w.s.len - w.s.n);
                 d.h = w.h;
             }
@@ -653,6 +674,16 @@ __device__ __forceinline__ void find_end(const ExtendParams& p, Shared& sh, cons
 // What a lane reads for a token that no row sees, or that has no page. (Two branches, one of them without a load, would meet in
 // copies of registers, and those wait for the load.)
 __device__ uint4 g_zeros[16];
+// ... and for K whose scale is not finite: NaN
+#define NANS_16 {0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu, 0x7F7F7F7Fu}
+#define NANS_64 NANS_16, NANS_16, NANS_16, NANS_16
+__device__ uint4 g_nans[16] = {NANS_64, NANS_64, NANS_64, NANS_64};
+#undef NANS_64
+#undef NANS_16
+
+// Where bytes of w are E4M3's NaN (0x7F, 0xFF): their highest bits.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nans(uint32_t w) { return w & ~((nan_bytes(w) >> 7) * 0xFFu); }
 
 // The loader's threads: a warp's load covers R rows of 64 or 128 bytes (whole lines of a row), a lane one 16-byte chunk, which
 // becomes two in the swizzled layout. The eight lanes of a store phase lie in an even row and the odd one after it, four chunks
@@ -691,28 +722,44 @@ __device__ __forceinline__ void load_tiles(const ExtendParams& p, Shared& sh, ui
             const uint8_t* src = base + static_cast<uint64_t>(row) * D;
             if (!(flags & kFull)) {
                 const int tok = head.y + r0 + g * R * kLoaderWarps;
-                if ((flags >> (8 + g0 + g * (R * kLoaderWarps / 16))) & 1 || tok >= head.w || (tok < head.z && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
+                const int group = flags >> (g0 + g * (R * kLoaderWarps / 16));
+                if (group & kMissing || tok >= head.w || (tok < head.z && tok >= p.sinks)) src = reinterpret_cast<const uint8_t*>(g_zeros);
+                else if (group & kNoNumber) src = reinterpret_cast<const uint8_t*>(kv ? g_zeros : g_nans);
             }
 #pragma unroll
             for (int c = 0; c < COLS; ++c) r[g * COLS + c] = ldg16(src + 64 * WIDE * c);
         }
+        uint32_t nans = 0u;
+        if (kv && (flags & kUneven))  // (here, where the warp waits anyway)
+#pragma unroll
+            for (int i = 0; i < N; ++i) nans |= nan_bytes(r[i].x) | nan_bytes(r[i].y) | nan_bytes(r[i].z) | nan_bytes(r[i].w);
         const uint32_t stage = n & 1u;
         warp_wait(empty + 8 * stage, ((n >> 1) & 1u) ^ 1u, dead);
         const uint32_t at = buf + stage * S_::KB, at1 = at ^ 16u;
+        auto store = [&](int g, int c, const uint4& x) {
+            const uint32_t off = WIDE * c * (S_::TK * 128) + g * (R * kLoaderWarps * 128);
+            uint32_t a[2], b[2];
+            e4m3x4_to_f16x2x2(x.x, a);
+            e4m3x4_to_f16x2x2(x.y, b);
+            sts16(at + off, a[0], a[1], b[0], b[1]);
+            e4m3x4_to_f16x2x2(x.z, a);
+            e4m3x4_to_f16x2x2(x.w, b);
+            sts16(at1 + off, a[0], a[1], b[0], b[1]);
+        };
 #pragma unroll
         for (int g = 0; g < LOADS; ++g)
 #pragma unroll
-            for (int c = 0; c < COLS; ++c) {
-                const uint4 x = r[g * COLS + c];
-                const uint32_t off = WIDE * c * (S_::TK * 128) + g * (R * kLoaderWarps * 128);
-                uint32_t a[2], b[2];
-                e4m3x4_to_f16x2x2(x.x, a);
-                e4m3x4_to_f16x2x2(x.y, b);
-                sts16(at + off, a[0], a[1], b[0], b[1]);
-                e4m3x4_to_f16x2x2(x.z, a);
-                e4m3x4_to_f16x2x2(x.w, b);
-                sts16(at1 + off, a[0], a[1], b[0], b[1]);
-            }
+            for (int c = 0; c < COLS; ++c) store(g, c, r[g * COLS + c]);
+        if (nans) {
+            p.plan[blockIdx.x].nan = 1;  // (the scout wrote 0 before the first place)
+#pragma unroll
+            for (int g = 0; g < LOADS; ++g)
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const uint4 x = r[g * COLS + c];
+                    store(g, c, make_uint4(without_nans(x.x), without_nans(x.y), without_nans(x.z), without_nans(x.w)));
+                }
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1148,13 +1195,62 @@ __device__ __forceinline__ float lanes_sum(float v) {
     return v;
 }
 
+// A warp's rows in the join: 32 / kJoinLanes of them from `first` on, and so on in steps of `step`.
+template <int D>
+constexpr int kJoinLanes = D == 64 ? 16 : 32;
+template <int D>
+__device__ __forceinline__ void join_rows(int& first, int& step) {
+    first = (blockIdx.y * 8 + (threadIdx.x >> 5)) * (32 / kJoinLanes<D>);
+    step = gridDim.y * 8 * (32 / kJoinLanes<D>);
+}
+
+// NaN into the dims of outputs of unit (b, h, qb) in which V of a token that the row sees is NaN, of the tiles that load_tiles leaves
+// NaN out of. (Only where there were any.)
+template <int D>
+__device__ __forceinline__ void put_nans(const ExtendParams& p, int b, int h, int qb) {
+    constexpr int EACH = D / 32;  // dims of a lane
+    const Seq s = sequence(p, b);
+    const Unit u = unit_of<D>(p, s, qb);
+    const int p0 = s.len - s.n, lane = threadIdx.x & 31;
+    int first, step;
+    join_rows<D>(first, step);
+    for (int row0 = first; row0 < Shape<D>::MT * kRowsM; row0 += step)
+        for (int row = row0; row < row0 + 32 / kJoinLanes<D>; ++row) {
+            const int x = row / kRowsM, r = row - x * kRowsM, t1 = u.t0 + x * p.per + r / p.G, pos = p0 + t1;
+            if (r / p.G >= p.per || t1 >= u.t1) continue;
+            uint32_t dims = 0u;
+            for (int j = 0; j < u.tiles; ++j) {
+                const int t0 = tile_start<D>(u, j);
+                if (!uneven<D>(p, u, p0 + u.t0, t0)) continue;
+                for (int t = t0; t < t0 + Shape<D>::TK && t <= pos; ++t) {
+                    if (t <= pos - p.window && t >= p.sinks) continue;
+                    const int idx = static_cast<int>(__umul64hi(static_cast<uint64_t>(t), p.t_magic));
+                    const int page = __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + idx);
+                    if (page < 0 || page >= p.pool_pages) continue;
+                    const uint8_t* v = p.v + ((static_cast<int64_t>(page) * p.H + h) * p.T + (t - idx * p.T)) * D + EACH * lane;
+                    for (int k = 0; k < EACH; ++k)
+                        if ((__ldg(v + k) & 0x7F) == 0x7F) dims |= 1u << k;
+                }
+            }
+            uint16_t* out = p.out + (s.first + t1) * p.out_stride + (h * p.G + r % p.G) * D + EACH * lane;
+            for (int k = 0; k < EACH; ++k)
+                if ((dims >> k) & 1u) out[k] = 0x7FC0u;
+        }
+}
+// ... of the units that CTA c begins.
+template <int D>
+__device__ __forceinline__ void put_nans_of(const ExtendParams& p, int c) {
+    Walk<D> w;
+    for (w.start(p, p.plan[c], p.plan[c + 1].cut); w.more(); w.next(p))
+        if (w.tile0 == 0) put_nans<D>(p, w.b, w.h, w.qb);
+}
+
 // Block (c, y): the unit that CTA c begins and others go on with, rows of it for every 8 gridDim.y warps; and the rows of
 // sequences with lengths out of range. A row's pieces lie side by side in a warp (maxima, sums) and its values are all loaded at
 // once, two rows to a warp at head_dim 64. Bound by latency: 8 blocks for each CTA (with 16 a call of one row took 12.5 us, so 11.3; with 6 a
-// chunk of 100 rows at 3000 tokens, ten pieces a unit, 35.5, so 33.4).
+// chunk of 100 rows at 3000 tokens, ten pieces a unit, 35.5, so 33.4). Returns whether a unit that CTA c begins has met NaN (put_nans).
 template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
-    pdl_enter();
+__device__ __forceinline__ bool join_rows_of(const ExtendParams& p) {
     using S_ = Shape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int worker = (blockIdx.x * gridDim.y + blockIdx.y) * 8 + warp, workers = gridDim.x * gridDim.y * 8;
@@ -1171,11 +1267,17 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
         }
     }
     const int c = blockIdx.x;
+    constexpr int N = kJoinLanes<D>, V = D / N;  // lanes of a row, values of a lane
+    const int64_t cut = p.plan[c].cut;
+    bool nan = p.plan[c].nan != 0;
     const PlanEntry next = p.plan[c + 1];
-    if (!(next.cut > next.begin && next.cut < next.end) || next.begin < p.plan[c].cut) return;
+    if (!(next.cut > next.begin && next.cut < next.end) || next.begin < cut) return nan;
+    nan |= next.nan != 0;
     int pieces = 2;  // of the unit: CTA c's, c + 1's and those of the ones after that begin before its end
     for (int k = c + 2;; k += 32) {
-        const int n = __popc(__ballot_sync(0xFFFFFFFFu, k + lane < p.ctas && p.plan[k + lane].cut < next.end));
+        const bool mine = k + lane < p.ctas && p.plan[k + lane].cut < next.end;
+        nan |= __any_sync(0xFFFFFFFFu, mine && p.plan[k + lane].nan != 0);
+        const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine));
         pieces += n;
         if (n < 32) break;
     }
@@ -1183,12 +1285,13 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
     const Unit u = unit_of<D>(p, s, next.qb);
     const int per = p.per;
     const float gv = scalar_or_1(p.gv);
-    constexpr int N = D == 64 ? 16 : 32, V = D / N;  // lanes of a row, values of a lane
     struct alignas(16) Values {
         float x[V];
     };
     const int at = lane % N;
-    for (int row0 = (blockIdx.y * 8 + warp) * (32 / N); row0 < S_::MT * kRowsM; row0 += gridDim.y * 8 * (32 / N)) {
+    int first, step;
+    join_rows<D>(first, step);
+    for (int row0 = first; row0 < S_::MT * kRowsM; row0 += step) {
         const int row = row0 + lane / N, x = row / kRowsM, r = row - x * kRowsM, tok = r / p.G, head = r - tok * p.G;
         const int t = u.t0 + x * per + tok;
         const bool real = tok < per && t < u.t1;
@@ -1238,6 +1341,14 @@ __global__ void __launch_bounds__(256) join_kernel(const ExtendParams p) {
         else *reinterpret_cast<uint4*>(dst) = make_uint4(b[0], b[1], b[2], b[3]);
         if (at == 0 && p.lse) p.lse[out_row * p.Hq + hq] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
+    return nan;
+}
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ ExtendParams p) {
+    pdl_enter();
+    const bool nan = join_rows_of<D>(p);
+    __syncwarp();  // (the rows' outputs are other lanes' stores)
+    if (nan) put_nans_of<D>(p, blockIdx.x);
 }
 
 // ------------------------------------------------------------------------------------------ host
