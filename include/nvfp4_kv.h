@@ -542,6 +542,8 @@ nvfp4kv_status nvfp4_kv_step_tables(
  * do not serve. For every listed page and head, over the page's first page_tokens[i] tokens:
  *   a = max |x|,  s = fp32(a / 448) (1 where that is below 2^-100),  r = fp32(1 / s)
  *   code = E4M3_rne_satfinite(fp32(x r)); the codes of the other tokens are 0
+ * A NaN among them makes s and all their codes NaN; an infinity makes s infinite, its own code NaN and the others 0.
+ * nvfp4_paged_extend_attention keeps such a page from the rows that see none of its tokens.
  * A page that grows is encoded again, as a whole, from its 16-bit copy.
  *   src_dtype      NVFP4KV_BF16, NVFP4KV_FP16: pages [src_pool_pages][H][T][D]; NVFP4KV_NVFP4: packed codes
  *                  in layout.packing with src_scales, x = fp32(v g) as nvfp4_kv_dequantize_pages has it

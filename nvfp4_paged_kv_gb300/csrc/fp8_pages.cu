@@ -4,7 +4,8 @@
 // value becomes E4M3_rne_satfinite(fp32(x fp32(1 / s))); tokens past the valid ones become 0. Each (page, head) is one
 // contiguous run of T x D values, so a CTA takes one run: it loads it once into registers (32 values a thread and
 // step, two 16-value blocks), reduces the maximum through shared memory, and converts what it holds. A run of more than
-// 32768 values is read twice instead, the second time out of L2.
+// 32768 values is read twice instead, the second time out of L2. Maxima are taken over the bits of magnitudes, where NaN is above all
+// else: NaN in a run makes its scale and its valid codes NaN, whatever the run's size.
 //
 // Bound: HBM, 3 bytes a value from 16 bits and 1.5625 from NVFP4. The maximum stands between the loads and the stores of a run,
 // so a CTA alternates between the two; the CTAs of an SM (8 of 128 threads at 64 x 128) keep both under way. 4096 BF16 pages of
@@ -143,15 +144,15 @@ __device__ __forceinline__ Codes unpack(const Packed& r, bool two) {
     return o;
 }
 
-// Largest e2m1 * e4m3 magnitude of a block (exact).
-__device__ __forceinline__ float largest(uint32_t c0, uint32_t c1, uint32_t scale) {
+// Largest e2m1 * e4m3 magnitude of a block (exact), as bits.
+__device__ __forceinline__ uint32_t largest(uint32_t c0, uint32_t c1, uint32_t scale) {
     uint32_t h[8];
     e2m1x8_to_f16x2x4(c0, *reinterpret_cast<uint32_t(*)[4]>(h));
     e2m1x8_to_f16x2x4(c1, *reinterpret_cast<uint32_t(*)[4]>(h + 4));
     __half2 m = __habs2(*reinterpret_cast<const __half2*>(&h[0]));
 #pragma unroll
     for (int k = 1; k < 8; ++k) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&h[k])));
-    return fmaxf(__low2float(m), __high2float(m)) * e4m3_to_f32(scale & 0xFFu);
+    return __float_as_uint(fmaxf(__low2float(m), __high2float(m)) * e4m3_to_f32(scale & 0xFFu)) & 0x7FFFFFFFu;
 }
 
 // Largest magnitudes of a step's low and high halves: positive FP16 and BF16 values order as their bits do.
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
     pdl_enter();
     constexpr bool kPacked = SRC != NVFP4KV_BF16 && SRC != NVFP4KV_FP16;
     constexpr int N = KEPT ? kKept : 1;
-    __shared__ float most[kMaxThreads / 32];
+    __shared__ uint32_t most[kMaxThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const uint32_t blocks = static_cast<uint32_t>(p.T) * p.nb, steps = (blocks + 1) / 2;
     const bool even = blocks % 2 == 0;
@@ -244,14 +245,13 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
         else
             load_16bit(v, p.src + run * blocks * 32, j, b0 < end, b1 < end);
     };
-    uint32_t bits = 0u;
-    float a = 0.0f;
+    uint32_t bits = 0u;  // of 16-bit values: of the low and high halves; packed: of a float
     auto look = [&](const Held& v, uint32_t j) {
         if constexpr (kPacked) {
             uint32_t b0, b1;
             blocks_of<SRC>(p, j, b0, b1);
             const Codes c = unpack<SRC>(v, b1 < end);
-            a = fmaxf(a, fmaxf(largest(c.c[0], c.c[1], c.scales), largest(c.c[2], c.c[3], c.scales >> 8)));
+            bits = max(bits, max(largest(c.c[0], c.c[1], c.scales), largest(c.c[2], c.c[3], c.scales >> 8)));
         } else {
             bits = largest(v, bits);
         }
@@ -288,19 +288,27 @@ __global__ void __launch_bounds__(kMaxThreads) fp8_pages_kernel(const Fp8Params 
     }
     if constexpr (!kPacked) {
         bits = max(bits & 0xFFFFu, bits >> 16);
-        a = SRC == NVFP4KV_BF16 ? __uint_as_float(bits << 16) : f16_lo(bits);
+        bits = SRC == NVFP4KV_BF16 ? bits << 16 : __float_as_uint(f16_lo(bits)) & 0x7FFFFFFFu;
     }
-    a = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(a)));  // (a >= 0: floats order as their bits)
+    bits = __reduce_max_sync(0xFFFFFFFFu, bits);
     if (warps > 1) {
-        if (lane == 0) most[warp] = a;
+        if (lane == 0) most[warp] = bits;
         __syncthreads();
-        for (int w = 0; w < warps; ++w) a = fmaxf(a, most[w]);
+        for (int w = 0; w < warps; ++w) bits = max(bits, most[w]);
     }
+    float a = __uint_as_float(bits);
     if constexpr (kPacked) a = __fmul_rn(a, fabsf(g));  // (the largest of fp32(|v| |g|))
     float s = __fdiv_rn(a, 448.0f);
     if (s < 7.8886090522101181e-31f) s = 1.0f;  // 2^-100: all values become 0
     const float r = __frcp_rn(s);
     if (tid == 0) p.dst_scales[out] = s;
+    if (s != s) {
+        for (uint32_t j = tid; j < blocks; j += blockDim.x) {
+            const uint32_t w = j < end ? 0x7F7F7F7Fu : 0u;
+            *reinterpret_cast<uint4*>(dst + static_cast<size_t>(j) * 16) = make_uint4(w, w, w, w);
+        }
+        return;
+    }
     if constexpr (KEPT) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
