@@ -527,6 +527,8 @@ nvfp4kv_status nvfp4_paged_sparse_decode_attention(
  *                  free_count outside 0 .. free_capacity, which is taken as the nearer of the two
  * A length or addition out of range (p < 0, a < -1, p + a > max_pages_per_seq * T) or rows past num_rows
  * set BAD_SEQ_LEN: the sequence is not served (a bad p counts as 0). Only page_size of the layout is read.
+ * The rows of a sequence that is not served stay between its row_starts, and its length is the old one: an attention
+ * over them is not of this step. Their outputs are to be dropped where slots is -1, and the rows given again.
  * Supported: batch <= 8192. With batch = 0 nothing is written, the padding of slots neither.
  * ------------------------------------------------------------------------------------------ */
 nvfp4kv_status nvfp4_kv_step_tables(
@@ -620,7 +622,9 @@ nvfp4kv_status nvfp4_paged_fp8_decode_attention(
  *   q              BF16, row n at q + n * q_row_stride elements, [heads][D] contiguous in a row; 16-byte
  *                  aligned, strides multiples of 8 and at least num_q_heads * D
  *   row_starts     int32 [batch + 1], ascending, as nvfp4_kv_step_tables writes them
- *   seq_lens       int32 [batch], the chunk included
+ *   seq_lens       int32 [batch], the chunk included: rows whose tokens are not in the pages (of a sequence that
+ *                  nvfp4_kv_step_tables did not serve, which keeps its length) are taken for its last tokens
+ *                  before them, without a status but where they are more than those
  *   k_pages ..     the FP8 pools and their scales, as in nvfp4_paged_fp8_decode_attention, as are window and
  *                  sink_tokens
  *   out            BF16, rows as those of q at out_row_stride; must not overlap q

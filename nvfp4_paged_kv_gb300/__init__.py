@@ -793,7 +793,8 @@ def nvfp4_kv_step_tables(layout: Layout, past_lens: torch.Tensor, new_lens: torc
     `page_table` [B, max pages] int32. Writes
     `seq_lens` [B] (may be past_lens), `row_starts` [B + 1] int32, `slots` int64 and `positions` int32 of the step's rows
     (-1 and 0: no row), `free_left` (None: free_count) and optionally `full_pages` int32, the pages that became full,
-    then -1, of B + rows // page_size entries or more."""
+    then -1, of B + rows // page_size entries or more. A sequence that finds too few pages keeps its length, and its rows, with
+    slots of -1, are to be given again: what an attention makes of them is not of this step."""
     B, maxp, rows = past_lens.shape[0], page_table.shape[-1], slots.shape[0]
     left = free_count if free_left is None else free_left
     dev = _first_device(past_lens, "past_lens")
