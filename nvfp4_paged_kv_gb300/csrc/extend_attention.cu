@@ -30,7 +30,8 @@
 // brought to [2^14, 2^15) by a power of two a row (exact in FP16 but for elements below 2^-31 of the row's largest); P is rounded
 // to FP16 (11 bits, where the output has 8). P is relative to the largest p s_V, so a page must not raise that for nothing: V of a page
 // without a value has scale 1, whatever the others' scales, and beside pages of 2^-20 it would leave them in FP16's subnormals. The
-// scout looks at groups of scale 1, and those that are all 0 take part with a scale of 2^-50 (any is right for them).
+// scout looks at groups of scale 1 where the sequence has others, and those that are all 0 take part with a scale of 2^-50 (any is right
+// for them).
 //
 // Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
 // 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
@@ -547,6 +548,26 @@ struct Shared {
     int never;  // (stays 0)
 };
 
+// Whether a page among the first ones of sequence b, of `tokens` tokens, has a V scale for head h that is not 1. A whole warp.
+__device__ __forceinline__ bool scales_differ(const ExtendParams& p, int b, int h, int tokens, int lane) {
+    const int pages = (tokens + p.T - 1) / p.T;
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int j0 = 0; j0 < pages; j0 += 32 * U) {
+        int page[U];
+        float s[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int j = j0 + 32 * k + lane;
+            page[k] = j < pages ? __ldg(p.table + static_cast<int64_t>(b) * p.max_pages + j) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) s[k] = page[k] >= 0 && page[k] < p.pool_pages ? __ldg(p.vbs + static_cast<int64_t>(page[k]) * p.H + h) : 1.0f;
+        if (__any_sync(0xFFFFFFFFu, s[0] != 1.0f || s[1] != 1.0f || s[2] != 1.0f || s[3] != 1.0f)) return true;
+    }
+    return false;
+}
+
 // The groups of a tile (a lane for each; `ones`: those to look at) whose V is 0 in every token that a row of the unit sees. `row` and
 // `a`: a group's first row in the pool and its first token. First a token of each group at once, which settles nearly all of them,
 // then the rest one by one. A whole warp.
@@ -603,6 +624,7 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
         const int unit = (w.whole() ? kWhole : 0) | (w.tile0 > 0 ? kGoesOn : 0) |
                          (S_::MT == 2 && w.u.t1 - w.u.t0 > p.per ? kTwo : 0);
         const bool final = w.unit_begin + kUnitCost + w.u.tiles >= w.end;
+        enum { kUnknown, kAllOne, kDiffer } scales = kUnknown;  // of V's pages, of this sequence and head
 #pragma unroll 1
         for (int j = 0; j < w.piece_tiles; ++j, ++n) {
             const int t0 = tile_start<D>(w.u, w.tile0 + j), a = t0 + 16 * lane;
@@ -626,8 +648,12 @@ __device__ __forceinline__ void scout_tiles(const ExtendParams& p, Shared& sh, c
                 }
             }
             const uint32_t no_numbers = __ballot_sync(0xFFFFFFFFu, no_number);
-            if (const uint32_t ones = __ballot_sync(0xFFFFFFFFu, p.vbs && row != kNoRow && sv == 1.0f && !no_number))
-                if ((zero_groups<D>(p, w.u, ones, row, a, lane) >> lane) & 1u) sv = kZeroScale;
+            // (where all scales are 1, which a look at the sequence's tells once, V of zeros hides nothing: its loads for every tile
+            // made the scout the slowest role, 16 chunks of 512 rows 594 us for 510)
+            if (const uint32_t ones = __ballot_sync(0xFFFFFFFFu, p.vbs && row != kNoRow && sv == 1.0f && !no_number)) {
+                if (scales == kUnknown) scales = scales_differ(p, w.b, w.h, w.u.hi, lane) ? kDiffer : kAllOne;
+                if (scales == kDiffer && (zero_groups<D>(p, w.u, ones, row, a, lane) >> lane) & 1u) sv = kZeroScale;
+            }
             const bool seen = t0 + S_::TK <= w.u.hi && (t0 >= w.u.lo || t0 + S_::TK <= p.sinks);
             const bool full = __all_sync(0xFFFFFFFFu, seen && (lane >= S_::GRP || row != kNoRow) && !no_number);
             // V of tile m is stored after the products with V of tile m - 2 are done, hence the weights of that tile made and the
