@@ -33,9 +33,11 @@
 // scout looks at groups of scale 1 where the sequence has others, and those that are all 0 take part with a scale of 2^-50 (any is right
 // for them).
 //
-// Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 509 us, 1150 TFLOP/s,
-// 0.60 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.63 ms, 1325 TFLOP/s, 0.69; 24 ragged sequences with a
-// window at head_dim 64 (15.6 GFLOP): 56.0 us.
+// Measured (one GB300): 16 chunks of 512 rows behind 4096 tokens, 32 heads on 8, head_dim 128 (584 GFLOP): 510 us, 1145 TFLOP/s,
+// 0.59 of the bf16 product rate; 2048 rows at 65536 tokens (2.16 TFLOP): 1.66 ms, 1300 TFLOP/s, 0.67; 24 ragged sequences with a
+// window at head_dim 64 (15.6 GFLOP): 60 us; 8 chunks of 256 rows behind 4096 tokens at head_dim 256 (284 GFLOP), which has one row
+// tile and 64 tokens a KV tile: 406 us, 700 TFLOP/s, 0.36. A few per cent from one GPU to another; further times here are from one each.
+// The flags for NaN cost 0.5 % of the long cases, 1 to 2 % of ragged ones, 1.4 of 18 us for a single row at 3000 tokens.
 // Bound, at head_dim 128: the tensor core, busy for nine tenths of the time (in the long case, 3600 clocks for 256 x 128 scores),
 // with products at less than its rate. A 128 x 64 x 16 product with both operands in shared memory takes 72 clocks, hardly more than
 // a 128 x 128 x 16 one (64): its 128 rows of Q have to be read either way. Scores of 128 tokens at once leave no room in TMEM (512

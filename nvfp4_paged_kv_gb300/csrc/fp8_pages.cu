@@ -9,9 +9,9 @@
 //
 // Bound: HBM, 3 bytes a value from 16 bits and 1.5625 from NVFP4. The maximum stands between the loads and the stores of a run,
 // so a CTA alternates between the two; the CTAs of an SM (8 of 128 threads at 64 x 128) keep both under way. 4096 BF16 pages of
-// 64 tokens, 8 heads, 128 dims (805 MB): 131 us, 6.1 TB/s, 0.90 of the copy rate. 1024 NVFP4 pages (105 MB): 24.9 us, 4.2 TB/s,
-// 0.62: 3 of it launch and the first loads, the rest 8.3 instructions a value and their waits (10.2 and 28 us with every value
-// converted by itself; CTAs that go on to further runs, 26.7, and load the next one ahead of the stores, the same).
+// 64 tokens, 8 heads, 128 dims (805 MB): 130 us, 6.2 TB/s, 0.91 of the copy rate. 1024 NVFP4 pages (105 MB): 24.0 us, 4.4 TB/s,
+// 0.64 (in token pairs 30 us): 3 of it launch and the first loads, the rest 8.4 instructions a value and their waits (10.2 and 28 us
+// with every value converted by itself; CTAs that go on to further runs, 2 us more, and load the next one ahead of the stores, the same).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>

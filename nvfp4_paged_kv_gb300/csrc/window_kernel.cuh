@@ -21,13 +21,13 @@
 // beside pages of 2^-20 it would leave them in FP16's subnormals. Before the maximum grows, a tile of scale 1 is therefore looked
 // at, and where all of it is 0 it takes part with a scale of 2^-50 (any is right for it).
 //
-// Measured (head_dim 128, 32 heads on 8): FP8, 32 sequences of 8192 tokens (537 MB) 99.9 us, 5.4 TB/s, 0.79 of the copy rate.
+// Measured (head_dim 128, 32 heads on 8): FP8, 32 sequences of 8192 tokens (537 MB) 98 to 101 us, 5.4 TB/s, 0.79 of the copy rate.
 // Bound by the latency of a warp's own chain (3 warps a scheduler, an instruction each 7 clocks): 10 % fewer instructions
 // gave 1.5 %, three slots instead of two at head_dim 64 and 256, where they fit, nothing; 12 warps instead of 8 at
-// head_dim 256 took 93 us for 87. NVFP4 with a window of 4096 and 4 first tokens, 32 sequences (151 MB) 43.0 us, of which start
-// and join are 15; one sequence of 1005 tokens 10.9 us, all latency. FP8, head_dim 256, 19 ragged sequences with a window of
-// 2048, pages of 16 (100 MB) 33.8 us.
-//
+// head_dim 256 took 93 us for 87. NVFP4 with a window of 4096 and 4 first tokens, 32 sequences (151 MB) 43 us, of which start
+// and join are 15; one sequence of 1005 tokens 11.5 us, all latency. FP8, head_dim 256, 19 ragged sequences with a window of
+// 2048, pages of 16 (100 MB) 27 to 33 us by their lengths, 34 to 50 with one to six sequences of length 0 among them: a thread of the
+// first CTA writes the outputs of each before that CTA's runs begin.
 #pragma once
 #include <algorithm>
 
